@@ -358,6 +358,95 @@ int moe_decode_fwd(const moe_shape *shape, const uint16_t *x,
                    const void *packed, uint16_t *out, void *ws,
                    size_t ws_bytes, void *stream);
 
+/* ------------------------------------------- rows sorted by expert and back */
+
+/* The layer's data movement as operators of its own, for experts computed
+ * elsewhere: tokens sorted by expert, the experts' rows returned with the
+ * routing weights applied, and the gradient of both -- for routings in which
+ * not every slot has a row here (one GPU's share of the experts, padded
+ * tokens), segments aligned to a GEMM's row tile, bf16, fp16 or fp32 rows of
+ * any width and stride (dispatch, combine and their two backward mirrors
+ * [KC §01]).
+ *
+ * Slot f = t*k + j is kept if first_expert <= topk_idx[f] < first_expert +
+ * experts; any other id (an expert of another GPU, -1 for a padded token)
+ * masks the slot: it has no row, adds nothing, and its weight, whatever it
+ * holds, is not used.  The rows of expert e (0-based here) are
+ * [offsets[e], offsets[e] + counts[e]), ascending in f; offsets[e] are
+ * multiples of align.  Rows [offsets[e] + counts[e], offsets[e+1]) are
+ * padding: zeros in x_sorted and dy, not read from y and dx_sorted.  Rows
+ * from offsets[experts] on are left as they were.
+ *
+ * Limits: 0 <= tokens <= 2^24, 1 <= top_k <= 16, 1 <= experts <= 1024,
+ * 1 <= width <= 2^20, align <= 1024, strides of at least width and at most
+ * 2^32 values.  Row buffers need their type's alignment only and must not
+ * overlap the outputs.  No entry point reads a host copy of any of these
+ * arrays, so all of them can be captured into a graph (with a workspace of
+ * its own where calls may overlap).  counts, offsets and inv_perm are as
+ * moe_sort_layout writes them and are not checked. */
+enum { MOE_ROW_BF16 = 0, MOE_ROW_F16 = 1, MOE_ROW_F32 = 2 };
+
+typedef struct moe_sort_shape {
+  int32_t tokens;       /* T; 0 is allowed */
+  int32_t experts;      /* E: experts held here */
+  int32_t top_k;        /* k */
+  int32_t width;        /* values of one row */
+  int32_t row_type;     /* MOE_ROW_* */
+  int32_t align;        /* rows an expert's segment starts at a multiple of (0, 1: none) */
+  int32_t first_expert; /* the id of expert 0 here */
+  int64_t token_stride; /* values from one token's row to the next: x, dx,
+                           out, add, dout (0: width) */
+  int64_t row_stride;   /* the same of the sorted rows: x_sorted, dx_sorted,
+                           y, dy (0: width) */
+} moe_sort_shape;
+
+/* Rows a sorted buffer must hold: T*k + min(E, T*k) * (align - 1), the most
+ * that offsets[E] can reach.  -1 for a shape that is refused. */
+int64_t moe_sort_max_rows(const moe_sort_shape *shape);
+
+/* Bytes of workspace of moe_sort_layout and moe_sort_fwd (0: refused). */
+size_t moe_sort_workspace_bytes(const moe_sort_shape *shape);
+
+/* The layout: topk_idx [T][k] -> counts [E], offsets [E+1], perm
+ * [moe_sort_max_rows] (the slot of each row; -1 in padding rows and from
+ * offsets[E] on), inv_perm [T][k] (the row of each slot, -1 if masked).
+ * Bit-exact and deterministic. */
+int moe_sort_layout(const moe_sort_shape *shape, const int32_t *topk_idx,
+                    int32_t *counts, int32_t *offsets, int32_t *perm,
+                    int32_t *inv_perm, void *ws, size_t ws_bytes, void *stream);
+
+/* x_sorted[inv_perm[t][j]] = x[t] for every kept slot; padding rows zero. */
+int moe_sort_rows(const moe_sort_shape *shape, const void *x,
+                  const int32_t *counts, const int32_t *offsets,
+                  const int32_t *inv_perm, void *x_sorted, void *stream);
+
+/* moe_sort_layout and moe_sort_rows in one call. */
+int moe_sort_fwd(const moe_sort_shape *shape, const void *x,
+                 const int32_t *topk_idx, int32_t *counts, int32_t *offsets,
+                 int32_t *perm, int32_t *inv_perm, void *x_sorted, void *ws,
+                 size_t ws_bytes, void *stream);
+
+/* Gradient of moe_sort_rows: dx[t] = sum over the kept slots of
+ * dx_sorted[inv_perm[t][j]], in fp32 in ascending j, rounded once. */
+int moe_sort_bwd(const moe_sort_shape *shape, const void *dx_sorted,
+                 const int32_t *inv_perm, void *dx, void *stream);
+
+/* Weighted return: out[t] = sum over the kept slots of topk_w[t][j] *
+ * y[inv_perm[t][j]], plus add[t] (NULL: nothing; its gradient is dout), in
+ * fp32 in ascending j, add last, rounded once.  topk_w [T][k] fp32 (NULL:
+ * ones).  A token without a kept slot gets add[t], or zeros. */
+int moe_unsort_fwd(const moe_sort_shape *shape, const void *y,
+                   const float *topk_w, const int32_t *inv_perm,
+                   const void *add, void *out, void *stream);
+
+/* Gradient of moe_unsort_fwd: dy[inv_perm[t][j]] = topk_w[t][j] * dout[t]
+ * (padding rows zero) and dtopk_w[t][j] = <dout[t], y[inv_perm[t][j]]> in
+ * fp32, 0 for a masked slot.  dtopk_w NULL: only dy, and y may be NULL. */
+int moe_unsort_bwd(const moe_sort_shape *shape, const void *dout, const void *y,
+                   const float *topk_w, const int32_t *counts,
+                   const int32_t *offsets, const int32_t *inv_perm, void *dy,
+                   float *dtopk_w, void *stream);
+
 /* Device pointers into a forward context (host call, no device work):
  * where moe_layer_fwd left each intermediate.  Any field may be NULL in
  * the result when the shape has no such tensor. */

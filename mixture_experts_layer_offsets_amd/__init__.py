@@ -7,12 +7,16 @@ libmoe's HIP kernels.
 """
 from ._lib import (MOE_BF16, MOE_ERR_DEVICE_TIMEOUT, MOE_MXFP8, MOE_MXFP8_W4,  # noqa: F401
                    MOE_MXFP8_W6, MOE_MXFP8_W6E3M2, MOE_OK, MoeError,
+                   MOE_ROW_BF16, MOE_ROW_F16, MOE_ROW_F32,
                    MOE_SCHED_PERSISTENT, MOE_SCHED_PIPELINED, MOE_SCHED_STAGED,
-                   MoeSched, Shape, WEIGHT_FORMAT, load,
+                   MoeSched, Shape, SortShape, WEIGHT_FORMAT, load,
                    moe_combine, moe_decode_fwd, moe_dispatch, moe_expert_ffn, moe_layer_bwd, moe_layer_fwd,
                    moe_layout, moe_layout_noalloc, moe_packed_pointers, moe_packed_weight_bytes,
                    moe_prepare_weights,
                    moe_read_status,
                    moe_route, moe_router_logits, moe_saved_bytes, moe_saved_pointers,
-                   moe_strerror, moe_workspace_bytes, moe_workspace_pointers)
+                   moe_sort_bwd, moe_sort_fwd, moe_sort_layout, moe_sort_max_rows, moe_sort_rows,
+                   moe_sort_workspace_bytes, moe_strerror, moe_unsort_bwd, moe_unsort_fwd,
+                   moe_workspace_bytes, moe_workspace_pointers)
 from .layer import MoeLayer  # noqa: F401
+from .sort import TokenSort  # noqa: F401

@@ -31,6 +31,9 @@ WEIGHT_FORMAT = {MOE_MXFP8: "e4m3", MOE_MXFP8_W4: "e2m1", MOE_MXFP8_W6: "e2m3",
 MOE_SCHED_STAGED = 0
 MOE_SCHED_PERSISTENT = 1
 MOE_SCHED_PIPELINED = 2
+MOE_ROW_BF16 = 0
+MOE_ROW_F16 = 1
+MOE_ROW_F32 = 2
 
 c_void_p = ctypes.c_void_p
 c_size_t = ctypes.c_size_t
@@ -78,6 +81,14 @@ SIGNATURES = {
     "moe_layer_fwd": (c_int, [c_void_p] * 10 + [c_void_p, c_size_t, c_void_p]),
     "moe_layer_bwd": (c_int, [c_void_p] * 14 + [c_void_p, c_size_t, c_void_p]),
     "moe_decode_fwd": (c_int, [c_void_p] * 8 + [c_void_p, c_size_t, c_void_p]),
+    "moe_sort_max_rows": (ctypes.c_int64, [c_void_p]),
+    "moe_sort_workspace_bytes": (c_size_t, [c_void_p]),
+    "moe_sort_layout": (c_int, [c_void_p] * 6 + [c_void_p, c_size_t, c_void_p]),
+    "moe_sort_rows": (c_int, [c_void_p] * 6 + [c_void_p]),
+    "moe_sort_fwd": (c_int, [c_void_p] * 8 + [c_void_p, c_size_t, c_void_p]),
+    "moe_sort_bwd": (c_int, [c_void_p] * 4 + [c_void_p]),
+    "moe_unsort_fwd": (c_int, [c_void_p] * 6 + [c_void_p]),
+    "moe_unsort_bwd": (c_int, [c_void_p] * 9 + [c_void_p]),
     "moe_saved_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
     "moe_packed_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
     "moe_workspace_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
@@ -126,6 +137,38 @@ class Shape:
                         self.shared_inter, self.dtype)
 
 
+class MoeSortShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("row_type", ctypes.c_int32), ("align", ctypes.c_int32),
+                ("first_expert", ctypes.c_int32), ("token_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+@dataclass(frozen=True)
+class SortShape:
+    """moe_sort_shape: rows of `width` values for the slots of `tokens` x
+    `top_k` that go to the `experts` held here."""
+    tokens: int
+    experts: int
+    top_k: int
+    width: int
+    row_type: int = MOE_ROW_BF16
+    align: int = 1
+    first_expert: int = 0
+    token_stride: int = 0
+    row_stride: int = 0
+
+    def c(self) -> MoeSortShape:
+        # kept with the (frozen) shape: one struct per shape, not per call
+        s = self.__dict__.get("_c")
+        if s is None:
+            s = MoeSortShape(self.tokens, self.experts, self.top_k, self.width, self.row_type,
+                             self.align, self.first_expert, self.token_stride, self.row_stride)
+            object.__setattr__(self, "_c", s)
+        return s
+
+
 def _p(t):
     """Pointer of a torch tensor (or None -> NULL)."""
     if t is None:
@@ -148,7 +191,7 @@ def _ck(rc: int, where: str):
 
 
 def _shape(shape) -> ctypes.Structure:
-    s = shape.c() if isinstance(shape, Shape) else shape
+    s = shape if isinstance(shape, ctypes.Structure) else shape.c()
     return ctypes.byref(s)
 
 
@@ -236,6 +279,47 @@ def moe_decode_fwd(shape, x, w_router, bias, topk_idx_in, topk_w_in, packed, out
     _ck(load().moe_decode_fwd(_shape(shape), _p(x), _p(w_router), _p(bias), _p(topk_idx_in),
                               _p(topk_w_in), _p(packed), _p(out), _p(ws),
                               ws.numel() * ws.element_size(), _stream(stream)), "moe_decode_fwd")
+
+
+def moe_sort_max_rows(shape) -> int:
+    return load().moe_sort_max_rows(_shape(shape))
+
+
+def moe_sort_workspace_bytes(shape) -> int:
+    return load().moe_sort_workspace_bytes(_shape(shape))
+
+
+def moe_sort_layout(shape, topk_idx, counts, offsets, perm, inv_perm, ws, stream=None):
+    _ck(load().moe_sort_layout(_shape(shape), _p(topk_idx), _p(counts), _p(offsets), _p(perm),
+                               _p(inv_perm), _p(ws), ws.numel() * ws.element_size(),
+                               _stream(stream)), "moe_sort_layout")
+
+
+def moe_sort_rows(shape, x, counts, offsets, inv_perm, x_sorted, stream=None):
+    _ck(load().moe_sort_rows(_shape(shape), _p(x), _p(counts), _p(offsets), _p(inv_perm),
+                             _p(x_sorted), _stream(stream)), "moe_sort_rows")
+
+
+def moe_sort_fwd(shape, x, topk_idx, counts, offsets, perm, inv_perm, x_sorted, ws, stream=None):
+    _ck(load().moe_sort_fwd(_shape(shape), _p(x), _p(topk_idx), _p(counts), _p(offsets), _p(perm),
+                            _p(inv_perm), _p(x_sorted), _p(ws), ws.numel() * ws.element_size(),
+                            _stream(stream)), "moe_sort_fwd")
+
+
+def moe_sort_bwd(shape, dx_sorted, inv_perm, dx, stream=None):
+    _ck(load().moe_sort_bwd(_shape(shape), _p(dx_sorted), _p(inv_perm), _p(dx), _stream(stream)),
+        "moe_sort_bwd")
+
+
+def moe_unsort_fwd(shape, y, topk_w, inv_perm, add, out, stream=None):
+    _ck(load().moe_unsort_fwd(_shape(shape), _p(y), _p(topk_w), _p(inv_perm), _p(add), _p(out),
+                              _stream(stream)), "moe_unsort_fwd")
+
+
+def moe_unsort_bwd(shape, dout, y, topk_w, counts, offsets, inv_perm, dy, dtopk_w, stream=None):
+    _ck(load().moe_unsort_bwd(_shape(shape), _p(dout), _p(y), _p(topk_w), _p(counts), _p(offsets),
+                              _p(inv_perm), _p(dy), _p(dtopk_w), _stream(stream)),
+        "moe_unsort_bwd")
 
 
 def moe_saved_pointers(shape, saved) -> dict:

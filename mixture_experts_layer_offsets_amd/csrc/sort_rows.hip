@@ -1,0 +1,638 @@
+// Tokens sorted by expert and back, with weights applied, and the gradients.
+//
+// With f = t k + j the flat (token, slot) index and e(f) = idx[f] - first the
+// slot's expert here, a slot is kept if 0 <= e(f) < E; the others (experts of
+// another GPU, padded tokens) have no row.
+//   counts[e]  = kept slots of expert e
+//   offsets[e] = sum over e' < e of counts[e'] rounded up to a multiple of A
+//   inv[f]     = offsets[e] + #{f' < f : e(f') = e(f)}, or -1; perm its
+//                inverse, -1 in the padding and behind offsets[E]
+//   sort:    xs[inv[f]] = x[t]                  backward: dx[t] = sum_j dxs[inv]
+//   unsort:  out[t] = sum_j w[f] y[inv[f]] (+ add[t])
+//            backward: dy[inv[f]] = w[f] dout[t],  dw[f] = <dout[t], y[inv[f]]>
+// Sums run in fp32 in ascending j (dw: a fixed tree over the columns), so
+// every result is the same from run to run.  A masked slot is never read: its
+// weight and whatever lies in rows that no slot owns have no effect.
+//
+// Every kernel here only moves rows, so the bound is HBM: each row read once,
+// each row written once.  A lane moves 16 bytes at a time whatever the row's
+// width, stride or alignment: global accesses of 16 bytes need no alignment
+// on this GPU, and a row whose bytes are no multiple of 16 ends with a chunk
+// that starts 16 bytes before the row's end and overlaps its neighbour (both
+// lanes store the same bytes).  Rows narrower than 16 bytes take the
+// `narrow` kernels, one lane per token.
+#include <algorithm>
+
+#include "common.h"
+#include "sort_rows.h"
+
+namespace moe {
+
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kSortMaxK = 16;   // top-k bound of the library
+constexpr int kRowBlock = 64;   // one wave per workgroup for the gathers (see combine_kernel)
+constexpr int kPadSplit = 8;    // workgroups that share one expert's padding rows
+
+// 16 bytes at any alignment, read or written once.
+__device__ __forceinline__ u32x4 ld16(const char *p) {
+  return __builtin_nontemporal_load((const u32x4u *)p);
+}
+__device__ __forceinline__ void st16(char *p, const u32x4 &v) { *(u32x4u *)p = v; }
+__device__ __forceinline__ void st16_once(char *p, const u32x4 &v) {
+  __builtin_nontemporal_store((u32x4u)v, (u32x4u *)p);
+}
+
+// A row element type: N values in 16 bytes, and both conversions (to nearest
+// even, NaN and infinities kept).
+struct Bf16 {
+  typedef uint16_t S;
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void widen(const u32x4 &v, float *f) {
+    const uint4 u = make_uint4(v.x, v.y, v.z, v.w);
+    unpack8(u, f);
+  }
+  static __device__ __forceinline__ u32x4 narrow(const float *f) {
+    f32x8 t;
+#pragma unroll
+    for (int q = 0; q < 8; q++) t[q] = f[q];
+    return __builtin_bit_cast(u32x4, __builtin_convertvector(t, bf16x8));
+  }
+  static __device__ __forceinline__ float get(S s) { return bf16_to_f32(s); }
+  static __device__ __forceinline__ S put(float f) { return __builtin_bit_cast(S, (__bf16)f); }
+};
+struct F16 {
+  typedef uint16_t S;
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void widen(const u32x4 &v, float *f) {
+    const f32x8 t = __builtin_convertvector(__builtin_bit_cast(f16x8, v), f32x8);
+#pragma unroll
+    for (int q = 0; q < 8; q++) f[q] = t[q];
+  }
+  static __device__ __forceinline__ u32x4 narrow(const float *f) {
+    f32x8 t;
+#pragma unroll
+    for (int q = 0; q < 8; q++) t[q] = f[q];
+    return __builtin_bit_cast(u32x4, __builtin_convertvector(t, f16x8));
+  }
+  static __device__ __forceinline__ float get(S s) { return (float)__builtin_bit_cast(_Float16, s); }
+  static __device__ __forceinline__ S put(float f) { return __builtin_bit_cast(S, (_Float16)f); }
+};
+struct F32 {
+  typedef uint32_t S;
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void widen(const u32x4 &v, float *f) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) f[q] = __uint_as_float(v[q]);
+  }
+  static __device__ __forceinline__ u32x4 narrow(const float *f) {
+    u32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; q++) v[q] = __float_as_uint(f[q]);
+    return v;
+  }
+  static __device__ __forceinline__ float get(S s) { return __uint_as_float(s); }
+  static __device__ __forceinline__ S put(float f) { return __float_as_uint(f); }
+};
+
+// Expert of a flat row here, or -1.  The difference is taken in 64 bits: ids
+// are the caller's and may be anything.
+__device__ __forceinline__ int local_expert(int32_t id, int first, int E) {
+  const int64_t e = (int64_t)id - first;
+  return e >= 0 && e < E ? (int)e : -1;
+}
+
+__device__ __forceinline__ int round_rows(int n, int align) {
+  return align > 1 ? (n + align - 1) / align * align : n;
+}
+
+// ---------------------------------------------------------------------------
+// Layout.  count: per-chunk histograms (kSortChunk flat rows a workgroup), and
+// perm filled with -1.  place: every workgroup adds up the histograms of all
+// chunks (totals) and of the chunks before its own, scans the totals over the
+// experts and ranks its rows: lanes of a wave with the same expert find each
+// other by ballots over the bits of the id.  Integers only, no order but f's.
+
+__global__ __launch_bounds__(256) void sort_count_kernel(const int32_t *__restrict__ idx, int R,
+                                                         int first, int E, int chunk,
+                                                         int32_t *__restrict__ chunk_counts,
+                                                         int32_t *__restrict__ perm, int cap) {
+  extern __shared__ int32_t cnt[];
+  for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * chunk;
+  for (int i = threadIdx.x; i < chunk; i += 256) {
+    const int64_t f = base + i;
+    if (f < R) {
+      const int e = local_expert(idx[f], first, E);
+      if (e >= 0) atomicAdd(&cnt[e], 1);
+    }
+  }
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < cap; r += (int64_t)gridDim.x * 256)
+    perm[r] = -1;
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256) chunk_counts[(size_t)blockIdx.x * E + e] = cnt[e];
+}
+
+// Exclusive scan over the experts of the padded counts: thread i owns experts
+// [i per, (i + 1) per).  cnt and off are LDS; off gets E + 1 entries.
+template <int THREADS>
+__device__ __forceinline__ void scan_experts(const int32_t *cnt, int32_t *off, int E, int align,
+                                             int32_t *wave_sum_lds) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (E + THREADS - 1) / THREADS;
+  int sum = 0;
+  for (int i = 0; i < per; i++) {
+    const int e = tid * per + i;
+    if (e < E) sum += round_rows(cnt[e], align);
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 63) wave_sum_lds[wave] = inc;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < wave; w++) at += wave_sum_lds[w];
+  for (int i = 0; i < per; i++) {
+    const int e = tid * per + i;
+    if (e < E) {
+      off[e] = at;
+      at += round_rows(cnt[e], align);
+      if (e == E - 1) off[E] = at;
+    }
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(256) void sort_place_kernel(
+    const int32_t *__restrict__ idx, int R, int first, int E, int align, int chunk, int nchunks,
+    const int32_t *__restrict__ chunk_counts, int32_t *__restrict__ counts,
+    int32_t *__restrict__ offsets, int32_t *__restrict__ perm, int32_t *__restrict__ inv) {
+  extern __shared__ int32_t sm[];
+  int32_t *tot = sm;             // [E] rows of each expert
+  int32_t *run = tot + E;        // [E] next free row of each expert for this chunk
+  int32_t *off = run + E;        // [E + 1]
+  int32_t *wcnt = off + E + 1;   // [4][E] rows of each expert per wave in this round
+  __shared__ int32_t wsum[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < E; e += 256) {
+    tot[e] = run[e] = 0;
+    wcnt[e] = wcnt[E + e] = wcnt[2 * E + e] = wcnt[3 * E + e] = 0;
+  }
+  __syncthreads();
+  // few experts: several threads share an expert's column of the histograms
+  int ep = 1;
+  while (ep < E && ep < 256) ep <<= 1;
+  const int parts = 256 / ep, part = tid / ep;
+  for (int e = tid % ep; e < E; e += ep) {
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int c = part; c < nchunks; c += parts) {
+      const int n = chunk_counts[(size_t)c * E + e];
+      all += n;
+      before += c < (int)blockIdx.x ? n : 0;
+    }
+    if (all) atomicAdd(&tot[e], all);
+    if (before) atomicAdd(&run[e], before);
+  }
+  __syncthreads();
+  scan_experts<256>(tot, off, E, align, wsum);
+  for (int e = tid; e < E; e += 256) {
+    run[e] += off[e];
+    if (blockIdx.x == 0) {
+      counts[e] = tot[e];
+      offsets[e] = off[e];
+      if (e == E - 1) offsets[E] = off[E];
+    }
+  }
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * chunk;
+  const int bits = 32 - __clz(E);  // ids -1 .. E - 1, as e + 1 <= E
+  for (int round = 0; round < chunk / 256; round++) {
+    const int64_t f = base + round * 256 + tid;
+    const int e = f < R ? local_expert(idx[f], first, E) : -1;
+    uint64_t mine = ~0ull;
+    for (int b = 0; b < bits; b++) {
+      const bool bit = ((e + 1) >> b) & 1;
+      const uint64_t m = __ballot(bit);
+      mine &= bit ? m : ~m;
+    }
+    const uint64_t below = lane ? (~0ull >> (64 - lane)) : 0ull;
+    const int rank = __popcll(mine & below), n = __popcll(mine);
+    const bool lead = e >= 0 && rank == 0;
+    if (lead) wcnt[wave * E + e] = n;
+    __syncthreads();
+    if (f < R) {
+      int pos = -1;
+      if (e >= 0) {
+        pos = run[e] + rank;
+        for (int w = 0; w < wave; w++) pos += wcnt[w * E + e];
+        perm[pos] = (int32_t)f;
+      }
+      inv[f] = pos;
+    }
+    __syncthreads();
+    if (lead) {
+      atomicAdd(&run[e], n);
+      wcnt[wave * E + e] = 0;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows.
+
+// How a launch maps lanes to rows: 2^lsh lanes share a token (all 64 when its
+// row has 64 chunks or more, then grid y walks the row), 64 >> lsh tokens a
+// wave; `token_blocks` workgroups hold tokens, the ones behind them (E x
+// kPadSplit) zero the padding rows.
+struct RowGrid {
+  int lsh, token_blocks;
+  unsigned y;
+};
+
+RowGrid row_grid(int T, long row_bytes) {
+  const long nc = (row_bytes + 15) / 16;
+  RowGrid g;
+  g.lsh = 0;
+  while (g.lsh < 6 && (1L << g.lsh) < nc) g.lsh++;
+  const int per = 64 >> g.lsh;
+  g.token_blocks = (T + per - 1) / per;
+  g.y = (unsigned)((nc + 63) >> 6);
+  return g;
+}
+
+// Zeroes the padding rows [offsets[e] + counts[e], offsets[e + 1]) of one
+// expert, this workgroup's share: `sub` of `subs` workgroups, and the wave's
+// lanes split over rows and chunks as for tokens.
+__device__ __forceinline__ void zero_padding(const int32_t *counts, const int32_t *offsets, int e,
+                                             int sub, int subs, int lsh, char *rows, long RB,
+                                             long stride) {
+  const int lane = threadIdx.x & 63;
+  const long c = ((long)blockIdx.y << 6) + (lane & ((1 << lsh) - 1));
+  if (c * 16 >= RB) return;
+  const long at = min(c * 16, RB - 16);
+  const int end = offsets[e + 1], per = 64 >> lsh;
+  for (int r = offsets[e] + counts[e] + sub * per + (lane >> lsh); r < end; r += subs * per)
+    st16(rows + r * stride + at, (u32x4){0, 0, 0, 0});
+}
+
+// xs[inv[t k + j]] = x[t]: each token's row is read once and stored to its
+// kept rows.
+template <int KMAX>
+__global__ __launch_bounds__(kRowBlock) void sort_rows_kernel(
+    const char *__restrict__ x, const int32_t *__restrict__ inv, const int32_t *__restrict__ counts,
+    const int32_t *__restrict__ offsets, char *__restrict__ xs, int T, int k, long RB, long xstride,
+    long rstride, RowGrid g) {
+  const int lane = threadIdx.x;
+  if ((int)blockIdx.x >= g.token_blocks) {
+    const int p = blockIdx.x - g.token_blocks;
+    zero_padding(counts, offsets, p / kPadSplit, p % kPadSplit, kPadSplit, g.lsh, xs, RB, rstride);
+    return;
+  }
+  const int t = blockIdx.x * (64 >> g.lsh) + (lane >> g.lsh);
+  const long c = ((long)blockIdx.y << 6) + (lane & ((1 << g.lsh) - 1));
+  if (t >= T || c * 16 >= RB) return;
+  const long at = min(c * 16, RB - 16);
+  int row[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; j++) row[j] = inv[(long)t * k + min(j, k - 1)];
+  const u32x4 v = ld16(x + t * xstride + at);
+#pragma unroll
+  for (int j = 0; j < KMAX; j++)
+    if (j < k && row[j] >= 0) st16(xs + row[j] * rstride + at, v);
+}
+
+// out[t] = sum_j (w) y[inv[t k + j]] (+ add[t]).
+template <class E, int KMAX, bool WEIGHT, bool ADD>
+__global__ __launch_bounds__(kRowBlock) void unsort_kernel(
+    const char *__restrict__ y, const float *__restrict__ w, const int32_t *__restrict__ inv,
+    const char *__restrict__ add, char *__restrict__ out, int T, int k, long RB, long tstride,
+    long rstride, RowGrid g) {
+  const int lane = threadIdx.x;
+  const int t = blockIdx.x * (64 >> g.lsh) + (lane >> g.lsh);
+  const long c = ((long)blockIdx.y << 6) + (lane & ((1 << g.lsh) - 1));
+  if (t >= T || c * 16 >= RB) return;
+  const long at = min(c * 16, RB - 16);
+  int row[KMAX];
+  float wt[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; j++) {
+    row[j] = inv[(long)t * k + min(j, k - 1)];
+    if constexpr (WEIGHT) wt[j] = w[(long)t * k + min(j, k - 1)];
+  }
+  // the indices are needed here: one round trip for all of them, then one for
+  // all rows
+#pragma unroll
+  for (int j = 0; j < KMAX; j++) asm volatile("" ::"v"(row[j]));
+  u32x4 rv[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; j++)
+    if (j < k && row[j] >= 0) rv[j] = ld16(y + row[j] * rstride + at);
+  u32x4 av;
+  if constexpr (ADD) av = ld16(add + t * tstride + at);
+  float acc[E::N];
+#pragma unroll
+  for (int q = 0; q < E::N; q++) acc[q] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < KMAX; j++) {
+    if (j < k && row[j] >= 0) {
+      float v[E::N];
+      E::widen(rv[j], v);
+#pragma unroll
+      for (int q = 0; q < E::N; q++) {
+        if constexpr (WEIGHT) acc[q] = fmaf(wt[j], v[q], acc[q]);
+        else acc[q] += v[q];
+      }
+    }
+  }
+  if constexpr (ADD) {
+    float v[E::N];
+    E::widen(av, v);
+#pragma unroll
+    for (int q = 0; q < E::N; q++) acc[q] += v[q];
+  }
+  st16_once(out + t * tstride + at, E::narrow(acc));
+}
+
+// dy[inv[f]] = w[f] dout[t]; dw[f] = <dout[t], y[inv[f]]>.  WPT waves share a
+// token: four for rows of more than 128 chunks (one token a workgroup), else
+// one (four tokens a workgroup).
+template <class E, int KMAX, bool DW, int WPT>
+__global__ __launch_bounds__(256) void unsort_bwd_kernel(
+    const char *__restrict__ dout, const char *__restrict__ y, const float *__restrict__ w,
+    const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets,
+    const int32_t *__restrict__ inv, char *__restrict__ dy, float *__restrict__ dw, int T, int k,
+    long RB, long tstride, long rstride, int token_blocks) {
+  __shared__ float red[KMAX][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if ((int)blockIdx.x >= token_blocks) {
+    const int p = blockIdx.x - token_blocks, e = p / kPadSplit;
+    const int end = offsets[e + 1];
+    for (int r = offsets[e] + counts[e] + p % kPadSplit; r < end; r += kPadSplit)
+      for (long c = tid; c * 16 < RB; c += 256)
+        st16(dy + r * rstride + min(c * 16, RB - 16), (u32x4){0, 0, 0, 0});
+    return;
+  }
+  const int t = WPT == 4 ? blockIdx.x : blockIdx.x * 4 + wave;
+  const bool live = t < T;
+  int row[KMAX];
+  float wt[KMAX], part[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; j++) {
+    part[j] = 0.0f;
+    row[j] = live ? inv[(long)t * k + min(j, k - 1)] : -1;
+    wt[j] = live ? w[(long)t * k + min(j, k - 1)] : 0.0f;
+  }
+  constexpr int kStep = 64 * WPT;
+  if (live) {
+    for (long c = WPT == 4 ? tid : lane; c * 16 < RB; c += kStep) {
+      const long at = min(c * 16, RB - 16);
+      const int skip = (int)(c * 16 - at) / (16 / E::N);  // values of an overlapping last chunk
+      const u32x4 dv = ld16(dout + t * tstride + at);
+      u32x4 yv[KMAX];
+      if constexpr (DW) {
+#pragma unroll
+        for (int j = 0; j < KMAX; j++)
+          if (j < k && row[j] >= 0) yv[j] = ld16(y + row[j] * rstride + at);
+      }
+      float d[E::N];
+      E::widen(dv, d);
+#pragma unroll
+      for (int j = 0; j < KMAX; j++) {
+        if (j < k && row[j] >= 0) {
+          float o[E::N];
+#pragma unroll
+          for (int q = 0; q < E::N; q++) o[q] = wt[j] * d[q];
+          st16(dy + row[j] * rstride + at, E::narrow(o));
+          if constexpr (DW) {
+            float v[E::N], s = 0.0f;
+            E::widen(yv[j], v);
+#pragma unroll
+            for (int q = 0; q < E::N; q++) s = q >= skip ? fmaf(d[q], v[q], s) : s;
+            part[j] += s;
+          }
+        }
+      }
+    }
+  }
+  if constexpr (DW) {
+#pragma unroll
+    for (int j = 0; j < KMAX; j++) part[j] = j < k ? wave_sum(part[j]) : 0.0f;
+    if constexpr (WPT == 4) {
+#pragma unroll
+      for (int j = 0; j < KMAX; j++)
+        if (lane == 0) red[j][wave] = part[j];
+      __syncthreads();
+      if (tid < k) dw[(long)t * k + tid] = (red[tid][0] + red[tid][1]) + (red[tid][2] + red[tid][3]);
+    } else if (live) {
+#pragma unroll
+      for (int j = 0; j < KMAX; j++)
+        if (lane == 0 && j < k) dw[(long)t * k + j] = part[j];
+    }
+  }
+}
+
+// Rows narrower than 16 bytes: one lane per token (and, behind them, one per
+// padding-row share of an expert), value by value.
+template <class E>
+__global__ __launch_bounds__(256) void narrow_kernel(
+    NarrowOp op, const typename E::S *__restrict__ a, const typename E::S *__restrict__ b,
+    const float *__restrict__ w, const int32_t *__restrict__ counts,
+    const int32_t *__restrict__ offsets, const int32_t *__restrict__ inv,
+    typename E::S *__restrict__ o, float *__restrict__ dw, int T, int experts, int k, int D,
+    long tstride, long rstride) {
+  const long id = (long)blockIdx.x * 256 + threadIdx.x;
+  if (id >= T) {
+    // padding rows of the row outputs (sort, unsort backward)
+    if (id >= (long)T + experts || !offsets) return;
+    const int e = (int)(id - T);
+    for (int r = offsets[e] + counts[e]; r < offsets[e + 1]; r++)
+      for (int q = 0; q < D; q++) o[r * rstride + q] = 0;
+    return;
+  }
+  const int t = (int)id;
+  for (int q = 0; op == NARROW_UNSORT && q < D; q++) {
+    float acc = 0.0f;
+    for (int j = 0; j < k; j++) {
+      const int r = inv[(long)t * k + j];
+      if (r < 0) continue;
+      const float v = E::get(a[r * rstride + q]);
+      acc = w ? fmaf(w[(long)t * k + j], v, acc) : acc + v;
+    }
+    if (b) acc += E::get(b[t * tstride + q]);
+    o[t * tstride + q] = E::put(acc);
+  }
+  for (int j = 0; op != NARROW_UNSORT && j < k; j++) {
+    const int r = inv[(long)t * k + j];
+    float s = 0.0f;
+    for (int q = 0; r >= 0 && q < D; q++) {
+      const typename E::S v = a[t * tstride + q];
+      if (op == NARROW_SORT) {
+        o[r * rstride + q] = v;
+        continue;
+      }
+      const float d = E::get(v);
+      o[r * rstride + q] = E::put(w[(long)t * k + j] * d);
+      if (dw) s = fmaf(d, E::get(b[r * rstride + q]), s);
+    }
+    if (op == NARROW_UNSORT_BWD && dw) dw[(long)t * k + j] = s;
+  }
+}
+
+}  // namespace
+
+int sort_chunk(long R) {
+  // at most kSortMaxChunks histograms, of whole rounds of 256 rows
+  const long c = (R + kSortMaxChunks - 1) / kSortMaxChunks;
+  return (int)std::max<long>(kSortChunk, (c + 255) / 256 * 256);
+}
+
+long sort_workspace_words(const SortDims &d) {
+  const int chunk = sort_chunk(d.R);
+  return (d.R + chunk - 1) / chunk * d.E;
+}
+
+void launch_sort_layout(const SortDims &d, const int32_t *idx, int32_t *counts, int32_t *offsets,
+                        int32_t *perm, int32_t *inv, int32_t *ws, hipStream_t s) {
+  const int chunk = sort_chunk(d.R), E = d.E;
+  // no rows: one empty chunk, so that counts, offsets and perm are written
+  const int n = (int)std::max<long>(1, (d.R + chunk - 1) / chunk);
+  hipLaunchKernelGGL(sort_count_kernel, dim3(n), dim3(256), E * sizeof(int32_t), s, idx, (int)d.R,
+                     d.first, E, chunk, ws, perm, (int)d.cap);
+  hipLaunchKernelGGL(sort_place_kernel, dim3(n), dim3(256), (7 * E + 1) * sizeof(int32_t), s, idx,
+                     (int)d.R, d.first, E, d.align, chunk, n, ws, counts, offsets, perm, inv);
+}
+
+namespace {
+
+template <class E>
+void launch_narrow(NarrowOp op, const SortDims &d, const void *a, const void *b, const float *w,
+                   const int32_t *counts, const int32_t *offsets, const int32_t *inv, void *o,
+                   float *dw, hipStream_t s) {
+  typedef typename E::S S;
+  const long n = d.T + (offsets ? d.E : 0);
+  hipLaunchKernelGGL(narrow_kernel<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, op,
+                     (const S *)a, (const S *)b, w, counts, offsets, inv, (S *)o, dw, (int)d.T, d.E,
+                     d.k, d.D, d.tstride, d.rstride);
+}
+
+void launch_narrow(NarrowOp op, const SortDims &d, const void *a, const void *b, const float *w,
+                   const int32_t *counts, const int32_t *offsets, const int32_t *inv, void *o,
+                   float *dw, hipStream_t s) {
+  if (d.type == kRowBf16) launch_narrow<Bf16>(op, d, a, b, w, counts, offsets, inv, o, dw, s);
+  else if (d.type == kRowF16) launch_narrow<F16>(op, d, a, b, w, counts, offsets, inv, o, dw, s);
+  else launch_narrow<F32>(op, d, a, b, w, counts, offsets, inv, o, dw, s);
+}
+
+}  // namespace
+
+void launch_sort_rows(const SortDims &d, const void *x, const int32_t *counts,
+                      const int32_t *offsets, const int32_t *inv, void *xs, hipStream_t s) {
+  if (d.T <= 0) return;
+  const long RB = (long)d.D * d.esize;
+  if (d.align <= 1) offsets = nullptr;  // packed segments have no padding rows
+  if (RB < 16) return launch_narrow(NARROW_SORT, d, x, nullptr, nullptr, counts, offsets, inv, xs,
+                                    nullptr, s);
+  const RowGrid g = row_grid((int)d.T, RB);
+  const dim3 grid(g.token_blocks + (offsets ? d.E * kPadSplit : 0), g.y), b(kRowBlock);
+  const long xst = d.tstride * d.esize, rst = d.rstride * d.esize;
+  if (d.k <= 8)
+    hipLaunchKernelGGL(sort_rows_kernel<8>, grid, b, 0, s, (const char *)x, inv, counts, offsets,
+                       (char *)xs, (int)d.T, d.k, RB, xst, rst, g);
+  else
+    hipLaunchKernelGGL(sort_rows_kernel<kSortMaxK>, grid, b, 0, s, (const char *)x, inv, counts,
+                       offsets, (char *)xs, (int)d.T, d.k, RB, xst, rst, g);
+}
+
+namespace {
+
+template <class E, int KMAX, bool WEIGHT, bool ADD>
+void go_unsort(const SortDims &d, const void *y, const float *w, const int32_t *inv,
+               const void *add, void *out, hipStream_t s) {
+  const long RB = (long)d.D * d.esize;
+  const RowGrid g = row_grid((int)d.T, RB);
+  hipLaunchKernelGGL((unsort_kernel<E, KMAX, WEIGHT, ADD>), dim3(g.token_blocks, g.y),
+                     dim3(kRowBlock), 0, s, (const char *)y, w, inv, (const char *)add, (char *)out,
+                     (int)d.T, d.k, RB, d.tstride * d.esize, d.rstride * d.esize, g);
+}
+
+template <class E>
+void pick_unsort(const SortDims &d, const void *y, const float *w, const int32_t *inv,
+                 const void *add, void *out, hipStream_t s) {
+  if (d.k <= 8) {
+    if (w && add) go_unsort<E, 8, true, true>(d, y, w, inv, add, out, s);
+    else if (w) go_unsort<E, 8, true, false>(d, y, w, inv, add, out, s);
+    else if (add) go_unsort<E, 8, false, true>(d, y, w, inv, add, out, s);
+    else go_unsort<E, 8, false, false>(d, y, w, inv, add, out, s);
+  } else {
+    if (w && add) go_unsort<E, kSortMaxK, true, true>(d, y, w, inv, add, out, s);
+    else if (w) go_unsort<E, kSortMaxK, true, false>(d, y, w, inv, add, out, s);
+    else if (add) go_unsort<E, kSortMaxK, false, true>(d, y, w, inv, add, out, s);
+    else go_unsort<E, kSortMaxK, false, false>(d, y, w, inv, add, out, s);
+  }
+}
+
+template <class E, int KMAX, bool DW>
+void go_unsort_bwd(const SortDims &d, const void *dout, const void *y, const float *w,
+                   const int32_t *counts, const int32_t *offsets, const int32_t *inv, void *dy,
+                   float *dw, hipStream_t s) {
+  const long RB = (long)d.D * d.esize;
+  const bool wide = RB > 128 * 16;
+  const int tb = wide ? (int)d.T : (int)((d.T + 3) / 4);
+  const dim3 grid(tb + (offsets ? d.E * kPadSplit : 0)), b(256);
+  const long ts = d.tstride * d.esize, rs = d.rstride * d.esize;
+  if (wide)
+    hipLaunchKernelGGL((unsort_bwd_kernel<E, KMAX, DW, 4>), grid, b, 0, s, (const char *)dout,
+                       (const char *)y, w, counts, offsets, inv, (char *)dy, dw, (int)d.T, d.k, RB,
+                       ts, rs, tb);
+  else
+    hipLaunchKernelGGL((unsort_bwd_kernel<E, KMAX, DW, 1>), grid, b, 0, s, (const char *)dout,
+                       (const char *)y, w, counts, offsets, inv, (char *)dy, dw, (int)d.T, d.k, RB,
+                       ts, rs, tb);
+}
+
+template <class E>
+void pick_unsort_bwd(const SortDims &d, const void *dout, const void *y, const float *w,
+                     const int32_t *counts, const int32_t *offsets, const int32_t *inv, void *dy,
+                     float *dw, hipStream_t s) {
+  if (d.k <= 8 && dw) go_unsort_bwd<E, 8, true>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+  else if (d.k <= 8) go_unsort_bwd<E, 8, false>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+  else if (dw) go_unsort_bwd<E, kSortMaxK, true>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+  else go_unsort_bwd<E, kSortMaxK, false>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+}
+
+}  // namespace
+
+void launch_unsort(const SortDims &d, const void *y, const float *w, const int32_t *inv,
+                   const void *add, void *out, hipStream_t s) {
+  if (d.T <= 0) return;
+  if ((long)d.D * d.esize < 16)
+    return launch_narrow(NARROW_UNSORT, d, y, add, w, nullptr, nullptr, inv, out, nullptr, s);
+  if (d.type == kRowBf16) pick_unsort<Bf16>(d, y, w, inv, add, out, s);
+  else if (d.type == kRowF16) pick_unsort<F16>(d, y, w, inv, add, out, s);
+  else pick_unsort<F32>(d, y, w, inv, add, out, s);
+}
+
+void launch_unsort_bwd(const SortDims &d, const void *dout, const void *y, const float *w,
+                       const int32_t *counts, const int32_t *offsets, const int32_t *inv, void *dy,
+                       float *dw, hipStream_t s) {
+  if (d.T <= 0) return;
+  if (d.align <= 1) offsets = nullptr;
+  if ((long)d.D * d.esize < 16)
+    return launch_narrow(NARROW_UNSORT_BWD, d, dout, y, w, counts, offsets, inv, dy, dw, s);
+  if (d.type == kRowBf16) pick_unsort_bwd<Bf16>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+  else if (d.type == kRowF16) pick_unsort_bwd<F16>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+  else pick_unsort_bwd<F32>(d, dout, y, w, counts, offsets, inv, dy, dw, s);
+}
+
+}  // namespace moe
