@@ -447,6 +447,105 @@ int moe_unsort_bwd(const moe_sort_shape *shape, const void *dout, const void *y,
                    const int32_t *offsets, const int32_t *inv_perm, void *dy,
                    float *dtopk_w, void *stream);
 
+/* ------------------------------------------------------- 4-bit expert weights */
+
+/* Products of a few rows with 4-bit weights and group scales, and the
+ * few-token layer on such experts: moe_decode_fwd's counterpart for weights
+ * kept in 4 bits, which are read as they are (the pages mention 4-bit expert
+ * kernels and a decode kernel for inference, noticiai.com.br, "Por que a
+ * camada MoE virou o gargalo" and [NA design]).  Activations are bf16, sums
+ * fp32; no weight is rounded beyond its 4-bit form.
+ *
+ * MOE_W4_MXFP4: w = 2^(s - 127) * E2M1(code), group_size 32, s an E8M0 byte
+ *   up to 252 (larger ones stand for values past bf16's range: the outputs
+ *   they reach are not finite).
+ * MOE_W4_INT4: w = s * (q - z), q in 0..15, group_size 32, 64 or 128, s bf16
+ *   or fp16, z a zero point in 0..15 per group, or 8 everywhere (zeros = 0).
+ *   The kernels form sums of x * (16 + q): x must stay below 2^120. */
+enum { MOE_W4_MXFP4 = 0, MOE_W4_INT4 = 1 };
+enum { MOE_SCALE_BF16 = 0, MOE_SCALE_F16 = 1 };
+
+/* 4-bit matrices [groups][k][n] of products x*W.  Limits: 1 <= groups <=
+ * 1024, n >= 1, k a multiple of 32 and of group_size, n and k at most 2^20. */
+typedef struct moe_w4_shape {
+  int32_t groups;
+  int32_t n;          /* outputs */
+  int32_t k;          /* contraction */
+  int32_t format;     /* MOE_W4_* */
+  int32_t group_size; /* values along k that share a scale */
+  int32_t scale_type; /* MOE_SCALE_* (INT4) */
+  int32_t zeros;      /* 1: zero points (INT4) */
+} moe_w4_shape;
+
+/* Bytes of the packed weights (0: refused). */
+size_t moe_w4_bytes(const moe_w4_shape *shape);
+
+/* Lay ready-made codes out for the kernels (once; `packed` is opaque).
+ * codes [groups][n][k/2] (byte i: value 2i in the low nibble, 2i+1 in the
+ * high one), scales [groups][n][k/group_size] (uint8 E8M0, or 16 bits of the
+ * scale type), zeros the same in uint8 (NULL without zero points). */
+int moe_w4_pack(const moe_w4_shape *shape, const uint8_t *codes,
+                const void *scales, const uint8_t *zeros, void *packed,
+                void *stream);
+
+/* Quantise bf16 weights w [groups][k][n] (finite values) into packed ones.
+ * MXFP4: the OCP MX conversion, as moe_prepare_weights makes it for
+ * MOE_MXFP8_W4.  INT4 without zero
+ * points: s = max|w| / 7, q = rint(w / s) + 8; with: s = (max(w, 0) -
+ * min(w, 0)) / 15, z = rint(-min(w, 0) / s), q = rint(w / s) + z, clamped to
+ * 0..15; s rounded to its type first; all steps in fp32. */
+int moe_w4_quantize(const moe_w4_shape *shape, const uint16_t *w, void *packed,
+                    void *stream);
+
+/* The values that packed weights stand for: w [groups][k][n] fp32. */
+int moe_w4_unpack(const moe_w4_shape *shape, const void *packed, float *w,
+                  void *stream);
+
+/* out[r] = bf16(x[r] * W_g) for the rows r in [offsets[g], offsets[g+1]) of
+ * each group (device, [groups+1], ascending, at most `rows`; other rows of out
+ * are left as they were), or with offsets NULL and groups = 1 for all rows.
+ * x: rows of k bf16 values, x_stride apart; out: rows of n, out_stride apart
+ * (strides in values).  Made for few rows per group: every 64 rows of a group
+ * read its weights once.  rows may be 0. */
+int moe_w4_linear(const moe_w4_shape *shape, int32_t rows, const uint16_t *x,
+                  int64_t x_stride, const int32_t *offsets, const void *packed,
+                  uint16_t *out, int64_t out_stride, void *stream);
+
+/* The experts of a layer in 4 bits: packed matrices of one format, gate and
+ * up [experts][H][I], down [experts][I][H], and the shared expert's [1][H][Is]
+ * and [1][Is][H] (all three NULL without one). */
+typedef struct moe_w4_experts {
+  int32_t format;
+  int32_t group_size;
+  int32_t scale_type;
+  int32_t zeros;
+  int32_t first_expert;  /* supplied routing: the id of expert 0 here; slots
+                            with ids outside [first_expert, first_expert +
+                            experts) add nothing */
+  const void *gate;
+  const void *up;
+  const void *down;
+  const void *shared_gate;
+  const void *shared_up;
+  const void *shared_down;
+} moe_w4_experts;
+
+/* Bytes of workspace of moe_w4_decode_fwd (0: refused). */
+size_t moe_w4_decode_workspace_bytes(const moe_shape *shape);
+
+/* Few-token inference forward on 4-bit experts: out[t] = bf16(sum over the
+ * slots of topk_w * (silu(x Wg) * (x Wu)) Wd, plus the shared expert), the
+ * product of silu rounded to bf16 as the layer does, all other sums in fp32 in
+ * a fixed order.  Arguments as moe_decode_fwd, with the experts in 4 bits;
+ * shape->dtype MOE_BF16, T*k <= 4096, H, I and the shared I multiples of the
+ * group size.  A router (first_expert 0) re-decides over the experts here;
+ * supplied routing may name experts elsewhere. */
+int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts,
+                      const uint16_t *x, const uint16_t *w_router,
+                      const float *bias, const int32_t *topk_idx_in,
+                      const float *topk_w_in, uint16_t *out, void *ws,
+                      size_t ws_bytes, void *stream);
+
 /* Device pointers into a forward context (host call, no device work):
  * where moe_layer_fwd left each intermediate.  Any field may be NULL in
  * the result when the shape has no such tensor. */

@@ -34,6 +34,10 @@ MOE_SCHED_PIPELINED = 2
 MOE_ROW_BF16 = 0
 MOE_ROW_F16 = 1
 MOE_ROW_F32 = 2
+MOE_W4_MXFP4 = 0
+MOE_W4_INT4 = 1
+MOE_SCALE_BF16 = 0
+MOE_SCALE_F16 = 1
 
 c_void_p = ctypes.c_void_p
 c_size_t = ctypes.c_size_t
@@ -89,6 +93,14 @@ SIGNATURES = {
     "moe_sort_bwd": (c_int, [c_void_p] * 4 + [c_void_p]),
     "moe_unsort_fwd": (c_int, [c_void_p] * 6 + [c_void_p]),
     "moe_unsort_bwd": (c_int, [c_void_p] * 9 + [c_void_p]),
+    "moe_w4_bytes": (c_size_t, [c_void_p]),
+    "moe_w4_pack": (c_int, [c_void_p] * 5 + [c_void_p]),
+    "moe_w4_quantize": (c_int, [c_void_p] * 3 + [c_void_p]),
+    "moe_w4_unpack": (c_int, [c_void_p] * 3 + [c_void_p]),
+    "moe_w4_linear": (c_int, [c_void_p, ctypes.c_int32, c_void_p, ctypes.c_int64] +
+                      [c_void_p] * 3 + [ctypes.c_int64, c_void_p]),
+    "moe_w4_decode_workspace_bytes": (c_size_t, [c_void_p]),
+    "moe_w4_decode_fwd": (c_int, [c_void_p] * 8 + [c_void_p, c_size_t, c_void_p]),
     "moe_saved_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
     "moe_packed_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
     "moe_workspace_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
@@ -167,6 +179,38 @@ class SortShape:
                              self.align, self.first_expert, self.token_stride, self.row_stride)
             object.__setattr__(self, "_c", s)
         return s
+
+
+class MoeW4Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("groups", "n", "k", "format", "group_size",
+                                              "scale_type", "zeros")]
+
+
+@dataclass(frozen=True)
+class W4Shape:
+    """moe_w4_shape: 4-bit matrices [groups][k][n] of products x*W."""
+    groups: int
+    n: int
+    k: int
+    format: int = MOE_W4_MXFP4
+    group_size: int = 32
+    scale_type: int = MOE_SCALE_BF16
+    zeros: int = 0
+
+    def c(self) -> MoeW4Shape:
+        s = self.__dict__.get("_c")
+        if s is None:
+            s = MoeW4Shape(self.groups, self.n, self.k, self.format, self.group_size,
+                           self.scale_type, self.zeros)
+            object.__setattr__(self, "_c", s)
+        return s
+
+
+class MoeW4Experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("format", "group_size", "scale_type", "zeros",
+                                              "first_expert")] + \
+               [(n, c_void_p) for n in ("gate", "up", "down", "shared_gate", "shared_up",
+                                        "shared_down")]
 
 
 def _p(t):
@@ -320,6 +364,45 @@ def moe_unsort_bwd(shape, dout, y, topk_w, counts, offsets, inv_perm, dy, dtopk_
     _ck(load().moe_unsort_bwd(_shape(shape), _p(dout), _p(y), _p(topk_w), _p(counts), _p(offsets),
                               _p(inv_perm), _p(dy), _p(dtopk_w), _stream(stream)),
         "moe_unsort_bwd")
+
+
+def moe_w4_bytes(shape) -> int:
+    return load().moe_w4_bytes(_shape(shape))
+
+
+def moe_w4_pack(shape, codes, scales, zeros, packed, stream=None):
+    _ck(load().moe_w4_pack(_shape(shape), _p(codes), _p(scales), _p(zeros), _p(packed),
+                           _stream(stream)), "moe_w4_pack")
+
+
+def moe_w4_quantize(shape, w, packed, stream=None):
+    _ck(load().moe_w4_quantize(_shape(shape), _p(w), _p(packed), _stream(stream)),
+        "moe_w4_quantize")
+
+
+def moe_w4_unpack(shape, packed, w, stream=None):
+    _ck(load().moe_w4_unpack(_shape(shape), _p(packed), _p(w), _stream(stream)), "moe_w4_unpack")
+
+
+def moe_w4_linear(shape, x, offsets, packed, out, stream=None):
+    """x [rows][k] and out [rows][n]: rows one stride apart, values contiguous."""
+    rows = x.shape[0]
+    # a single row's stride says nothing
+    xs, os_ = (x.stride(0), out.stride(0)) if rows > 1 else (x.shape[1], out.shape[1])
+    _ck(load().moe_w4_linear(_shape(shape), rows, _p(x), xs, _p(offsets), _p(packed), _p(out), os_,
+                             _stream(stream)), "moe_w4_linear")
+
+
+def moe_w4_decode_workspace_bytes(shape) -> int:
+    return load().moe_w4_decode_workspace_bytes(_shape(shape))
+
+
+def moe_w4_decode_fwd(shape, experts, x, w_router, bias, topk_idx_in, topk_w_in, out, ws,
+                      stream=None):
+    _ck(load().moe_w4_decode_fwd(_shape(shape), _shape(experts), _p(x), _p(w_router), _p(bias),
+                                 _p(topk_idx_in), _p(topk_w_in), _p(out), _p(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)),
+        "moe_w4_decode_fwd")
 
 
 def moe_saved_pointers(shape, saved) -> dict:

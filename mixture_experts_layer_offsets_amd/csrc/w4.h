@@ -1,0 +1,44 @@
+// Host-side launchers of w4.hip (all asynchronous on stream `s`).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kW4Mx = 0, kW4Int = 1;
+constexpr int kW4MaxSlots = 4096;  // T*k of one few-token layer call, at most
+
+// A checked moe_w4_shape and the pieces of its packed buffer.  Tiles of 16
+// outputs x 128 contraction values: nt = ceil(n / 16), ks = ceil(k / 128);
+// spg scales per output and tile.  See w4.hip for the layout of a tile.
+struct W4Dims {
+  int groups, n, k, fmt, group, f16_scales, zeros;
+  int nt, ks, spg;
+  size_t code_bytes, scale_bytes, zero_bytes;  // each piece, rounded up to 256
+  size_t bytes() const { return code_bytes + scale_bytes + zero_bytes; }
+};
+
+void launch_w4_pack(const W4Dims &d, const uint8_t *codes, const void *scales,
+                    const uint8_t *zeros, void *packed, hipStream_t s);
+void launch_w4_quantize(const W4Dims &d, const uint16_t *w, void *packed, hipStream_t s);
+void launch_w4_unpack(const W4Dims &d, const void *packed, float *w, hipStream_t s);
+
+// out[r][:] = x[r] W_g for the rows r in [offsets[g], offsets[g + 1]) (offsets
+// null: one group, all rows).
+void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride,
+                      const int32_t *offsets, const void *packed, uint16_t *out, long ostride,
+                      hipStream_t s);
+
+// The few-token expert FFN.  idx [slots]: the slots' expert ids (first = id of
+// expert 0; others are masked); idx null: one expert, every token a slot
+// (k = 1).  act [slots][I] bf16, y [slots][H] fp32, at the slots' places.
+void launch_w4_ffn(const W4Dims &up, const W4Dims &down, const uint16_t *x, const int32_t *idx,
+                   int slots, int k, int first, const void *gate, const void *upw,
+                   const void *downw, uint16_t *act, float *y, hipStream_t s);
+// out[t] = sum_j w[t][j] y[t k + j] over the kept slots (+ ys[t]).
+void launch_w4_combine(const float *y, const float *w, const int32_t *idx, int first, int E,
+                       const float *ys, uint16_t *out, int T, int k, int H, hipStream_t s);
+
+}  // namespace moe
