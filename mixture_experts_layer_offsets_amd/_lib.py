@@ -222,10 +222,20 @@ def _p(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            # the raw handle of the current device's current stream: without
+            # the Stream object that torch.cuda.current_stream() makes (0.3
+            # instead of 2.8 us a call)
+            dev, raw = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+            _current_stream = lambda: raw(dev())  # noqa: E731
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -34,6 +34,14 @@ size_t workspace_bytes(const SortDims &d) {
   return ((size_t)(sort_workspace_words(d) + 1) * sizeof(int32_t) + 255) & ~(size_t)255;
 }
 
+int check_layout(const SortDims &d, const int32_t *topk_idx, const int32_t *counts,
+                 const int32_t *offsets, const int32_t *perm, const int32_t *inv_perm,
+                 const void *ws, size_t ws_bytes) {
+  if (!counts || !offsets || !ws || (d.R && (!topk_idx || !perm || !inv_perm)))
+    return MOE_ERR_INVALID_ARG;
+  return ws_bytes < workspace_bytes(d) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -54,9 +62,7 @@ int moe_sort_layout(const moe_sort_shape *shape, const int32_t *topk_idx, int32_
   SortDims d;
   const int rc = check_sort(shape, &d);
   if (rc) return rc;
-  if (!counts || !offsets || !ws || (d.R && (!topk_idx || !perm || !inv_perm)))
-    return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < workspace_bytes(d)) return MOE_ERR_WORKSPACE;
+  if (int bad = check_layout(d, topk_idx, counts, offsets, perm, inv_perm, ws, ws_bytes)) return bad;
   launch_sort_layout(d, topk_idx, counts, offsets, perm, inv_perm, (int32_t *)ws,
                      (hipStream_t)stream);
   return status();
@@ -78,10 +84,14 @@ int moe_sort_fwd(const moe_sort_shape *shape, const void *x, const int32_t *topk
   SortDims d;
   int rc = check_sort(shape, &d);
   if (rc) return rc;
-  if (d.R && (!x || !x_sorted)) return MOE_ERR_INVALID_ARG;
-  rc = moe_sort_layout(shape, topk_idx, counts, offsets, perm, inv_perm, ws, ws_bytes, stream);
+  rc = check_layout(d, topk_idx, counts, offsets, perm, inv_perm, ws, ws_bytes);
   if (rc) return rc;
-  launch_sort_rows(d, x, counts, offsets, inv_perm, x_sorted, (hipStream_t)stream);
+  if (d.R && (!x || !x_sorted)) return MOE_ERR_INVALID_ARG;
+  hipStream_t s = (hipStream_t)stream;
+  if (!launch_sort_small(d, x, topk_idx, counts, offsets, perm, inv_perm, x_sorted, s)) {
+    launch_sort_layout(d, topk_idx, counts, offsets, perm, inv_perm, (int32_t *)ws, s);
+    launch_sort_rows(d, x, counts, offsets, inv_perm, x_sorted, s);
+  }
   return status();
 }
 

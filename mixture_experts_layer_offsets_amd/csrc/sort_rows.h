@@ -25,6 +25,9 @@ void launch_sort_layout(const SortDims &d, const int32_t *idx, int32_t *counts, 
                         int32_t *perm, int32_t *inv, int32_t *ws, hipStream_t s);
 void launch_sort_rows(const SortDims &d, const void *x, const int32_t *counts,
                       const int32_t *offsets, const int32_t *inv, void *xs, hipStream_t s);
+// Both at once in one launch, where it takes the sizes (else false, nothing done).
+bool launch_sort_small(const SortDims &d, const void *x, const int32_t *idx, int32_t *counts,
+                       int32_t *offsets, int32_t *perm, int32_t *inv, void *xs, hipStream_t s);
 // w and add may be null (weights one, nothing added).
 void launch_unsort(const SortDims &d, const void *y, const float *w, const int32_t *inv,
                    const void *add, void *out, hipStream_t s);

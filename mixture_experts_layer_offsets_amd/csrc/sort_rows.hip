@@ -38,6 +38,12 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kSortMaxK = 16;   // top-k bound of the library
 constexpr int kRowBlock = 64;   // one wave per workgroup for the gathers (see combine_kernel)
 constexpr int kPadSplit = 8;    // workgroups that share one expert's padding rows
+// One-launch sort: slots, rows of the sorted buffer (one workgroup fills perm)
+// and bytes of a row (a wave's worth) it takes; rows a padding workgroup checks.
+constexpr int kSortSmallSlots = 1024, kSortSmallRows = 16384, kSortSmallBytes = 1024;
+constexpr int kSmallPadRows = 16;
+constexpr int kRawBuffer = 0x00020000;  // raw buffer descriptor, gfx9 family
+constexpr int kNonTemporal = 2;         // cache policy of a buffer access: nt
 
 // 16 bytes at any alignment, read or written once.
 __device__ __forceinline__ u32x4 ld16(const char *p) {
@@ -286,9 +292,35 @@ __device__ __forceinline__ void zero_padding(const int32_t *counts, const int32_
     st16(rows + r * stride + at, (u32x4){0, 0, 0, 0});
 }
 
+// The token of a lane: with WIDE (64 chunks or more) one token a workgroup, so
+// its slots' rows come by scalar loads and their addresses stay in scalar
+// registers.
+template <bool WIDE>
+__device__ __forceinline__ int lane_token(const RowGrid &g) {
+  if constexpr (WIDE) return blockIdx.x;
+  return blockIdx.x * (64 >> g.lsh) + ((int)threadIdx.x >> g.lsh);
+}
+
+// Row `row` (uniform in the wave) as a buffer of its own: a masked row is an
+// empty one, whose loads return zeros without touching memory.  So a token's
+// loads need no branches, which would keep them from being in flight together.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const char *rows, int row, long stride,
+                                                             long RB) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)(rows + max(row, 0) * stride), (short)0,
+                                           row >= 0 ? (int)RB : 0, kRawBuffer);
+}
+__device__ __forceinline__ u32x4 ld16(__amdgpu_buffer_rsrc_t r, long at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, kNonTemporal);
+}
+
 // xs[inv[t k + j]] = x[t]: each token's row is read once and stored to its
-// kept rows.
-template <int KMAX>
+// kept rows.  A token without one is not read (an eighth of 256 experts held,
+// 8192 x 8 slots of 7168 bf16: 61 -> 55 us; with every slot kept, where the
+// load could go out before the rows are known, 235 -> 236 us).  The sorted rows
+// are stored to stay in the caches, for the products that read them next:
+// non-temporal stores took 4 us off that sort, but a sort followed by a reader
+// of its 235 MB went from 85 to 102 us.
+template <int KMAX, bool WIDE>
 __global__ __launch_bounds__(kRowBlock) void sort_rows_kernel(
     const char *__restrict__ x, const int32_t *__restrict__ inv, const int32_t *__restrict__ counts,
     const int32_t *__restrict__ offsets, char *__restrict__ xs, int T, int k, long RB, long xstride,
@@ -299,60 +331,162 @@ __global__ __launch_bounds__(kRowBlock) void sort_rows_kernel(
     zero_padding(counts, offsets, p / kPadSplit, p % kPadSplit, kPadSplit, g.lsh, xs, RB, rstride);
     return;
   }
-  const int t = blockIdx.x * (64 >> g.lsh) + (lane >> g.lsh);
+  const int t = lane_token<WIDE>(g);
   const long c = ((long)blockIdx.y << 6) + (lane & ((1 << g.lsh) - 1));
   if (t >= T || c * 16 >= RB) return;
   const long at = min(c * 16, RB - 16);
   int row[KMAX];
+  int some = -1;
 #pragma unroll
-  for (int j = 0; j < KMAX; j++) row[j] = inv[(long)t * k + min(j, k - 1)];
+  for (int j = 0; j < KMAX; j++) {
+    row[j] = inv[(long)t * k + min(j, k - 1)];
+    some = max(some, row[j]);
+  }
+  if (some < 0) return;
   const u32x4 v = ld16(x + t * xstride + at);
 #pragma unroll
   for (int j = 0; j < KMAX; j++)
     if (j < k && row[j] >= 0) st16(xs + row[j] * rstride + at, v);
 }
 
+// ---------------------------------------------------------------------------
+// Layout and rows in one launch, for the few slots of a decode batch: no
+// workgroup waits for another, each finds its token's rows itself.  With f's
+// expert e, the row of f is the number of slots of lower experts (rounded per
+// expert to the alignment) plus those of e before f; every lane holds up to NI
+// ids and the wave counts them by ballots.  The last workgroup of the grid
+// writes the layout; the ones between (align > 1) zero the padding rows.
+
+// Counts and offsets of up to kSortSmallSlots slots in LDS (cnt [E], off [E+1]).
+__device__ __forceinline__ void small_layout(const int32_t *idx, int R, int first, int E, int align,
+                                             int32_t *cnt, int32_t *off, int32_t *wsum) {
+  for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+  __syncthreads();
+  for (int f = threadIdx.x; f < R; f += 256) {
+    const int e = local_expert(idx[f], first, E);
+    if (e >= 0) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  scan_experts<256>(cnt, off, E, align, wsum);
+}
+
+template <int NI>
+__global__ __launch_bounds__(256) void sort_small_kernel(
+    const char *__restrict__ x, const int32_t *__restrict__ idx, int32_t *__restrict__ counts,
+    int32_t *__restrict__ offsets, int32_t *__restrict__ perm, int32_t *__restrict__ inv,
+    char *__restrict__ xs, int T, int k, int first, int E, int align, int cap, long RB, long xstride,
+    long rstride) {
+  extern __shared__ int32_t lds[];
+  __shared__ int32_t wsum[4];
+  int32_t *cnt = lds, *off = lds + E;
+  const int tid = threadIdx.x, lane = tid & 63, R = T * k, t = blockIdx.x;
+  const long c = (long)blockIdx.y * 256 + tid;
+  const long at = min(c * 16, RB - 16);
+  if (t < T) {
+    const u32x4 v = ld16(x + t * xstride + at);
+    int id[NI];
+#pragma unroll
+    for (int i = 0; i < NI; i++) {
+      const int f = lane + 64 * i;
+      id[i] = f < R ? local_expert(idx[f], first, E) : -1;
+    }
+    if (align > 1) small_layout(idx, R, first, E, align, cnt, off, wsum);
+    for (int j = 0; j < k; j++) {
+      const int f = t * k + j, e = local_expert(idx[f], first, E);
+      if (e < 0) continue;
+      int row = align > 1 ? off[e] : 0;
+#pragma unroll
+      for (int i = 0; i < NI; i++) {
+        const bool before = id[i] == e && lane + 64 * i < f;
+        row += __popcll(__ballot(before || (align <= 1 && id[i] >= 0 && id[i] < e)));
+      }
+      if (c * 16 < RB) st16(xs + row * rstride + at, v);
+    }
+    return;
+  }
+  small_layout(idx, R, first, E, align, cnt, off, wsum);
+  if (blockIdx.x < gridDim.x - 1) {
+    if (c * 16 >= RB) return;
+    const int r0 = (t - T) * kSmallPadRows;
+    for (int r = r0; r < min(r0 + kSmallPadRows, off[E]); r++) {
+      int lo = 0, hi = E;  // off[lo] <= r < off[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+      if (r >= off[lo] + cnt[lo]) st16(xs + r * rstride + at, (u32x4){0, 0, 0, 0});
+    }
+    return;
+  }
+  if (blockIdx.y) return;
+  for (int e = tid; e <= E; e += 256) {
+    offsets[e] = off[e];
+    if (e < E) counts[e] = cnt[e];
+  }
+  for (int r = tid; r < cap; r += 256) perm[r] = -1;
+  // the ids, for each slot's rank (the counts and the scan are done with)
+  __syncthreads();
+  int32_t *ids = off + E + 1;
+  for (int f = tid; f < R; f += 256) ids[f] = local_expert(idx[f], first, E);
+  __syncthreads();  // and perm's fill before its rows
+  for (int f = tid; f < R; f += 256) {
+    const int e = ids[f];
+    int rank = 0;
+    for (int g = 0; g < f; g++) rank += ids[g] == e;
+    const int row = e >= 0 ? off[e] + rank : -1;
+    inv[f] = row;
+    if (row >= 0) perm[row] = f;
+  }
+}
+
 // out[t] = sum_j (w) y[inv[t k + j]] (+ add[t]).
-template <class E, int KMAX, bool WEIGHT, bool ADD>
+template <class E, int KMAX, bool WEIGHT, bool ADD, bool WIDE>
 __global__ __launch_bounds__(kRowBlock) void unsort_kernel(
     const char *__restrict__ y, const float *__restrict__ w, const int32_t *__restrict__ inv,
     const char *__restrict__ add, char *__restrict__ out, int T, int k, long RB, long tstride,
     long rstride, RowGrid g) {
   const int lane = threadIdx.x;
-  const int t = blockIdx.x * (64 >> g.lsh) + (lane >> g.lsh);
+  const int t = lane_token<WIDE>(g);
   const long c = ((long)blockIdx.y << 6) + (lane & ((1 << g.lsh) - 1));
   if (t >= T || c * 16 >= RB) return;
   const long at = min(c * 16, RB - 16);
+  u32x4 av;
+  if constexpr (ADD) av = ld16(add + t * tstride + at);
   int row[KMAX];
   float wt[KMAX];
+  int some = -1;
 #pragma unroll
   for (int j = 0; j < KMAX; j++) {
     row[j] = inv[(long)t * k + min(j, k - 1)];
     if constexpr (WEIGHT) wt[j] = w[(long)t * k + min(j, k - 1)];
+    if (j >= k) row[j] = -1;
+    some = max(some, row[j]);
   }
-  // the indices are needed here: one round trip for all of them, then one for
-  // all rows
-#pragma unroll
-  for (int j = 0; j < KMAX; j++) asm volatile("" ::"v"(row[j]));
+  // All rows' loads go out before the first sum.  WIDE: a masked slot's row is
+  // an empty buffer, and its zeros are added with weight zero.  Else its lanes
+  // load the token's last row once more and leave the sum alone.
   u32x4 rv[KMAX];
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int j = 0; j < KMAX; j++)
-    if (j < k && row[j] >= 0) rv[j] = ld16(y + row[j] * rstride + at);
-  u32x4 av;
-  if constexpr (ADD) av = ld16(add + t * tstride + at);
+    for (int j = 0; j < KMAX; j++) rv[j] = ld16(row_buffer(y, row[j], rstride, RB), at);
+  } else if (some >= 0) {
+#pragma unroll
+    for (int j = 0; j < KMAX; j++)
+      rv[j] = ld16(y + (row[j] >= 0 ? row[j] : some) * rstride + at);
+  }
   float acc[E::N];
 #pragma unroll
   for (int q = 0; q < E::N; q++) acc[q] = 0.0f;
 #pragma unroll
   for (int j = 0; j < KMAX; j++) {
-    if (j < k && row[j] >= 0) {
-      float v[E::N];
-      E::widen(rv[j], v);
+    float v[E::N];
+    E::widen(rv[j], v);
+    const float wj = WEIGHT ? (row[j] >= 0 ? wt[j] : 0.0f) : 1.0f;
 #pragma unroll
-      for (int q = 0; q < E::N; q++) {
-        if constexpr (WEIGHT) acc[q] = fmaf(wt[j], v[q], acc[q]);
-        else acc[q] += v[q];
-      }
+    for (int q = 0; q < E::N; q++) {
+      const float sum = WEIGHT ? fmaf(wj, v[q], acc[q]) : acc[q] + v[q];
+      acc[q] = WIDE || row[j] >= 0 ? sum : acc[q];
     }
   }
   if constexpr (ADD) {
@@ -383,14 +517,14 @@ __global__ __launch_bounds__(256) void unsort_bwd_kernel(
         st16(dy + r * rstride + min(c * 16, RB - 16), (u32x4){0, 0, 0, 0});
     return;
   }
-  const int t = WPT == 4 ? blockIdx.x : blockIdx.x * 4 + wave;
+  const int t = WPT == 4 ? blockIdx.x : blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wave);
   const bool live = t < T;
   int row[KMAX];
   float wt[KMAX], part[KMAX];
 #pragma unroll
-  for (int j = 0; j < KMAX; j++) {
+  for (int j = 0; j < KMAX; j++) {  // one token a wave: scalar loads
     part[j] = 0.0f;
-    row[j] = live ? inv[(long)t * k + min(j, k - 1)] : -1;
+    row[j] = live && j < k ? inv[(long)t * k + min(j, k - 1)] : -1;
     wt[j] = live ? w[(long)t * k + min(j, k - 1)] : 0.0f;
   }
   constexpr int kStep = 64 * WPT;
@@ -402,14 +536,13 @@ __global__ __launch_bounds__(256) void unsort_bwd_kernel(
       u32x4 yv[KMAX];
       if constexpr (DW) {
 #pragma unroll
-        for (int j = 0; j < KMAX; j++)
-          if (j < k && row[j] >= 0) yv[j] = ld16(y + row[j] * rstride + at);
+        for (int j = 0; j < KMAX; j++) yv[j] = ld16(row_buffer(y, row[j], rstride, RB), at);
       }
       float d[E::N];
       E::widen(dv, d);
 #pragma unroll
       for (int j = 0; j < KMAX; j++) {
-        if (j < k && row[j] >= 0) {
+        if (row[j] >= 0) {
           float o[E::N];
 #pragma unroll
           for (int q = 0; q < E::N; q++) o[q] = wt[j] * d[q];
@@ -546,12 +679,31 @@ void launch_sort_rows(const SortDims &d, const void *x, const int32_t *counts,
   const RowGrid g = row_grid((int)d.T, RB);
   const dim3 grid(g.token_blocks + (offsets ? d.E * kPadSplit : 0), g.y), b(kRowBlock);
   const long xst = d.tstride * d.esize, rst = d.rstride * d.esize;
-  if (d.k <= 8)
-    hipLaunchKernelGGL(sort_rows_kernel<8>, grid, b, 0, s, (const char *)x, inv, counts, offsets,
-                       (char *)xs, (int)d.T, d.k, RB, xst, rst, g);
-  else
-    hipLaunchKernelGGL(sort_rows_kernel<kSortMaxK>, grid, b, 0, s, (const char *)x, inv, counts,
-                       offsets, (char *)xs, (int)d.T, d.k, RB, xst, rst, g);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, b, 0, s, (const char *)x, inv, counts, offsets, (char *)xs,
+                       (int)d.T, d.k, RB, xst, rst, g);
+  };
+  if (g.lsh == 6) d.k <= 8 ? go(sort_rows_kernel<8, true>) : go(sort_rows_kernel<kSortMaxK, true>);
+  else d.k <= 8 ? go(sort_rows_kernel<8, false>) : go(sort_rows_kernel<kSortMaxK, false>);
+}
+
+bool launch_sort_small(const SortDims &d, const void *x, const int32_t *idx, int32_t *counts,
+                       int32_t *offsets, int32_t *perm, int32_t *inv, void *xs, hipStream_t s) {
+  const long RB = (long)d.D * d.esize;
+  if (d.R < 1 || d.R > kSortSmallSlots || d.cap > kSortSmallRows || RB < kSortSmallBytes)
+    return false;
+  const long pads = d.align > 1 ? (d.cap + kSmallPadRows - 1) / kSmallPadRows : 0;
+  const dim3 grid((unsigned)(d.T + pads + 1), (unsigned)((RB + 4095) / 4096)), b(256);
+  const size_t lds = (2 * d.E + 1 + d.R) * sizeof(int32_t);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, b, lds, s, (const char *)x, idx, counts, offsets, perm, inv,
+                       (char *)xs, (int)d.T, d.k, d.first, d.E, d.align, (int)d.cap, RB,
+                       d.tstride * d.esize, d.rstride * d.esize);
+  };
+  if (d.R <= 64) go(sort_small_kernel<1>);
+  else if (d.R <= 256) go(sort_small_kernel<4>);
+  else go(sort_small_kernel<kSortSmallSlots / 64>);
+  return true;
 }
 
 namespace {
@@ -561,9 +713,13 @@ void go_unsort(const SortDims &d, const void *y, const float *w, const int32_t *
                const void *add, void *out, hipStream_t s) {
   const long RB = (long)d.D * d.esize;
   const RowGrid g = row_grid((int)d.T, RB);
-  hipLaunchKernelGGL((unsort_kernel<E, KMAX, WEIGHT, ADD>), dim3(g.token_blocks, g.y),
-                     dim3(kRowBlock), 0, s, (const char *)y, w, inv, (const char *)add, (char *)out,
-                     (int)d.T, d.k, RB, d.tstride * d.esize, d.rstride * d.esize, g);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(g.token_blocks, g.y), dim3(kRowBlock), 0, s, (const char *)y, w,
+                       inv, (const char *)add, (char *)out, (int)d.T, d.k, RB, d.tstride * d.esize,
+                       d.rstride * d.esize, g);
+  };
+  if (g.lsh == 6) go(unsort_kernel<E, KMAX, WEIGHT, ADD, true>);
+  else go(unsort_kernel<E, KMAX, WEIGHT, ADD, false>);
 }
 
 template <class E>

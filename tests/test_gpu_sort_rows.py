@@ -51,6 +51,16 @@ CASES = {
     "E1024": (300, 5, 1024, 64, "bf16", 2, 0, 0, 0, 0.1),
     "two-chunks": (700, 3, 17, 40, "f32", 1, 0, 0, 0, 0.1),
     "many-chunks": (9000, 16, 6, 16, "bf16", 32, 0, 0, 0, 0.1),
+    # one-launch sorts at their limits: 1024 slots, padded segments, one slot more
+    "slots-64": (8, 8, 12, 600, "bf16", 4, 0, 0, 0, 0.3),
+    "slots-1024": (128, 8, 40, 512, "bf16", 1, 3, 0, 0, 0.2),
+    "slots-1024-align": (64, 16, 9, 520, "bf16", 128, -2, 8, 0, 0.1),
+    "slots-1025": (205, 5, 40, 512, "bf16", 1, 0, 0, 0, 0.2),
+    "small-E1024": (16, 16, 1024, 1000, "f16", 16, 0, 0, 0, 0.1),
+    # rows of many chunks at odd byte offsets (tokens and sorted rows)
+    "wide-odd": (21, 5, 6, 1031, "bf16", 4, 2, 0, 0, 0.3),
+    "wide-odd-stride": (21, 16, 6, 1030, "f16", 1, 0, 3, 5, 0.5),
+    "wide-f32": (40, 12, 9, 515, "f32", 2, 0, 0, 2, 0.2),
     "wide": (3, 2, 4, 20000, "bf16", 1, 0, 0, 0, 0.0),
 }
 
@@ -109,6 +119,11 @@ def test_layout_and_rows(name):
     want[live, :D] = x[torch.from_numpy(perm[perm >= 0] // k).long().cuda()]
     want[torch.from_numpy(ro.padding_rows(counts, offsets)).cuda(), :D] = 0
     assert torch.equal(full, want)       # rows behind the last segment and the gaps untouched
+    # the layout alone
+    alone = [torch.full_like(b, -7) for b in (op.counts, op.offsets, op.perm, op.inv_perm)]
+    m.moe_sort_layout(shape, torch.from_numpy(idx).cuda(), *alone, op.ws)
+    for a, b in zip(alone, (op.counts, op.offsets, op.perm, op.inv_perm)):
+        assert torch.equal(a, b)
     # the same layout again, other rows
     x2 = rows(rng, T, D, (shape.token_stride or D) - D, dtype)
     op.sort_again(x2, out=full[:, :D])
