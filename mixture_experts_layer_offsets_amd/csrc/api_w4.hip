@@ -1,4 +1,4 @@
-// C ABI of the 4-bit expert weights: argument checks and launches (w4.hip).
+// C ABI of the 4-bit expert weights: argument checks and launches (w4_*.hip).
 #include <algorithm>
 
 #include "../../include/moe.h"
@@ -46,7 +46,7 @@ int check_w4(const moe_w4_shape *s, W4Dims *d) {
 // Workspace of the few-token layer.
 struct Work {
   uint16_t *act, *act_s;
-  float *y, *y_s, *logits, *w;
+  float *logits, *w;
   int32_t *idx, *offsets, *tiles, *order;
 };
 
@@ -60,8 +60,11 @@ int check_layer(const moe_shape *s) {
   if (s->hidden % 64 || s->inter % 64 || s->shared_inter % 64) return MOE_ERR_UNSUPPORTED;
   if (s->experts > 1024 || s->top_k > 16 || (int64_t)s->tokens * s->top_k > kW4MaxSlots)
     return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)s->hidden * s->experts >= (1L << 31) || s->hidden > (1 << 20) ||
-      s->inter > (1 << 20) || s->shared_inter > (1 << 20))
+  if ((int64_t)s->hidden * s->experts >= (1L << 31) || s->hidden > (1 << 20))
+    return MOE_ERR_UNSUPPORTED;
+  // the hidden rows are one buffer with 31-bit byte offsets
+  if ((int64_t)s->tokens * s->top_k * s->inter >= (1L << 30) ||
+      (int64_t)s->tokens * s->shared_inter >= (1L << 30))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -74,11 +77,9 @@ size_t carve(const moe_shape *s, void *ws, Work *w) {
     off += up256(bytes);
     return p;
   };
-  const size_t T = s->tokens, R = T * s->top_k, H = s->hidden, E = s->experts;
+  const size_t T = s->tokens, R = T * s->top_k, E = s->experts;
   w->act = (uint16_t *)take(R * s->inter * 2);
-  w->y = (float *)take(R * H * 4);
   w->act_s = (uint16_t *)take(T * s->shared_inter * 2);
-  w->y_s = (float *)take(s->shared_inter ? T * H * 4 : 0);
   w->logits = (float *)take(T * E * 4);
   w->idx = (int32_t *)take(R * 4);
   w->w = (float *)take(R * 4);
@@ -193,12 +194,16 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts, con
     idx = w.idx;
     wts = w.w;
   }
-  launch_w4_ffn(up, down, x, idx, T * k, k, first, experts->gate, experts->up, experts->down, w.act,
-                w.y, s);
-  if (shared)
-    launch_w4_ffn(up_s, down_s, x, nullptr, T, 1, 0, experts->shared_gate, experts->shared_up,
-                  experts->shared_down, w.act_s, w.y_s, s);
-  launch_w4_combine(w.y, wts, idx, first, E, shared ? w.y_s : nullptr, out, T, k, H, s);
+  W4Layer a{};
+  a.up = up; a.down = down;
+  a.shared = shared;
+  if (shared) { a.up_s = up_s; a.down_s = down_s; }
+  a.T = T; a.k = k; a.first = first;
+  a.x = x; a.idx = idx; a.w = wts;
+  a.w_gate = experts->gate; a.w_up = experts->up; a.w_down = experts->down;
+  a.ws_gate = experts->shared_gate; a.ws_up = experts->shared_up; a.ws_down = experts->shared_down;
+  a.act = w.act; a.act_s = w.act_s; a.out = out;
+  launch_w4_ffn(a, s);
   return status();
 }
 

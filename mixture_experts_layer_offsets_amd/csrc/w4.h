@@ -1,4 +1,4 @@
-// Host-side launchers of w4.hip (all asynchronous on stream `s`).
+// Host-side launchers of the w4_*.hip files (all asynchronous on stream `s`).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -12,7 +12,8 @@ constexpr int kW4MaxSlots = 4096;  // T*k of one few-token layer call, at most
 
 // A checked moe_w4_shape and the pieces of its packed buffer.  Tiles of 16
 // outputs x 128 contraction values: nt = ceil(n / 16), ks = ceil(k / 128);
-// spg scales per output and tile.  See w4.hip for the layout of a tile.
+// spg scales per output and tile.  See
+// w4_device.h for the layout of a tile.
 struct W4Dims {
   int groups, n, k, fmt, group, f16_scales, zeros;
   int nt, ks, spg;
@@ -31,14 +32,19 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
                       const int32_t *offsets, const void *packed, uint16_t *out, long ostride,
                       hipStream_t s);
 
-// The few-token expert FFN.  idx [slots]: the slots' expert ids (first = id of
-// expert 0; others are masked); idx null: one expert, every token a slot
-// (k = 1).  act [slots][I] bf16, y [slots][H] fp32, at the slots' places.
-void launch_w4_ffn(const W4Dims &up, const W4Dims &down, const uint16_t *x, const int32_t *idx,
-                   int slots, int k, int first, const void *gate, const void *upw,
-                   const void *downw, uint16_t *act, float *y, hipStream_t s);
-// out[t] = sum_j w[t][j] y[t k + j] over the kept slots (+ ys[t]).
-void launch_w4_combine(const float *y, const float *w, const int32_t *idx, int first, int E,
-                       const float *ys, uint16_t *out, int T, int k, int H, hipStream_t s);
+// The few-token expert FFN: gate/up [E][H][I] and down [E][I][H], routing idx
+// and w [T][k] (ids less `first`; others are masked), the shared expert's
+// matrices if `shared`.  act [T k][I] and act_s [T][Is] are scratch.
+struct W4Layer {
+  W4Dims up, down, up_s, down_s;
+  bool shared;
+  int T, k, first;
+  const uint16_t *x;
+  const int32_t *idx;
+  const float *w;
+  const void *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
+  uint16_t *act, *act_s, *out;
+};
+void launch_w4_ffn(const W4Layer &a, hipStream_t s);
 
 }  // namespace moe

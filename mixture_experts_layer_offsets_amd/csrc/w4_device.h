@@ -1,0 +1,282 @@
+// Products of a few rows with 4-bit weights and group scales: formats, packed
+// layout and the streaming loop shared by w4_linear.hip and w4_ffn.hip.
+//
+//   y[r][n] = sum_k x[r][k] w[k][n],  x bf16, sums in fp32
+//   MXFP4: w = 2^(s - 127) E2M1(code), one E8M0 scale s per 32 along k
+//   INT4:  w = s (q - z), one bf16/fp16 scale s (and zero point z, else 8) per
+//          32, 64 or 128 along k
+//
+// With few rows the bound is reading the weights (4.25 bits each for MXFP4):
+// 2 M FLOP per weight are nothing for the matrix cores, but unpacking costs
+// VALU work per weight, so it has to stay near one operation each.
+//
+// The products run on v_mfma_f32_16x16x32_bf16 with A = 16 rows of x and B =
+// 16 outputs: lane l holds row (or output) l % 16 and the contraction values
+// 8 (l / 16) .. + 7 of a 32-wide step, and receives outputs (row 4 (l / 16) +
+// v, output l % 16).  MXFP4 codes become scaled bf16 pairs in one conversion
+// instruction (exact: E2M1 times a power of two).  INT4 codes become 16 + q:
+// the nibble is or-ed into the top mantissa bits of 16.0, two values per
+// operation; the offset comes off through the group's sum of x, and the group's
+// scale is applied to the fp32 partial sum, so no weight is ever rounded.
+//
+// Packed layout: a tile is 16 outputs x 128 contraction values, 1 KB, in the
+// order in which one wave's 16-byte loads take it: lane l's four dwords are
+// the 8 codes of output l % 16 at k = 32 i + 8 (l / 16), i = 0..3.  Tiles are
+// [group][n / 16][k / 128], so the K loop of one tile row is one contiguous
+// stream.  In a dword the MXFP4 code of value q sits at bits 4 q; INT4 puts
+// values 2 p and 2 p + 1 at bits 3 + 4 p and 19 + 4 p (the last one wraps), the
+// halves of one bf16 pair.
+// Scales follow tile by tile: [group][n / 16][k / 128][16 outputs][spg], spg =
+// 4 bytes for MXFP4, 128 / group_size 16-bit scales (and as many zero-point
+// bytes) for INT4.  Outputs past n and values past k have zero weights.
+#pragma once
+
+#include "common.h"
+#include "w4.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int w4_u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int w4_u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+// Packed pieces of one matrix per group.
+struct W4Mat {
+  const uint8_t *codes, *scales, *zeros;
+  int n, k, nt, ks, f16;
+};
+
+inline W4Mat w4_view(const W4Dims &d, const void *packed) {
+  const uint8_t *p = (const uint8_t *)packed;
+  return {p, p + d.code_bytes, p + d.code_bytes + d.scale_bytes, d.n, d.k, d.nt, d.ks,
+          d.f16_scales};
+}
+
+__device__ __forceinline__ float scale_value(uint32_t u16, int f16) {
+  return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)u16) : bf16_to_f32(u16);
+}
+
+// One lane's scales of one tile, as loaded.
+struct MxFmt {
+  static constexpr bool kGrouped = false;  // scaled while unpacking
+  static constexpr int SPG = 4;
+  static constexpr bool ZERO = false;
+  struct Scales { uint32_t d; };
+  static __device__ __forceinline__ Scales load(const W4Mat &m, size_t tile, int n) {
+    return {((const uint32_t *)m.scales)[tile * 16 + n]};
+  }
+  static __device__ __forceinline__ bf16x8 unpack(uint32_t d, const Scales &s, int i) {
+    const float sc = __uint_as_float(((s.d >> (8 * i)) & 0xFFu) << 23);
+    bf16x8 v;
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 0);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 1);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 2);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 3);
+    v[0] = p0[0]; v[1] = p0[1]; v[2] = p1[0]; v[3] = p1[1];
+    v[4] = p2[0]; v[5] = p2[1]; v[6] = p3[0]; v[7] = p3[1];
+    return v;
+  }
+};
+
+template <int SPG_, bool ZERO_>
+struct IntFmt {
+  static constexpr bool kGrouped = true;
+  static constexpr int SPG = SPG_;
+  static constexpr bool ZERO = ZERO_;
+  struct Scales { uint16_t s[SPG_]; uint8_t z[SPG_]; };
+  static __device__ __forceinline__ Scales load(const W4Mat &m, size_t tile, int n) {
+    Scales s;
+    const size_t at = (tile * 16 + n) * SPG_;
+    __builtin_memcpy(s.s, __builtin_assume_aligned(m.scales + at * 2, 2 * SPG_), 2 * SPG_);
+    if constexpr (ZERO_)
+      __builtin_memcpy(s.z, __builtin_assume_aligned(m.zeros + at, SPG_), SPG_);
+    return s;
+  }
+  // 16 + q: the nibble in bits 3..6 of bf16 16.0 (0x4180)
+  static __device__ __forceinline__ bf16x8 unpack(uint32_t d, const Scales &, int) {
+    uint32_t u[4];
+    u[0] = (d & 0x00780078u) | 0x41804180u;
+    u[1] = ((d >> 4) & 0x00780078u) | 0x41804180u;
+    u[2] = ((d >> 8) & 0x00780078u) | 0x41804180u;
+    u[3] = (__builtin_amdgcn_alignbit(d, d, 12) & 0x00780078u) | 0x41804180u;
+    bf16x8 v;
+    __builtin_memcpy(&v, u, 16);
+    return v;
+  }
+};
+
+// f(F{}) for the format of d.
+template <class Fn>
+void with_format(const W4Dims &d, Fn &&f) {
+  if (d.fmt == kW4Mx) f(MxFmt{});
+  else if (d.spg == 1 && !d.zeros) f(IntFmt<1, false>{});
+  else if (d.spg == 2 && !d.zeros) f(IntFmt<2, false>{});
+  else if (d.spg == 4 && !d.zeros) f(IntFmt<4, false>{});
+  else if (d.spg == 1) f(IntFmt<1, true>{});
+  else if (d.spg == 2) f(IntFmt<2, true>{});
+  else f(IntFmt<4, true>{});
+}
+
+__device__ __forceinline__ bf16x8 splat(float f) {
+  bf16x8 v;
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = (__bf16)f;
+  return v;
+}
+
+// Rows of x by address (a lane past the rows holds the last one again: its
+// results are dropped) ...
+struct RowPtr {
+  const uint16_t *p;
+  __device__ __forceinline__ bf16x8 load(int k) const {
+    return __builtin_bit_cast(bf16x8, *(const w4_u32x4u *)(p + k));
+  }
+};
+// ... or by byte offset into a buffer; an offset past its end is a row of zeros
+// that is not read.
+struct RowBuf {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t at;
+  __device__ __forceinline__ bf16x8 load(int k) const {
+    return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, at + 2 * k, 0, 0));
+  }
+};
+constexpr uint32_t kNoRow = 0x80000000u;  // past the end of any buffer here
+
+// Steps whose loads a wave has in flight together, for NB row blocks: their
+// rows take 16 NB registers a step.
+constexpr int w4_unroll(int NB) { return NB == 1 ? 4 : (NB == 2 ? 2 : 1); }
+
+// acc[j][p] += rows of block p times output tile j over the steps [s0, s1).
+// tile[j]: index of step 0's tile; x[p]: this lane's row of block p.  The rows,
+// codes and scales of a batch of steps are loaded together, one memory round
+// trip; steps past the end load the last step again and are not used.  Values
+// of k past K meet zero weights: their lanes load the row's last values.
+template <class F, int NTW, int NB, class Row>
+__device__ __forceinline__ void w4_stream(const W4Mat (&m)[NTW], const size_t (&tile)[NTW],
+                                          const Row (&x)[NB], int K, int s0, int s1,
+                                          f32x4 (&acc)[NTW][NB]) {
+  constexpr int U = w4_unroll(NB);
+  const int lane = threadIdx.x & 63, h8 = 8 * (lane >> 4);
+  for (int s = s0; s < s1; s += U) {
+    uint4 cw[U][NTW];
+    typename F::Scales sc[U][NTW];
+    bf16x8 a[U][NB][4];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int st = min(s + u, s1 - 1);
+#pragma unroll
+      for (int p = 0; p < NB; p++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) a[u][p][i] = x[p].load(min(128 * st + 32 * i + h8, K - 8));
+#pragma unroll
+      for (int j = 0; j < NTW; j++) {
+        cw[u][j] = ld_once((const uint4 *)m[j].codes + (tile[j] + st) * 64 + lane);
+        sc[u][j] = F::load(m[j], tile[j] + st, lane & 15);
+      }
+    }
+    // the batch's loads all go out before the first use (else the scheduler
+    // saves registers by moving loads to their uses)
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (s + u >= s1) break;
+      if constexpr (!F::kGrouped) {
+#pragma unroll
+        for (int j = 0; j < NTW; j++) {
+          const uint32_t d[4] = {cw[u][j].x, cw[u][j].y, cw[u][j].z, cw[u][j].w};
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const bf16x8 b = F::unpack(d[i], sc[u][j], i);
+#pragma unroll
+            for (int p = 0; p < NB; p++)
+              acc[j][p] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][p][i], b, acc[j][p], 0, 0, 0);
+          }
+        }
+      } else {
+        constexpr int kPer = 4 / F::SPG;  // MFMA steps of one scale group
+#pragma unroll
+        for (int g = 0; g < F::SPG; g++) {
+          // the offset: -24 sum x (zero point 8), or sum x for a zero point
+          // of each output's own
+          f32x4 off[NB];
+#pragma unroll
+          for (int p = 0; p < NB; p++) {
+            off[p] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < kPer; i++)
+              off[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  a[u][p][g * kPer + i], splat(F::ZERO ? 1.0f : -24.0f), off[p], 0, 0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < NTW; j++) {
+            const uint32_t d[4] = {cw[u][j].x, cw[u][j].y, cw[u][j].z, cw[u][j].w};
+            const float scale = scale_value(sc[u][j].s[g], m[j].f16);
+            f32x4 part[NB];
+#pragma unroll
+            for (int p = 0; p < NB; p++)
+              part[p] = F::ZERO ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : off[p];
+#pragma unroll
+            for (int i = 0; i < kPer; i++) {
+              const bf16x8 b = F::unpack(d[g * kPer + i], sc[u][j], i);
+#pragma unroll
+              for (int p = 0; p < NB; p++)
+                part[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][p][g * kPer + i], b, part[p],
+                                                                  0, 0, 0);
+            }
+#pragma unroll
+            for (int p = 0; p < NB; p++)
+#pragma unroll
+              for (int v = 0; v < 4; v++) {
+                float t = part[p][v];
+                if constexpr (F::ZERO) t = fmaf(-(16.0f + (float)sc[u][j].z[g]), off[p][v], t);
+                acc[j][p][v] = fmaf(scale, t, acc[j][p][v]);
+              }
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int NTW, int NB>
+__device__ __forceinline__ void zero_acc(f32x4 (&acc)[NTW][NB]) {
+#pragma unroll
+  for (int j = 0; j < NTW; j++)
+#pragma unroll
+    for (int p = 0; p < NB; p++) acc[j][p] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// The waves' partial sums meet in LDS and are added in wave order.  Afterwards
+// red[q * 64 + lane] (q = (j NB + p) 4 + v) holds output tile j, row 16 p + 4
+// (lane / 16) + v, output lane % 16.  red: WAVES NTW NB 256 floats.  The caller
+// synchronises before red is written again.
+template <int WAVES, int NTW, int NB>
+__device__ __forceinline__ void w4_join(const f32x4 (&acc)[NTW][NB], float *red) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kQ = NTW * NB * 4;
+#pragma unroll
+  for (int j = 0; j < NTW; j++)
+#pragma unroll
+    for (int p = 0; p < NB; p++)
+#pragma unroll
+      for (int v = 0; v < 4; v++)
+        red[(wave * kQ + (j * NB + p) * 4 + v) * 64 + lane] = acc[j][p][v];
+  __syncthreads();
+  for (int i = tid; i < kQ * 64; i += WAVES * 64) {
+    float t = red[i];
+#pragma unroll
+    for (int w = 1; w < WAVES; w++) t += red[w * kQ * 64 + i];
+    red[i] = t;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+}  // namespace
+}  // namespace moe

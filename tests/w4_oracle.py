@@ -45,8 +45,9 @@ def values(codes, scales, zeros, fmt, group):
 def product(x, w, sabs, fmt, group):
     """x [M][k], w [n][k] -> (y, bound on the fp32 sums' error).
 
-    MXFP4: each wave adds at most a quarter of the products one by one, every
-    step off by ULP of a partial sum that the absolute sum bounds.  INT4: the
+    MXFP4: a 32-wide matrix step is taken to round the running sum eight times
+    (at most ULP of a partial sum that the absolute sum bounds), so k / 4 times
+    in all, and the waves' sums are added.  INT4: the
     partial sums of a group hold x (16 + q) and the offset, at most 31 + 31
     |x|, `group` terms of them; then k / group scaled groups are added."""
     y = x @ w.T
@@ -67,34 +68,44 @@ def silu(z):
 
 
 def expert(x, gate, up, down, fmt, group):
-    """One expert's rows in 64 bits, and the bound of their fp32 results.
-    gate, up, down: (w, sabs) pairs.  d silu / dz lies in [-0.1, 1.1]; silu's
-    own evaluation is taken as off by 2^-20 (1 + |z|) of its value."""
+    """One expert's rows in 64 bits, the bound of the error that reaches them
+    through the hidden values, and the absolute sums of the last product (and
+    of |a| |scale|, for INT4's offset).  gate, up, down: (w, sabs) pairs.
+    d silu / dz lies in [-0.1, 1.1]; silu's own evaluation is taken as off by
+    2^-20 (1 + |z|) of its value; a (times its weight) is rounded to bf16."""
     g, dg = product(x, *gate, fmt, group)
     u, du = product(x, *up, fmt, group)
     a = silu(g) * u
     da = 1.1 * dg * (np.abs(u) + du) + np.abs(silu(g)) * du + 2.0 ** -20 * (1 + np.abs(g)) * np.abs(a)
-    da = da + (np.abs(a) + da) * 2.0 ** -8            # stored as bf16
-    y, dy = product(a, *down, fmt, group)
-    # the operand's own error, through the weights; dy grows with it too
-    return y, dy + 1.01 * (da @ np.abs(down[0]).T)
+    da = da + (np.abs(a) + da) * (2.0 ** -8 + 4 * ULP)
+    return (a @ down[0].T, da @ np.abs(down[0]).T, (np.abs(a) + da) @ np.abs(down[0]).T,
+            (np.abs(a) + da) @ down[1].T)
 
 
 def layer(x, idx, wt, experts, first, fmt, group, shared=None):
-    """experts: per expert (gate, up, down) pairs.  Returns (out, bound)."""
+    """experts: per expert (gate, up, down) pairs.  Returns (out, bound).  The
+    experts' products accumulate in one sum: every rounding of the running sum
+    is bounded by ULP of the absolute sum over all of them."""
     T, k = idx.shape
-    out = np.zeros((T, experts[0][2][0].shape[0]))
-    bound = np.zeros_like(out)
+    n, K = experts[0][2][0].shape
+    out, through, mag, off = (np.zeros((T, n)) for _ in range(4))
+
+    def add(t, w, mats):
+        y, d, a, s = expert(x[t], *mats, fmt, group)
+        for to, v in ((out, w * y), (through, np.abs(w) * d), (mag, np.abs(w) * a),
+                      (off, np.abs(w) * s)):
+            np.add.at(to, t, v)
+
     for e, mats in enumerate(experts):
         t, j = np.nonzero(idx.astype(np.int64) - first == e)
-        if len(t) == 0:
-            continue
-        y, dy = expert(x[t], *mats, fmt, group)
-        w = wt[t, j][:, None].astype(np.float64)
-        np.add.at(out, t, w * y)
-        np.add.at(bound, t, np.abs(w) * (dy + (k + 4) * ULP * np.abs(y)))
+        if len(t):
+            add(t, wt[t, j][:, None].astype(np.float64), mats)
+    terms = k * K
     if shared is not None:
-        y, dy = expert(x, *shared, fmt, group)
-        out += y
-        bound += dy + 2 * ULP * np.abs(y)
-    return out, rounded(out, bound)
+        add(np.arange(T), np.ones((T, 1)), shared)
+        terms += shared[2][0].shape[1]
+    if fmt == "mxfp4":
+        sums = (terms / 4 + 40) * ULP * mag
+    else:
+        sums = (group + 4) * ULP * 62 * off + (terms / group + 40) * ULP * mag
+    return out, rounded(out, through + sums)
