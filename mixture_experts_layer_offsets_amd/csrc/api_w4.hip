@@ -47,7 +47,7 @@ int check_w4(const moe_w4_shape *s, W4Dims *d) {
 struct Work {
   uint16_t *act, *act_s;
   float *logits, *w;
-  int32_t *idx, *offsets, *tiles, *order;
+  int32_t *plan, *idx, *offsets, *tiles, *order;
 };
 
 int check_layer(const moe_shape *s) {
@@ -80,6 +80,7 @@ size_t carve(const moe_shape *s, void *ws, Work *w) {
   const size_t T = s->tokens, R = T * s->top_k, E = s->experts;
   w->act = (uint16_t *)take(R * s->inter * 2);
   w->act_s = (uint16_t *)take(T * s->shared_inter * 2);
+  w->plan = (int32_t *)take(w4_plan_words((int)R, (int)E) * 4);
   w->logits = (float *)take(T * E * 4);
   w->idx = (int32_t *)take(R * 4);
   w->w = (float *)take(R * 4);
@@ -202,7 +203,7 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts, con
   a.x = x; a.idx = idx; a.w = wts;
   a.w_gate = experts->gate; a.w_up = experts->up; a.w_down = experts->down;
   a.ws_gate = experts->shared_gate; a.ws_up = experts->shared_up; a.ws_down = experts->shared_down;
-  a.act = w.act; a.act_s = w.act_s; a.out = out;
+  a.act = w.act; a.act_s = w.act_s; a.plan = w.plan; a.out = out;
   launch_w4_ffn(a, s);
   return status();
 }

@@ -34,7 +34,8 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
 
 // The few-token expert FFN: gate/up [E][H][I] and down [E][I][H], routing idx
 // and w [T][k] (ids less `first`; others are masked), the shared expert's
-// matrices if `shared`.  act [T k][I] and act_s [T][Is] are scratch.
+// matrices if `shared`.  act [T k][I], act_s [T][Is] and plan (w4_plan_words)
+// are scratch.
 struct W4Layer {
   W4Dims up, down, up_s, down_s;
   bool shared;
@@ -44,7 +45,9 @@ struct W4Layer {
   const float *w;
   const void *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
   uint16_t *act, *act_s, *out;
+  int32_t *plan;
 };
+size_t w4_plan_words(int slots, int E);
 void launch_w4_ffn(const W4Layer &a, hipStream_t s);
 
 }  // namespace moe

@@ -31,7 +31,10 @@
 // bytes) for INT4.  Outputs past n and values past k have zero weights.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
+#include "gemm_common.h"
 #include "w4.h"
 
 namespace moe {
@@ -57,14 +60,20 @@ __device__ __forceinline__ float scale_value(uint32_t u16, int f16) {
   return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)u16) : bf16_to_f32(u16);
 }
 
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+__device__ __forceinline__ rsrc_t w4_buffer(const void *p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, bytes, kBufferDword3);
+}
+
 // One lane's scales of one tile, as loaded.
 struct MxFmt {
   static constexpr bool kGrouped = false;  // scaled while unpacking
-  static constexpr int SPG = 4;
+  static constexpr int SPG = 4, kScaleBytes = 64;  // bytes of a tile's scales
   static constexpr bool ZERO = false;
   struct Scales { uint32_t d; };
-  static __device__ __forceinline__ Scales load(const W4Mat &m, size_t tile, int n) {
-    return {((const uint32_t *)m.scales)[tile * 16 + n]};
+  static __device__ __forceinline__ Scales load(rsrc_t s, rsrc_t, int step, int n) {
+    return {__builtin_amdgcn_raw_buffer_load_b32(s, 4 * n, step * kScaleBytes, 0)};
   }
   static __device__ __forceinline__ bf16x8 unpack(uint32_t d, const Scales &s, int i) {
     const float sc = __uint_as_float(((s.d >> (8 * i)) & 0xFFu) << 23);
@@ -82,16 +91,31 @@ struct MxFmt {
 template <int SPG_, bool ZERO_>
 struct IntFmt {
   static constexpr bool kGrouped = true;
-  static constexpr int SPG = SPG_;
+  static constexpr int SPG = SPG_, kScaleBytes = 32 * SPG_;
   static constexpr bool ZERO = ZERO_;
-  struct Scales { uint16_t s[SPG_]; uint8_t z[SPG_]; };
-  static __device__ __forceinline__ Scales load(const W4Mat &m, size_t tile, int n) {
+  // as loaded, two scales a register, taken apart at their use
+  struct Scales { uint32_t s[(SPG_ + 1) / 2], z; };
+  static __device__ __forceinline__ Scales load(rsrc_t ps, rsrc_t pz, int step, int n) {
     Scales s;
-    const size_t at = (tile * 16 + n) * SPG_;
-    __builtin_memcpy(s.s, __builtin_assume_aligned(m.scales + at * 2, 2 * SPG_), 2 * SPG_);
-    if constexpr (ZERO_)
-      __builtin_memcpy(s.z, __builtin_assume_aligned(m.zeros + at, SPG_), SPG_);
+    const int at = step * kScaleBytes, az = step * (kScaleBytes / 2);
+    if constexpr (SPG_ == 1) s.s[0] = __builtin_amdgcn_raw_buffer_load_b16(ps, 2 * n, at, 0);
+    else if constexpr (SPG_ == 2) s.s[0] = __builtin_amdgcn_raw_buffer_load_b32(ps, 4 * n, at, 0);
+    else {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(ps, 8 * n, at, 0);
+      s.s[0] = v[0];
+      s.s[1] = v[1];
+    }
+    if constexpr (!ZERO_) s.z = 0;
+    else if constexpr (SPG_ == 1) s.z = __builtin_amdgcn_raw_buffer_load_b8(pz, n, az, 0);
+    else if constexpr (SPG_ == 2) s.z = __builtin_amdgcn_raw_buffer_load_b16(pz, 2 * n, az, 0);
+    else s.z = __builtin_amdgcn_raw_buffer_load_b32(pz, 4 * n, az, 0);
     return s;
+  }
+  static __device__ __forceinline__ uint32_t scale(const Scales &s, int g) {
+    return g & 1 ? s.s[g / 2] >> 16 : s.s[g / 2] & 0xFFFFu;
+  }
+  static __device__ __forceinline__ float zero(const Scales &s, int g) {
+    return (float)((s.z >> (8 * g)) & 0xFFu);
   }
   // 16 + q: the nibble in bits 3..6 of bf16 16.0 (0x4180)
   static __device__ __forceinline__ bf16x8 unpack(uint32_t d, const Scales &, int) {
@@ -103,6 +127,28 @@ struct IntFmt {
     bf16x8 v;
     __builtin_memcpy(&v, u, 16);
     return v;
+  }
+};
+
+// The steps of one row of tiles (16 outputs, the whole contraction) as buffers
+// of their own: a step's loads then need one scalar offset, and no address
+// registers.
+template <class F>
+struct W4Row {
+  rsrc_t c, s, z;
+  W4Row() = default;
+  __device__ __forceinline__ W4Row(const W4Mat &m, size_t row) {
+    c = w4_buffer(m.codes + row * m.ks * 1024, m.ks * 1024);
+    s = w4_buffer(m.scales + row * m.ks * F::kScaleBytes, m.ks * F::kScaleBytes);
+    z = F::ZERO ? w4_buffer(m.zeros + row * m.ks * (F::kScaleBytes / 2), m.ks * (F::kScaleBytes / 2))
+                : s;
+  }
+  __device__ __forceinline__ uint4 codes(int step) const {  // read once: not kept in the caches
+    return __builtin_bit_cast(
+        uint4, __builtin_amdgcn_raw_buffer_load_b128(c, 16 * (threadIdx.x & 63), step * 1024, 2));
+  }
+  __device__ __forceinline__ typename F::Scales scales(int step) const {
+    return F::load(s, z, step, threadIdx.x & 15);
   }
 };
 
@@ -125,40 +171,98 @@ __device__ __forceinline__ bf16x8 splat(float f) {
   return v;
 }
 
-// Rows of x by address (a lane past the rows holds the last one again: its
-// results are dropped) ...
+// A lane's row of x, in memory (a lane past the rows holds the last one again:
+// its results are dropped) ...
 struct RowPtr {
   const uint16_t *p;
   __device__ __forceinline__ bf16x8 load(int k) const {
     return __builtin_bit_cast(bf16x8, *(const w4_u32x4u *)(p + k));
   }
 };
-// ... or by byte offset into a buffer; an offset past its end is a row of zeros
-// that is not read.
-struct RowBuf {
-  __amdgpu_buffer_rsrc_t r;
-  uint32_t at;
+// ... or in LDS, rows `pitch` bytes apart: 16 more than the values, so that 16
+// rows' reads of the same columns fall into different banks.
+struct RowLds {
+  const char *p;
   __device__ __forceinline__ bf16x8 load(int k) const {
-    return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, at + 2 * k, 0, 0));
+    return __builtin_bit_cast(bf16x8, *(const w4_u32x4 *)(p + 2 * k));
   }
 };
-constexpr uint32_t kNoRow = 0x80000000u;  // past the end of any buffer here
+__host__ __device__ constexpr int w4_pitch(int values) { return 2 * values + 16; }
+
+// One step: acc[j][p] += a[p] times the codes of tile j, 128 contraction values.
+template <class F, int NTW, int NB>
+__device__ __forceinline__ void w4_step(int f16, const uint4 (&cw)[NTW],
+                                        const typename F::Scales (&sc)[NTW],
+                                        const bf16x8 (&a)[NB][4], f32x4 (&acc)[NTW][NB]) {
+  if constexpr (!F::kGrouped) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {  // the tiles' chains of products side by side
+#pragma unroll
+      for (int j = 0; j < NTW; j++) {
+        const uint32_t d[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
+        const bf16x8 b = F::unpack(d[i], sc[j], i);
+#pragma unroll
+        for (int p = 0; p < NB; p++)
+          acc[j][p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][i], b, acc[j][p], 0, 0, 0);
+      }
+    }
+  } else {
+    constexpr int kPer = 4 / F::SPG;  // MFMA steps of one scale group
+#pragma unroll
+    for (int g = 0; g < F::SPG; g++) {
+      // the offset: -24 sum x (zero point 8), or sum x for a zero point of each
+      // output's own
+      f32x4 off[NB];
+#pragma unroll
+      for (int p = 0; p < NB; p++) {
+        off[p] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+          off[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a[p][g * kPer + i], splat(F::ZERO ? 1.0f : -24.0f), off[p], 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < NTW; j++) {
+        const uint32_t d[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
+        const float scale = scale_value(F::scale(sc[j], g), f16);
+        f32x4 part[NB];
+#pragma unroll
+        for (int p = 0; p < NB; p++) part[p] = F::ZERO ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : off[p];
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+          const bf16x8 b = F::unpack(d[g * kPer + i], sc[j], i);
+#pragma unroll
+          for (int p = 0; p < NB; p++)
+            part[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][g * kPer + i], b, part[p], 0, 0,
+                                                              0);
+        }
+#pragma unroll
+        for (int p = 0; p < NB; p++)
+#pragma unroll
+          for (int v = 0; v < 4; v++) {
+            float t = part[p][v];
+            if constexpr (F::ZERO) t = fmaf(-(16.0f + F::zero(sc[j], g)), off[p][v], t);
+            acc[j][p][v] = fmaf(scale, t, acc[j][p][v]);
+          }
+      }
+    }
+  }
+}
 
 // Steps whose loads a wave has in flight together, for NB row blocks: their
 // rows take 16 NB registers a step.
 constexpr int w4_unroll(int NB) { return NB == 1 ? 4 : (NB == 2 ? 2 : 1); }
 
-// acc[j][p] += rows of block p times output tile j over the steps [s0, s1).
-// tile[j]: index of step 0's tile; x[p]: this lane's row of block p.  The rows,
+// acc[j][p] += rows of block p times the row j of tiles over the steps [s0,
+// s1), the rows read from memory; x[p]: this lane's row of block p.  The rows,
 // codes and scales of a batch of steps are loaded together, one memory round
 // trip; steps past the end load the last step again and are not used.  Values
 // of k past K meet zero weights: their lanes load the row's last values.
 template <class F, int NTW, int NB, class Row>
-__device__ __forceinline__ void w4_stream(const W4Mat (&m)[NTW], const size_t (&tile)[NTW],
-                                          const Row (&x)[NB], int K, int s0, int s1,
-                                          f32x4 (&acc)[NTW][NB]) {
-  constexpr int U = w4_unroll(NB);
-  const int lane = threadIdx.x & 63, h8 = 8 * (lane >> 4);
+__device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, const Row (&x)[NB],
+                                          int K, int s0, int s1, f32x4 (&acc)[NTW][NB]) {
+  constexpr int U = NTW == 1 ? w4_unroll(NB) : (w4_unroll(NB) + 1) / 2;
+  const int h8 = 8 * ((threadIdx.x & 63) >> 4);
   for (int s = s0; s < s1; s += U) {
     uint4 cw[U][NTW];
     typename F::Scales sc[U][NTW];
@@ -172,72 +276,43 @@ __device__ __forceinline__ void w4_stream(const W4Mat (&m)[NTW], const size_t (&
         for (int i = 0; i < 4; i++) a[u][p][i] = x[p].load(min(128 * st + 32 * i + h8, K - 8));
 #pragma unroll
       for (int j = 0; j < NTW; j++) {
-        cw[u][j] = ld_once((const uint4 *)m[j].codes + (tile[j] + st) * 64 + lane);
-        sc[u][j] = F::load(m[j], tile[j] + st, lane & 15);
+        cw[u][j] = m[j].codes(st);
+        sc[u][j] = m[j].scales(st);
       }
     }
     // the batch's loads all go out before the first use (else the scheduler
     // saves registers by moving loads to their uses)
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (s + u >= s1) break;
-      if constexpr (!F::kGrouped) {
+    for (int u = 0; u < U; u++)
+      if (s + u < s1) w4_step<F>(f16, cw[u], sc[u], a[u], acc);
+  }
+}
+
+// A ring of D steps whose codes and scales are in flight, refilled step by step
+// (the rows lie in LDS): it never drains between the tiles that a workgroup
+// works on.
+template <class F, int NTW, int D>
+struct W4Ring {
+  uint4 cw[D][NTW];
+  typename F::Scales sc[D][NTW];
+
+  template <int d>
+  __device__ __forceinline__ void load(const W4Row<F> (&m)[NTW], int step) {
 #pragma unroll
-        for (int j = 0; j < NTW; j++) {
-          const uint32_t d[4] = {cw[u][j].x, cw[u][j].y, cw[u][j].z, cw[u][j].w};
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const bf16x8 b = F::unpack(d[i], sc[u][j], i);
-#pragma unroll
-            for (int p = 0; p < NB; p++)
-              acc[j][p] =
-                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][p][i], b, acc[j][p], 0, 0, 0);
-          }
-        }
-      } else {
-        constexpr int kPer = 4 / F::SPG;  // MFMA steps of one scale group
-#pragma unroll
-        for (int g = 0; g < F::SPG; g++) {
-          // the offset: -24 sum x (zero point 8), or sum x for a zero point
-          // of each output's own
-          f32x4 off[NB];
-#pragma unroll
-          for (int p = 0; p < NB; p++) {
-            off[p] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < kPer; i++)
-              off[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  a[u][p][g * kPer + i], splat(F::ZERO ? 1.0f : -24.0f), off[p], 0, 0, 0);
-          }
-#pragma unroll
-          for (int j = 0; j < NTW; j++) {
-            const uint32_t d[4] = {cw[u][j].x, cw[u][j].y, cw[u][j].z, cw[u][j].w};
-            const float scale = scale_value(sc[u][j].s[g], m[j].f16);
-            f32x4 part[NB];
-#pragma unroll
-            for (int p = 0; p < NB; p++)
-              part[p] = F::ZERO ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : off[p];
-#pragma unroll
-            for (int i = 0; i < kPer; i++) {
-              const bf16x8 b = F::unpack(d[g * kPer + i], sc[u][j], i);
-#pragma unroll
-              for (int p = 0; p < NB; p++)
-                part[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][p][g * kPer + i], b, part[p],
-                                                                  0, 0, 0);
-            }
-#pragma unroll
-            for (int p = 0; p < NB; p++)
-#pragma unroll
-              for (int v = 0; v < 4; v++) {
-                float t = part[p][v];
-                if constexpr (F::ZERO) t = fmaf(-(16.0f + (float)sc[u][j].z[g]), off[p][v], t);
-                acc[j][p][v] = fmaf(scale, t, acc[j][p][v]);
-              }
-          }
-        }
-      }
+    for (int j = 0; j < NTW; j++) {
+      cw[d][j] = m[j].codes(step);
+      sc[d][j] = m[j].scales(step);
     }
+  }
+};
+
+// f(integral_constant<int, d>) for d = 0 .. N - 1
+template <int N, int d = 0, class Fn>
+__device__ __forceinline__ void each(Fn &&f) {
+  if constexpr (d < N) {
+    f(std::integral_constant<int, d>{});
+    each<N, d + 1>(f);
   }
 }
 

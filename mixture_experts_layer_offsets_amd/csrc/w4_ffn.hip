@@ -1,13 +1,12 @@
-// Few-token FFN of experts with 4-bit weights (w4_device.h), in two launches:
-//   gate_up: a[f] = w silu(x Wg) (x Wu) for every token and expert it uses, at
-//            the place f of its first slot with that expert (w: the routing
-//            weight, summed if the token names the expert twice);
-//   down:    out[t] = sum over the experts of a Wd (+ the shared expert), one
-//            long contraction over all used experts: the weighted sum of the
-//            experts' outputs is the matrix product's own accumulation, and
-//            neither expert outputs nor a combine exist.
-// No layout is made: at a few hundred slots every workgroup finds its expert's
-// slots itself (a launch of its own would cost more than the search).
+// Few-token FFN of experts with 4-bit weights (w4_device.h):
+//   plan:    (more than one token) the used experts, and for each the slots
+//            that are its tokens' first ones with it, with the routing weight
+//            (summed if a token names the expert twice); one token's few slots
+//            are looked up by every workgroup itself;
+//   gate_up: a[f] = w silu(x Wg) (x Wu) at the place f of such a slot;
+//   down:    out[t] = sum over the experts of a Wd (+ the shared expert): the
+//            weighted sum of the experts' outputs is the matrix product's own
+//            accumulation, and neither expert outputs nor a combine exist.
 #include <algorithm>
 
 #include "w4_device.h"
@@ -16,143 +15,157 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1; }
+constexpr int kWaves = 8;           // waves of a workgroup
+constexpr int kRowLds = 64 * 1024;  // most LDS for staged rows
+constexpr int kTokenBlock = 64;     // tokens of one down workgroup
 
-// Bit u (counted from 0) of the set bits of m, or -1.
-__device__ __forceinline__ int nth_bit(uint64_t m, int u) {
-  for (; u > 0 && m; u--) m &= m - 1;
-  return m ? __ffsll((unsigned long long)m) - 1 : -1;
-}
+__device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1; }
 
 __device__ __forceinline__ int local_id(int32_t id, int first, int E) {
   const int64_t e = (int64_t)id - first;
   return e >= 0 && e < E ? (int)e : -1;
 }
 
-// The used experts of a call, found by each workgroup.  Up to 64 slots: one
-// slot a lane, in every wave, without LDS or barriers; the u-th expert is that
-// of the u-th lane that is its expert's first.  More: ids in LDS, experts in
-// ascending order.
-struct Few {
-  int e;              // this lane's expert, or -1
-  uint64_t mine;      // lanes with the same expert
-  uint64_t firsts;    // lanes that are the first of their expert
-};
-
-__device__ __forceinline__ Few few_slots(const int32_t *idx, int slots, int first, int E) {
-  const int lane = threadIdx.x & 63;
-  Few s;
-  s.e = lane < slots ? local_id(idx[lane], first, E) : -1;
-  s.mine = ~0ull;
-  const int bits = 32 - __clz(E);  // of e + 1 <= E
-  for (int b = 0; b < bits; b++) {
-    const bool bit = ((s.e + 1) >> b) & 1;
+// Lanes whose e equals this lane's (e >= -1, below E).
+__device__ __forceinline__ uint64_t same_expert(int e, int E) {
+  uint64_t mine = ~0ull;
+  for (int b = 0; b < 32 - __clz(E); b++) {  // the bits of e + 1 <= E
+    const bool bit = ((e + 1) >> b) & 1;
     const uint64_t m = __ballot(bit);
-    s.mine &= bit ? m : ~m;
+    mine &= bit ? m : ~m;
   }
-  s.firsts = __ballot(s.e >= 0 && !(s.mine & below(lane)));
-  return s;
+  return mine;
 }
 
-__device__ __forceinline__ uint64_t read_mask(uint64_t m, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)m, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(m >> 32), lane);
-  return ((uint64_t)hi << 32) | lo;
-}
+// ---------------------------------------------------------------------------
+// Plan: one workgroup.  rows[roff[i] .. roff[i + 1]) are the slots of the i-th
+// used expert elist[i] (ascending), wrow their weights.
 
-// LDS of the many-slots search.
-struct Many {
-  int16_t *ids;      // [slots] local expert ids
-  uint32_t *used;    // [32] experts that have slots, one bit each
+struct Plan {
+  int32_t *used, *elist, *roff, *rows;
+  float *wrow;
 };
 
-template <int THREADS>
-__device__ __forceinline__ void many_slots(const int32_t *idx, int slots, int first, int E, Many s) {
-  const int tid = threadIdx.x;
-  if (tid < 32) s.used[tid] = 0;
-  __syncthreads();
-  for (int f = tid; f < slots; f += THREADS) {
-    const int e = local_id(idx[f], first, E);
-    s.ids[f] = (int16_t)e;
-    if (e >= 0) atomicOr(&s.used[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-}
+constexpr int kPlanThreads = 1024;
 
-// Used experts in the words before this lane's (lanes 0..31 hold the words).
-__device__ __forceinline__ int used_before(uint32_t word) {
-  const int lane = threadIdx.x & 63, n = __popc(word);
-  int inc = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += v;
-  }
-  return inc - n;
-}
-
-// Rows of the u-th used expert: list[r] = f, the first slot of its r-th token
-// with it, ascending.  Returns the expert (-1: no u-th one) and the count.
-template <int THREADS>
-__device__ __forceinline__ int find_rows(const int32_t *idx, int slots, int k, int first, int E,
-                                         int u, uint16_t *list, Many ms, int *count) {
-  __shared__ int chunk_rows[kW4MaxSlots / 64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  if (slots <= 64) {
-    const Few s = few_slots(idx, slots, first, E);
-    const int at = nth_bit(s.firsts, u);
-    if (at < 0) return -1;
-    const uint64_t members = read_mask(s.mine, at);
-    const int t0 = lane / k * k;  // the lane's token's first slot
-    const bool row = (members >> lane & 1) && !(members & below(lane) & ~below(t0));
-    const uint64_t rows = __ballot(row);
-    // every wave writes, and then reads, the same values
-    if (row) list[__popcll(rows & below(lane))] = (uint16_t)lane;
-    *count = __popcll(rows);
-    return __builtin_amdgcn_readlane(s.e, at);
-  }
-  many_slots<THREADS>(idx, slots, first, E, ms);
-  const uint32_t word = lane < 32 ? ms.used[lane] : 0;
-  const int before = used_before(word);
-  const uint64_t hit = __ballot(before <= u && u < before + __popc(word));
-  if (!hit) return -1;
-  const int wl = __ffsll((unsigned long long)hit) - 1;
-  const int e = 32 * wl + nth_bit(__builtin_amdgcn_readlane(word, wl),
-                                  u - __builtin_amdgcn_readlane(before, wl));
-  // the first slot of each token with e, 64 slots a wave and turn: counts,
-  // then places
-  auto is_row = [&](int f) {
-    if (f >= slots || ms.ids[f] != e) return false;
+__global__ __launch_bounds__(kPlanThreads) void w4_plan_kernel(const int32_t *__restrict__ idx,
+                                                               const float *__restrict__ w,
+                                                               int slots, int k, int first, int E,
+                                                               Plan p) {
+  extern __shared__ int32_t lds[];
+  int32_t *cnt = lds;                 // [E] rows of each expert, then its next free row
+  int32_t *wcnt = cnt + E;            // [16][E] rows per wave in this round
+  int16_t *ids = (int16_t *)(wcnt + 16 * E);  // [slots]
+  __shared__ int32_t wsum[16], wused[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < 17 * E; i += kPlanThreads) lds[i] = 0;
+  for (int f = tid; f < slots; f += kPlanThreads) ids[f] = (int16_t)local_id(idx[f], first, E);
+  __syncthreads();
+  // slot f is a row if no earlier slot of its token has the same expert
+  auto row_expert = [&](int f) {
+    if (f >= slots || ids[f] < 0) return -1;
+    const int e = ids[f];
     for (int g = f / k * k; g < f; g++)
-      if (ms.ids[g] == e) return false;
-    return true;
+      if (ids[g] == e) return -1;
+    return e;
   };
-  const int chunks = (slots + 63) / 64, wave = tid >> 6;
-  for (int c = wave; c < chunks; c += THREADS / 64) {
-    const int n = __popcll(__ballot(is_row(64 * c + lane)));
-    if (lane == 0) chunk_rows[c] = n;
+  for (int f = tid; f < slots; f += kPlanThreads) {
+    const int e = row_expert(f);
+    if (e >= 0) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  int inc = lane < chunks ? chunk_rows[lane] : 0;
-  const int own = inc;
+  // one thread per expert (E <= 1024): exclusive scans of rows and of use
+  const int n = tid < E ? cnt[tid] : 0;
+  int inc = n;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int v = __shfl_up(inc, o, 64);
     if (lane >= o) inc += v;
   }
-  *count = __builtin_amdgcn_readlane(inc, 63);
-  for (int c = wave; c < chunks; c += THREADS / 64) {
-    const bool row = is_row(64 * c + lane);
-    const uint64_t rows = __ballot(row);
-    const int at = __builtin_amdgcn_readlane(inc - own, c);
-    if (row) list[at + __popcll(rows & below(lane))] = (uint16_t)(64 * c + lane);
+  const uint64_t use = __ballot(n > 0);
+  if (lane == 63) {
+    wsum[wave] = inc;
+    wused[wave] = __popcll(use);
   }
   __syncthreads();
-  return e;
+  int at = inc - n, rank = __popcll(use & below(lane));
+  for (int v = 0; v < wave; v++) {
+    at += wsum[v];
+    rank += wused[v];
+  }
+  if (n > 0) {
+    p.elist[rank] = tid;
+    p.roff[rank] = at;
+  }
+  if (tid == kPlanThreads - 1) {
+    p.used[0] = rank + (n > 0);
+    p.roff[rank + (n > 0)] = at + n;
+  }
+  if (tid < E) cnt[tid] = at;
+  __syncthreads();
+  // stable places, 1024 slots a round
+  for (int f0 = 0; f0 < slots; f0 += kPlanThreads) {
+    const int f = f0 + tid, e = row_expert(f);
+    const uint64_t mine = same_expert(e, E);
+    const int before = __popcll(mine & below(lane));
+    const bool lead = e >= 0 && before == 0;
+    if (lead) wcnt[wave * E + e] = __popcll(mine);
+    __syncthreads();
+    if (e >= 0) {
+      int pos = cnt[e] + before;
+      for (int v = 0; v < wave; v++) pos += wcnt[v * E + e];
+      float sum = w[f];
+      for (int g = f + 1; g < f / k * k + k; g++)
+        if (ids[g] == e) sum += w[g];
+      p.rows[pos] = f;
+      p.wrow[pos] = sum;
+    }
+    __syncthreads();
+    if (lead) {
+      atomicAdd(&cnt[e], __popcll(mine));
+      wcnt[wave * E + e] = 0;
+    }
+    __syncthreads();
+  }
 }
 
-// One FFN's matrices and slots.  idx null: the shared expert, every token a
-// row with weight one (k = 1).
+// One token's slots (at most 16), in every wave: its distinct experts in slot
+// order, one a lane.
+struct Token {
+  int used, e, f;  // lane i < used: expert, first slot
+  float w;         // and weight
+};
+
+__device__ __forceinline__ Token one_token(const int32_t *idx, const float *w, int k, int first,
+                                           int E) {
+  const int lane = threadIdx.x & 63;
+  const int e = lane < k ? local_id(idx[lane], first, E) : -1;
+  const float own = lane < k ? w[lane] : 0.0f;
+  const uint64_t mine = same_expert(e, E);
+  const bool head = e >= 0 && !(mine & below(lane));
+  float sum = own;
+  for (int j = 1; j < k; j++) {  // later slots with the same expert
+    const float v = __shfl_down(own, j, 64);
+    if (lane + j < k && (mine >> (lane + j) & 1)) sum += v;
+  }
+  Token t{0, -1, 0, 0.0f};
+  for (uint64_t heads = __ballot(head); heads; heads &= heads - 1) {
+    const int at = __ffsll((unsigned long long)heads) - 1;
+    const int he = __builtin_amdgcn_readlane(e, at);
+    const float hw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sum), at));
+    if (lane == t.used) {
+      t.e = he;
+      t.f = at;
+      t.w = hw;
+    }
+    t.used++;
+  }
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// gate_up.
+
 struct Ffn {
   W4Mat gate, up;
   const int32_t *idx;
@@ -161,198 +174,371 @@ struct Ffn {
   uint16_t *act;
 };
 
+// The rows of one expert: n of them, at slots f[r] with weights w[r]; f null: n
+// consecutive slots from f1 on, with weight w1.
+struct Rows {
+  int e, n, f1;
+  float w1;
+  const int32_t *f;
+  const float *w;
+  __device__ __forceinline__ int slot(int r) const { return f ? f[r] : f1 + r; }
+  __device__ __forceinline__ float weight(int r) const { return f ? w[r] : w1; }
+};
+
+// Rows of workgroup row u (u == used: the shared expert's, every token).
+template <bool SINGLE>
+__device__ __forceinline__ Rows find_rows(const Ffn &q, const Plan &plan, int u, bool shared) {
+  if (shared) return {0, q.slots, 0, 1.0f, nullptr, nullptr};
+  if constexpr (SINGLE) {
+    const Token t = one_token(q.idx, q.w, q.k, q.first, q.E);
+    if (u >= t.used) return {0, 0, 0, 0.0f, nullptr, nullptr};
+    return {__builtin_amdgcn_readlane(t.e, u), 1, __builtin_amdgcn_readlane(t.f, u),
+            __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(t.w), u)), nullptr, nullptr};
+  }
+  if (u >= __builtin_amdgcn_readfirstlane(plan.used[0])) return {0, 0, 0, 0.0f, nullptr, nullptr};
+  const int at = __builtin_amdgcn_readfirstlane(plan.roff[u]);
+  return {__builtin_amdgcn_readfirstlane(plan.elist[u]),
+          __builtin_amdgcn_readfirstlane(plan.roff[u + 1]) - at, 0, 0.0f, plan.rows + at,
+          plan.wrow + at};
+}
+
+// a[f] of row r and output n, from the sums of its gate and up products:
+// rounded to bf16 once, weight included, as the matrix operand of down.
+__device__ __forceinline__ void put_act(const Ffn &q, const Rows &rows, int r, int n, float g,
+                                        float u) {
+  if (n < q.gate.n)
+    q.act[(size_t)rows.slot(r) * q.gate.n + n] = to_bf16(rows.weight(r) * silu_f(g) * u);
+}
+
+// Rows in LDS (16 a pass, at most kRowLds).  A workgroup takes `tpw` tile pairs
+// of one expert; its waves take their steps in turn.  Grid (tile groups, used
+// experts [+ 1: the shared expert]).
+template <class F, int D, bool SINGLE>
+__global__ __launch_bounds__(kWaves * 64, 4) void w4_gate_up_lds_kernel(Ffn routed, Ffn shared,
+                                                                     Plan plan, int used, int tpw,
+                                                                     const uint16_t *x) {
+  extern __shared__ __attribute__((aligned(16))) char xs[];
+  __shared__ float red[kWaves * 2 * 256];
+  const bool is_shared = (int)blockIdx.y == used;
+  const Ffn q = is_shared ? shared : routed;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int K = q.gate.k, ks = q.gate.ks, nt = q.gate.nt, KC = K / 8, pitch = w4_pitch(K);
+  const int j0 = blockIdx.x * tpw, j1 = min(j0 + tpw, nt);
+  if (j0 >= nt) return;
+  const Rows rows = find_rows<SINGLE>(q, plan, blockIdx.y, is_shared);
+  if (rows.n == 0) return;
+  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
+  const int n = wave < ks ? (ks - wave + kWaves - 1) / kWaves : 0;  // steps of this wave
+  const int rounds = max((n + D - 1) / D, 1);
+  for (int r0 = 0; r0 < rows.n; r0 += 16) {
+    const int nr = min(16, rows.n - r0);
+    W4Ring<F, 2, D> ring;
+    // slot d: step i of this wave
+    auto refill = [&](auto d, const W4Row<F>(&m)[2], int i) {
+      ring.template load<decltype(d)::value>(m, min(wave + kWaves * i, ks - 1));
+    };
+    W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j0), W4Row<F>(q.up, base + j0)};
+    each<D>([&](auto d) { refill(d, mm, d); });
+    for (int c0 = tid; c0 < nr * KC; c0 += kWaves * 64 * 4) {
+      w4_u32x4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int c = min(c0 + kWaves * 64 * u, nr * KC - 1), r = c / KC;
+        v[u] = *(const w4_u32x4u *)(x + (size_t)(rows.slot(r0 + r) / q.k) * K + (c - r * KC) * 8);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int c = c0 + kWaves * 64 * u, r = c / KC;
+        if (c < nr * KC) *(w4_u32x4 *)(xs + r * pitch + (c - r * KC) * 16) = v[u];
+      }
+    }
+    lds_barrier();
+    const RowLds xr = {xs + min(lane & 15, nr - 1) * pitch};
+    for (int j = j0; j < j1; j++) {
+      const size_t follow = base + min(j + 1, nt - 1);
+      const W4Row<F> after[2] = {W4Row<F>(q.gate, follow), W4Row<F>(q.up, follow)};
+      f32x4 acc[2][1];
+      zero_acc(acc);
+      for (int i0 = 0; i0 < rounds * D; i0 += D) {
+        each<D>([&](auto d) {
+          const int i = i0 + d;
+          if (i < n) {
+            bf16x8 a[1][4];
+#pragma unroll
+            for (int b = 0; b < 4; b++)
+              a[0][b] = xr.load(min(128 * (wave + kWaves * i) + 32 * b + 8 * (lane >> 4), K - 8));
+            w4_step<F>(q.gate.f16, ring.cw[d], ring.sc[d], a, acc);
+          }
+          // the next step of this tile, or of the one after it
+          const int next = i + D;
+          if (next < rounds * D) refill(d, mm, next);
+          else refill(d, after, next - rounds * D);
+        });
+      }
+#pragma unroll
+      for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int v = 0; v < 4; v++) red[(wave * 8 + m * 4 + v) * 64 + lane] = acc[m][0][v];
+      lds_barrier();
+      const int v = tid >> 6, row = 4 * ((tid & 63) >> 4) + v;
+      if (tid < 256 && row < nr) {
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) {
+          g += red[(w * 8 + v) * 64 + (tid & 63)];
+          u += red[(w * 8 + 4 + v) * 64 + (tid & 63)];
+        }
+        put_act(q, rows, r0 + row, 16 * j + (tid & 15), g, u);
+      }
+      lds_barrier();
+      mm[0] = after[0];
+      mm[1] = after[1];
+    }
+  }
+}
+
+// Rows from memory, 16 NB a pass: wide rows of several tokens.  Grid (tiles,
+// used experts [+ 1]).
 constexpr int kGuWaves = 4;
 
-// Grid (output tiles, used experts [+ 1: the shared expert]).
 template <class F, int NB>
-__global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, Ffn shared, int used,
-                                                                   const uint16_t *x) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+__global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, Ffn shared, Plan plan,
+                                                                   int used, const uint16_t *x) {
   __shared__ float red[kGuWaves * 2 * NB * 256];
-  __shared__ float wrow[16 * NB];
   const bool is_shared = (int)blockIdx.y == used;
-  const Ffn &q = is_shared ? shared : routed;
-  const W4Mat mm[2] = {q.gate, q.up};
-  const int I = q.gate.n, K = q.gate.k, ks = q.gate.ks;
+  const Ffn q = is_shared ? shared : routed;
   if ((int)blockIdx.x >= q.gate.nt) return;
-  uint16_t *list = (uint16_t *)dyn;
-  int expert = 0, count = q.slots;
-  if (!is_shared) {
-    const Many ms = {(int16_t *)(list + q.slots), (uint32_t *)(dyn + 4 * ((q.slots + 3) & ~3))};
-    expert = find_rows<kGuWaves * 64>(q.idx, q.slots, q.k, q.first, q.E, blockIdx.y, list, ms,
-                                      &count);
-    if (expert < 0) return;
-  }
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const size_t base = ((size_t)expert * q.gate.nt + blockIdx.x) * ks;
-  const size_t tile[2] = {base, base};
-  for (int r0 = 0; r0 < count; r0 += 16 * NB) {
-    const int nr = min(16 * NB, count - r0);
-    auto slot = [&](int r) { return is_shared ? r0 + r : (int)list[r0 + r]; };
+  const Rows rows = find_rows<false>(q, plan, blockIdx.y, is_shared);
+  const int tid = threadIdx.x, lane = tid & 63, K = q.gate.k, ks = q.gate.ks;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * q.gate.nt + blockIdx.x;
+  const W4Row<F> mm[2] = {W4Row<F>(q.gate, base), W4Row<F>(q.up, base)};
+  for (int r0 = 0; r0 < rows.n; r0 += 16 * NB) {
+    const int nr = min(16 * NB, rows.n - r0);
     RowPtr xr[NB];
 #pragma unroll
     for (int p = 0; p < NB; p++)
-      xr[p].p = x + (size_t)(slot(min(16 * p + (lane & 15), nr - 1)) / q.k) * K;
-    if (tid < nr) {
-      float w = 1.0f;
-      if (!is_shared) {
-        const int f = slot(tid);
-        w = q.w[f];
-        for (int g = f + 1; g < f / q.k * q.k + q.k; g++)
-          if (local_id(q.idx[g], q.first, q.E) == expert) w += q.w[g];
-      }
-      wrow[tid] = w;
-    }
+      xr[p].p = x + (size_t)(rows.slot(r0 + min(16 * p + (lane & 15), nr - 1)) / q.k) * K;
     f32x4 acc[2][NB];
     zero_acc(acc);
-    w4_stream<F>(mm, tile, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+    w4_stream<F>(mm, q.gate.f16, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
     w4_join<kGuWaves>(acc, red);
     for (int i = tid; i < NB * 256; i += kGuWaves * 64) {
-      const int l = i & 63, v = (i >> 6) & 3;
-      const int row = 16 * (i >> 8) + 4 * (l >> 4) + v, n = 16 * blockIdx.x + (l & 15);
-      // rounded to bf16 once, weight included: the matrix operand of down
-      if (row < nr && n < I)
-        q.act[(size_t)slot(row) * I + n] =
-            to_bf16(wrow[row] * silu_f(red[i]) * red[NB * 256 + i]);
+      const int row = 16 * (i >> 8) + 4 * ((i & 63) >> 4) + ((i >> 6) & 3);
+      if (row < nr) put_act(q, rows, r0 + row, 16 * blockIdx.x + (i & 15), red[i], red[NB * 256 + i]);
     }
     __syncthreads();
   }
 }
 
+// ---------------------------------------------------------------------------
+// down.
+
 struct Down {
   W4Mat m, shared;  // shared.ks == 0: no shared expert
   const int32_t *idx;
+  const float *w;
   int slots, k, first, E, T;
   const uint16_t *act, *act_s;
 };
 
-// Grid (output tiles, token blocks of 16 NB).  The steps of all used experts
-// and of the shared one are one sequence, split over the waves.
-template <class F, int NB, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void w4_down_kernel(Down q, uint16_t *__restrict__ out) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  __shared__ float red[WAVES * NB * 256];
+// One token: the hidden rows of its experts (and the shared one) lie in LDS one
+// behind the other, and their steps are one sequence, taken in turn by the
+// waves.  Grid: output tiles.
+template <class F, int D>
+__global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
+                                                                    uint16_t *__restrict__ out) {
+  extern __shared__ __attribute__((aligned(16))) char xs[];
+  __shared__ float red[kWaves * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.y * 16 * NB, ks = q.m.ks, k = q.k;
-  const bool few = q.slots <= 64;
-  const Many ms = {(int16_t *)dyn, (uint32_t *)(dyn + 2 * ((q.slots + 7) & ~7))};
-  uint16_t *ulist = (uint16_t *)(ms.used + 32);
-  Few s{};
-  int used;
-  if (few) {
-    s = few_slots(q.idx, q.slots, q.first, q.E);
-    used = __popcll(s.firsts);
-  } else {
-    many_slots<WAVES * 64>(q.idx, q.slots, q.first, q.E, ms);
-    const uint32_t word = lane < 32 ? ms.used[lane] : 0;
-    int at = used_before(word);
-    used = __builtin_amdgcn_readlane(at + __popc(word), 31);
-    if (wave == 0)
-      for (uint32_t b = word; b; b &= b - 1) ulist[at++] = (uint16_t)(32 * lane + __ffs(b) - 1);
-    __syncthreads();
-  }
-  const int total = used * ks + q.shared.ks;
-  int a = total * wave / WAVES;
-  const int b = total * (wave + 1) / WAVES;
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      (void *)q.act, (short)0, (int)((size_t)q.slots * q.m.k * 2), 0x00020000);
-  f32x4 acc[1][NB];
+  const Token t = one_token(q.idx, q.w, q.k, q.first, q.E);
+  f32x4 acc[1][1];
   zero_acc(acc);
-  int u = a / ks;
-  uint64_t firsts = s.firsts;
-  for (int i = 0; i < u && firsts; i++) firsts &= firsts - 1;
-  RowBuf xr[NB];
-  while (a < b && u < used) {
-    const int end = min(b, (u + 1) * ks);
-    int e;
-    uint64_t members = 0;
-    if (few) {
-      const int at = __ffsll((unsigned long long)firsts) - 1;
-      firsts &= firsts - 1;
-      e = __builtin_amdgcn_readlane(s.e, at);
-      members = read_mask(s.mine, at);
-    } else {
-      e = ulist[u];
-    }
-    bool any = false;
+  // the steps of `count` matrices, matrix i that of expert (lane i of e), its
+  // row at LDS x0 + i rows of K values; put() stages those rows
+  auto run = [&](const W4Mat &m, int count, int e, const char *x0, auto put) {
+    const int ks = m.ks, K = m.k, total = count * ks;
+    const int a = total * wave / kWaves, n = total * (wave + 1) / kWaves - a;
+    W4Ring<F, 1, D> ring;
+    // the next step to load, and to use: matrix and step in it
+    int lu = a / ks, ls = a - lu * ks, cu = lu, cs = ls;
+    auto refill = [&](auto d) {
+      const size_t row = (size_t)__builtin_amdgcn_readlane(e, lu) * m.nt + blockIdx.x;
+      const W4Row<F> mm[1] = {W4Row<F>(m, row)};
+      ring.template load<decltype(d)::value>(mm, ls);
+      const bool last = ls + 1 == ks;  // at the end: the last step again
+      ls = last ? (lu + 1 < count ? 0 : ls) : ls + 1;
+      lu += last && lu + 1 < count;
+    };
+    each<D>([&](auto d) { refill(d); });
+    put();
+    lds_barrier();
+    for (int i0 = 0; i0 < n; i0 += D) {
+      each<D>([&](auto d) {
+        if (i0 + d < n) {
+          const RowLds xr = {x0 + 2 * cu * K};
+          bf16x8 x[1][4];
 #pragma unroll
-    for (int p = 0; p < NB; p++) {
-      const int t = t0 + 16 * p + (lane & 15);
-      int f = -1;
-      if (t < q.T) {
-        if (few) {
-          const uint64_t mt = members >> (t * k) & below(k);
-          if (mt) f = t * k + __ffsll((unsigned long long)mt) - 1;
-        } else {
-          for (int j = k - 1; j >= 0; j--)
-            if (ms.ids[t * k + j] == e) f = t * k + j;
+          for (int b = 0; b < 4; b++)
+            x[0][b] = xr.load(min(128 * cs + 32 * b + 8 * (lane >> 4), K - 8));
+          w4_step<F>(m.f16, ring.cw[d], ring.sc[d], x, acc);
+          const bool last = cs + 1 == ks;
+          cs = last ? 0 : cs + 1;
+          cu += last;
         }
-      }
-      xr[p] = {ra, f >= 0 ? (uint32_t)f * (uint32_t)(q.m.k * 2) : kNoRow};
-      any |= f >= 0;
+        refill(d);
+      });
     }
-    // an expert that no token of this block uses adds nothing
-    if (__ballot(any)) {
-      const W4Mat mm[1] = {q.m};
-      const size_t tile[1] = {((size_t)__builtin_amdgcn_readfirstlane(e) * q.m.nt + blockIdx.x) * ks};
-      w4_stream<F>(mm, tile, xr, q.m.k, a - u * ks, end - u * ks, acc);
-    }
-    a = end;
-    u++;
+  };
+  auto stage = [&](const uint16_t *src, int K, char *dst) {
+    for (int c = tid; c < K / 8; c += kWaves * 64) ((w4_u32x4 *)dst)[c] = ((const w4_u32x4 *)src)[c];
+  };
+  const int I = q.m.k;
+  if (t.used > 0)
+    run(q.m, t.used, t.e, xs, [&] {
+      for (int i = 0; i < t.used; i++)
+        stage(q.act + (size_t)__builtin_amdgcn_readlane(t.f, i) * I, I, xs + 2 * i * I);
+    });
+  if (q.shared.ks) {
+    char *x0 = xs + 2 * t.used * I;
+    run(q.shared, 1, 0, x0, [&] { stage(q.act_s, q.shared.k, x0); });
   }
-  if (a < b) {
-    const W4Mat mm[1] = {q.shared};
-    const size_t tile[1] = {(size_t)blockIdx.x * q.shared.ks};
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)q.act_s, (short)0, (int)((size_t)q.T * q.shared.k * 2), 0x00020000);
+  // row 0 of the product: lanes 0..15, first value
+  if (lane < 16) red[wave * 16 + lane] = acc[0][0][0];
+  lds_barrier();
+  const int nn = 16 * blockIdx.x + tid;
+  if (tid < 16 && nn < q.m.n) {
+    float s = 0.0f;
 #pragma unroll
-    for (int p = 0; p < NB; p++) {
-      const int t = t0 + 16 * p + (lane & 15);
-      xr[p] = {rs, t < q.T ? (uint32_t)t * (uint32_t)(q.shared.k * 2) : kNoRow};
-    }
-    w4_stream<F>(mm, tile, xr, q.shared.k, a - used * ks, b - used * ks, acc);
+    for (int w = 0; w < kWaves; w++) s += red[w * 16 + tid];
+    out[nn] = to_bf16(s);
   }
-  w4_join<WAVES>(acc, red);
-  for (int i = tid; i < NB * 256; i += WAVES * 64) {
-    const int l = i & 63, v = (i >> 6) & 3;
-    const int t = t0 + 16 * (i >> 8) + 4 * (l >> 4) + v, n = 16 * blockIdx.x + (l & 15);
-    if (t < q.T && n < q.m.n) out[(size_t)t * q.m.n + n] = to_bf16(red[i]);
+}
+
+// More tokens, kTokenBlock a workgroup: the steps of all used experts (and the
+// shared one) are one sequence, split over the waves; an expert's rows are its
+// own tokens, and their sums are added to the wave's [tokens][16] tile in LDS
+// at the end of each expert.  Grid (output tiles, token blocks).
+template <class F>
+__global__ __launch_bounds__(kWaves * 64, 4) void w4_down_kernel(Down q, Plan plan,
+                                                              uint16_t *__restrict__ out) {
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][tokens][16]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int t0 = blockIdx.y * kTokenBlock, tb = min(q.T - t0, kTokenBlock);
+  const int used = plan.used[0], ks = q.m.ks, k = q.k;
+  float *mine = sums + wave * tb * 16;
+  for (int i = lane; i < tb * 16; i += 64) mine[i] = 0.0f;
+  const int total = used * ks + q.shared.ks;
+  int a = total * wave / kWaves;
+  const int b = total * (wave + 1) / kWaves;
+  // rows [0, n) of matrix m's row of tiles at `row`, steps [s0, s1): slot(r) is
+  // the place of row r, its token slot(r) / kk
+  auto segment = [&](const W4Mat &m, size_t row, const uint16_t *act, int n, auto slot, int kk,
+                     int s0, int s1) {
+    const W4Row<F> mm[1] = {W4Row<F>(m, row * m.nt + blockIdx.x)};
+    for (int r0 = 0; r0 < n; r0 += 16) {
+      const int nr = min(16, n - r0);
+      const int f = slot(r0 + min(lane & 15, nr - 1));
+      const RowPtr xr[1] = {{act + (size_t)f * m.k}};
+      f32x4 acc[1][1];
+      zero_acc(acc);
+      w4_stream<F>(mm, m.f16, xr, m.k, s0, s1, acc);
+#pragma unroll
+      for (int v = 0; v < 4; v++) {
+        const int r = 4 * (lane >> 4) + v, t = __shfl(f, r, 64) / kk - t0;
+        if (r < nr) mine[t * 16 + (lane & 15)] += acc[0][0][v];
+      }
+    }
+  };
+  for (int u = a / ks; a < b && u < used; u++) {
+    const int end = min(b, (u + 1) * ks);
+    int r0 = plan.roff[u], r1 = plan.roff[u + 1];
+    if (q.T > kTokenBlock) {  // the rows of this block's tokens: slots ascend
+      int lo = 0, hi = 0;
+      for (int r = r0; r < r1; r += 64) {
+        const int f = r + lane < r1 ? plan.rows[r + lane] : 0x7FFFFFFF;
+        lo += __popcll(__ballot(f < t0 * k));
+        hi += __popcll(__ballot(f < (t0 + tb) * k));
+      }
+      r1 = r0 + hi;
+      r0 += lo;
+    }
+    const int32_t *rows = plan.rows + r0;
+    segment(q.m, __builtin_amdgcn_readfirstlane(plan.elist[u]), q.act, r1 - r0, [&](int r) { return rows[r]; }, k, a - u * ks,
+            end - u * ks);
+    a = end;
+  }
+  if (a < b)
+    segment(q.shared, 0, q.act_s, tb, [&](int r) { return t0 + r; }, 1, a - used * ks,
+            b - used * ks);
+  __syncthreads();
+  for (int i = tid; i < tb * 16; i += kWaves * 64) {
+    float s = 0.0f;
+    for (int w = 0; w < kWaves; w++) s += sums[w * tb * 16 + i];
+    const int n = 16 * blockIdx.x + (i & 15);
+    if (n < q.m.n) out[(size_t)(t0 + (i >> 4)) * q.m.n + n] = to_bf16(s);
   }
 }
 
 }  // namespace
 
+size_t w4_plan_words(int slots, int E) { return 64 + 2 * (size_t)E + 64 + 2 * (size_t)slots; }
+
 void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
-  Ffn r{w4_view(a.up, a.w_gate), w4_view(a.up, a.w_up), a.idx, a.w, a.T * a.k, a.k, a.first,
-        a.up.groups, a.act};
+  const int slots = a.T * a.k, E = a.up.groups, H = a.up.k, I = a.down.k;
+  Ffn r{w4_view(a.up, a.w_gate), w4_view(a.up, a.w_up), a.idx, a.w, slots, a.k, a.first, E, a.act};
   Ffn sh = r;
-  Down d{w4_view(a.down, a.w_down), {}, a.idx, r.slots, a.k, a.first, r.E, a.T, a.act, nullptr};
+  Down d{w4_view(a.down, a.w_down), {}, a.idx, a.w, slots, a.k, a.first, E, a.T, a.act, nullptr};
+  long token_lds = 2L * a.k * I;
   if (a.shared) {
     sh = {w4_view(a.up_s, a.ws_gate), w4_view(a.up_s, a.ws_up), nullptr, nullptr, a.T, 1, 0, 1,
           a.act_s};
     d.shared = w4_view(a.down_s, a.ws_down);
     d.act_s = a.act_s;
+    token_lds += 2L * a.down_s.k;
   }
-  const int used = std::min(r.E, r.slots), avg = r.slots / r.E;
-  const dim3 gu(a.shared ? std::max(a.up.nt, a.up_s.nt) : a.up.nt, used + (a.shared ? 1 : 0));
-  const size_t lds_gu = (size_t)4 * ((r.slots + 3) & ~3) + 128;
-  const size_t lds_dn = (size_t)2 * ((r.slots + 7) & ~7) + 128 + 2 * 1024;
+  Plan p;
+  p.used = a.plan;
+  p.elist = p.used + 64;
+  p.roff = p.elist + E;
+  p.rows = p.roff + E + 64;
+  p.wrow = (float *)(p.rows + slots);
+  const int used = std::min(E, slots), avg = slots / E;
+  const int nt = a.shared ? std::max(a.up.nt, a.up_s.nt) : a.up.nt;
+  const long row_lds = (long)std::min(a.T, 16) * w4_pitch(H);
+  const bool staged = row_lds <= kRowLds && avg <= 16;
+  const bool single = a.T == 1 && staged && token_lds <= kRowLds;
+  if (!single)
+    hipLaunchKernelGGL(w4_plan_kernel, dim3(1), dim3(kPlanThreads),
+                       (17 * E + (slots + 1) / 2) * sizeof(int32_t), s, a.idx, a.w, slots, a.k,
+                       a.first, E, p);
+  const unsigned gy = used + (a.shared ? 1 : 0);
   with_format(a.up, [&](auto f) {
     using F = decltype(f);
-    auto up = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, gu, dim3(kGuWaves * 64), lds_gu, s, r, sh, used, a.x);
-    };
-    if (avg <= 16) up(w4_gate_up_kernel<F, 1>);
-    else if (avg <= 32) up(w4_gate_up_kernel<F, 2>);
-    else up(w4_gate_up_kernel<F, 4>);
-    auto down = [&](auto kernel, int nb, int waves) {
-      hipLaunchKernelGGL(kernel, dim3(a.down.nt, (a.T + 16 * nb - 1) / (16 * nb)), dim3(waves * 64),
-                         lds_dn, s, d, a.out);
-    };
-    if (a.T <= 16 && a.down.nt >= 256) down(w4_down_kernel<F, 1, 8>, 1, 8);
-    else if (a.T <= 16) down(w4_down_kernel<F, 1, 16>, 1, 16);
-    else if (a.T <= 32) down(w4_down_kernel<F, 2, 16>, 2, 16);
-    else down(w4_down_kernel<F, 4, 8>, 4, 8);
+    if (staged) {
+      // about two workgroups a CU
+      const int tpw = std::max(1, (int)(((long)nt * gy + 511) / 512));
+      auto up = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((nt + tpw - 1) / tpw, gy), dim3(kWaves * 64), row_lds, s, r,
+                           sh, p, used, tpw, a.x);
+      };
+      if (single) up(w4_gate_up_lds_kernel<F, 4, true>);
+      else up(w4_gate_up_lds_kernel<F, 4, false>);
+    } else {
+      auto up = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(nt, gy), dim3(kGuWaves * 64), 0, s, r, sh, p, used, a.x);
+      };
+      if (avg <= 16) up(w4_gate_up_kernel<F, 1>);
+      else if (avg <= 32) up(w4_gate_up_kernel<F, 2>);
+      else up(w4_gate_up_kernel<F, 4>);
+    }
+    if (single)
+      hipLaunchKernelGGL((w4_down_token_kernel<F, 8>), dim3(a.down.nt), dim3(kWaves * 64), token_lds,
+                         s, d, a.out);
+    else
+      hipLaunchKernelGGL(w4_down_kernel<F>,
+                         dim3(a.down.nt, (a.T + kTokenBlock - 1) / kTokenBlock), dim3(kWaves * 64),
+                         kWaves * 64 * std::min(a.T, kTokenBlock), s, d, p, a.out);
   });
 }
 

@@ -18,9 +18,8 @@ __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
   // offsets are the caller's: kept inside [0, rows]
   const int rb = offsets ? min(max(offsets[g], 0), rows) : 0;
   const int re = offsets ? min(max(offsets[g + 1], 0), rows) : rows;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const W4Mat mm[1] = {m};
-  const size_t tile[1] = {((size_t)g * m.nt + t0) * m.ks};
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const W4Row<F> mm[1] = {W4Row<F>(m, (size_t)g * m.nt + t0)};
   for (int r0 = rb; r0 < re; r0 += 16 * NB) {
     const int nr = min(16 * NB, re - r0);
     RowPtr xr[NB];
@@ -29,7 +28,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
       xr[p].p = x + (r0 + min(16 * p + (lane & 15), nr - 1)) * xstride;
     f32x4 acc[1][NB];
     zero_acc(acc);
-    w4_stream<F>(mm, tile, xr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
+    w4_stream<F>(mm, m.f16, xr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
     w4_join<WAVES>(acc, red);
     for (int i = threadIdx.x; i < NB * 256; i += WAVES * 64) {
       const int l = i & 63, v = (i >> 6) & 3;
