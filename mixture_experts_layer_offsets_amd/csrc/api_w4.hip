@@ -46,7 +46,7 @@ int check_w4(const moe_w4_shape *s, W4Dims *d) {
 // Workspace of the few-token layer.
 struct Work {
   uint16_t *act, *act_s;
-  float *logits, *w;
+  float *y, *y_s, *logits, *w;
   int32_t *plan, *idx, *offsets, *tiles, *order;
 };
 
@@ -77,9 +77,11 @@ size_t carve(const moe_shape *s, void *ws, Work *w) {
     off += up256(bytes);
     return p;
   };
-  const size_t T = s->tokens, R = T * s->top_k, E = s->experts;
+  const size_t T = s->tokens, R = T * s->top_k, H = s->hidden, E = s->experts;
   w->act = (uint16_t *)take(R * s->inter * 2);
   w->act_s = (uint16_t *)take(T * s->shared_inter * 2);
+  w->y = (float *)take(R * H * 4);
+  w->y_s = (float *)take(s->shared_inter ? T * H * 4 : 0);
   w->plan = (int32_t *)take(w4_plan_words((int)R, (int)E) * 4);
   w->logits = (float *)take(T * E * 4);
   w->idx = (int32_t *)take(R * 4);
@@ -203,7 +205,7 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts, con
   a.x = x; a.idx = idx; a.w = wts;
   a.w_gate = experts->gate; a.w_up = experts->up; a.w_down = experts->down;
   a.ws_gate = experts->shared_gate; a.ws_up = experts->shared_up; a.ws_down = experts->shared_down;
-  a.act = w.act; a.act_s = w.act_s; a.plan = w.plan; a.out = out;
+  a.act = w.act; a.act_s = w.act_s; a.y = w.y; a.y_s = w.y_s; a.plan = w.plan; a.out = out;
   launch_w4_ffn(a, s);
   return status();
 }

@@ -34,8 +34,8 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
 
 // The few-token expert FFN: gate/up [E][H][I] and down [E][I][H], routing idx
 // and w [T][k] (ids less `first`; others are masked), the shared expert's
-// matrices if `shared`.  act [T k][I], act_s [T][Is] and plan (w4_plan_words)
-// are scratch.
+// matrices if `shared`.  act [T k][I], y [T k][H], act_s [T][Is], y_s [T][H] and
+// plan (w4_plan_words) are scratch.
 struct W4Layer {
   W4Dims up, down, up_s, down_s;
   bool shared;
@@ -45,6 +45,7 @@ struct W4Layer {
   const float *w;
   const void *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
   uint16_t *act, *act_s, *out;
+  float *y, *y_s;
   int32_t *plan;
 };
 size_t w4_plan_words(int slots, int E);

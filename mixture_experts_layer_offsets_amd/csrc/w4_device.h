@@ -245,23 +245,19 @@ __device__ __forceinline__ void w4_step(int f16, const uint4 (&cw)[NTW],
             acc[j][p][v] = fmaf(scale, t, acc[j][p][v]);
           }
       }
+      // a group at a time: groups side by side would take hundreds of registers
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 
-// Steps whose loads a wave has in flight together, for NB row blocks: their
-// rows take 16 NB registers a step.
-constexpr int w4_unroll(int NB) { return NB == 1 ? 4 : (NB == 2 ? 2 : 1); }
-
 // acc[j][p] += rows of block p times the row j of tiles over the steps [s0,
 // s1), the rows read from memory; x[p]: this lane's row of block p.  The rows,
-// codes and scales of a batch of steps are loaded together, one memory round
-// trip; steps past the end load the last step again and are not used.  Values
+// codes and scales of U steps are loaded together, one memory round trip; steps past the end load the last step again and are not used.  Values
 // of k past K meet zero weights: their lanes load the row's last values.
-template <class F, int NTW, int NB, class Row>
+template <class F, int U, int NTW, int NB, class Row>
 __device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, const Row (&x)[NB],
                                           int K, int s0, int s1, f32x4 (&acc)[NTW][NB]) {
-  constexpr int U = NTW == 1 ? w4_unroll(NB) : (w4_unroll(NB) + 1) / 2;
   const int h8 = 8 * ((threadIdx.x & 63) >> 4);
   for (int s = s0; s < s1; s += U) {
     uint4 cw[U][NTW];

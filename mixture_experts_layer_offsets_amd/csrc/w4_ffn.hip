@@ -16,8 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 8;           // waves of a workgroup
-constexpr int kRowLds = 64 * 1024;  // most LDS for staged rows
-constexpr int kTokenBlock = 64;     // tokens of one down workgroup
+constexpr int kRowLds = 66 * 1024;  // most LDS for staged rows: 16 of 2048 values, padded
 
 __device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1; }
 
@@ -164,170 +163,157 @@ __device__ __forceinline__ Token one_token(const int32_t *idx, const float *w, i
 }
 
 // ---------------------------------------------------------------------------
-// gate_up.
+// Rows of one expert.
 
+// One FFN's matrices and slots.  idx null: the shared expert, every token a
+// row with weight one (k = 1).
 struct Ffn {
-  W4Mat gate, up;
+  W4Mat gate, up, down;
   const int32_t *idx;
   const float *w;
   int slots, k, first, E;
   uint16_t *act;
+  float *y;
 };
 
-// The rows of one expert: n of them, at slots f[r] with weights w[r]; f null: n
-// consecutive slots from f1 on, with weight w1.
+// n rows, at slots f[r] (f null: 0, 1, ...).
+template <bool PLAN>
 struct Rows {
-  int e, n, f1;
-  float w1;
-  const int32_t *f;
-  const float *w;
-  __device__ __forceinline__ int slot(int r) const { return f ? f[r] : f1 + r; }
-  __device__ __forceinline__ float weight(int r) const { return f ? w[r] : w1; }
+  int e, n;
+  const int32_t *planned, *idx;
+  const float *wrow;
+  const uint16_t *list;  // LDS
+  const float *wlist;    // LDS
+  __device__ __forceinline__ int slot(int r) const {
+    if (!idx) return r;
+    if constexpr (PLAN) return planned[r];
+    return list[r];
+  }
+  // the routing weight, added up over the token's slots with this expert
+  __device__ __forceinline__ float weight(int r) const {
+    if (!idx) return 1.0f;
+    if constexpr (PLAN) return wrow[r];
+    return wlist[r];
+  }
 };
 
-// Rows of workgroup row u (u == used: the shared expert's, every token).
-template <bool SINGLE>
-__device__ __forceinline__ Rows find_rows(const Ffn &q, const Plan &plan, int u, bool shared) {
-  if (shared) return {0, q.slots, 0, 1.0f, nullptr, nullptr};
-  if constexpr (SINGLE) {
-    const Token t = one_token(q.idx, q.w, q.k, q.first, q.E);
-    if (u >= t.used) return {0, 0, 0, 0.0f, nullptr, nullptr};
-    return {__builtin_amdgcn_readlane(t.e, u), 1, __builtin_amdgcn_readlane(t.f, u),
-            __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(t.w), u)), nullptr, nullptr};
-  }
-  if (u >= __builtin_amdgcn_readfirstlane(plan.used[0])) return {0, 0, 0, 0.0f, nullptr, nullptr};
-  const int at = __builtin_amdgcn_readfirstlane(plan.roff[u]);
-  return {__builtin_amdgcn_readfirstlane(plan.elist[u]),
-          __builtin_amdgcn_readfirstlane(plan.roff[u + 1]) - at, 0, 0.0f, plan.rows + at,
-          plan.wrow + at};
-}
-
-// a[f] of row r and output n, from the sums of its gate and up products:
-// rounded to bf16 once, weight included, as the matrix operand of down.
-__device__ __forceinline__ void put_act(const Ffn &q, const Rows &rows, int r, int n, float g,
-                                        float u) {
-  if (n < q.gate.n)
-    q.act[(size_t)rows.slot(r) * q.gate.n + n] = to_bf16(rows.weight(r) * silu_f(g) * u);
-}
-
-// Rows in LDS (16 a pass, at most kRowLds).  A workgroup takes `tpw` tile pairs
-// of one expert; its waves take their steps in turn.  Grid (tile groups, used
-// experts [+ 1: the shared expert]).
-template <class F, int D, bool SINGLE>
-__global__ __launch_bounds__(kWaves * 64, 4) void w4_gate_up_lds_kernel(Ffn routed, Ffn shared,
-                                                                     Plan plan, int used, int tpw,
-                                                                     const uint16_t *x) {
-  extern __shared__ __attribute__((aligned(16))) char xs[];
-  __shared__ float red[kWaves * 2 * 256];
-  const bool is_shared = (int)blockIdx.y == used;
-  const Ffn q = is_shared ? shared : routed;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int K = q.gate.k, ks = q.gate.ks, nt = q.gate.nt, KC = K / 8, pitch = w4_pitch(K);
-  const int j0 = blockIdx.x * tpw, j1 = min(j0 + tpw, nt);
-  if (j0 >= nt) return;
-  const Rows rows = find_rows<SINGLE>(q, plan, blockIdx.y, is_shared);
-  if (rows.n == 0) return;
-  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
-  const int n = wave < ks ? (ks - wave + kWaves - 1) / kWaves : 0;  // steps of this wave
-  const int rounds = max((n + D - 1) / D, 1);
-  for (int r0 = 0; r0 < rows.n; r0 += 16) {
-    const int nr = min(16, rows.n - r0);
-    W4Ring<F, 2, D> ring;
-    // slot d: step i of this wave
-    auto refill = [&](auto d, const W4Row<F>(&m)[2], int i) {
-      ring.template load<decltype(d)::value>(m, min(wave + kWaves * i, ks - 1));
-    };
-    W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j0), W4Row<F>(q.up, base + j0)};
-    each<D>([&](auto d) { refill(d, mm, d); });
-    for (int c0 = tid; c0 < nr * KC; c0 += kWaves * 64 * 4) {
-      w4_u32x4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        const int c = min(c0 + kWaves * 64 * u, nr * KC - 1), r = c / KC;
-        v[u] = *(const w4_u32x4u *)(x + (size_t)(rows.slot(r0 + r) / q.k) * K + (c - r * KC) * 8);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        const int c = c0 + kWaves * 64 * u, r = c / KC;
-        if (c < nr * KC) *(w4_u32x4 *)(xs + r * pitch + (c - r * KC) * 16) = v[u];
-      }
-    }
-    lds_barrier();
-    const RowLds xr = {xs + min(lane & 15, nr - 1) * pitch};
-    for (int j = j0; j < j1; j++) {
-      const size_t follow = base + min(j + 1, nt - 1);
-      const W4Row<F> after[2] = {W4Row<F>(q.gate, follow), W4Row<F>(q.up, follow)};
-      f32x4 acc[2][1];
-      zero_acc(acc);
-      for (int i0 = 0; i0 < rounds * D; i0 += D) {
-        each<D>([&](auto d) {
-          const int i = i0 + d;
-          if (i < n) {
-            bf16x8 a[1][4];
-#pragma unroll
-            for (int b = 0; b < 4; b++)
-              a[0][b] = xr.load(min(128 * (wave + kWaves * i) + 32 * b + 8 * (lane >> 4), K - 8));
-            w4_step<F>(q.gate.f16, ring.cw[d], ring.sc[d], a, acc);
-          }
-          // the next step of this tile, or of the one after it
-          const int next = i + D;
-          if (next < rounds * D) refill(d, mm, next);
-          else refill(d, after, next - rounds * D);
-        });
-      }
-#pragma unroll
-      for (int m = 0; m < 2; m++)
-#pragma unroll
-        for (int v = 0; v < 4; v++) red[(wave * 8 + m * 4 + v) * 64 + lane] = acc[m][0][v];
-      lds_barrier();
-      const int v = tid >> 6, row = 4 * ((tid & 63) >> 4) + v;
-      if (tid < 256 && row < nr) {
-        float g = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) {
-          g += red[(w * 8 + v) * 64 + (tid & 63)];
-          u += red[(w * 8 + 4 + v) * 64 + (tid & 63)];
-        }
-        put_act(q, rows, r0 + row, 16 * j + (tid & 15), g, u);
-      }
-      lds_barrier();
-      mm[0] = after[0];
-      mm[1] = after[1];
-    }
-  }
-}
-
-// Rows from memory, 16 NB a pass: wide rows of several tokens.  Grid (tiles,
-// used experts [+ 1]).
 constexpr int kGuWaves = 4;
+constexpr int kFewSlots = 256;  // slots that a workgroup looks through by itself
 
-template <class F, int NB>
+// The rows of the u-th used expert (u == used: the shared expert's); n = 0: there
+// is none.  Up to kFewSlots slots are looked through here, one a thread: the used
+// experts as bits in LDS, then the expert's slots by ballots, in every wave.
+// WEIGHT: their weights too (complete after the next barrier).
+template <bool PLAN, bool WEIGHT>
+__device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, int u) {
+  __shared__ uint16_t list[kFewSlots];
+  __shared__ float wlist[kFewSlots], ws[kFewSlots];
+  Rows<PLAN> r{0, q.slots, nullptr, q.idx, nullptr, list, wlist};
+  if (!q.idx) return r;
+  r.n = 0;
+  if constexpr (PLAN) {
+    if (u >= __builtin_amdgcn_readfirstlane(plan.used[0])) return r;
+    const int at = __builtin_amdgcn_readfirstlane(plan.roff[u]);
+    r.e = __builtin_amdgcn_readfirstlane(plan.elist[u]);
+    r.n = __builtin_amdgcn_readfirstlane(plan.roff[u + 1]) - at;
+    r.planned = plan.rows + at;
+    r.wrow = plan.wrow + at;
+    return r;
+  }
+  __shared__ uint32_t used[32];
+  __shared__ int16_t ids[kFewSlots];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int mine = tid < q.slots ? local_id(q.idx[tid], q.first, q.E) : -1;
+  if (tid < 32) used[tid] = 0;
+  ids[tid] = (int16_t)mine;
+  if (WEIGHT && mine >= 0) ws[tid] = q.w[tid];
+  __syncthreads();
+  if (mine >= 0) atomicOr(&used[mine >> 5], 1u << (mine & 31));
+  __syncthreads();
+  // the u-th set bit, word by word
+  const uint32_t word = lane < 32 ? used[lane] : 0;
+  int32_t id[kFewSlots / 64];
+#pragma unroll
+  for (int i = 0; i < kFewSlots / 64; i++) id[i] = ids[64 * i + lane];
+  uint32_t bits = 0;
+  int at = -1, left = u;
+  while (++at < (q.E + 31) / 32) {
+    bits = __builtin_amdgcn_readlane(word, at);
+    if (left < __popc(bits)) break;
+    left -= __popc(bits);
+  }
+  if (at == (q.E + 31) / 32) return r;
+  for (; left > 0; left--) bits &= bits - 1;
+  r.e = 32 * at + __ffs(bits) - 1;
+  // its slots, without those whose token has an earlier one (one of the `back`
+  // bits before them); every wave writes, and then reads, the same list
+  uint64_t prev = 0;
+#pragma unroll
+  for (int i = 0; i < kFewSlots / 64; i++) {
+    const int f = 64 * i + lane, back = f % q.k;
+    const uint64_t m = __ballot(id[i] == r.e);
+    const uint64_t earlier =
+        back <= lane ? m >> (lane - back) & below(back)
+                     : (m & below(lane)) | (prev >> (64 - (back - lane)));
+    const bool row = id[i] == r.e && !earlier;
+    const uint64_t rows = __ballot(row);
+    if (row) list[r.n + __popcll(rows & below(lane))] = (uint16_t)f;
+    r.n += __popcll(rows);
+    prev = m;
+  }
+  if (WEIGHT && tid < r.n) {
+    const int f = list[tid];
+    float sum = ws[f];
+    for (int g = f + 1; g < f / q.k * q.k + q.k; g++) sum += ids[g] == r.e ? ws[g] : 0.0f;
+    wlist[tid] = sum;
+  }
+  return r;
+}
+
+// act[f] = w silu(x Wg) (x Wu), rows from memory, 16 NB a pass; a workgroup
+// takes tp pairs of tiles of one expert, one after the other; its waves split
+// the contraction.  Grid (tile pairs / tp, used experts [+ 1: the shared expert]).
+#ifndef GU_U
+#define GU_U 2
+#endif
+#ifndef GU_WG
+#define GU_WG 1024
+#endif
+template <class F, int NB, bool PLAN>
 __global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, Ffn shared, Plan plan,
-                                                                   int used, const uint16_t *x) {
+                                                                   int used, int tp,
+                                                                   const uint16_t *x) {
   __shared__ float red[kGuWaves * 2 * NB * 256];
-  const bool is_shared = (int)blockIdx.y == used;
-  const Ffn q = is_shared ? shared : routed;
-  if ((int)blockIdx.x >= q.gate.nt) return;
-  const Rows rows = find_rows<false>(q, plan, blockIdx.y, is_shared);
+  const Ffn q = (int)blockIdx.y == used ? shared : routed;
+  const int nt = q.gate.nt, j0 = blockIdx.x * tp;
+  if (j0 >= nt) return;
+  const Rows<PLAN> rows = find_rows<PLAN, true>(q, plan, blockIdx.y);
   const int tid = threadIdx.x, lane = tid & 63, K = q.gate.k, ks = q.gate.ks;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * q.gate.nt + blockIdx.x;
-  const W4Row<F> mm[2] = {W4Row<F>(q.gate, base), W4Row<F>(q.up, base)};
+  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
   for (int r0 = 0; r0 < rows.n; r0 += 16 * NB) {
     const int nr = min(16 * NB, rows.n - r0);
     RowPtr xr[NB];
 #pragma unroll
     for (int p = 0; p < NB; p++)
       xr[p].p = x + (size_t)(rows.slot(r0 + min(16 * p + (lane & 15), nr - 1)) / q.k) * K;
-    f32x4 acc[2][NB];
-    zero_acc(acc);
-    w4_stream<F>(mm, q.gate.f16, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
-    w4_join<kGuWaves>(acc, red);
-    for (int i = tid; i < NB * 256; i += kGuWaves * 64) {
-      const int row = 16 * (i >> 8) + 4 * ((i & 63) >> 4) + ((i >> 6) & 3);
-      if (row < nr) put_act(q, rows, r0 + row, 16 * blockIdx.x + (i & 15), red[i], red[NB * 256 + i]);
+    for (int j = j0; j < min(j0 + tp, nt); j++) {
+      const W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j), W4Row<F>(q.up, base + j)};
+      f32x4 acc[2][NB];
+      zero_acc(acc);
+      w4_stream<F, (NB == 1 ? GU_U : 1)>(mm, q.gate.f16, xr, K, ks * wave / kGuWaves,
+                                         ks * (wave + 1) / kGuWaves, acc);
+      w4_join<kGuWaves>(acc, red);
+      for (int i = tid; i < NB * 256; i += kGuWaves * 64) {
+        const int row = 16 * (i >> 8) + 4 * ((i & 63) >> 4) + ((i >> 6) & 3);
+        const int n = 16 * j + (i & 15);
+        // rounded to bf16 once, weight included, as the matrix operand of down
+        if (row < nr && n < q.gate.n)
+          q.act[(size_t)rows.slot(r0 + row) * q.gate.n + n] =
+              to_bf16(rows.weight(r0 + row) * silu_f(red[i]) * red[NB * 256 + i]);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -362,10 +348,12 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
     W4Ring<F, 1, D> ring;
     // the next step to load, and to use: matrix and step in it
     int lu = a / ks, ls = a - lu * ks, cu = lu, cs = ls;
+    const int rot = (int)(blockIdx.x * 5) % ks;  // as in gate_up; one for all waves of a row
+    auto turn = [&](int step) { return step + rot >= ks ? step + rot - ks : step + rot; };
     auto refill = [&](auto d) {
       const size_t row = (size_t)__builtin_amdgcn_readlane(e, lu) * m.nt + blockIdx.x;
       const W4Row<F> mm[1] = {W4Row<F>(m, row)};
-      ring.template load<decltype(d)::value>(mm, ls);
+      ring.template load<decltype(d)::value>(mm, turn(ls));
       const bool last = ls + 1 == ks;  // at the end: the last step again
       ls = last ? (lu + 1 < count ? 0 : ls) : ls + 1;
       lu += last && lu + 1 < count;
@@ -380,7 +368,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
           bf16x8 x[1][4];
 #pragma unroll
           for (int b = 0; b < 4; b++)
-            x[0][b] = xr.load(min(128 * cs + 32 * b + 8 * (lane >> 4), K - 8));
+            x[0][b] = xr.load(min(128 * turn(cs) + 32 * b + 8 * (lane >> 4), K - 8));
           w4_step<F>(m.f16, ring.cw[d], ring.sc[d], x, acc);
           const bool last = cs + 1 == ks;
           cs = last ? 0 : cs + 1;
@@ -415,69 +403,76 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
   }
 }
 
-// More tokens, kTokenBlock a workgroup: the steps of all used experts (and the
-// shared one) are one sequence, split over the waves; an expert's rows are its
-// own tokens, and their sums are added to the wave's [tokens][16] tile in LDS
-// at the end of each expert.  Grid (output tiles, token blocks).
-template <class F>
-__global__ __launch_bounds__(kWaves * 64, 4) void w4_down_kernel(Down q, Plan plan,
-                                                              uint16_t *__restrict__ out) {
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][tokens][16]
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.y * kTokenBlock, tb = min(q.T - t0, kTokenBlock);
-  const int used = plan.used[0], ks = q.m.ks, k = q.k;
-  float *mine = sums + wave * tb * 16;
-  for (int i = lane; i < tb * 16; i += 64) mine[i] = 0.0f;
-  const int total = used * ks + q.shared.ks;
-  int a = total * wave / kWaves;
-  const int b = total * (wave + 1) / kWaves;
-  // rows [0, n) of matrix m's row of tiles at `row`, steps [s0, s1): slot(r) is
-  // the place of row r, its token slot(r) / kk
-  auto segment = [&](const W4Mat &m, size_t row, const uint16_t *act, int n, auto slot, int kk,
-                     int s0, int s1) {
-    const W4Row<F> mm[1] = {W4Row<F>(m, row * m.nt + blockIdx.x)};
-    for (int r0 = 0; r0 < n; r0 += 16) {
-      const int nr = min(16, n - r0);
-      const int f = slot(r0 + min(lane & 15, nr - 1));
-      const RowPtr xr[1] = {{act + (size_t)f * m.k}};
-      f32x4 acc[1][1];
-      zero_acc(acc);
-      w4_stream<F>(mm, m.f16, xr, m.k, s0, s1, acc);
+// More tokens: y[f] = act[f] Wd in fp32 at the places of the rows, 16 NB rows a
+// pass, TN tiles of one expert a workgroup.  Grid (tiles / TN, used experts [+ 1]).
+#ifndef DN_U
+#define DN_U 1
+#endif
+#ifndef DN_TN
+#define DN_TN 4
+#endif
+template <class F, int NB, int TN, bool PLAN>
+__global__ __launch_bounds__(kGuWaves * 64) void w4_down_kernel(Ffn routed, Ffn shared, Plan plan,
+                                                                int used) {
+  __shared__ float red[kGuWaves * TN * NB * 256];
+  const Ffn q = (int)blockIdx.y == used ? shared : routed;
+  const int nt = q.down.nt, j0 = blockIdx.x * TN;
+  const Rows<PLAN> rows = find_rows<PLAN, false>(q, plan, blockIdx.y);
+  const int tid = threadIdx.x, lane = tid & 63, K = q.down.k, ks = q.down.ks;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
+  W4Row<F> mm[TN];
 #pragma unroll
-      for (int v = 0; v < 4; v++) {
-        const int r = 4 * (lane >> 4) + v, t = __shfl(f, r, 64) / kk - t0;
-        if (r < nr) mine[t * 16 + (lane & 15)] += acc[0][0][v];
-      }
+  for (int t = 0; t < TN; t++) mm[t] = W4Row<F>(q.down, base + min(j0 + t, nt - 1));
+  for (int r0 = 0; r0 < rows.n; r0 += 16 * NB) {
+    const int nr = min(16 * NB, rows.n - r0);
+    RowPtr xr[NB];
+#pragma unroll
+    for (int p = 0; p < NB; p++)
+      xr[p].p = q.act + (size_t)rows.slot(r0 + min(16 * p + (lane & 15), nr - 1)) * K;
+    f32x4 acc[TN][NB];
+    zero_acc(acc);
+    w4_stream<F, (NB == 1 ? DN_U : 1)>(mm, q.down.f16, xr, K, ks * wave / kGuWaves,
+                                       ks * (wave + 1) / kGuWaves, acc);
+    w4_join<kGuWaves>(acc, red);
+    for (int i = tid; i < TN * NB * 256; i += kGuWaves * 64) {
+      const int t = i / (NB * 256), j = i % (NB * 256);
+      const int row = 16 * (j >> 8) + 4 * ((j & 63) >> 4) + ((j >> 6) & 3);
+      const int n = 16 * (j0 + t) + (j & 15);
+      if (row < nr && n < q.down.n) q.y[(size_t)rows.slot(r0 + row) * q.down.n + n] = red[i];
     }
-  };
-  for (int u = a / ks; a < b && u < used; u++) {
-    const int end = min(b, (u + 1) * ks);
-    int r0 = plan.roff[u], r1 = plan.roff[u + 1];
-    if (q.T > kTokenBlock) {  // the rows of this block's tokens: slots ascend
-      int lo = 0, hi = 0;
-      for (int r = r0; r < r1; r += 64) {
-        const int f = r + lane < r1 ? plan.rows[r + lane] : 0x7FFFFFFF;
-        lo += __popcll(__ballot(f < t0 * k));
-        hi += __popcll(__ballot(f < (t0 + tb) * k));
-      }
-      r1 = r0 + hi;
-      r0 += lo;
-    }
-    const int32_t *rows = plan.rows + r0;
-    segment(q.m, __builtin_amdgcn_readfirstlane(plan.elist[u]), q.act, r1 - r0, [&](int r) { return rows[r]; }, k, a - u * ks,
-            end - u * ks);
-    a = end;
+    __syncthreads();
   }
-  if (a < b)
-    segment(q.shared, 0, q.act_s, tb, [&](int r) { return t0 + r; }, 1, a - used * ks,
-            b - used * ks);
-  __syncthreads();
-  for (int i = tid; i < tb * 16; i += kWaves * 64) {
-    float s = 0.0f;
-    for (int w = 0; w < kWaves; w++) s += sums[w * tb * 16 + i];
-    const int n = 16 * blockIdx.x + (i & 15);
-    if (n < q.m.n) out[(size_t)(t0 + (i >> 4)) * q.m.n + n] = to_bf16(s);
+}
+
+// out[t] = the sum of the token's rows of y (a token's slots that are its first
+// with their expert, ascending), then the shared expert's; rounded once.
+__global__ __launch_bounds__(256) void w4_combine_kernel(const float4 *__restrict__ y,
+                                                         const int32_t *__restrict__ idx, int first,
+                                                         int E, const float4 *__restrict__ ys,
+                                                         uint2 *__restrict__ out, int k, int HC) {
+  const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= HC) return;
+  float4 v[16];
+  bool has[16];
+#pragma unroll
+  for (int j = 0; j < 16; j++) {
+    has[j] = j < k && local_id(idx[t * k + min(j, k - 1)], first, E) >= 0;
+    for (int g = 0; g < j && has[j]; g++) has[j] = idx[t * k + g] != idx[t * k + j];
+    v[j] = has[j] ? y[(size_t)(t * k + j) * HC + c] : make_float4(0, 0, 0, 0);
   }
+  float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 16; j++) {
+    a.x += v[j].x; a.y += v[j].y; a.z += v[j].z; a.w += v[j].w;
+  }
+  if (ys) {
+    const float4 s = ys[(size_t)t * HC + c];
+    a.x += s.x; a.y += s.y; a.z += s.z; a.w += s.w;
+  }
+  const bf16x2 lo = {(__bf16)a.x, (__bf16)a.y}, hi = {(__bf16)a.z, (__bf16)a.w};
+  out[(size_t)t * HC + c] = make_uint2(__builtin_bit_cast(uint32_t, lo),
+                                       __builtin_bit_cast(uint32_t, hi));
 }
 
 }  // namespace
@@ -486,15 +481,13 @@ size_t w4_plan_words(int slots, int E) { return 64 + 2 * (size_t)E + 64 + 2 * (s
 
 void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
   const int slots = a.T * a.k, E = a.up.groups, H = a.up.k, I = a.down.k;
-  Ffn r{w4_view(a.up, a.w_gate), w4_view(a.up, a.w_up), a.idx, a.w, slots, a.k, a.first, E, a.act};
+  Ffn r{w4_view(a.up, a.w_gate), w4_view(a.up, a.w_up), w4_view(a.down, a.w_down), a.idx, a.w,
+        slots, a.k, a.first, E, a.act, a.y};
   Ffn sh = r;
-  Down d{w4_view(a.down, a.w_down), {}, a.idx, a.w, slots, a.k, a.first, E, a.T, a.act, nullptr};
   long token_lds = 2L * a.k * I;
   if (a.shared) {
-    sh = {w4_view(a.up_s, a.ws_gate), w4_view(a.up_s, a.ws_up), nullptr, nullptr, a.T, 1, 0, 1,
-          a.act_s};
-    d.shared = w4_view(a.down_s, a.ws_down);
-    d.act_s = a.act_s;
+    sh = {w4_view(a.up_s, a.ws_gate), w4_view(a.up_s, a.ws_up), w4_view(a.down_s, a.ws_down),
+          nullptr, nullptr, a.T, 1, 0, 1, a.act_s, a.y_s};
     token_lds += 2L * a.down_s.k;
   }
   Plan p;
@@ -504,41 +497,46 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
   p.rows = p.roff + E + 64;
   p.wrow = (float *)(p.rows + slots);
   const int used = std::min(E, slots), avg = slots / E;
+  const unsigned gy = used + (a.shared ? 1 : 0);
   const int nt = a.shared ? std::max(a.up.nt, a.up_s.nt) : a.up.nt;
-  const long row_lds = (long)std::min(a.T, 16) * w4_pitch(H);
-  const bool staged = row_lds <= kRowLds && avg <= 16;
-  const bool single = a.T == 1 && staged && token_lds <= kRowLds;
-  if (!single)
+  const bool plan = slots > kFewSlots, single = a.T == 1 && token_lds <= kRowLds;
+  if (plan)
     hipLaunchKernelGGL(w4_plan_kernel, dim3(1), dim3(kPlanThreads),
                        (17 * E + (slots + 1) / 2) * sizeof(int32_t), s, a.idx, a.w, slots, a.k,
                        a.first, E, p);
-  const unsigned gy = used + (a.shared ? 1 : 0);
   with_format(a.up, [&](auto f) {
     using F = decltype(f);
-    if (staged) {
-      // about two workgroups a CU
-      const int tpw = std::max(1, (int)(((long)nt * gy + 511) / 512));
-      auto up = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((nt + tpw - 1) / tpw, gy), dim3(kWaves * 64), row_lds, s, r,
-                           sh, p, used, tpw, a.x);
-      };
-      if (single) up(w4_gate_up_lds_kernel<F, 4, true>);
-      else up(w4_gate_up_lds_kernel<F, 4, false>);
-    } else {
-      auto up = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(nt, gy), dim3(kGuWaves * 64), 0, s, r, sh, p, used, a.x);
-      };
-      if (avg <= 16) up(w4_gate_up_kernel<F, 1>);
-      else if (avg <= 32) up(w4_gate_up_kernel<F, 2>);
-      else up(w4_gate_up_kernel<F, 4>);
-    }
-    if (single)
+    const dim3 b(kGuWaves * 64);
+    auto up = [&](auto kernel, int tp) {
+      hipLaunchKernelGGL(kernel, dim3((nt + tp - 1) / tp, gy), b, 0, s, r, sh, p, used, tp, a.x);
+    };
+    auto down = [&](auto kernel, int tn) {
+      hipLaunchKernelGGL(kernel, dim3((a.down.nt + tn - 1) / tn, gy), b, 0, s, r, sh, p, used);
+    };
+    const bool many = avg > 16;
+    const int tp = std::max(1, (int)((long)nt * gy / GU_WG));
+    if (plan && many) up(w4_gate_up_kernel<F, 4, true>, tp);
+    else if (plan) up(w4_gate_up_kernel<F, 1, true>, tp);
+    else if (many) up(w4_gate_up_kernel<F, 4, false>, tp);
+    else up(w4_gate_up_kernel<F, 1, false>, tp);
+    if (single) {
+      Down d{r.down, {}, a.idx, a.w, slots, a.k, a.first, E, a.T, a.act, nullptr};
+      if (a.shared) {
+        d.shared = sh.down;
+        d.act_s = a.act_s;
+      }
       hipLaunchKernelGGL((w4_down_token_kernel<F, 8>), dim3(a.down.nt), dim3(kWaves * 64), token_lds,
                          s, d, a.out);
-    else
-      hipLaunchKernelGGL(w4_down_kernel<F>,
-                         dim3(a.down.nt, (a.T + kTokenBlock - 1) / kTokenBlock), dim3(kWaves * 64),
-                         kWaves * 64 * std::min(a.T, kTokenBlock), s, d, p, a.out);
+      return;
+    }
+    if (plan && many) down(w4_down_kernel<F, 4, 2, true>, 2);
+    else if (plan) down(w4_down_kernel<F, 1, DN_TN, true>, DN_TN);
+    else if (many) down(w4_down_kernel<F, 4, 2, false>, 2);
+    else down(w4_down_kernel<F, 1, DN_TN, false>, DN_TN);
+    const int HC = H / 4;
+    hipLaunchKernelGGL(w4_combine_kernel, dim3((HC + 255) / 256, a.T), dim3(256), 0, s,
+                       (const float4 *)a.y, a.idx, a.first, E, (const float4 *)(a.shared ? a.y_s : nullptr),
+                       (uint2 *)a.out, a.k, HC);
   });
 }
 

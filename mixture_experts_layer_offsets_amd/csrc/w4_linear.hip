@@ -28,7 +28,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
       xr[p].p = x + (r0 + min(16 * p + (lane & 15), nr - 1)) * xstride;
     f32x4 acc[1][NB];
     zero_acc(acc);
-    w4_stream<F>(mm, m.f16, xr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
+    w4_stream<F, (NB == 1 ? 4 : (NB == 2 ? 2 : 1))>(mm, m.f16, xr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
     w4_join<WAVES>(acc, red);
     for (int i = threadIdx.x; i < NB * 256; i += WAVES * 64) {
       const int l = i & 63, v = (i >> 6) & 3;
