@@ -303,15 +303,6 @@ struct W4Ring {
   }
 };
 
-// f(integral_constant<int, d>) for d = 0 .. N - 1
-template <int N, int d = 0, class Fn>
-__device__ __forceinline__ void each(Fn &&f) {
-  if constexpr (d < N) {
-    f(std::integral_constant<int, d>{});
-    each<N, d + 1>(f);
-  }
-}
-
 template <int NTW, int NB>
 __device__ __forceinline__ void zero_acc(f32x4 (&acc)[NTW][NB]) {
 #pragma unroll
@@ -343,6 +334,109 @@ __device__ __forceinline__ void w4_join(const f32x4 (&acc)[NTW][NB], float *red)
     red[i] = t;
   }
   __syncthreads();
+}
+
+// f(integral_constant<int, d>) for d = 0 .. N - 1
+template <int N, int d = 0, class Fn>
+__device__ __forceinline__ void each(Fn &&f) {
+  if constexpr (d < N) {
+    f(std::integral_constant<int, d>{});
+    each<N, d + 1>(f);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (16 NB a pass, NB > 1): here every tile would read all the rows
+// again, so the rows go through LDS, a step (128 values) at a time, shared by
+// the four waves of a group, each with its own NTW tiles.  A workgroup is two
+// such groups, which take half of the contraction each.
+constexpr int kBlockWaves = 4;    // waves of a group
+constexpr int kBlockGroups = 2;
+constexpr int kBlockDepth = 4;    // steps in flight
+constexpr int kBlockPitch = 256 + 16;
+// Row blocks of a long pass: groups of 32 keep four scales and offsets a step,
+// which leaves registers for two blocks only.
+template <class F>
+constexpr int kLongBlocks = F::kGrouped && F::SPG == 4 ? 2 : 4;
+template <int NB>
+constexpr int w4_block_lds() { return kBlockGroups * 2 * 16 * NB * kBlockPitch; }
+
+// acc += rows times tiles m over this group's half of the ks steps.  x[p]:
+// address of the 16 bytes that this thread stages of row 16 p + (thread of the
+// group) / 16, chunk thread % 16, at step 0.  xs: the workgroup's LDS.  All
+// threads of the workgroup call.  A step's rows travel through registers with
+// the codes (loads complete in order: rows fetched later than the codes of
+// their step would empty the pipeline at every step) into one of two buffers.
+template <class F, int NTW, int NB>
+__device__ __forceinline__ void w4_block(const W4Row<F> (&m)[NTW], int f16,
+                                         const uint16_t *const (&x)[NB], int K, int ks, char *xs,
+                                         f32x4 (&acc)[NTW][NB]) {
+  constexpr int D = kBlockDepth;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int group = __builtin_amdgcn_readfirstlane(tid / (64 * kBlockWaves));
+  const int s0 = ks * group / kBlockGroups, n = ks * (group + 1) / kBlockGroups - s0;
+  const int most = (ks + kBlockGroups - 1) / kBlockGroups;  // both groups meet at every barrier
+  const int gt = tid % (64 * kBlockWaves), chunk = gt % 16;
+  char *mine = xs + group * (2 * 16 * NB * kBlockPitch);
+  uint4 cw[D][NTW];
+  typename F::Scales sc[D][NTW];
+  w4_u32x4 xv[D][NB];
+  auto load = [&](auto d, int i) __attribute__((always_inline)) {
+    const int st = min(s0 + i, ks - 1), k = min(128 * st, K - 8 - 8 * chunk);
+#pragma unroll
+    for (int p = 0; p < NB; p++) xv[d][p] = *(const w4_u32x4u *)(x[p] + k);
+#pragma unroll
+    for (int j = 0; j < NTW; j++) {
+      cw[d][j] = m[j].codes(st);
+      sc[d][j] = m[j].scales(st);
+    }
+  };
+  auto put = [&](auto d, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < NB; p++)
+      *(w4_u32x4 *)(mine + (buf * 16 * NB + 16 * p + gt / 16) * kBlockPitch + 16 * chunk) = xv[d][p];
+  };
+  each<D>([&](auto d) __attribute__((always_inline)) { load(d, d); });
+  put(std::integral_constant<int, 0>{}, 0);
+  for (int i0 = 0; i0 < most; i0 += D) {
+    each<D>([&](auto d) __attribute__((always_inline)) {
+      constexpr int dn = (decltype(d)::value + 1) % D;
+      const int i = i0 + d;
+      lds_barrier();  // step i's rows are there, and step i - 1's have been read
+      if (i + 1 < most) put(std::integral_constant<int, dn>{}, (d + 1) & 1);
+      if (i < n) {
+        bf16x8 a[NB][4];
+#pragma unroll
+        for (int p = 0; p < NB; p++)
+#pragma unroll
+          for (int b = 0; b < 4; b++)
+            a[p][b] = __builtin_bit_cast(
+                bf16x8, *(const w4_u32x4 *)(mine + ((d & 1) * 16 * NB + 16 * p + (lane & 15)) *
+                                                       kBlockPitch + 64 * b + 16 * (lane >> 4)));
+        w4_step<F>(f16, cw[d], sc[d], a, acc);
+      }
+      load(d, i + D);
+    });
+  }
+}
+
+// The two groups' sums: group 1 leaves its own in LDS (the rows' buffers are
+// free then), group 0 adds them.  Returns whether this wave holds results.
+template <int NTW, int NB>
+__device__ __forceinline__ bool w4_block_join(f32x4 (&acc)[NTW][NB], char *xs) {
+  const int gt = threadIdx.x % (64 * kBlockWaves);
+  const bool second = threadIdx.x >= 64 * kBlockWaves;
+  float *at = (float *)xs + gt;
+  lds_barrier();
+#pragma unroll
+  for (int q = 0; q < NTW * NB * 4; q++)
+    if (second) at[q * 64 * kBlockWaves] = acc[q / (NB * 4)][q / 4 % NB][q % 4];
+  lds_barrier();
+  if (second) return false;
+#pragma unroll
+  for (int q = 0; q < NTW * NB * 4; q++)
+    acc[q / (NB * 4)][q / 4 % NB][q % 4] += at[q * 64 * kBlockWaves];
+  return true;
 }
 
 __device__ __forceinline__ uint16_t to_bf16(float f) {

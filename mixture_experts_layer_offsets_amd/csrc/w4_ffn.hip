@@ -198,6 +198,7 @@ struct Rows {
 };
 
 constexpr int kGuWaves = 4;
+constexpr int kBlockThreads = 64 * kBlockWaves * kBlockGroups;
 constexpr int kFewSlots = 256;  // slots that a workgroup looks through by itself
 
 // The rows of the u-th used expert (u == used: the shared expert's); n = 0: there
@@ -225,7 +226,7 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
   const int tid = threadIdx.x, lane = tid & 63;
   const int mine = tid < q.slots ? local_id(q.idx[tid], q.first, q.E) : -1;
   if (tid < 32) used[tid] = 0;
-  ids[tid] = (int16_t)mine;
+  if (tid < kFewSlots) ids[tid] = (int16_t)mine;
   if (WEIGHT && mine >= 0) ws[tid] = q.w[tid];
   __syncthreads();
   if (mine >= 0) atomicOr(&used[mine >> 5], 1u << (mine & 31));
@@ -270,20 +271,23 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
   return r;
 }
 
-// act[f] = w silu(x Wg) (x Wu), rows from memory, 16 NB a pass; a workgroup
-// takes tp pairs of tiles of one expert, one after the other; its waves split
-// the contraction.  Grid (tile pairs / tp, used experts [+ 1: the shared expert]).
-#ifndef GU_U
-#define GU_U 2
-#endif
-#ifndef GU_WG
-#define GU_WG 1024
-#endif
-template <class F, int NB, bool PLAN>
+// act[f] of one row and output, from the sums of its gate and up products:
+// rounded to bf16 once, weight included, as the matrix operand of down.
+template <bool PLAN>
+__device__ __forceinline__ void put_act(const Ffn &q, const Rows<PLAN> &rows, int r, int n, float g,
+                                        float u) {
+  if (r < rows.n && n < q.gate.n)
+    q.act[(size_t)rows.slot(r) * q.gate.n + n] = to_bf16(rows.weight(r) * silu_f(g) * u);
+}
+
+// gate_up, 16 rows a pass from memory: a workgroup takes tp pairs of tiles of
+// one expert, one after the other; its waves split the contraction.  Grid (tile
+// pairs / tp, used experts [+ 1: the shared expert]).
+template <class F, bool PLAN>
 __global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, Ffn shared, Plan plan,
                                                                    int used, int tp,
                                                                    const uint16_t *x) {
-  __shared__ float red[kGuWaves * 2 * NB * 256];
+  __shared__ float red[kGuWaves * 2 * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
   const int nt = q.gate.nt, j0 = blockIdx.x * tp;
   if (j0 >= nt) return;
@@ -291,29 +295,52 @@ __global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, F
   const int tid = threadIdx.x, lane = tid & 63, K = q.gate.k, ks = q.gate.ks;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
-  for (int r0 = 0; r0 < rows.n; r0 += 16 * NB) {
-    const int nr = min(16 * NB, rows.n - r0);
-    RowPtr xr[NB];
-#pragma unroll
-    for (int p = 0; p < NB; p++)
-      xr[p].p = x + (size_t)(rows.slot(r0 + min(16 * p + (lane & 15), nr - 1)) / q.k) * K;
+  for (int r0 = 0; r0 < rows.n; r0 += 16) {
+    const int nr = min(16, rows.n - r0);
+    const RowPtr xr[1] = {{x + (size_t)(rows.slot(r0 + min(lane & 15, nr - 1)) / q.k) * K}};
     for (int j = j0; j < min(j0 + tp, nt); j++) {
       const W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j), W4Row<F>(q.up, base + j)};
-      f32x4 acc[2][NB];
+      f32x4 acc[2][1];
       zero_acc(acc);
-      w4_stream<F, (NB == 1 ? GU_U : 1)>(mm, q.gate.f16, xr, K, ks * wave / kGuWaves,
-                                         ks * (wave + 1) / kGuWaves, acc);
+      w4_stream<F, 2>(mm, q.gate.f16, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
       w4_join<kGuWaves>(acc, red);
-      for (int i = tid; i < NB * 256; i += kGuWaves * 64) {
-        const int row = 16 * (i >> 8) + 4 * ((i & 63) >> 4) + ((i >> 6) & 3);
-        const int n = 16 * j + (i & 15);
-        // rounded to bf16 once, weight included, as the matrix operand of down
-        if (row < nr && n < q.gate.n)
-          q.act[(size_t)rows.slot(r0 + row) * q.gate.n + n] =
-              to_bf16(rows.weight(r0 + row) * silu_f(red[i]) * red[NB * 256 + i]);
-      }
+      put_act(q, rows, r0 + 4 * ((tid & 63) >> 4) + (tid >> 6), 16 * j + (tid & 15), red[tid],
+              red[256 + tid]);
       __syncthreads();
     }
+  }
+}
+
+// gate_up of many rows: a workgroup takes kBlockWaves pairs of tiles.
+template <class F, int NB, bool PLAN>
+__global__ __launch_bounds__(kBlockThreads, 2) void w4_gate_up_rows_kernel(Ffn routed, Ffn shared,
+                                                                           Plan plan, int used,
+                                                                           const uint16_t *x) {
+  __shared__ __attribute__((aligned(16))) char xs[w4_block_lds<NB>()];
+  const Ffn q = (int)blockIdx.y == used ? shared : routed;
+  const int nt = q.gate.nt, tid = threadIdx.x, lane = tid & 63, K = q.gate.k;
+  if ((int)blockIdx.x * kBlockWaves >= nt) return;
+  const Rows<PLAN> rows = find_rows<PLAN, true>(q, plan, blockIdx.y);
+  const int gt = tid % (64 * kBlockWaves);
+  const int j = blockIdx.x * kBlockWaves + __builtin_amdgcn_readfirstlane(gt >> 6);
+  const size_t row = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt + min(j, nt - 1);
+  const W4Row<F> mm[2] = {W4Row<F>(q.gate, row), W4Row<F>(q.up, row)};
+  for (int r0 = 0; r0 < rows.n; r0 += 16 * NB) {
+    const uint16_t *xr[NB];
+#pragma unroll
+    for (int p = 0; p < NB; p++)
+      xr[p] = x + (size_t)(rows.slot(min(r0 + 16 * p + gt / 16, rows.n - 1)) / q.k) * K + 8 * (gt % 16);
+    f32x4 acc[2][NB];
+    zero_acc(acc);
+    w4_block<F>(mm, q.gate.f16, xr, K, q.gate.ks, xs, acc);
+    if (w4_block_join(acc, xs) && j < nt)
+#pragma unroll
+      for (int p = 0; p < NB; p++)
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+          put_act(q, rows, r0 + 16 * p + 4 * (lane >> 4) + v, 16 * j + (lane & 15), acc[0][p][v],
+                  acc[1][p][v]);
+    lds_barrier();
   }
 }
 
@@ -403,45 +430,75 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
   }
 }
 
-// More tokens: y[f] = act[f] Wd in fp32 at the places of the rows, 16 NB rows a
-// pass, TN tiles of one expert a workgroup.  Grid (tiles / TN, used experts [+ 1]).
-#ifndef DN_U
-#define DN_U 1
-#endif
-#ifndef DN_TN
-#define DN_TN 4
-#endif
-template <class F, int NB, int TN, bool PLAN>
+// More tokens: y[f] = act[f] Wd in fp32 at the places of the rows, 16 rows a
+// pass, kDownTiles tiles of one expert a workgroup.  Grid (tiles / kDownTiles,
+// used experts [+ 1]).
+constexpr int kDownTiles = 4;
+
+template <bool PLAN>
+__device__ __forceinline__ void put_y(const Ffn &q, const Rows<PLAN> &rows, int r, int n, float v) {
+  if (r < rows.n && n < q.down.n) q.y[(size_t)rows.slot(r) * q.down.n + n] = v;
+}
+
+template <class F, bool PLAN>
 __global__ __launch_bounds__(kGuWaves * 64) void w4_down_kernel(Ffn routed, Ffn shared, Plan plan,
                                                                 int used) {
-  __shared__ float red[kGuWaves * TN * NB * 256];
+  __shared__ float red[kGuWaves * kDownTiles * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
-  const int nt = q.down.nt, j0 = blockIdx.x * TN;
+  const int nt = q.down.nt, j0 = blockIdx.x * kDownTiles;
   const Rows<PLAN> rows = find_rows<PLAN, false>(q, plan, blockIdx.y);
   const int tid = threadIdx.x, lane = tid & 63, K = q.down.k, ks = q.down.ks;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
-  W4Row<F> mm[TN];
+  W4Row<F> mm[kDownTiles];
 #pragma unroll
-  for (int t = 0; t < TN; t++) mm[t] = W4Row<F>(q.down, base + min(j0 + t, nt - 1));
+  for (int t = 0; t < kDownTiles; t++) mm[t] = W4Row<F>(q.down, base + min(j0 + t, nt - 1));
+  for (int r0 = 0; r0 < rows.n; r0 += 16) {
+    const int nr = min(16, rows.n - r0);
+    const RowPtr xr[1] = {{q.act + (size_t)rows.slot(r0 + min(lane & 15, nr - 1)) * K}};
+    f32x4 acc[kDownTiles][1];
+    zero_acc(acc);
+    w4_stream<F, 1>(mm, q.down.f16, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+    w4_join<kGuWaves>(acc, red);
+#pragma unroll
+    for (int t = 0; t < kDownTiles; t++)
+      put_y(q, rows, r0 + 4 * ((tid & 63) >> 4) + (tid >> 6), 16 * (j0 + t) + (tid & 15),
+            red[256 * t + tid]);
+    __syncthreads();
+  }
+}
+
+// down of many rows: a workgroup takes 2 kBlockWaves tiles.
+template <class F, int NB, bool PLAN>
+__global__ __launch_bounds__(kBlockThreads, 2) void w4_down_rows_kernel(Ffn routed, Ffn shared,
+                                                                        Plan plan, int used) {
+  __shared__ __attribute__((aligned(16))) char xs[w4_block_lds<NB>()];
+  const Ffn q = (int)blockIdx.y == used ? shared : routed;
+  const int nt = q.down.nt, tid = threadIdx.x, lane = tid & 63, K = q.down.k;
+  const Rows<PLAN> rows = find_rows<PLAN, false>(q, plan, blockIdx.y);
+  const int gt = tid % (64 * kBlockWaves);
+  const int j = 2 * (blockIdx.x * kBlockWaves + __builtin_amdgcn_readfirstlane(gt >> 6));
+  const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
+  const W4Row<F> mm[2] = {W4Row<F>(q.down, base + min(j, nt - 1)),
+                          W4Row<F>(q.down, base + min(j + 1, nt - 1))};
   for (int r0 = 0; r0 < rows.n; r0 += 16 * NB) {
-    const int nr = min(16 * NB, rows.n - r0);
-    RowPtr xr[NB];
+    const uint16_t *xr[NB];
 #pragma unroll
     for (int p = 0; p < NB; p++)
-      xr[p].p = q.act + (size_t)rows.slot(r0 + min(16 * p + (lane & 15), nr - 1)) * K;
-    f32x4 acc[TN][NB];
+      xr[p] = q.act + (size_t)rows.slot(min(r0 + 16 * p + gt / 16, rows.n - 1)) * K + 8 * (gt % 16);
+    f32x4 acc[2][NB];
     zero_acc(acc);
-    w4_stream<F, (NB == 1 ? DN_U : 1)>(mm, q.down.f16, xr, K, ks * wave / kGuWaves,
-                                       ks * (wave + 1) / kGuWaves, acc);
-    w4_join<kGuWaves>(acc, red);
-    for (int i = tid; i < TN * NB * 256; i += kGuWaves * 64) {
-      const int t = i / (NB * 256), j = i % (NB * 256);
-      const int row = 16 * (j >> 8) + 4 * ((j & 63) >> 4) + ((j >> 6) & 3);
-      const int n = 16 * (j0 + t) + (j & 15);
-      if (row < nr && n < q.down.n) q.y[(size_t)rows.slot(r0 + row) * q.down.n + n] = red[i];
-    }
-    __syncthreads();
+    w4_block<F>(mm, q.down.f16, xr, K, q.down.ks, xs, acc);
+    if (w4_block_join(acc, xs))
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int p = 0; p < NB; p++)
+#pragma unroll
+          for (int v = 0; v < 4; v++)
+            put_y(q, rows, r0 + 16 * p + 4 * (lane >> 4) + v, 16 * (j + t) + (lane & 15),
+                  acc[t][p][v]);
+    lds_barrier();
   }
 }
 
@@ -506,19 +563,26 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
                        a.first, E, p);
   with_format(a.up, [&](auto f) {
     using F = decltype(f);
-    const dim3 b(kGuWaves * 64);
-    auto up = [&](auto kernel, int tp) {
+    const dim3 b(kGuWaves * 64), bb(kBlockThreads);
+    // two rounds of row blocks at most wasted: 32 rows a pass up to an average
+    // of 32 a expert, else 64
+    auto up = [&](auto kernel) {
+      const int tp = std::max(1, (int)((long)nt * gy / 768));
       hipLaunchKernelGGL(kernel, dim3((nt + tp - 1) / tp, gy), b, 0, s, r, sh, p, used, tp, a.x);
     };
-    auto down = [&](auto kernel, int tn) {
-      hipLaunchKernelGGL(kernel, dim3((a.down.nt + tn - 1) / tn, gy), b, 0, s, r, sh, p, used);
+    auto up_rows = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((nt + kBlockWaves - 1) / kBlockWaves, gy), bb, 0, s, r, sh, p,
+                         used, a.x);
     };
-    const bool many = avg > 16;
-    const int tp = std::max(1, (int)((long)nt * gy / GU_WG));
-    if (plan && many) up(w4_gate_up_kernel<F, 4, true>, tp);
-    else if (plan) up(w4_gate_up_kernel<F, 1, true>, tp);
-    else if (many) up(w4_gate_up_kernel<F, 4, false>, tp);
-    else up(w4_gate_up_kernel<F, 1, false>, tp);
+    auto down = [&](auto kernel, int tiles, dim3 block) {
+      hipLaunchKernelGGL(kernel, dim3((a.down.nt + tiles - 1) / tiles, gy), block, 0, s, r, sh, p,
+                         used);
+    };
+    if (avg > 32) plan ? up_rows(w4_gate_up_rows_kernel<F, kLongBlocks<F>, true>)
+                       : up_rows(w4_gate_up_rows_kernel<F, kLongBlocks<F>, false>);
+    else if (avg > 16) plan ? up_rows(w4_gate_up_rows_kernel<F, 2, true>)
+                            : up_rows(w4_gate_up_rows_kernel<F, 2, false>);
+    else plan ? up(w4_gate_up_kernel<F, true>) : up(w4_gate_up_kernel<F, false>);
     if (single) {
       Down d{r.down, {}, a.idx, a.w, slots, a.k, a.first, E, a.T, a.act, nullptr};
       if (a.shared) {
@@ -529,10 +593,12 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
                          s, d, a.out);
       return;
     }
-    if (plan && many) down(w4_down_kernel<F, 4, 2, true>, 2);
-    else if (plan) down(w4_down_kernel<F, 1, DN_TN, true>, DN_TN);
-    else if (many) down(w4_down_kernel<F, 4, 2, false>, 2);
-    else down(w4_down_kernel<F, 1, DN_TN, false>, DN_TN);
+    if (avg > 32) plan ? down(w4_down_rows_kernel<F, kLongBlocks<F>, true>, 2 * kBlockWaves, bb)
+                       : down(w4_down_rows_kernel<F, kLongBlocks<F>, false>, 2 * kBlockWaves, bb);
+    else if (avg > 16) plan ? down(w4_down_rows_kernel<F, 2, true>, 2 * kBlockWaves, bb)
+                            : down(w4_down_rows_kernel<F, 2, false>, 2 * kBlockWaves, bb);
+    else plan ? down(w4_down_kernel<F, true>, kDownTiles, b)
+              : down(w4_down_kernel<F, false>, kDownTiles, b);
     const int HC = H / 4;
     hipLaunchKernelGGL(w4_combine_kernel, dim3((HC + 255) / 256, a.T), dim3(256), 0, s,
                        (const float4 *)a.y, a.idx, a.first, E, (const float4 *)(a.shared ? a.y_s : nullptr),
