@@ -190,7 +190,8 @@ struct RowLds {
 __host__ __device__ constexpr int w4_pitch(int values) { return 2 * values + 16; }
 
 // One step: acc[j][p] += a[p] times the codes of tile j, 128 contraction values.
-template <class F, int NTW, int NB>
+// V: values of a lane's results that are wanted (INT4 scales them one by one).
+template <class F, int V, int NTW, int NB>
 __device__ __forceinline__ void w4_step(int f16, const uint4 (&cw)[NTW],
                                         const typename F::Scales (&sc)[NTW],
                                         const bf16x8 (&a)[NB][4], f32x4 (&acc)[NTW][NB]) {
@@ -239,7 +240,7 @@ __device__ __forceinline__ void w4_step(int f16, const uint4 (&cw)[NTW],
 #pragma unroll
         for (int p = 0; p < NB; p++)
 #pragma unroll
-          for (int v = 0; v < 4; v++) {
+          for (int v = 0; v < V; v++) {
             float t = part[p][v];
             if constexpr (F::ZERO) t = fmaf(-(16.0f + F::zero(sc[j], g)), off[p][v], t);
             acc[j][p][v] = fmaf(scale, t, acc[j][p][v]);
@@ -251,25 +252,34 @@ __device__ __forceinline__ void w4_step(int f16, const uint4 (&cw)[NTW],
   }
 }
 
-// acc[j][p] += rows of block p times the row j of tiles over the steps [s0,
-// s1), the rows read from memory; x[p]: this lane's row of block p.  The rows,
-// codes and scales of U steps are loaded together, one memory round trip; steps past the end load the last step again and are not used.  Values
-// of k past K meet zero weights: their lanes load the row's last values.
-template <class F, int U, int NTW, int NB, class Row>
-__device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, const Row (&x)[NB],
-                                          int K, int s0, int s1, f32x4 (&acc)[NTW][NB]) {
+// Up to 16 rows.  Row r is the matrix instruction's row 4 (r % 4) + r / 4, so that
+// lane l's v-th result is row l / 16 + 4 v: up to 4 rows need one value of each
+// lane only.
+__device__ __forceinline__ int w4_row_of_lane() {  // that this lane loads
+  return ((threadIdx.x >> 2) & 3) + 4 * (threadIdx.x & 3);
+}
+__device__ __forceinline__ int w4_row_of(int i) {  // of sum i of w4_join
+  return ((i & 63) >> 4) + 4 * ((i >> 6) & 3);
+}
+
+// acc[j] += the rows times the row j of tiles over the steps [s0, s1), the rows
+// read from memory; x: this lane's row.  The rows, codes and scales of U steps
+// are loaded together, one memory round trip; steps past the end load the last
+// step again and are not used.  Values of k past K meet zero weights: their
+// lanes load the row's last values.
+template <class F, int U, int V, int NTW, class Row>
+__device__ __forceinline__ void w4_batches(const W4Row<F> (&m)[NTW], int f16, const Row &x, int K,
+                                           int s0, int s1, f32x4 (&acc)[NTW][1]) {
   const int h8 = 8 * ((threadIdx.x & 63) >> 4);
   for (int s = s0; s < s1; s += U) {
     uint4 cw[U][NTW];
     typename F::Scales sc[U][NTW];
-    bf16x8 a[U][NB][4];
+    bf16x8 a[U][1][4];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int st = min(s + u, s1 - 1);
 #pragma unroll
-      for (int p = 0; p < NB; p++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) a[u][p][i] = x[p].load(min(128 * st + 32 * i + h8, K - 8));
+      for (int i = 0; i < 4; i++) a[u][0][i] = x.load(min(128 * st + 32 * i + h8, K - 8));
 #pragma unroll
       for (int j = 0; j < NTW; j++) {
         cw[u][j] = m[j].codes(st);
@@ -281,8 +291,15 @@ __device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, con
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < U; u++)
-      if (s + u < s1) w4_step<F>(f16, cw[u], sc[u], a[u], acc);
+      if (s + u < s1) w4_step<F, V>(f16, cw[u], sc[u], a[u], acc);
   }
+}
+
+template <class F, int U, int NTW, class Row>
+__device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, const Row &x, int rows,
+                                          int K, int s0, int s1, f32x4 (&acc)[NTW][1]) {
+  if (F::kGrouped && rows <= 4) w4_batches<F, U, 1>(m, f16, x, K, s0, s1, acc);
+  else w4_batches<F, U, 4>(m, f16, x, K, s0, s1, acc);
 }
 
 // A ring of D steps whose codes and scales are in flight, refilled step by step
@@ -312,20 +329,16 @@ __device__ __forceinline__ void zero_acc(f32x4 (&acc)[NTW][NB]) {
 }
 
 // The waves' partial sums meet in LDS and are added in wave order.  Afterwards
-// red[q * 64 + lane] (q = (j NB + p) 4 + v) holds output tile j, row 16 p + 4
-// (lane / 16) + v, output lane % 16.  red: WAVES NTW NB 256 floats.  The caller
-// synchronises before red is written again.
-template <int WAVES, int NTW, int NB>
-__device__ __forceinline__ void w4_join(const f32x4 (&acc)[NTW][NB], float *red) {
+// red[256 j + i] is output i % 16 of tile j, of row w4_row_of(i).  red: WAVES NTW
+// 256 floats.  The caller synchronises before red is written again.
+template <int WAVES, int NTW>
+__device__ __forceinline__ void w4_join(const f32x4 (&acc)[NTW][1], float *red) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int kQ = NTW * NB * 4;
+  constexpr int kQ = NTW * 4;
 #pragma unroll
   for (int j = 0; j < NTW; j++)
 #pragma unroll
-    for (int p = 0; p < NB; p++)
-#pragma unroll
-      for (int v = 0; v < 4; v++)
-        red[(wave * kQ + (j * NB + p) * 4 + v) * 64 + lane] = acc[j][p][v];
+    for (int v = 0; v < 4; v++) red[(wave * kQ + j * 4 + v) * 64 + lane] = acc[j][0][v];
   __syncthreads();
   for (int i = tid; i < kQ * 64; i += WAVES * 64) {
     float t = red[i];
@@ -413,7 +426,7 @@ __device__ __forceinline__ void w4_block(const W4Row<F> (&m)[NTW], int f16,
             a[p][b] = __builtin_bit_cast(
                 bf16x8, *(const w4_u32x4 *)(mine + ((d & 1) * 16 * NB + 16 * p + (lane & 15)) *
                                                        kBlockPitch + 64 * b + 16 * (lane >> 4)));
-        w4_step<F>(f16, cw[d], sc[d], a, acc);
+        w4_step<F, 4>(f16, cw[d], sc[d], a, acc);
       }
       load(d, i + D);
     });

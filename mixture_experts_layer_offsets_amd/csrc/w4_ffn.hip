@@ -132,30 +132,19 @@ __global__ __launch_bounds__(kPlanThreads) void w4_plan_kernel(const int32_t *__
 // order, one a lane.
 struct Token {
   int used, e, f;  // lane i < used: expert, first slot
-  float w;         // and weight
 };
 
-__device__ __forceinline__ Token one_token(const int32_t *idx, const float *w, int k, int first,
-                                           int E) {
+__device__ __forceinline__ Token one_token(const int32_t *idx, int k, int first, int E) {
   const int lane = threadIdx.x & 63;
   const int e = lane < k ? local_id(idx[lane], first, E) : -1;
-  const float own = lane < k ? w[lane] : 0.0f;
-  const uint64_t mine = same_expert(e, E);
-  const bool head = e >= 0 && !(mine & below(lane));
-  float sum = own;
-  for (int j = 1; j < k; j++) {  // later slots with the same expert
-    const float v = __shfl_down(own, j, 64);
-    if (lane + j < k && (mine >> (lane + j) & 1)) sum += v;
-  }
-  Token t{0, -1, 0, 0.0f};
-  for (uint64_t heads = __ballot(head); heads; heads &= heads - 1) {
+  Token t{0, -1, 0};
+  for (uint64_t heads = __ballot(e >= 0 && !(same_expert(e, E) & below(lane))); heads;
+       heads &= heads - 1) {
     const int at = __ffsll((unsigned long long)heads) - 1;
     const int he = __builtin_amdgcn_readlane(e, at);
-    const float hw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sum), at));
     if (lane == t.used) {
       t.e = he;
       t.f = at;
-      t.w = hw;
     }
     t.used++;
   }
@@ -292,19 +281,19 @@ __global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, F
   const int nt = q.gate.nt, j0 = blockIdx.x * tp;
   if (j0 >= nt) return;
   const Rows<PLAN> rows = find_rows<PLAN, true>(q, plan, blockIdx.y);
-  const int tid = threadIdx.x, lane = tid & 63, K = q.gate.k, ks = q.gate.ks;
+  const int tid = threadIdx.x, K = q.gate.k, ks = q.gate.ks;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
   for (int r0 = 0; r0 < rows.n; r0 += 16) {
     const int nr = min(16, rows.n - r0);
-    const RowPtr xr[1] = {{x + (size_t)(rows.slot(r0 + min(lane & 15, nr - 1)) / q.k) * K}};
+    const RowPtr xr = {x + (size_t)(rows.slot(r0 + min(w4_row_of_lane(), nr - 1)) / q.k) * K};
     for (int j = j0; j < min(j0 + tp, nt); j++) {
       const W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j), W4Row<F>(q.up, base + j)};
       f32x4 acc[2][1];
       zero_acc(acc);
-      w4_stream<F, 2>(mm, q.gate.f16, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+      w4_stream<F, 2>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
       w4_join<kGuWaves>(acc, red);
-      put_act(q, rows, r0 + 4 * ((tid & 63) >> 4) + (tid >> 6), 16 * j + (tid & 15), red[tid],
+      put_act(q, rows, r0 + w4_row_of(tid), 16 * j + (tid & 15), red[tid],
               red[256 + tid]);
       __syncthreads();
     }
@@ -364,7 +353,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
   extern __shared__ __attribute__((aligned(16))) char xs[];
   __shared__ float red[kWaves * 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Token t = one_token(q.idx, q.w, q.k, q.first, q.E);
+  const Token t = one_token(q.idx, q.k, q.first, q.E);
   f32x4 acc[1][1];
   zero_acc(acc);
   // the steps of `count` matrices, matrix i that of expert (lane i of e), its
@@ -396,7 +385,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
 #pragma unroll
           for (int b = 0; b < 4; b++)
             x[0][b] = xr.load(min(128 * turn(cs) + 32 * b + 8 * (lane >> 4), K - 8));
-          w4_step<F>(m.f16, ring.cw[d], ring.sc[d], x, acc);
+          w4_step<F, 1>(m.f16, ring.cw[d], ring.sc[d], x, acc);
           const bool last = cs + 1 == ks;
           cs = last ? 0 : cs + 1;
           cu += last;
@@ -447,7 +436,7 @@ __global__ __launch_bounds__(kGuWaves * 64) void w4_down_kernel(Ffn routed, Ffn 
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
   const int nt = q.down.nt, j0 = blockIdx.x * kDownTiles;
   const Rows<PLAN> rows = find_rows<PLAN, false>(q, plan, blockIdx.y);
-  const int tid = threadIdx.x, lane = tid & 63, K = q.down.k, ks = q.down.ks;
+  const int tid = threadIdx.x, K = q.down.k, ks = q.down.ks;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const size_t base = (size_t)__builtin_amdgcn_readfirstlane(rows.e) * nt;
   W4Row<F> mm[kDownTiles];
@@ -455,14 +444,14 @@ __global__ __launch_bounds__(kGuWaves * 64) void w4_down_kernel(Ffn routed, Ffn 
   for (int t = 0; t < kDownTiles; t++) mm[t] = W4Row<F>(q.down, base + min(j0 + t, nt - 1));
   for (int r0 = 0; r0 < rows.n; r0 += 16) {
     const int nr = min(16, rows.n - r0);
-    const RowPtr xr[1] = {{q.act + (size_t)rows.slot(r0 + min(lane & 15, nr - 1)) * K}};
+    const RowPtr xr = {q.act + (size_t)rows.slot(r0 + min(w4_row_of_lane(), nr - 1)) * K};
     f32x4 acc[kDownTiles][1];
     zero_acc(acc);
-    w4_stream<F, 1>(mm, q.down.f16, xr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+    w4_stream<F, 1>(mm, q.down.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
     w4_join<kGuWaves>(acc, red);
 #pragma unroll
     for (int t = 0; t < kDownTiles; t++)
-      put_y(q, rows, r0 + 4 * ((tid & 63) >> 4) + (tid >> 6), 16 * (j0 + t) + (tid & 15),
+      put_y(q, rows, r0 + w4_row_of(tid), 16 * (j0 + t) + (tid & 15),
             red[256 * t + tid]);
     __syncthreads();
   }

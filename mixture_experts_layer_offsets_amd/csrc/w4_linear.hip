@@ -23,46 +23,47 @@ __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
     W4Mat m, const uint16_t *x, long xstride, const int32_t *__restrict__ offsets, int rows,
     uint16_t *__restrict__ out, long ostride) {
   __shared__ float red[WAVES * 256];
-  const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int g = blockIdx.y, tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Span sp = span_of(offsets, g, rows);
   const W4Row<F> mm[1] = {W4Row<F>(m, (size_t)g * m.nt + blockIdx.x)};
   for (int r0 = sp.begin; r0 < sp.end; r0 += 16) {
     const int nr = min(16, sp.end - r0);
-    const RowPtr xr[1] = {{x + (r0 + min(lane & 15, nr - 1)) * xstride}};
+    const RowPtr xr = {x + (r0 + min(w4_row_of_lane(), nr - 1)) * xstride};
     f32x4 acc[1][1];
     zero_acc(acc);
-    w4_stream<F, 4>(mm, m.f16, xr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
+    w4_stream<F, 4>(mm, m.f16, xr, nr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
     w4_join<WAVES>(acc, red);
-    const int row = 4 * ((tid & 63) >> 4) + (tid >> 6), n = 16 * blockIdx.x + (tid & 15);
+    const int row = w4_row_of(tid), n = 16 * blockIdx.x + (tid & 15);
     if (tid < 256 && row < nr && n < m.n) out[(r0 + row) * ostride + n] = to_bf16(red[tid]);
     __syncthreads();
   }
 }
 
-// Many rows, 16 NB a pass: a workgroup takes 2 kBlockWaves tiles.
-template <class F, int NB>
+// Many rows, 16 NB a pass: a workgroup takes NTW kBlockWaves tiles.  Grid (output
+// tiles, groups, passes that run side by side).
+template <class F, int NTW, int NB>
 __global__ __launch_bounds__(64 * kBlockWaves * kBlockGroups, 2) void w4_linear_rows_kernel(
     W4Mat m, const uint16_t *x, long xstride, const int32_t *__restrict__ offsets, int rows,
     uint16_t *__restrict__ out, long ostride) {
   __shared__ __attribute__((aligned(16))) char xs[w4_block_lds<NB>()];
   const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 63, gt = tid % (64 * kBlockWaves);
   const Span sp = span_of(offsets, g, rows);
-  const int j = 2 * (blockIdx.x * kBlockWaves + __builtin_amdgcn_readfirstlane(gt >> 6));
-  const size_t base = (size_t)g * m.nt;
-  const W4Row<F> mm[2] = {W4Row<F>(m, base + min(j, m.nt - 1)),
-                          W4Row<F>(m, base + min(j + 1, m.nt - 1))};
-  for (int r0 = sp.begin; r0 < sp.end; r0 += 16 * NB) {
+  const int j = NTW * (blockIdx.x * kBlockWaves + __builtin_amdgcn_readfirstlane(gt >> 6));
+  W4Row<F> mm[NTW];
+#pragma unroll
+  for (int t = 0; t < NTW; t++) mm[t] = W4Row<F>(m, (size_t)g * m.nt + min(j + t, m.nt - 1));
+  for (int r0 = sp.begin + 16 * NB * blockIdx.z; r0 < sp.end; r0 += 16 * NB * gridDim.z) {
     const uint16_t *xr[NB];
 #pragma unroll
     for (int p = 0; p < NB; p++)
       xr[p] = x + min(r0 + 16 * p + gt / 16, sp.end - 1) * xstride + 8 * (gt % 16);
-    f32x4 acc[2][NB];
+    f32x4 acc[NTW][NB];
     zero_acc(acc);
     w4_block<F>(mm, m.f16, xr, m.k, m.ks, xs, acc);
     if (w4_block_join(acc, xs))
 #pragma unroll
-      for (int t = 0; t < 2; t++)
+      for (int t = 0; t < NTW; t++)
 #pragma unroll
         for (int p = 0; p < NB; p++)
 #pragma unroll
@@ -85,15 +86,26 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
   const int avg = (rows + d.groups - 1) / d.groups;
   with_format(d, [&](auto f) {
     using F = decltype(f);
-    auto go = [&](auto kernel, int tiles, int waves) {
-      hipLaunchKernelGGL(kernel, dim3((d.nt + tiles - 1) / tiles, d.groups), dim3(waves * 64), 0, s,
-                         m, x, xstride, offsets, rows, out, ostride);
+    auto go = [&](auto kernel, int tiles, int waves, int passes) {
+      hipLaunchKernelGGL(kernel, dim3((d.nt + tiles - 1) / tiles, d.groups, passes),
+                         dim3(waves * 64), 0, s, m, x, xstride, offsets, rows, out, ostride);
     };
-    constexpr int kBlock = kBlockWaves * kBlockGroups;
-    if (avg > 32) go(w4_linear_rows_kernel<F, kLongBlocks<F>>, 2 * kBlockWaves, kBlock);
-    else if (avg > 16) go(w4_linear_rows_kernel<F, 2>, 2 * kBlockWaves, kBlock);
-    else if ((long)d.nt * d.groups < 512) go(w4_linear_kernel<F, 16>, 1, 16);
-    else go(w4_linear_kernel<F, 4>, 1, 4);
+    constexpr int kBlock = kBlockWaves * kBlockGroups, kLong = kLongBlocks<F>;
+    auto rows_kernel = [&](auto one, auto two, int nb) {
+      const int passes = (avg + 16 * nb - 1) / (16 * nb);
+      const bool wide = (long)d.nt * d.groups * passes >= 256 * 2 * kBlockWaves;
+      if (wide) go(two, 2 * kBlockWaves, kBlock, passes);
+      else go(one, kBlockWaves, kBlock, passes);
+    };
+    // staged rows pay from 9 rows on where there are 128 workgroups of them (16
+    // rows, 8192 x 8192 MXFP4: 14.2 against 19.0 us; 2048 outputs of 7168, 32
+    // workgroups: 16.6 against 11.8 us), and below that the split contraction;
+    // few tiles: 16 waves for each
+    if (avg > 32) rows_kernel(w4_linear_rows_kernel<F, 1, kLong>, w4_linear_rows_kernel<F, 2, kLong>, kLong);
+    else if (avg > 16) rows_kernel(w4_linear_rows_kernel<F, 1, 2>, w4_linear_rows_kernel<F, 2, 2>, 2);
+    else if (avg > 8 && (long)d.nt * d.groups >= 512) rows_kernel(w4_linear_rows_kernel<F, 1, 1>, w4_linear_rows_kernel<F, 2, 1>, 1);
+    else if ((long)d.nt * d.groups < 512) go(w4_linear_kernel<F, 16>, 1, 16, 1);
+    else go(w4_linear_kernel<F, 4>, 1, 4, 1);
   });
 }
 
