@@ -124,25 +124,25 @@ __device__ __forceinline__ int round_rows(int n, int align) {
 // experts and ranks its rows: lanes of a wave with the same expert find each
 // other by ballots over the bits of the id.  Integers only, no order but f's.
 
-__global__ __launch_bounds__(256) void sort_count_kernel(const int32_t *__restrict__ idx, int R,
-                                                         int first, int E, int chunk,
-                                                         int32_t *__restrict__ chunk_counts,
-                                                         int32_t *__restrict__ perm, int cap) {
+__global__ __launch_bounds__(1024) void sort_count_kernel(const int32_t *__restrict__ idx, int R,
+                                                          int first, int E, int chunk,
+                                                          int32_t *__restrict__ chunk_counts,
+                                                          int32_t *__restrict__ perm, int cap) {
   extern __shared__ int32_t cnt[];
-  for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+  for (int e = threadIdx.x; e < E; e += 1024) cnt[e] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * chunk;
-  for (int i = threadIdx.x; i < chunk; i += 256) {
+  for (int i = threadIdx.x; i < chunk; i += 1024) {
     const int64_t f = base + i;
     if (f < R) {
       const int e = local_expert(idx[f], first, E);
       if (e >= 0) atomicAdd(&cnt[e], 1);
     }
   }
-  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < cap; r += (int64_t)gridDim.x * 256)
+  for (int64_t r = (int64_t)blockIdx.x * 1024 + threadIdx.x; r < cap; r += (int64_t)gridDim.x * 1024)
     perm[r] = -1;
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 256) chunk_counts[(size_t)blockIdx.x * E + e] = cnt[e];
+  for (int e = threadIdx.x; e < E; e += 1024) chunk_counts[(size_t)blockIdx.x * E + e] = cnt[e];
 }
 
 // Exclusive scan over the experts of the padded counts: thread i owns experts
@@ -178,29 +178,31 @@ __device__ __forceinline__ void scan_experts(const int32_t *cnt, int32_t *off, i
   __syncthreads();
 }
 
-__global__ __launch_bounds__(256) void sort_place_kernel(
+// THREADS: the workgroup's, and the rows it ranks a round.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void sort_place_kernel(
     const int32_t *__restrict__ idx, int R, int first, int E, int align, int chunk, int nchunks,
     const int32_t *__restrict__ chunk_counts, int32_t *__restrict__ counts,
     int32_t *__restrict__ offsets, int32_t *__restrict__ perm, int32_t *__restrict__ inv) {
+  constexpr int kWaves = THREADS / 64;
   extern __shared__ int32_t sm[];
   int32_t *tot = sm;             // [E] rows of each expert
   int32_t *run = tot + E;        // [E] next free row of each expert for this chunk
   int32_t *off = run + E;        // [E + 1]
-  int32_t *wcnt = off + E + 1;   // [4][E] rows of each expert per wave in this round
-  __shared__ int32_t wsum[4];
+  int32_t *wcnt = off + E + 1;   // [kWaves][E] rows of each expert per wave in this round
+  __shared__ int32_t wsum[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < E; e += 256) {
-    tot[e] = run[e] = 0;
-    wcnt[e] = wcnt[E + e] = wcnt[2 * E + e] = wcnt[3 * E + e] = 0;
-  }
+  for (int e = tid; e < E; e += THREADS) tot[e] = run[e] = 0;
+  for (int i = tid; i < kWaves * E; i += THREADS) wcnt[i] = 0;
   __syncthreads();
-  // few experts: several threads share an expert's column of the histograms
+  // several threads share an expert's column of the histograms, so that few
+  // loads follow one another
   int ep = 1;
-  while (ep < E && ep < 256) ep <<= 1;
-  const int parts = 256 / ep, part = tid / ep;
+  while (ep < E && ep < THREADS) ep <<= 1;
+  const int parts = THREADS / ep, part = tid / ep;
   for (int e = tid % ep; e < E; e += ep) {
     int all = 0, before = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int c = part; c < nchunks; c += parts) {
       const int n = chunk_counts[(size_t)c * E + e];
       all += n;
@@ -210,8 +212,8 @@ __global__ __launch_bounds__(256) void sort_place_kernel(
     if (before) atomicAdd(&run[e], before);
   }
   __syncthreads();
-  scan_experts<256>(tot, off, E, align, wsum);
-  for (int e = tid; e < E; e += 256) {
+  scan_experts<THREADS>(tot, off, E, align, wsum);
+  for (int e = tid; e < E; e += THREADS) {
     run[e] += off[e];
     if (blockIdx.x == 0) {
       counts[e] = tot[e];
@@ -222,8 +224,8 @@ __global__ __launch_bounds__(256) void sort_place_kernel(
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * chunk;
   const int bits = 32 - __clz(E);  // ids -1 .. E - 1, as e + 1 <= E
-  for (int round = 0; round < chunk / 256; round++) {
-    const int64_t f = base + round * 256 + tid;
+  for (int round = 0; round < chunk / THREADS; round++) {
+    const int64_t f = base + round * THREADS + tid;
     const int e = f < R ? local_expert(idx[f], first, E) : -1;
     uint64_t mine = ~0ull;
     for (int b = 0; b < bits; b++) {
@@ -625,9 +627,9 @@ __global__ __launch_bounds__(256) void narrow_kernel(
 }  // namespace
 
 int sort_chunk(long R) {
-  // at most kSortMaxChunks histograms, of whole rounds of 256 rows
+  // at most kSortMaxChunks histograms, of whole rounds of 1024 rows
   const long c = (R + kSortMaxChunks - 1) / kSortMaxChunks;
-  return (int)std::max<long>(kSortChunk, (c + 255) / 256 * 256);
+  return (int)std::max<long>(kSortChunk, (c + 1023) / 1024 * 1024);
 }
 
 long sort_workspace_words(const SortDims &d) {
@@ -640,10 +642,16 @@ void launch_sort_layout(const SortDims &d, const int32_t *idx, int32_t *counts, 
   const int chunk = sort_chunk(d.R), E = d.E;
   // no rows: one empty chunk, so that counts, offsets and perm are written
   const int n = (int)std::max<long>(1, (d.R + chunk - 1) / chunk);
-  hipLaunchKernelGGL(sort_count_kernel, dim3(n), dim3(256), E * sizeof(int32_t), s, idx, (int)d.R,
+  hipLaunchKernelGGL(sort_count_kernel, dim3(n), dim3(1024), E * sizeof(int32_t), s, idx, (int)d.R,
                      d.first, E, chunk, ws, perm, (int)d.cap);
-  hipLaunchKernelGGL(sort_place_kernel, dim3(n), dim3(256), (7 * E + 1) * sizeof(int32_t), s, idx,
-                     (int)d.R, d.first, E, d.align, chunk, n, ws, counts, offsets, perm, inv);
+  // more experts: fewer waves' counts, which all lie in 64 KB of LDS
+  auto place = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(n), dim3(threads), ((3 + threads / 64) * E + 1) * sizeof(int32_t),
+                       s, idx, (int)d.R, d.first, E, d.align, chunk, n, ws, counts, offsets, perm,
+                       inv);
+  };
+  if (E <= 512) place(sort_place_kernel<1024>, 1024);
+  else place(sort_place_kernel<512>, 512);
 }
 
 namespace {

@@ -273,7 +273,7 @@ __device__ __forceinline__ void put_act(const Ffn &q, const Rows<PLAN> &rows, in
 // one expert, one after the other; its waves split the contraction.  Grid (tile
 // pairs / tp, used experts [+ 1: the shared expert]).
 template <class F, bool PLAN>
-__global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, Ffn shared, Plan plan,
+__global__ __launch_bounds__(kGuWaves * 64, 4) void w4_gate_up_kernel(Ffn routed, Ffn shared, Plan plan,
                                                                    int used, int tp,
                                                                    const uint16_t *x) {
   __shared__ float red[kGuWaves * 2 * 256];
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kGuWaves * 64) void w4_gate_up_kernel(Ffn routed, F
       const W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j), W4Row<F>(q.up, base + j)};
       f32x4 acc[2][1];
       zero_acc(acc);
-      w4_stream<F, 2>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+      w4_stream<F, (F::kGrouped && F::SPG == 4 ? 1 : 2)>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
       w4_join<kGuWaves>(acc, red);
       put_act(q, rows, r0 + w4_row_of(tid), 16 * j + (tid & 15), red[tid],
               red[256 + tid]);
@@ -430,7 +430,7 @@ __device__ __forceinline__ void put_y(const Ffn &q, const Rows<PLAN> &rows, int 
 }
 
 template <class F, bool PLAN>
-__global__ __launch_bounds__(kGuWaves * 64) void w4_down_kernel(Ffn routed, Ffn shared, Plan plan,
+__global__ __launch_bounds__(kGuWaves * 64, 3) void w4_down_kernel(Ffn routed, Ffn shared, Plan plan,
                                                                 int used) {
   __shared__ float red[kGuWaves * kDownTiles * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
