@@ -461,7 +461,8 @@ int moe_unsort_bwd(const moe_sort_shape *shape, const void *dout, const void *y,
  *   they reach are not finite).
  * MOE_W4_INT4: w = s * (q - z), q in 0..15, group_size 32, 64 or 128, s bf16
  *   or fp16, z a zero point in 0..15 per group, or 8 everywhere (zeros = 0).
- *   The kernels form sums of x * (16 + q): x must stay below 2^120. */
+ *   The kernels form sums of x * (16 + q) over a group: |x| must stay below
+ *   2^115 (a group with a larger one gives NaN). */
 enum { MOE_W4_MXFP4 = 0, MOE_W4_INT4 = 1 };
 enum { MOE_SCALE_BF16 = 0, MOE_SCALE_F16 = 1 };
 

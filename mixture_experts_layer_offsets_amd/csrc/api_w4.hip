@@ -38,8 +38,7 @@ int check_w4(const moe_w4_shape *s, W4Dims *d) {
   d->code_bytes = tiles * 1024;
   d->scale_bytes = up256(tiles * 16 * d->spg * (mx ? 1 : 2));
   d->zero_bytes = d->zeros ? up256(tiles * 16 * d->spg) : 0;
-  // one thread per dword of codes when packing
-  if (tiles >= (1ull << 31)) return MOE_ERR_UNSUPPORTED;
+  if (tiles >= (1ull << 31)) return MOE_ERR_UNSUPPORTED;  // 2 TiB of codes
   return MOE_OK;
 }
 

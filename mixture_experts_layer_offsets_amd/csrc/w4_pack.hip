@@ -28,11 +28,11 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(W4Dims d, const uint8_t *_
                                                       const void *__restrict__ scales,
                                                       const uint8_t *__restrict__ zeros,
                                                       uint8_t *__restrict__ packed) {
-  const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
-  const size_t tiles = (size_t)d.groups * d.nt * d.ks;
-  if (id >= tiles * 256) return;
-  const int i = id & 3, l = (id >> 2) & 63;
-  const size_t tile = id >> 8;
+  // a tile a workgroup
+  const size_t tile = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (tile >= (size_t)d.groups * d.nt * d.ks) return;
+  const size_t id = tile * 256 + threadIdx.x;
+  const int i = threadIdx.x & 3, l = threadIdx.x >> 2;
   const int step = (int)(tile % d.ks);
   const size_t gt = tile / d.ks;
   const int n = (int)(gt % d.nt) * 16 + (l & 15);
@@ -153,9 +153,9 @@ __global__ __launch_bounds__(256) void w4_unpack_kernel(W4Dims d, const uint8_t 
 
 void launch_w4_pack(const W4Dims &d, const uint8_t *codes, const void *scales,
                     const uint8_t *zeros, void *packed, hipStream_t s) {
-  const size_t n = (size_t)d.groups * d.nt * d.ks * 256;
-  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, d, codes,
-                     scales, zeros, (uint8_t *)packed);
+  const size_t n = (size_t)d.groups * d.nt * d.ks, gx = std::min<size_t>(n, 1 << 20);
+  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)gx, (unsigned)((n + gx - 1) / gx)), dim3(256), 0,
+                     s, d, codes, scales, zeros, (uint8_t *)packed);
 }
 
 void launch_w4_quantize(const W4Dims &d, const uint16_t *w, void *packed, hipStream_t s) {

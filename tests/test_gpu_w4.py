@@ -112,6 +112,73 @@ def test_dense_product(f, rows, n, k):
     assert torch.equal(out, lin(x.cuda()))
 
 
+@pytest.mark.parametrize("f", [f for f in FORMATS if f[1] == 32], ids=[i for f, i in zip(FORMATS, IDS) if f[1] == 32])
+@pytest.mark.parametrize("k", [32, 96, 160, 416])
+@pytest.mark.parametrize("rows,n", [(1, 20), (5, 33), (12, 8200), (20, 130), (40, 130), (70, 30)])
+def test_contraction_ends_inside_a_tile(f, k, rows, n):
+    """k not a multiple of the 128 of a tile, for every way rows are taken."""
+    rng = np.random.default_rng([rows, n, k])
+    lin, codes, scales, zeros = make(rng, 1, n, k, f)
+    x = bf16(rng.standard_normal((rows, k)))
+    note(f"w4 tail {f} rows={rows} n={n} k={k}")
+    w, sabs = wo.values(codes, scales, zeros, f[0], f[1])
+    y, bound = wo.product(f64(x), w[0], sabs[0], f[0], f[1])
+    # the values behind the rows are NaN: they must not be read into a product
+    wide = torch.full((rows, k + 8), float("nan"), dtype=torch.bfloat16)
+    wide[:, :k] = x
+    within("tail", lin(wide.cuda()[:, :k]), y, wo.rounded(y, bound))
+
+
+@pytest.mark.parametrize("f", [FORMATS[0], FORMATS[4]], ids=[IDS[0], IDS[4]])
+@pytest.mark.parametrize("rows", [9, 20, 70, 200])
+def test_many_outputs(f, rows):
+    """Enough tiles for the workgroups that take two of them a wave."""
+    n, k = 33000, 128
+    rng = np.random.default_rng(rows)
+    lin, codes, scales, zeros = make(rng, 1, n, k, f)
+    x = bf16(rng.standard_normal((rows, k)))
+    note(f"w4 many outputs {f} rows={rows}")
+    w, sabs = wo.values(codes, scales, zeros, f[0], f[1])
+    y, bound = wo.product(f64(x), w[0], sabs[0], f[0], f[1])
+    within("many outputs", lin(x.cuda()), y, wo.rounded(y, bound))
+
+
+def test_strides_past_four_gib():
+    """Rows of x and out whose byte offsets pass 32 bits."""
+    f = FORMATS[0]
+    rng = np.random.default_rng(4)
+    lin, codes, scales, zeros = make(rng, 1, 40, 256, f)
+    w, sabs = wo.values(codes, scales, zeros, f[0], f[1])
+    big = torch.empty((5, 1 << 30), dtype=torch.bfloat16, device="cuda")
+    for rows in (3, 5):
+        x = bf16(rng.standard_normal((rows, 256)))
+        big[:rows, :256] = x.cuda()
+        lin(big[:rows, :256], out=big[:rows, 512:552])
+        y, bound = wo.product(f64(x), w[0], sabs[0], f[0], f[1])
+        within("strides", big[:rows, 512:552], y, wo.rounded(y, bound))
+
+
+def test_packed_past_four_gib():
+    """Codes whose byte offsets pass 32 bits: the last of 40 matrices."""
+    groups, n, k = 40, 8192, 32768
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(0, 256, (groups, n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(118, 124, (groups, n, k // 32), generator=g, device="cuda",
+                           dtype=torch.uint8)
+    lin = m.W4Linear.pack(m.W4Shape(groups, n, k), codes, scales)
+    assert lin.packed.numel() > 1 << 32
+    off = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    off[groups] = 2
+    x = torch.randn((2, k), generator=g, device="cuda").to(torch.bfloat16)
+    note("w4 packed past 4 GiB")
+    out = f64(lin(x, off))
+    part = slice(n - 64, n)
+    c = codes[-1, part].cpu().numpy()
+    w, sabs = wo.values(c, scales[-1, part].cpu().numpy(), None, "mxfp4", 32)
+    y, bound = wo.product(f64(x), w, sabs, "mxfp4", 32)
+    assert np.all(np.abs(out[:, part] - y) <= wo.rounded(y, bound))
+
+
 @pytest.mark.parametrize("f", FORMATS, ids=IDS)
 def test_grouped_strided_product(f):
     """Ragged groups (empty ones, one longer than a pass, rows before the
@@ -197,10 +264,23 @@ def test_quantize(f, k, n):
 LAYERS = {
     "one-token": (1, 8, 12, 0, 0, 12, 512, 256, 0),
     "one-slot": (1, 1, 1, 0, 0, 1, 64, 64, 0),
+    "one-shared": (1, 4, 6, 0, 0, 6, 256, 128, 192),
+    "one-elsewhere": (1, 2, 4, 100, 0, 50, 128, 64, 0),
+    "one-elsewhere-shared": (1, 2, 4, 100, 0, 50, 128, 64, 64),
+    # hidden rows too long to be staged together
+    "one-token-wide": (1, 16, 16, 0, 0, 16, 128, 2176, 0),
     "few": (5, 4, 16, 0, 0, 16, 384, 128, 0),
     "share": (9, 6, 8, 16, 0, 40, 256, 192, 0),
     "all-elsewhere": (3, 2, 4, 100, 0, 50, 128, 64, 0),
     "heavy-expert": (40, 4, 2, 0, 0, 2, 256, 128, 0),
+    # contractions that end inside a tile, with few rows an expert and with many
+    "tails": (6, 3, 5, 0, 0, 5, 192, 320, 64),
+    "heavy-tails": (40, 4, 2, 0, 0, 2, 192, 320, 0),
+    # more slots than a workgroup looks through: planned, at each average
+    "planned": (100, 4, 64, 5, 0, 80, 128, 64, 64),
+    "planned-more": (80, 4, 16, 0, 0, 16, 128, 192, 0),
+    "slots-256": (64, 4, 40, 0, 0, 44, 128, 64, 0),
+    "slots-257": (257, 1, 40, 0, 0, 44, 128, 64, 0),
     "shared": (7, 2, 6, 0, 0, 6, 256, 128, 320),
     "shared-heavy": (70, 2, 6, -3, -3, 6, 128, 64, 64),
     "k16-E1024": (6, 16, 1024, 0, 0, 1024, 64, 64, 0),
