@@ -260,13 +260,25 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(
 // Rows.
 
 // How a launch maps lanes to rows: 2^lsh lanes share a token (all 64 when its
-// row has 64 chunks or more, then grid y walks the row), 64 >> lsh tokens a
-// wave; `token_blocks` workgroups hold tokens, the ones behind them (E x
-// kPadSplit) zero the padding rows.
+// row has 64 chunks or more, then grid x walks the row), 64 >> lsh tokens a
+// wave.  Grid y and z count the workgroups that differ in their tokens:
+// `token_blocks` of them hold tokens, the ones behind them (E x kPadSplit) zero
+// the padding rows.  The row's chunks are the fastest index, so that a row is
+// written at one time: with them as the slowest index the sort of 65536 rows of
+// 7168 bf16 took 232 us instead of 224, the backward sort of 8192 rows 24.8 us
+// instead of 20.4, and the weighted return of 32768 kept rows 55 instead of 48.
 struct RowGrid {
   int lsh, token_blocks;
-  unsigned y;
+  unsigned x;
+  dim3 grid(long blocks) const {
+    const long y = std::min<long>(blocks, 65535);
+    return dim3(x, (unsigned)y, (unsigned)((blocks + y - 1) / y));
+  }
 };
+__device__ __forceinline__ int row_block() { return blockIdx.z * gridDim.y + blockIdx.y; }
+__device__ __forceinline__ long row_chunk(int lsh) {
+  return ((long)blockIdx.x << 6) + (threadIdx.x & ((1 << lsh) - 1));
+}
 
 RowGrid row_grid(int T, long row_bytes) {
   const long nc = (row_bytes + 15) / 16;
@@ -275,7 +287,7 @@ RowGrid row_grid(int T, long row_bytes) {
   while (g.lsh < 6 && (1L << g.lsh) < nc) g.lsh++;
   const int per = 64 >> g.lsh;
   g.token_blocks = (T + per - 1) / per;
-  g.y = (unsigned)((nc + 63) >> 6);
+  g.x = (unsigned)((nc + 63) >> 6);
   return g;
 }
 
@@ -286,7 +298,7 @@ __device__ __forceinline__ void zero_padding(const int32_t *counts, const int32_
                                              int sub, int subs, int lsh, char *rows, long RB,
                                              long stride) {
   const int lane = threadIdx.x & 63;
-  const long c = ((long)blockIdx.y << 6) + (lane & ((1 << lsh) - 1));
+  const long c = row_chunk(lsh);
   if (c * 16 >= RB) return;
   const long at = min(c * 16, RB - 16);
   const int end = offsets[e + 1], per = 64 >> lsh;
@@ -299,8 +311,8 @@ __device__ __forceinline__ void zero_padding(const int32_t *counts, const int32_
 // registers.
 template <bool WIDE>
 __device__ __forceinline__ int lane_token(const RowGrid &g) {
-  if constexpr (WIDE) return blockIdx.x;
-  return blockIdx.x * (64 >> g.lsh) + ((int)threadIdx.x >> g.lsh);
+  if constexpr (WIDE) return row_block();
+  return row_block() * (64 >> g.lsh) + ((int)threadIdx.x >> g.lsh);
 }
 
 // Row `row` (uniform in the wave) as a buffer of its own: a masked row is an
@@ -325,16 +337,16 @@ __device__ __forceinline__ u32x4 ld16(__amdgpu_buffer_rsrc_t r, long at) {
 template <int KMAX, bool WIDE>
 __global__ __launch_bounds__(kRowBlock) void sort_rows_kernel(
     const char *__restrict__ x, const int32_t *__restrict__ inv, const int32_t *__restrict__ counts,
-    const int32_t *__restrict__ offsets, char *__restrict__ xs, int T, int k, long RB, long xstride,
-    long rstride, RowGrid g) {
-  const int lane = threadIdx.x;
-  if ((int)blockIdx.x >= g.token_blocks) {
-    const int p = blockIdx.x - g.token_blocks;
-    zero_padding(counts, offsets, p / kPadSplit, p % kPadSplit, kPadSplit, g.lsh, xs, RB, rstride);
+    const int32_t *__restrict__ offsets, char *__restrict__ xs, int T, int k, int E, long RB,
+    long xstride, long rstride, RowGrid g) {
+  const int p = row_block() - g.token_blocks;
+  if (p >= 0) {
+    if (offsets && p < E * kPadSplit)
+      zero_padding(counts, offsets, p / kPadSplit, p % kPadSplit, kPadSplit, g.lsh, xs, RB, rstride);
     return;
   }
   const int t = lane_token<WIDE>(g);
-  const long c = ((long)blockIdx.y << 6) + (lane & ((1 << g.lsh) - 1));
+  const long c = row_chunk(g.lsh);
   if (t >= T || c * 16 >= RB) return;
   const long at = min(c * 16, RB - 16);
   int row[KMAX];
@@ -448,9 +460,8 @@ __global__ __launch_bounds__(kRowBlock) void unsort_kernel(
     const char *__restrict__ y, const float *__restrict__ w, const int32_t *__restrict__ inv,
     const char *__restrict__ add, char *__restrict__ out, int T, int k, long RB, long tstride,
     long rstride, RowGrid g) {
-  const int lane = threadIdx.x;
   const int t = lane_token<WIDE>(g);
-  const long c = ((long)blockIdx.y << 6) + (lane & ((1 << g.lsh) - 1));
+  const long c = row_chunk(g.lsh);
   if (t >= T || c * 16 >= RB) return;
   const long at = min(c * 16, RB - 16);
   u32x4 av;
@@ -685,11 +696,11 @@ void launch_sort_rows(const SortDims &d, const void *x, const int32_t *counts,
   if (RB < 16) return launch_narrow(NARROW_SORT, d, x, nullptr, nullptr, counts, offsets, inv, xs,
                                     nullptr, s);
   const RowGrid g = row_grid((int)d.T, RB);
-  const dim3 grid(g.token_blocks + (offsets ? d.E * kPadSplit : 0), g.y), b(kRowBlock);
+  const dim3 grid = g.grid(g.token_blocks + (offsets ? (long)d.E * kPadSplit : 0)), b(kRowBlock);
   const long xst = d.tstride * d.esize, rst = d.rstride * d.esize;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, b, 0, s, (const char *)x, inv, counts, offsets, (char *)xs,
-                       (int)d.T, d.k, RB, xst, rst, g);
+                       (int)d.T, d.k, d.E, RB, xst, rst, g);
   };
   if (g.lsh == 6) d.k <= 8 ? go(sort_rows_kernel<8, true>) : go(sort_rows_kernel<kSortMaxK, true>);
   else d.k <= 8 ? go(sort_rows_kernel<8, false>) : go(sort_rows_kernel<kSortMaxK, false>);
@@ -722,7 +733,7 @@ void go_unsort(const SortDims &d, const void *y, const float *w, const int32_t *
   const long RB = (long)d.D * d.esize;
   const RowGrid g = row_grid((int)d.T, RB);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(g.token_blocks, g.y), dim3(kRowBlock), 0, s, (const char *)y, w,
+    hipLaunchKernelGGL(kernel, g.grid(g.token_blocks), dim3(kRowBlock), 0, s, (const char *)y, w,
                        inv, (const char *)add, (char *)out, (int)d.T, d.k, RB, d.tstride * d.esize,
                        d.rstride * d.esize, g);
   };

@@ -179,15 +179,13 @@ struct RowPtr {
     return __builtin_bit_cast(bf16x8, *(const w4_u32x4u *)(p + k));
   }
 };
-// ... or in LDS, rows `pitch` bytes apart: 16 more than the values, so that 16
-// rows' reads of the same columns fall into different banks.
+// ... or in LDS.
 struct RowLds {
   const char *p;
   __device__ __forceinline__ bf16x8 load(int k) const {
     return __builtin_bit_cast(bf16x8, *(const w4_u32x4 *)(p + 2 * k));
   }
 };
-__host__ __device__ constexpr int w4_pitch(int values) { return 2 * values + 16; }
 
 // One step: acc[j][p] += a[p] times the codes of tile j, 128 contraction values.
 // V: values of a lane's results that are wanted (INT4 scales them one by one).
@@ -303,8 +301,7 @@ __device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, con
 }
 
 // A ring of D steps whose codes and scales are in flight, refilled step by step
-// (the rows lie in LDS): it never drains between the tiles that a workgroup
-// works on.
+// (the rows lie in LDS).
 template <class F, int NTW, int D>
 struct W4Ring {
   uint4 cw[D][NTW];
@@ -366,6 +363,8 @@ __device__ __forceinline__ void each(Fn &&f) {
 constexpr int kBlockWaves = 4;    // waves of a group
 constexpr int kBlockGroups = 2;
 constexpr int kBlockDepth = 4;    // steps in flight
+// LDS bytes from one row's step to the next: 16 more than its values, so that 16
+// rows' reads of the same columns fall into different banks
 constexpr int kBlockPitch = 256 + 16;
 // Row blocks of a long pass: groups of 32 keep four scales and offsets a step,
 // which leaves registers for two blocks only.

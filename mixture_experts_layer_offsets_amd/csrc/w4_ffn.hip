@@ -1,12 +1,20 @@
-// Few-token FFN of experts with 4-bit weights (w4_device.h):
-//   plan:    (more than one token) the used experts, and for each the slots
-//            that are its tokens' first ones with it, with the routing weight
-//            (summed if a token names the expert twice); one token's few slots
-//            are looked up by every workgroup itself;
-//   gate_up: a[f] = w silu(x Wg) (x Wu) at the place f of such a slot;
-//   down:    out[t] = sum over the experts of a Wd (+ the shared expert): the
-//            weighted sum of the experts' outputs is the matrix product's own
-//            accumulation, and neither expert outputs nor a combine exist.
+// Few-token FFN of experts with 4-bit weights (w4_device.h).  A row is a (token,
+// expert) pair, at the place f of the token's first slot with that expert:
+//   gate_up: a[f] = w silu(x Wg) (x Wu), w the routing weight (summed if the token
+//            names the expert twice), rounded to bf16;
+//   down:    y[f] = a[f] Wd in fp32, and out[t] = the sum of the token's y (+ the
+//            shared expert's).  For one token both are one kernel: its hidden
+//            rows, one behind the other, times its experts' matrices, one behind
+//            the other, is one long contraction.
+// No layout is made for up to 256 slots: each workgroup finds its expert's rows
+// itself, since a launch costs about 4 us here and the search about one.
+//
+// Bound by reading the used experts' codes and scales: about 6 us a kernel (launch,
+// search, the last workgroups) and then 5.5 to 6 TB/s, of 5.9 TB/s that a plain
+// read reaches.  MXFP4, 7168 x 2048, 8 of 48 experts, one token: gate_up 24.8 us
+// (125 MB), down 17.9 us (62 MB).  INT4 in groups of 64 with fp16 scales, 2048 x
+// 1408, 32 tokens over about 30 of 32 experts: 25.3 us (94 MB), 16.7 us (47 MB),
+// combine 4.6 us.
 #include <algorithm>
 
 #include "w4_device.h"
@@ -15,8 +23,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 8;           // waves of a workgroup
-constexpr int kRowLds = 66 * 1024;  // most LDS for staged rows: 16 of 2048 values, padded
+constexpr int kWaves = 8;            // waves of a one-token down workgroup
+constexpr int kTokenLds = 64 * 1024;  // most bytes of one token's hidden rows in its LDS
 
 __device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1; }
 
@@ -270,12 +278,17 @@ __device__ __forceinline__ void put_act(const Ffn &q, const Rows<PLAN> &rows, in
 }
 
 // gate_up, 16 rows a pass from memory: a workgroup takes tp pairs of tiles of
-// one expert, one after the other; its waves split the contraction.  Grid (tile
-// pairs / tp, used experts [+ 1: the shared expert]).
+// one expert, one after the other; its waves split the contraction.  Two steps a
+// batch, so that five workgroups share a CU: with four steps (three workgroups, a
+// second, mostly empty round of them at one token) 29.2 us for the 125 MB above
+// instead of 24.2.  The rows in LDS with a ring of codes over all pairs, and the
+// rows in registers over all pairs where the contraction is short, were no faster
+// (28.0 us; 27.4 against 25.3 us at 32 tokens).  Grid (tile pairs / tp, used
+// experts [+ 1: the shared expert]).
 template <class F, bool PLAN>
-__global__ __launch_bounds__(kGuWaves * 64, 4) void w4_gate_up_kernel(Ffn routed, Ffn shared, Plan plan,
-                                                                   int used, int tp,
-                                                                   const uint16_t *x) {
+__global__ __launch_bounds__(kGuWaves * 64, 4) void w4_gate_up_kernel(Ffn routed, Ffn shared,
+                                                                      Plan plan, int used, int tp,
+                                                                      const uint16_t *x) {
   __shared__ float red[kGuWaves * 2 * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
   const int nt = q.gate.nt, j0 = blockIdx.x * tp;
@@ -291,10 +304,12 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void w4_gate_up_kernel(Ffn routed
       const W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j), W4Row<F>(q.up, base + j)};
       f32x4 acc[2][1];
       zero_acc(acc);
-      w4_stream<F, (F::kGrouped && F::SPG == 4 ? 1 : 2)>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+      // groups of 32 of INT4: one, for their scales' registers
+      constexpr int U = F::kGrouped && F::SPG == 4 ? 1 : 2;
+      w4_stream<F, U>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves,
+                      acc);
       w4_join<kGuWaves>(acc, red);
-      put_act(q, rows, r0 + w4_row_of(tid), 16 * j + (tid & 15), red[tid],
-              red[256 + tid]);
+      put_act(q, rows, r0 + w4_row_of(tid), 16 * j + (tid & 15), red[tid], red[256 + tid]);
       __syncthreads();
     }
   }
@@ -339,14 +354,16 @@ __global__ __launch_bounds__(kBlockThreads, 2) void w4_gate_up_rows_kernel(Ffn r
 struct Down {
   W4Mat m, shared;  // shared.ks == 0: no shared expert
   const int32_t *idx;
-  const float *w;
-  int slots, k, first, E, T;
+  int k, first, E;
   const uint16_t *act, *act_s;
 };
 
 // One token: the hidden rows of its experts (and the shared one) lie in LDS one
-// behind the other, and their steps are one sequence, taken in turn by the
-// waves.  Grid: output tiles.
+// behind the other, and their steps are one sequence, split over the waves, each
+// with D steps of codes in flight.  17.9 us for the 62 MB above, of which the
+// stream takes about 11; the batches of gate_up here took 18.9 (the rows' loads
+// keep registers that the codes need), waves that take every eighth step 18.3.
+// Grid: output tiles.
 template <class F, int D>
 __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
                                                                     uint16_t *__restrict__ out) {
@@ -364,12 +381,10 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
     W4Ring<F, 1, D> ring;
     // the next step to load, and to use: matrix and step in it
     int lu = a / ks, ls = a - lu * ks, cu = lu, cs = ls;
-    const int rot = (int)(blockIdx.x * 5) % ks;  // as in gate_up; one for all waves of a row
-    auto turn = [&](int step) { return step + rot >= ks ? step + rot - ks : step + rot; };
     auto refill = [&](auto d) {
       const size_t row = (size_t)__builtin_amdgcn_readlane(e, lu) * m.nt + blockIdx.x;
       const W4Row<F> mm[1] = {W4Row<F>(m, row)};
-      ring.template load<decltype(d)::value>(mm, turn(ls));
+      ring.template load<decltype(d)::value>(mm, ls);
       const bool last = ls + 1 == ks;  // at the end: the last step again
       ls = last ? (lu + 1 < count ? 0 : ls) : ls + 1;
       lu += last && lu + 1 < count;
@@ -384,7 +399,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
           bf16x8 x[1][4];
 #pragma unroll
           for (int b = 0; b < 4; b++)
-            x[0][b] = xr.load(min(128 * turn(cs) + 32 * b + 8 * (lane >> 4), K - 8));
+            x[0][b] = xr.load(min(128 * cs + 32 * b + 8 * (lane >> 4), K - 8));
           w4_step<F, 1>(m.f16, ring.cw[d], ring.sc[d], x, acc);
           const bool last = cs + 1 == ks;
           cs = last ? 0 : cs + 1;
@@ -420,8 +435,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
 }
 
 // More tokens: y[f] = act[f] Wd in fp32 at the places of the rows, 16 rows a
-// pass, kDownTiles tiles of one expert a workgroup.  Grid (tiles / kDownTiles,
-// used experts [+ 1]).
+// pass, kDownTiles tiles of one expert a workgroup: at the 32 tokens above 14.4
+// us with four tiles, 18.5 with two and 28 with one (the search for the rows is
+// the same for all).  Grid (tiles / kDownTiles, used experts [+ 1]).
 constexpr int kDownTiles = 4;
 
 template <bool PLAN>
@@ -430,8 +446,8 @@ __device__ __forceinline__ void put_y(const Ffn &q, const Rows<PLAN> &rows, int 
 }
 
 template <class F, bool PLAN>
-__global__ __launch_bounds__(kGuWaves * 64, 3) void w4_down_kernel(Ffn routed, Ffn shared, Plan plan,
-                                                                int used) {
+__global__ __launch_bounds__(kGuWaves * 64, 3) void w4_down_kernel(Ffn routed, Ffn shared,
+                                                                   Plan plan, int used) {
   __shared__ float red[kGuWaves * kDownTiles * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
   const int nt = q.down.nt, j0 = blockIdx.x * kDownTiles;
@@ -447,12 +463,12 @@ __global__ __launch_bounds__(kGuWaves * 64, 3) void w4_down_kernel(Ffn routed, F
     const RowPtr xr = {q.act + (size_t)rows.slot(r0 + min(w4_row_of_lane(), nr - 1)) * K};
     f32x4 acc[kDownTiles][1];
     zero_acc(acc);
-    w4_stream<F, 1>(mm, q.down.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves, acc);
+    w4_stream<F, 1>(mm, q.down.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves,
+                    acc);
     w4_join<kGuWaves>(acc, red);
 #pragma unroll
     for (int t = 0; t < kDownTiles; t++)
-      put_y(q, rows, r0 + w4_row_of(tid), 16 * (j0 + t) + (tid & 15),
-            red[256 * t + tid]);
+      put_y(q, rows, r0 + w4_row_of(tid), 16 * (j0 + t) + (tid & 15), red[256 * t + tid]);
     __syncthreads();
   }
 }
@@ -545,7 +561,7 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
   const int used = std::min(E, slots), avg = slots / E;
   const unsigned gy = used + (a.shared ? 1 : 0);
   const int nt = a.shared ? std::max(a.up.nt, a.up_s.nt) : a.up.nt;
-  const bool plan = slots > kFewSlots, single = a.T == 1 && token_lds <= kRowLds;
+  const bool plan = slots > kFewSlots, single = a.T == 1 && token_lds <= kTokenLds;
   if (plan)
     hipLaunchKernelGGL(w4_plan_kernel, dim3(1), dim3(kPlanThreads),
                        (17 * E + (slots + 1) / 2) * sizeof(int32_t), s, a.idx, a.w, slots, a.k,
@@ -553,9 +569,11 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
   with_format(a.up, [&](auto f) {
     using F = decltype(f);
     const dim3 b(kGuWaves * 64), bb(kBlockThreads);
-    // two rounds of row blocks at most wasted: 32 rows a pass up to an average
-    // of 32 a expert, else 64
+    // Staged rows from an average of 16 a expert on (32 tokens x 8 slots over 8
+    // experts of 7168 x 2048: 58 us, and 122 us with rows from memory, which
+    // every tile reads again), 32 a pass up to an average of 32.
     auto up = [&](auto kernel) {
+      // about 768 workgroups: 32 tokens above 26.1 us, with 512 32.0, with 1024 27.4
       const int tp = std::max(1, (int)((long)nt * gy / 768));
       hipLaunchKernelGGL(kernel, dim3((nt + tp - 1) / tp, gy), b, 0, s, r, sh, p, used, tp, a.x);
     };
@@ -573,7 +591,7 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
                             : up_rows(w4_gate_up_rows_kernel<F, 2, false>);
     else plan ? up(w4_gate_up_kernel<F, true>) : up(w4_gate_up_kernel<F, false>);
     if (single) {
-      Down d{r.down, {}, a.idx, a.w, slots, a.k, a.first, E, a.T, a.act, nullptr};
+      Down d{r.down, {}, a.idx, a.k, a.first, E, a.act, nullptr};
       if (a.shared) {
         d.shared = sh.down;
         d.act_s = a.act_s;

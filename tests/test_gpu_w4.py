@@ -286,6 +286,7 @@ LAYERS = {
     "k16-E1024": (6, 16, 1024, 0, 0, 1024, 64, 64, 0),
     "most-slots": (256, 16, 24, 0, 0, 24, 128, 64, 0),
     "long": (3, 3, 5, 0, 0, 5, 7168, 2048, 0),
+    "wide-plan-E1024": (20, 16, 1024, 0, 0, 1024, 64, 64, 0),
 }
 
 
