@@ -47,17 +47,21 @@ typedef unsigned int w4_u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 // Packed pieces of one matrix per group.
 struct W4Mat {
   const uint8_t *codes, *scales, *zeros;
-  int n, k, nt, ks, f16;
+  int n, k, nt, ks;
+  uint32_t f16;  // mask of scale_value
 };
 
 inline W4Mat w4_view(const W4Dims &d, const void *packed) {
   const uint8_t *p = (const uint8_t *)packed;
   return {p, p + d.code_bytes, p + d.code_bytes + d.scale_bytes, d.n, d.k, d.nt, d.ks,
-          d.f16_scales};
+          d.f16_scales ? ~0u : 0u};
 }
 
-__device__ __forceinline__ float scale_value(uint32_t u16, int f16) {
-  return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)u16) : bf16_to_f32(u16);
+// f16: all bits, or none.  Both readings are made and one masked in: as a choice it
+// becomes a branch at every scale, which no load or product moves past.
+__device__ __forceinline__ float scale_value(uint32_t u16, uint32_t f16) {
+  const uint32_t h = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)u16));
+  return __uint_as_float((h & f16) | (u16 << 16 & ~f16));
 }
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
@@ -119,11 +123,14 @@ struct IntFmt {
   }
   // 16 + q: the nibble in bits 3..6 of bf16 16.0 (0x4180)
   static __device__ __forceinline__ bf16x8 unpack(uint32_t d, const Scales &, int) {
-    uint32_t u[4];
-    u[0] = (d & 0x00780078u) | 0x41804180u;
-    u[1] = ((d >> 4) & 0x00780078u) | 0x41804180u;
-    u[2] = ((d >> 8) & 0x00780078u) | 0x41804180u;
-    u[3] = (__builtin_amdgcn_alignbit(d, d, 12) & 0x00780078u) | 0x41804180u;
+    uint32_t u[4], mask = 0x00780078u, one = 0x41804180u;
+    // in registers, for one and-or each: as literals they take two instructions
+    asm("" : "+s"(mask));
+    asm("" : "+v"(one));
+    u[0] = (d & mask) | one;
+    u[1] = ((d >> 4) & mask) | one;
+    u[2] = ((d >> 8) & mask) | one;
+    u[3] = (__builtin_amdgcn_alignbit(d, d, 12) & mask) | one;
     bf16x8 v;
     __builtin_memcpy(&v, u, 16);
     return v;
@@ -190,7 +197,7 @@ struct RowLds {
 // One step: acc[j][p] += a[p] times the codes of tile j, 128 contraction values.
 // V: values of a lane's results that are wanted (INT4 scales them one by one).
 template <class F, int V, int NTW, int NB>
-__device__ __forceinline__ void w4_step(int f16, const uint4 (&cw)[NTW],
+__device__ __forceinline__ void w4_step(uint32_t f16, const uint4 (&cw)[NTW],
                                         const typename F::Scales (&sc)[NTW],
                                         const bf16x8 (&a)[NB][4], f32x4 (&acc)[NTW][NB]) {
   if constexpr (!F::kGrouped) {
@@ -266,7 +273,7 @@ __device__ __forceinline__ int w4_row_of(int i) {  // of sum i of w4_join
 // step again and are not used.  Values of k past K meet zero weights: their
 // lanes load the row's last values.
 template <class F, int U, int V, int NTW, class Row>
-__device__ __forceinline__ void w4_batches(const W4Row<F> (&m)[NTW], int f16, const Row &x, int K,
+__device__ __forceinline__ void w4_batches(const W4Row<F> (&m)[NTW], uint32_t f16, const Row &x, int K,
                                            int s0, int s1, f32x4 (&acc)[NTW][1]) {
   const int h8 = 8 * ((threadIdx.x & 63) >> 4);
   for (int s = s0; s < s1; s += U) {
@@ -294,7 +301,7 @@ __device__ __forceinline__ void w4_batches(const W4Row<F> (&m)[NTW], int f16, co
 }
 
 template <class F, int U, int NTW, class Row>
-__device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], int f16, const Row &x, int rows,
+__device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], uint32_t f16, const Row &x, int rows,
                                           int K, int s0, int s1, f32x4 (&acc)[NTW][1]) {
   if (F::kGrouped && rows <= 4) w4_batches<F, U, 1>(m, f16, x, K, s0, s1, acc);
   else w4_batches<F, U, 4>(m, f16, x, K, s0, s1, acc);
@@ -326,24 +333,28 @@ __device__ __forceinline__ void zero_acc(f32x4 (&acc)[NTW][NB]) {
 }
 
 // The waves' partial sums meet in LDS and are added in wave order.  Afterwards
-// red[256 j + i] is output i % 16 of tile j, of row w4_row_of(i).  red: WAVES NTW
-// 256 floats.  The caller synchronises before red is written again.
+// red[256 j + i] is output i % 16 of tile j, of row w4_row_of(i), for the first
+// `rows` rows.  red: WAVES NTW 256 floats.  The caller synchronises before red is
+// written again.
 template <int WAVES, int NTW>
-__device__ __forceinline__ void w4_join(const f32x4 (&acc)[NTW][1], float *red) {
+__device__ __forceinline__ void w4_join(const f32x4 (&acc)[NTW][1], float *red, int rows) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool few = rows <= 4;  // one value a lane
   constexpr int kQ = NTW * 4;
 #pragma unroll
   for (int j = 0; j < NTW; j++)
 #pragma unroll
-    for (int v = 0; v < 4; v++) red[(wave * kQ + j * 4 + v) * 64 + lane] = acc[j][0][v];
-  __syncthreads();
-  for (int i = tid; i < kQ * 64; i += WAVES * 64) {
+    for (int v = 0; v < 4; v++)
+      if (v == 0 || !few) red[(wave * kQ + j * 4 + v) * 64 + lane] = acc[j][0][v];
+  lds_barrier();
+  for (int q = tid; q < (few ? NTW : kQ) * 64; q += WAVES * 64) {
+    const int i = few ? (q & ~63) * 4 + lane : q;
     float t = red[i];
 #pragma unroll
     for (int w = 1; w < WAVES; w++) t += red[w * kQ * 64 + i];
     red[i] = t;
   }
-  __syncthreads();
+  lds_barrier();
 }
 
 // f(integral_constant<int, d>) for d = 0 .. N - 1
@@ -380,7 +391,7 @@ constexpr int w4_block_lds() { return kBlockGroups * 2 * 16 * NB * kBlockPitch; 
 // the codes (loads complete in order: rows fetched later than the codes of
 // their step would empty the pipeline at every step) into one of two buffers.
 template <class F, int NTW, int NB>
-__device__ __forceinline__ void w4_block(const W4Row<F> (&m)[NTW], int f16,
+__device__ __forceinline__ void w4_block(const W4Row<F> (&m)[NTW], uint32_t f16,
                                          const uint16_t *const (&x)[NB], int K, int ks, char *xs,
                                          f32x4 (&acc)[NTW][NB]) {
   constexpr int D = kBlockDepth;

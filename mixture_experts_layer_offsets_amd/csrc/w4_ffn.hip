@@ -221,10 +221,16 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
   __shared__ uint32_t used[32];
   __shared__ int16_t ids[kFewSlots];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int mine = tid < q.slots ? local_id(q.idx[tid], q.first, q.E) : -1;
+  int mine = -1;
+  float weight = 0.0f;
+  if (tid < q.slots) {
+    const int32_t given = q.idx[tid];
+    if (WEIGHT) weight = q.w[tid];  // of a masked slot: not used
+    mine = local_id(given, q.first, q.E);
+  }
   if (tid < 32) used[tid] = 0;
   if (tid < kFewSlots) ids[tid] = (int16_t)mine;
-  if (WEIGHT && mine >= 0) ws[tid] = q.w[tid];
+  if (WEIGHT && tid < q.slots) ws[tid] = weight;
   __syncthreads();
   if (mine >= 0) atomicOr(&used[mine >> 5], 1u << (mine & 31));
   __syncthreads();
@@ -277,21 +283,47 @@ __device__ __forceinline__ void put_act(const Ffn &q, const Rows<PLAN> &rows, in
     q.act[(size_t)rows.slot(r) * q.gate.n + n] = to_bf16(rows.weight(r) * silu_f(g) * u);
 }
 
-// gate_up, 16 rows a pass from memory: a workgroup takes tp pairs of tiles of
-// one expert, one after the other; its waves split the contraction.  Two steps a
-// batch, so that five workgroups share a CU: with four steps (three workgroups, a
-// second, mostly empty round of them at one token) 29.2 us for the 125 MB above
-// instead of 24.2.  The rows in LDS with a ring of codes over all pairs, and the
-// rows in registers over all pairs where the contraction is short, were no faster
-// (28.0 us; 27.4 against 25.3 us at 32 tokens).  Grid (tile pairs / tp, used
-// experts [+ 1: the shared expert]).
+// Waves a SIMD: groups of 32 of INT4 keep more scales than 128 registers hold.
+template <class F>
+constexpr int kPairWaves = F::kGrouped && F::SPG == 4 ? 3 : 4;
+
+// The product of 16 rows with NP pairs of tiles (lo[i], hi[i]), sums in acc[i] and
+// acc[NP + i]; at once where a lane's scaled sums are few, else pair by pair: the
+// registers of all at once (more than 128) would take a quarter of the waves.
+template <class F, int NP>
+__device__ __forceinline__ void stream_pairs(const W4Row<F> (&mm)[2 * NP], uint32_t f16,
+                                             const RowPtr &x, int nr, int K, int s0, int s1,
+                                             f32x4 (&acc)[2 * NP][1]) {
+  if (!F::kGrouped) return w4_batches<F, 1, 4>(mm, f16, x, K, s0, s1, acc);
+  if (nr <= 4) return w4_batches<F, 1, 1>(mm, f16, x, K, s0, s1, acc);
+#pragma unroll
+  for (int i = 0; i < NP; i++) {
+    const W4Row<F> pair[2] = {mm[i], mm[NP + i]};
+    f32x4 sum[2][1];
+    zero_acc(sum);
+    w4_batches<F, 1, 4>(pair, f16, x, K, s0, s1, sum);
+    acc[i][0] = sum[0][0];
+    acc[NP + i][0] = sum[1][0];
+  }
+}
+
+// gate_up, 16 rows a pass from memory: a workgroup takes tp sets of kGuPairs pairs
+// of tiles of one expert, one set after the other; its waves split the contraction.
+// Two pairs share a load of the rows: 22.7 us for the 125 MB above, and 24.3 with
+// one pair and two steps of the contraction loaded together.  Four workgroups fit
+// on a CU.  No faster, all at one token / at 32: a ring of steps over all sets
+// (25.2 / 31.6 us), four steps together (26.5 / 29.2), rows staged through LDS
+// (22.9 / 25.0), five workgroups (24.4 / 25.0); with the rows, the scales and the
+// products left out the codes alone take 21.5 / 17.4.  Grid (sets of tile pairs /
+// tp, used experts [+ 1: the shared expert]).
+constexpr int kGuPairs = 2;
+
 template <class F, bool PLAN>
-__global__ __launch_bounds__(kGuWaves * 64, 4) void w4_gate_up_kernel(Ffn routed, Ffn shared,
-                                                                      Plan plan, int used, int tp,
-                                                                      const uint16_t *x) {
-  __shared__ float red[kGuWaves * 2 * 256];
+__global__ __launch_bounds__(kGuWaves * 64, kPairWaves<F>) void w4_gate_up_kernel(
+    Ffn routed, Ffn shared, Plan plan, int used, int tp, const uint16_t *x) {
+  __shared__ float red[kGuWaves * 2 * kGuPairs * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
-  const int nt = q.gate.nt, j0 = blockIdx.x * tp;
+  const int nt = q.gate.nt, j0 = blockIdx.x * tp * kGuPairs;
   if (j0 >= nt) return;
   const Rows<PLAN> rows = find_rows<PLAN, true>(q, plan, blockIdx.y);
   const int tid = threadIdx.x, K = q.gate.k, ks = q.gate.ks;
@@ -300,16 +332,22 @@ __global__ __launch_bounds__(kGuWaves * 64, 4) void w4_gate_up_kernel(Ffn routed
   for (int r0 = 0; r0 < rows.n; r0 += 16) {
     const int nr = min(16, rows.n - r0);
     const RowPtr xr = {x + (size_t)(rows.slot(r0 + min(w4_row_of_lane(), nr - 1)) / q.k) * K};
-    for (int j = j0; j < min(j0 + tp, nt); j++) {
-      const W4Row<F> mm[2] = {W4Row<F>(q.gate, base + j), W4Row<F>(q.up, base + j)};
-      f32x4 acc[2][1];
+    for (int j = j0; j < min(j0 + tp * kGuPairs, nt); j += kGuPairs) {
+      W4Row<F> mm[2 * kGuPairs];
+#pragma unroll
+      for (int i = 0; i < kGuPairs; i++) {
+        mm[i] = W4Row<F>(q.gate, base + min(j + i, nt - 1));
+        mm[kGuPairs + i] = W4Row<F>(q.up, base + min(j + i, nt - 1));
+      }
+      f32x4 acc[2 * kGuPairs][1];
       zero_acc(acc);
-      // groups of 32 of INT4: one, for their scales' registers
-      constexpr int U = F::kGrouped && F::SPG == 4 ? 1 : 2;
-      w4_stream<F, U>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves,
-                      acc);
-      w4_join<kGuWaves>(acc, red);
-      put_act(q, rows, r0 + w4_row_of(tid), 16 * j + (tid & 15), red[tid], red[256 + tid]);
+      stream_pairs<F, kGuPairs>(mm, q.gate.f16, xr, nr, K, ks * wave / kGuWaves,
+                                ks * (wave + 1) / kGuWaves, acc);
+      w4_join<kGuWaves>(acc, red, nr);
+#pragma unroll
+      for (int i = 0; i < kGuPairs; i++)
+        put_act(q, rows, r0 + w4_row_of(tid), 16 * (j + i) + (tid & 15), red[256 * i + tid],
+                red[256 * (kGuPairs + i) + tid]);
       __syncthreads();
     }
   }
@@ -446,8 +484,8 @@ __device__ __forceinline__ void put_y(const Ffn &q, const Rows<PLAN> &rows, int 
 }
 
 template <class F, bool PLAN>
-__global__ __launch_bounds__(kGuWaves * 64, 3) void w4_down_kernel(Ffn routed, Ffn shared,
-                                                                   Plan plan, int used) {
+__global__ __launch_bounds__(kGuWaves * 64, kPairWaves<F>) void w4_down_kernel(
+    Ffn routed, Ffn shared, Plan plan, int used) {
   __shared__ float red[kGuWaves * kDownTiles * 256];
   const Ffn q = (int)blockIdx.y == used ? shared : routed;
   const int nt = q.down.nt, j0 = blockIdx.x * kDownTiles;
@@ -463,9 +501,9 @@ __global__ __launch_bounds__(kGuWaves * 64, 3) void w4_down_kernel(Ffn routed, F
     const RowPtr xr = {q.act + (size_t)rows.slot(r0 + min(w4_row_of_lane(), nr - 1)) * K};
     f32x4 acc[kDownTiles][1];
     zero_acc(acc);
-    w4_stream<F, 1>(mm, q.down.f16, xr, nr, K, ks * wave / kGuWaves, ks * (wave + 1) / kGuWaves,
-                    acc);
-    w4_join<kGuWaves>(acc, red);
+    stream_pairs<F, kDownTiles / 2>(mm, q.down.f16, xr, nr, K, ks * wave / kGuWaves,
+                                    ks * (wave + 1) / kGuWaves, acc);
+    w4_join<kGuWaves>(acc, red, nr);
 #pragma unroll
     for (int t = 0; t < kDownTiles; t++)
       put_y(q, rows, r0 + w4_row_of(tid), 16 * (j0 + t) + (tid & 15), red[256 * t + tid]);
@@ -573,9 +611,10 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
     // experts of 7168 x 2048: 58 us, and 122 us with rows from memory, which
     // every tile reads again), 32 a pass up to an average of 32.
     auto up = [&](auto kernel) {
-      // about 768 workgroups: 32 tokens above 26.1 us, with 512 32.0, with 1024 27.4
-      const int tp = std::max(1, (int)((long)nt * gy / 768));
-      hipLaunchKernelGGL(kernel, dim3((nt + tp - 1) / tp, gy), b, 0, s, r, sh, p, used, tp, a.x);
+      // sets a workgroup, for about 768 of them: 32 tokens above 24.4 us, with 512 28.3
+      const int sets = (nt + kGuPairs - 1) / kGuPairs;
+      const int tp = std::max(1, (int)((long)sets * gy / 768));
+      hipLaunchKernelGGL(kernel, dim3((sets + tp - 1) / tp, gy), b, 0, s, r, sh, p, used, tp, a.x);
     };
     auto up_rows = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((nt + kBlockWaves - 1) / kBlockWaves, gy), bb, 0, s, r, sh, p,

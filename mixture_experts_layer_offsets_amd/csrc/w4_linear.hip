@@ -33,7 +33,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
     f32x4 acc[1][1];
     zero_acc(acc);
     w4_stream<F, 4>(mm, m.f16, xr, nr, m.k, m.ks * wave / WAVES, m.ks * (wave + 1) / WAVES, acc);
-    w4_join<WAVES>(acc, red);
+    w4_join<WAVES>(acc, red, nr);
     const int row = w4_row_of(tid), n = 16 * blockIdx.x + (tid & 15);
     if (tid < 256 && row < nr && n < m.n) out[(r0 + row) * ostride + n] = to_bf16(red[tid]);
     __syncthreads();

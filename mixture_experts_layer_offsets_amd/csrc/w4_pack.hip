@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4Dims d, const uint16
     s = d.zeros ? (hi - lo) / 15.0f : fmaxf(-lo, hi) / 7.0f;
     const uint16_t bits = d.f16_scales ? __builtin_bit_cast(uint16_t, (_Float16)s)
                                        : __builtin_bit_cast(uint16_t, (__bf16)s);
-    s = scale_value(bits, d.f16_scales);
+    s = scale_value(bits, d.f16_scales ? ~0u : 0u);
     ((uint16_t *)ps)[to] = in ? bits : 0;
     if (d.zeros) {
       z = s > 0.0f ? (int)fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 0;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256) void w4_unpack_kernel(W4Dims d, const uint8_t 
       v = ldexpf(c & 8 ? -mag : mag, (int)ps[at] - 127);
     } else {
       const int z = d.zeros ? (ps + d.scale_bytes)[at] : 8;
-      v = scale_value(((const uint16_t *)ps)[at], d.f16_scales) * (float)((int)c - z);
+      v = scale_value(((const uint16_t *)ps)[at], d.f16_scales ? ~0u : 0u) * (float)((int)c - z);
     }
     w[(g * d.k + k) * d.n + n] = v;
   }
