@@ -462,7 +462,9 @@ int moe_unsort_bwd(const moe_sort_shape *shape, const void *dout, const void *y,
  * MOE_W4_INT4: w = s * (q - z), q in 0..15, group_size 32, 64 or 128, s bf16
  *   or fp16, z a zero point in 0..15 per group, or 8 everywhere (zeros = 0).
  *   The kernels form sums of x * (16 + q) over a group: |x| must stay below
- *   2^115 (a group with a larger one gives NaN). */
+ *   2^115 (a group with a larger one gives NaN).
+ * Infinite activations give NaN or infinite outputs of their own row; no row's
+ * values reach another's. */
 enum { MOE_W4_MXFP4 = 0, MOE_W4_INT4 = 1 };
 enum { MOE_SCALE_BF16 = 0, MOE_SCALE_F16 = 1 };
 
@@ -506,8 +508,9 @@ int moe_w4_unpack(const moe_w4_shape *shape, const void *packed, float *w,
  * each group (device, [groups+1], ascending, at most `rows`; other rows of out
  * are left as they were), or with offsets NULL and groups = 1 for all rows.
  * x: rows of k bf16 values, x_stride apart; out: rows of n, out_stride apart
- * (strides in values).  Made for few rows per group: every 64 rows of a group
- * read its weights once.  rows may be 0. */
+ * (strides in values, at most 2^32).  out must not overlap x.  Made for few rows
+ * per group: the weights are read once per 16 to 64 rows of a group, more rows
+ * at a time the more there are.  0 <= rows <= 2^30. */
 int moe_w4_linear(const moe_w4_shape *shape, int32_t rows, const uint16_t *x,
                   int64_t x_stride, const int32_t *offsets, const void *packed,
                   uint16_t *out, int64_t out_stride, void *stream);
@@ -538,9 +541,10 @@ size_t moe_w4_decode_workspace_bytes(const moe_shape *shape);
  * slots of topk_w * (silu(x Wg) * (x Wu)) Wd, plus the shared expert), the
  * product of silu rounded to bf16 as the layer does, all other sums in fp32 in
  * a fixed order.  Arguments as moe_decode_fwd, with the experts in 4 bits;
- * shape->dtype MOE_BF16, T*k <= 4096, H, I and the shared I multiples of the
- * group size.  A router (first_expert 0) re-decides over the experts here;
- * supplied routing may name experts elsewhere. */
+ * shape->dtype MOE_BF16, T*k <= 4096, T*k*I and T times the shared I below
+ * 2^30, H, I and the shared I multiples of 64 and of the group size.  A router
+ * (first_expert 0) re-decides over the experts here; supplied routing may name
+ * experts elsewhere. */
 int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts,
                       const uint16_t *x, const uint16_t *w_router,
                       const float *bias, const int32_t *topk_idx_in,

@@ -61,7 +61,7 @@ int check_layer(const moe_shape *s) {
     return MOE_ERR_UNSUPPORTED;
   if ((int64_t)s->hidden * s->experts >= (1L << 31) || s->hidden > (1 << 20))
     return MOE_ERR_UNSUPPORTED;
-  // the hidden rows are one buffer with 31-bit byte offsets
+  // the hidden rows' buffers stay below 2 GiB
   if ((int64_t)s->tokens * s->top_k * s->inter >= (1L << 30) ||
       (int64_t)s->tokens * s->shared_inter >= (1L << 30))
     return MOE_ERR_UNSUPPORTED;
@@ -138,7 +138,10 @@ int moe_w4_linear(const moe_w4_shape *shape, int32_t rows, const uint16_t *x, in
   if (rows < 0 || x_stride < d.k || out_stride < d.n || !packed || (rows && (!x || !out)) ||
       (!offsets && d.groups != 1))
     return MOE_ERR_INVALID_ARG;
-  if (x_stride > (1L << 32) || out_stride > (1L << 32)) return MOE_ERR_UNSUPPORTED;
+  // row indices, and a pass past them, take 31 bits
+  if (x_stride > (1L << 32) || out_stride > (1L << 32) || rows > (1 << 30))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows && x == out) return MOE_ERR_INVALID_ARG;
   launch_w4_linear(d, rows, x, x_stride, offsets, packed, out, out_stride, (hipStream_t)stream);
   return status();
 }

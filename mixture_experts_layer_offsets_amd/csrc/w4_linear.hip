@@ -92,7 +92,7 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
     };
     constexpr int kBlock = kBlockWaves * kBlockGroups, kLong = kLongBlocks<F>;
     auto rows_kernel = [&](auto one, auto two, int nb) {
-      const int passes = (avg + 16 * nb - 1) / (16 * nb);
+      const int passes = std::min((avg + 16 * nb - 1) / (16 * nb), 65535);  // grid z's bound
       const bool wide = (long)d.nt * d.groups * passes >= 256 * 2 * kBlockWaves;
       if (wide) go(two, 2 * kBlockWaves, kBlock, passes);
       else go(one, kBlockWaves, kBlock, passes);

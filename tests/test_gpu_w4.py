@@ -143,6 +143,23 @@ def test_many_outputs(f, rows):
     within("many outputs", lin(x.cuda()), y, wo.rounded(y, bound))
 
 
+def test_more_passes_than_a_grid_dimension():
+    """More than 65535 passes of 32 rows (groups of 32 of INT4), the same 2048
+    rows again and again: every one of their outputs is the same."""
+    f, n, k, part = FORMATS[4], 8, 32, 2048
+    assert f[0] == "int4" and f[1] == 32
+    rng = np.random.default_rng(65)
+    lin, codes, scales, zeros = make(rng, 1, n, k, f)
+    x = bf16(rng.standard_normal((part, k)))
+    times = 65536 * 32 // part + 1
+    note(f"w4 {times * part} rows")
+    out = lin(x.cuda().repeat(times, 1)).view(times, part, n)
+    w, sabs = wo.values(codes, scales, zeros, f[0], f[1])
+    y, bound = wo.product(f64(x), w[0], sabs[0], f[0], f[1])
+    within("first rows", out[0], y, wo.rounded(y, bound))
+    assert torch.equal(out, out[:1].expand_as(out))
+
+
 def test_strides_past_four_gib():
     """Rows of x and out whose byte offsets pass 32 bits."""
     f = FORMATS[0]

@@ -66,6 +66,9 @@ def test_missing_pointers(lib):
                  (3, FAKE, 256, FAKE, FAKE, None, 48)):
         assert lib.moe_w4_linear(s, *args, None) == INVALID, args
     assert lib.moe_w4_linear(s, 3, FAKE, (1 << 32) + 1, FAKE, FAKE, FAKE, 48, None) == UNSUPPORTED
+    # more rows than the kernels index; out over x
+    assert lib.moe_w4_linear(s, (1 << 30) + 1, FAKE, 256, FAKE, FAKE, FAKE, 48, None) == UNSUPPORTED
+    assert lib.moe_w4_linear(s, 3, FAKE, 256, FAKE, FAKE, FAKE, 48, None) == INVALID
 
 
 def test_sizes(lib):
