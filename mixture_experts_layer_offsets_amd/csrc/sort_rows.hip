@@ -38,9 +38,13 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kSortMaxK = 16;   // top-k bound of the library
 constexpr int kRowBlock = 64;   // one wave per workgroup for the gathers (see combine_kernel)
 constexpr int kPadSplit = 8;    // workgroups that share one expert's padding rows
-// One-launch sort: slots, rows of the sorted buffer (one workgroup fills perm)
-// and bytes of a row (a wave's worth) it takes; rows a padding workgroup checks.
-constexpr int kSortSmallSlots = 1024, kSortSmallRows = 16384, kSortSmallBytes = 1024;
+// One-launch sort: slots it takes (512: 7.5 us, layout and rows apart 12.8; 1024:
+// 13.7 and 13.5), slots if aligned, where every workgroup makes the layout (256 of
+// 256 experts to 16 rows: 18.9 and 19.1; 512: 24.3 and 19.5), rows of the sorted
+// buffer (one workgroup fills perm's end) and bytes of a row (a wave's worth); rows
+// a padding workgroup checks.
+constexpr int kSortSmallSlots = 512, kSortSmallAligned = 256;
+constexpr int kSortSmallRows = 16384, kSortSmallBytes = 1024;
 constexpr int kSmallPadRows = 16;
 constexpr int kRawBuffer = 0x00020000;  // raw buffer descriptor, gfx9 family
 constexpr int kNonTemporal = 2;         // cache policy of a buffer access: nt
@@ -368,8 +372,10 @@ __global__ __launch_bounds__(kRowBlock) void sort_rows_kernel(
 // workgroup waits for another, each finds its token's rows itself.  With f's
 // expert e, the row of f is the number of slots of lower experts (rounded per
 // expert to the alignment) plus those of e before f; every lane holds up to NI
-// ids and the wave counts them by ballots.  The last workgroup of the grid
-// writes the layout; the ones between (align > 1) zero the padding rows.
+// ids and the wave counts them by ballots.  A token's workgroups write its
+// slots' part of the layout, those behind them (align > 1) the padding rows',
+// the last one the rest.  7168 bf16, 8 of 256 experts a token: 6.0 us at 8 to
+// 256 slots, layout and rows apart 13.6.
 
 // Counts and offsets of up to kSortSmallSlots slots in LDS (cnt [E], off [E+1]).
 __device__ __forceinline__ void small_layout(const int32_t *idx, int R, int first, int E, int align,
@@ -404,10 +410,15 @@ __global__ __launch_bounds__(256) void sort_small_kernel(
       const int f = lane + 64 * i;
       id[i] = f < R ? local_expert(idx[f], first, E) : -1;
     }
+    const int own = lane < k ? local_expert(idx[t * k + lane], first, E) : -1;
     if (align > 1) small_layout(idx, R, first, E, align, cnt, off, wsum);
     for (int j = 0; j < k; j++) {
-      const int f = t * k + j, e = local_expert(idx[f], first, E);
-      if (e < 0) continue;
+      const int f = t * k + j, e = __builtin_amdgcn_readlane(own, j);
+      const bool writes = blockIdx.y == 0 && tid == 0;
+      if (e < 0) {
+        if (writes) inv[f] = -1;
+        continue;
+      }
       int row = align > 1 ? off[e] : 0;
 #pragma unroll
       for (int i = 0; i < NI; i++) {
@@ -415,12 +426,15 @@ __global__ __launch_bounds__(256) void sort_small_kernel(
         row += __popcll(__ballot(before || (align <= 1 && id[i] >= 0 && id[i] < e)));
       }
       if (c * 16 < RB) st16(xs + row * rstride + at, v);
+      if (writes) {
+        inv[f] = row;
+        perm[row] = f;
+      }
     }
     return;
   }
   small_layout(idx, R, first, E, align, cnt, off, wsum);
   if (blockIdx.x < gridDim.x - 1) {
-    if (c * 16 >= RB) return;
     const int r0 = (t - T) * kSmallPadRows;
     for (int r = r0; r < min(r0 + kSmallPadRows, off[E]); r++) {
       int lo = 0, hi = E;  // off[lo] <= r < off[hi]
@@ -429,7 +443,9 @@ __global__ __launch_bounds__(256) void sort_small_kernel(
         if (off[mid] <= r) lo = mid;
         else hi = mid;
       }
-      if (r >= off[lo] + cnt[lo]) st16(xs + r * rstride + at, (u32x4){0, 0, 0, 0});
+      if (r < off[lo] + cnt[lo]) continue;
+      if (c * 16 < RB) st16(xs + r * rstride + at, (u32x4){0, 0, 0, 0});
+      if (blockIdx.y == 0 && tid == 0) perm[r] = -1;
     }
     return;
   }
@@ -438,20 +454,7 @@ __global__ __launch_bounds__(256) void sort_small_kernel(
     offsets[e] = off[e];
     if (e < E) counts[e] = cnt[e];
   }
-  for (int r = tid; r < cap; r += 256) perm[r] = -1;
-  // the ids, for each slot's rank (the counts and the scan are done with)
-  __syncthreads();
-  int32_t *ids = off + E + 1;
-  for (int f = tid; f < R; f += 256) ids[f] = local_expert(idx[f], first, E);
-  __syncthreads();  // and perm's fill before its rows
-  for (int f = tid; f < R; f += 256) {
-    const int e = ids[f];
-    int rank = 0;
-    for (int g = 0; g < f; g++) rank += ids[g] == e;
-    const int row = e >= 0 ? off[e] + rank : -1;
-    inv[f] = row;
-    if (row >= 0) perm[row] = f;
-  }
+  for (int r = off[E] + tid; r < cap; r += 256) perm[r] = -1;
 }
 
 // out[t] = sum_j (w) y[inv[t k + j]] (+ add[t]).
@@ -709,11 +712,12 @@ void launch_sort_rows(const SortDims &d, const void *x, const int32_t *counts,
 bool launch_sort_small(const SortDims &d, const void *x, const int32_t *idx, int32_t *counts,
                        int32_t *offsets, int32_t *perm, int32_t *inv, void *xs, hipStream_t s) {
   const long RB = (long)d.D * d.esize;
-  if (d.R < 1 || d.R > kSortSmallSlots || d.cap > kSortSmallRows || RB < kSortSmallBytes)
+  if (d.R < 1 || d.R > (d.align > 1 ? kSortSmallAligned : kSortSmallSlots) ||
+      d.cap > kSortSmallRows || RB < kSortSmallBytes)
     return false;
   const long pads = d.align > 1 ? (d.cap + kSmallPadRows - 1) / kSmallPadRows : 0;
   const dim3 grid((unsigned)(d.T + pads + 1), (unsigned)((RB + 4095) / 4096)), b(256);
-  const size_t lds = (2 * d.E + 1 + d.R) * sizeof(int32_t);
+  const size_t lds = (2 * d.E + 1) * sizeof(int32_t);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, b, lds, s, (const char *)x, idx, counts, offsets, perm, inv,
                        (char *)xs, (int)d.T, d.k, d.first, d.E, d.align, (int)d.cap, RB,

@@ -51,7 +51,7 @@ CASES = {
     "E1024": (300, 5, 1024, 64, "bf16", 2, 0, 0, 0, 0.1),
     "two-chunks": (700, 3, 17, 40, "f32", 1, 0, 0, 0, 0.1),
     "many-chunks": (9000, 16, 6, 16, "bf16", 32, 0, 0, 0, 0.1),
-    # one-launch sorts at their limits: 1024 slots, padded segments, one slot more
+    # few slots: in one launch, or layout and rows apart
     "slots-64": (8, 8, 12, 600, "bf16", 4, 0, 0, 0, 0.3),
     "slots-1024": (128, 8, 40, 512, "bf16", 1, 3, 0, 0, 0.2),
     "slots-1024-align": (64, 16, 9, 520, "bf16", 128, -2, 8, 0, 0.1),
@@ -62,6 +62,11 @@ CASES = {
     "wide-odd-stride": (21, 16, 6, 1030, "f16", 1, 0, 3, 5, 0.5),
     "wide-f32": (40, 12, 9, 515, "f32", 2, 0, 0, 2, 0.2),
     "wide": (3, 2, 4, 20000, "bf16", 1, 0, 0, 0, 0.0),
+    # one-launch sorts at their limits (x: the others keep their inputs)
+    "x-slots-512": (64, 8, 40, 2056, "bf16", 1, 3, 0, 0, 0.2),
+    "x-slots-513": (171, 3, 40, 512, "bf16", 1, 0, 0, 0, 0.2),
+    "x-slots-256-align": (64, 4, 9, 520, "bf16", 128, -2, 8, 0, 0.1),
+    "x-slots-272-align": (17, 16, 9, 520, "f32", 128, -2, 8, 0, 0.1),
 }
 
 
