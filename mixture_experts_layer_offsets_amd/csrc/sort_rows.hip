@@ -193,7 +193,7 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(
   int32_t *tot = sm;             // [E] rows of each expert
   int32_t *run = tot + E;        // [E] next free row of each expert for this chunk
   int32_t *off = run + E;        // [E + 1]
-  int32_t *wcnt = off + E + 1;   // [kWaves][E] rows of each expert per wave in this round
+  int32_t *wcnt = off + E + 1;   // [kWaves][E] rows of each expert per wave in this pass
   __shared__ int32_t wsum[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < E; e += THREADS) tot[e] = run[e] = 0;

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kPlanThreads) void w4_plan_kernel(const int32_t *__
                                                                Plan p) {
   extern __shared__ int32_t lds[];
   int32_t *cnt = lds;                 // [E] rows of each expert, then its next free row
-  int32_t *wcnt = cnt + E;            // [16][E] rows per wave in this round
+  int32_t *wcnt = cnt + E;            // [16][E] rows per wave in this pass
   int16_t *ids = (int16_t *)(wcnt + 16 * E);  // [slots]
   __shared__ int32_t wsum[16], wused[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
