@@ -199,9 +199,12 @@ constexpr int kBlockThreads = 64 * kBlockWaves * kBlockGroups;
 constexpr int kFewSlots = 256;  // slots that a workgroup looks through by itself
 
 // The rows of the u-th used expert (u == used: the shared expert's); n = 0: there
-// is none.  Up to kFewSlots slots are looked through here, one a thread: the used
-// experts as bits in LDS, then the expert's slots by ballots, in every wave.
-// WEIGHT: their weights too (complete after the next barrier).
+// is none.  Up to kFewSlots slots are looked through here, by each wave for
+// itself: the expert's slots by ballots over the ids, four a lane.  With as many
+// slots as experts the u-th is expert u; with up to 64 slots the used experts are
+// counted by their first slots; else as bits in LDS (which costs two barriers:
+// 2.6 us until the rows are known at the 32 tokens above, FOUND without).
+// WEIGHT: the rows' weights too.
 template <bool PLAN, bool WEIGHT>
 __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, int u) {
   __shared__ uint16_t list[kFewSlots];
@@ -218,42 +221,57 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
     r.wrow = plan.wrow + at;
     return r;
   }
-  __shared__ uint32_t used[32];
-  __shared__ int16_t ids[kFewSlots];
+  constexpr int kIds = kFewSlots / 64;
   const int tid = threadIdx.x, lane = tid & 63;
-  int mine = -1;
-  float weight = 0.0f;
-  if (tid < q.slots) {
-    const int32_t given = q.idx[tid];
-    if (WEIGHT) weight = q.w[tid];  // of a masked slot: not used
-    mine = local_id(given, q.first, q.E);
-  }
-  if (tid < 32) used[tid] = 0;
-  if (tid < kFewSlots) ids[tid] = (int16_t)mine;
-  if (WEIGHT && tid < q.slots) ws[tid] = weight;
-  __syncthreads();
-  if (mine >= 0) atomicOr(&used[mine >> 5], 1u << (mine & 31));
-  __syncthreads();
-  // the u-th set bit, word by word
-  const uint32_t word = lane < 32 ? used[lane] : 0;
-  int32_t id[kFewSlots / 64];
+  int32_t id[kIds];
+  float wt[kIds];
 #pragma unroll
-  for (int i = 0; i < kFewSlots / 64; i++) id[i] = ids[64 * i + lane];
-  uint32_t bits = 0;
-  int at = -1, left = u;
-  while (++at < (q.E + 31) / 32) {
-    bits = __builtin_amdgcn_readlane(word, at);
-    if (left < __popc(bits)) break;
-    left -= __popc(bits);
+  for (int i = 0; i < kIds; i++) {
+    const int f = min(64 * i + lane, q.slots - 1);
+    id[i] = q.idx[f];
+    wt[i] = WEIGHT ? q.w[f] : 0.0f;  // of a masked slot: not used
   }
-  if (at == (q.E + 31) / 32) return r;
-  for (; left > 0; left--) bits &= bits - 1;
-  r.e = 32 * at + __ffs(bits) - 1;
+#pragma unroll
+  for (int i = 0; i < kIds; i++)
+    id[i] = 64 * i + lane < q.slots ? local_id(id[i], q.first, q.E) : -1;
+  if (q.E <= q.slots) {
+    r.e = u;
+  } else if (q.slots <= 64) {
+    uint64_t heads = __ballot(id[0] >= 0 && !(same_expert(id[0], q.E) & below(lane)));
+    if (u >= __popcll(heads)) return r;
+    for (int left = u; left > 0; left--) heads &= heads - 1;
+    r.e = __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)heads) - 1);
+  } else {
+    __shared__ uint32_t used[32];
+    if (tid < 32) used[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kIds; i++)
+      if (tid < 64 && id[i] >= 0) atomicOr(&used[id[i] >> 5], 1u << (id[i] & 31));
+    __syncthreads();
+    // the u-th set bit, word by word
+    const uint32_t word = lane < 32 ? used[lane] : 0;
+    uint32_t bits = 0;
+    int at = -1, left = u;
+    while (++at < (q.E + 31) / 32) {
+      bits = __builtin_amdgcn_readlane(word, at);
+      if (left < __popc(bits)) break;
+      left -= __popc(bits);
+    }
+    if (at == (q.E + 31) / 32) return r;
+    for (; left > 0; left--) bits &= bits - 1;
+    r.e = 32 * at + __ffs(bits) - 1;
+  }
   // its slots, without those whose token has an earlier one (one of the `back`
-  // bits before them); every wave writes, and then reads, the same list
+  // bits before them), whose weights go to that one; every wave writes, and then
+  // reads, the same list
+  if (WEIGHT)
+#pragma unroll
+    for (int i = 0; i < kIds; i++) ws[64 * i + lane] = id[i] == r.e ? wt[i] : 0.0f;
+  __builtin_amdgcn_wave_barrier();  // a wave's own LDS accesses stay in order
   uint64_t prev = 0;
 #pragma unroll
-  for (int i = 0; i < kFewSlots / 64; i++) {
+  for (int i = 0; i < kIds; i++) {
     const int f = 64 * i + lane, back = f % q.k;
     const uint64_t m = __ballot(id[i] == r.e);
     const uint64_t earlier =
@@ -261,16 +279,19 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
                      : (m & below(lane)) | (prev >> (64 - (back - lane)));
     const bool row = id[i] == r.e && !earlier;
     const uint64_t rows = __ballot(row);
-    if (row) list[r.n + __popcll(rows & below(lane))] = (uint16_t)f;
+    if (row) {
+      const int at = r.n + __popcll(rows & below(lane));
+      list[at] = (uint16_t)f;
+      if (WEIGHT) {
+        float sum = wt[i];
+        for (int g = f + 1; g < min(f - back + q.k, q.slots); g++) sum += ws[g];
+        wlist[at] = sum;
+      }
+    }
     r.n += __popcll(rows);
     prev = m;
   }
-  if (WEIGHT && tid < r.n) {
-    const int f = list[tid];
-    float sum = ws[f];
-    for (int g = f + 1; g < f / q.k * q.k + q.k; g++) sum += ids[g] == r.e ? ws[g] : 0.0f;
-    wlist[tid] = sum;
-  }
+  __builtin_amdgcn_wave_barrier();
   return r;
 }
 
