@@ -539,8 +539,8 @@ size_t moe_w4_decode_workspace_bytes(const moe_shape *shape);
 
 /* Few-token inference forward on 4-bit experts: out[t] = bf16(sum over the
  * slots of topk_w * (silu(x Wg) * (x Wu)) Wd, plus the shared expert), the
- * product of silu rounded to bf16 as the layer does, all other sums in fp32 in
- * a fixed order.  Arguments as moe_decode_fwd, with the experts in 4 bits;
+ * hidden rows rounded to bf16 once, their routing weight included, all sums in
+ * fp32 in a fixed order.  Arguments as moe_decode_fwd, with the experts in 4 bits;
  * shape->dtype MOE_BF16, T*k <= 4096, T*k*I and T times the shared I below
  * 2^30, H, I and the shared I multiples of 64 and of the group size.  A router
  * (first_expert 0) re-decides over the experts here; supplied routing may name

@@ -214,12 +214,13 @@ class MoeW4Experts(ctypes.Structure):
 
 
 def _p(t):
-    """Pointer of a torch tensor (or None -> NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    """Pointer of a torch tensor (or None -> NULL, or an int as it is)."""
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
 
 
 _current_stream = None
@@ -244,9 +245,11 @@ def _ck(rc: int, where: str):
         raise MoeError(rc, where)
 
 
-def _shape(shape) -> ctypes.Structure:
-    s = shape if isinstance(shape, ctypes.Structure) else shape.c()
-    return ctypes.byref(s)
+def _shape(shape):
+    try:
+        return ctypes.byref(shape._c)  # of the shapes that keep their struct
+    except AttributeError:
+        return ctypes.byref(shape if isinstance(shape, ctypes.Structure) else shape.c())
 
 
 def moe_workspace_bytes(shape) -> int:

@@ -9,12 +9,12 @@
 // No layout is made for up to 256 slots: each workgroup finds its expert's rows
 // itself, since a launch costs about 4 us here and the search about one.
 //
-// Bound by reading the used experts' codes and scales: about 6 us a kernel (launch,
-// search, the last workgroups) and then 5.5 to 6 TB/s, of 5.9 TB/s that a plain
-// read reaches.  MXFP4, 7168 x 2048, 8 of 48 experts, one token: gate_up 24.8 us
-// (125 MB), down 17.9 us (62 MB).  INT4 in groups of 64 with fp16 scales, 2048 x
-// 1408, 32 tokens over about 30 of 32 experts: 25.3 us (94 MB), 16.7 us (47 MB),
-// combine 4.6 us.
+// Bound by reading the used experts' codes and scales: some 3 us a kernel until
+// the first codes are there, then 6 to 7 TB/s until the workgroups end one by one.
+// MXFP4, 7168 x 2048, 8 of 48 experts, one token: gate_up 22.7 us (125 MB, which a
+// plain read takes 19.5 for), down 17.8 us (62 MB, 10.3).  INT4 in groups of 64
+// with fp16 scales, 2048 x 1408, 32 tokens over about 30 of 32 experts: 24.5 us
+// (94 MB, 15.0), 13.9 us (47 MB, 8.2), combine 4.
 #include <algorithm>
 
 #include "w4_device.h"
@@ -203,7 +203,7 @@ constexpr int kFewSlots = 256;  // slots that a workgroup looks through by itsel
 // itself: the expert's slots by ballots over the ids, four a lane.  With as many
 // slots as experts the u-th is expert u; with up to 64 slots the used experts are
 // counted by their first slots; else as bits in LDS (which costs two barriers:
-// 2.6 us until the rows are known at the 32 tokens above, FOUND without).
+// 2.8 us until the rows are known at the 32 tokens above, 2.4 without).
 // WEIGHT: the rows' weights too.
 template <bool PLAN, bool WEIGHT>
 __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, int u) {
@@ -494,9 +494,11 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
 }
 
 // More tokens: y[f] = act[f] Wd in fp32 at the places of the rows, 16 rows a
-// pass, kDownTiles tiles of one expert a workgroup: at the 32 tokens above 14.4
-// us with four tiles, 18.5 with two and 28 with one (the search for the rows is
-// the same for all).  Grid (tiles / kDownTiles, used experts [+ 1]).
+// pass, kDownTiles tiles of one expert a workgroup: at the 32 tokens above 13.9 us
+// with four tiles; before other steps 14.4, where two took 18.5 and one 28 (the
+// search for the rows is the same for all).  With three waves a SIMD a second,
+// mostly empty round of workgroups made it 16.5.  Grid (tiles / kDownTiles, used
+// experts [+ 1]).
 constexpr int kDownTiles = 4;
 
 template <bool PLAN>

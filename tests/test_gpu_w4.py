@@ -433,3 +433,64 @@ def test_captured_and_replayed_on_another_stream():
         step(eager, ref, lref)
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and torch.equal(lin_out, lref)
+
+
+@pytest.mark.parametrize("name", ["one-token", "planned", "heavy-expert", "share"])
+def test_each_way_of_the_layer_captured(name):
+    """One token, planned, staged and few-row layers in a graph, replayed with
+    new inputs, routings and a spoiled workspace between the replays."""
+    f = FORMATS[2]
+    shape, lins, x0, idx0, wt0, *_, first = layer_case(name, f, 7)
+    experts = m.W4Experts.of(*lins, first_expert=first)
+    dec, eager = m.W4Decoder(shape, experts), m.W4Decoder(shape, experts)
+    x, idx, wt = x0.cuda(), torch.from_numpy(idx0).cuda(), torch.from_numpy(wt0).cuda()
+    out = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        dec(x, topk_idx=idx, topk_w=wt, out=out)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dec(x, topk_idx=idx, topk_w=wt, out=out)
+    _, _, _, _, lo, hi, *_ = LAYERS[name]
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        x.copy_(bf16(rng.standard_normal(x0.shape)))
+        idx.copy_(torch.from_numpy(rng.integers(lo - 1, hi + 1, idx0.shape).astype(np.int32)))
+        wt.copy_(torch.from_numpy(rng.random(wt0.shape).astype(np.float32)))
+        dec.ws.fill_(seed)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager(x, topk_idx=idx, topk_w=wt))
+
+
+def test_two_layers_and_a_product_at_once():
+    """Decoders of the same experts on two streams of their own, and a product
+    on a third: the same as one after the other."""
+    f = FORMATS[0]
+    cases = [layer_case(n, f, 9) for n in ("few", "few")]
+    shape, lins = cases[0][0], cases[0][1]
+    experts = m.W4Experts.of(*lins)
+    decs = [m.W4Decoder(shape, experts) for _ in cases]
+    rng = np.random.default_rng(12)
+    xs = [bf16(rng.standard_normal((shape.tokens, shape.hidden))).cuda() for _ in cases]
+    ids = [torch.from_numpy(rng.integers(0, shape.experts, c[3].shape).astype(np.int32)).cuda()
+           for c in cases]
+    wts = [torch.from_numpy(c[4]).cuda() for c in cases]
+    rows = bf16(rng.standard_normal((7, shape.hidden))).cuda()
+    off = torch.arange(shape.experts + 1, dtype=torch.int32, device="cuda").clamp_(max=7)
+    want = [d(x, topk_idx=i, topk_w=w) for d, x, i, w in zip(decs, xs, ids, wts)]
+    want.append(lins[0](rows, off))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        got = []
+        for s, d, x, i, w in zip(streams, decs, xs, ids, wts):
+            with torch.cuda.stream(s):
+                got.append(d(x, topk_idx=i, topk_w=w))
+        with torch.cuda.stream(streams[2]):
+            got.append(lins[0](rows, off))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
