@@ -17,7 +17,7 @@ __device__ __forceinline__ Span span_of(const int32_t *offsets, int g, int rows)
 }
 
 // 16 rows a pass from memory; the waves of a workgroup split the contraction of
-// one tile.  Grid (output tiles, groups).
+// one tile.  Grid (output tiles, groups, passes that run side by side).
 template <class F, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
     W4Mat m, const uint16_t *x, long xstride, const int32_t *__restrict__ offsets, int rows,
@@ -27,7 +27,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4_linear_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Span sp = span_of(offsets, g, rows);
   const W4Row<F> mm[1] = {W4Row<F>(m, (size_t)g * m.nt + blockIdx.x)};
-  for (int r0 = sp.begin; r0 < sp.end; r0 += 16) {
+  for (int r0 = sp.begin + 16 * blockIdx.z; r0 < sp.end; r0 += 16 * gridDim.z) {
     const int nr = min(16, sp.end - r0);
     const RowPtr xr = {x + (r0 + min(w4_row_of_lane(), nr - 1)) * xstride};
     f32x4 acc[1][1];
@@ -91,21 +91,33 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
                          dim3(waves * 64), 0, s, m, x, xstride, offsets, rows, out, ostride);
     };
     constexpr int kBlock = kBlockWaves * kBlockGroups, kLong = kLongBlocks<F>;
+    const long tiles = (long)d.nt * d.groups;
+    auto passes = [&](int nb) { return std::min((avg + 16 * nb - 1) / (16 * nb), 65535); };
     auto rows_kernel = [&](auto one, auto two, int nb) {
-      const int passes = std::min((avg + 16 * nb - 1) / (16 * nb), 65535);  // grid z's bound
-      const bool wide = (long)d.nt * d.groups * passes >= 256 * 2 * kBlockWaves;
-      if (wide) go(two, 2 * kBlockWaves, kBlock, passes);
-      else go(one, kBlockWaves, kBlock, passes);
+      const bool wide = tiles * passes(nb) >= 256 * 2 * kBlockWaves;
+      if (wide) go(two, 2 * kBlockWaves, kBlock, passes(nb));
+      else go(one, kBlockWaves, kBlock, passes(nb));
     };
-    // staged rows pay from 9 rows on where there are 128 workgroups of them (16
-    // rows, 8192 x 8192 MXFP4: 14.2 against 19.0 us; 2048 outputs of 7168, 32
-    // workgroups: 16.6 against 11.8 us), and below that the split contraction;
-    // few tiles: 16 waves for each
-    if (avg > 32) rows_kernel(w4_linear_rows_kernel<F, 1, kLong>, w4_linear_rows_kernel<F, 2, kLong>, kLong);
-    else if (avg > 16) rows_kernel(w4_linear_rows_kernel<F, 1, 2>, w4_linear_rows_kernel<F, 2, 2>, 2);
-    else if (avg > 8 && (long)d.nt * d.groups >= 512) rows_kernel(w4_linear_rows_kernel<F, 1, 1>, w4_linear_rows_kernel<F, 2, 1>, 1);
-    else if ((long)d.nt * d.groups < 512) go(w4_linear_kernel<F, 16>, 1, 16, 1);
-    else go(w4_linear_kernel<F, 4>, 1, 4, 1);
+    // Rows staged through LDS, the more at a time the fewer reads of the weights,
+    // as long as the workgroups that are left fill the chip (64 rows, 8192 x 8192
+    // MXFP4: 32.4 us in 128 workgroups of 64 rows, 20.0 in 256 of 32; 32 rows: 19.5
+    // in 128 of 32, 14.5 in 256 of 16; 16 rows: 14.0 in 128 of 16, 19.0 from
+    // memory).  From memory up to 6 rows (8 rows: 13.4 us staged, 14.6; 5: 13.5,
+    // 12.2), INT4, whose sums are scaled row by row, up to 8 (8 rows: 17.0, 14.4) ...
+    auto blocks = [&](int nb) { return tiles * passes(nb) / kBlockWaves; };
+    if (avg > 32 && blocks(kLong) >= 256)
+      rows_kernel(w4_linear_rows_kernel<F, 1, kLong>, w4_linear_rows_kernel<F, 2, kLong>, kLong);
+    else if (avg > 16 && blocks(2) >= 192)
+      rows_kernel(w4_linear_rows_kernel<F, 1, 2>, w4_linear_rows_kernel<F, 2, 2>, 2);
+    else if (avg > (F::kGrouped ? 8 : 6) && blocks(1) >= 96)
+      rows_kernel(w4_linear_rows_kernel<F, 1, 1>, w4_linear_rows_kernel<F, 2, 1>, 1);
+    // ... and where tiles are few (32 rows, 512 outputs of 8192: 10.2 us, staged in 8
+    // workgroups 17.9): then more waves split the contraction of one, up to what
+    // the CUs hold at once (48 rows, 2048 of 7168: 384 workgroups, 16 waves 19.2 us,
+    // 8 waves 18.4)
+    else if (tiles * passes(1) <= 256) go(w4_linear_kernel<F, 16>, 1, 16, passes(1));
+    else if (tiles * passes(1) <= 512) go(w4_linear_kernel<F, 8>, 1, 8, passes(1));
+    else go(w4_linear_kernel<F, 4>, 1, 4, passes(1));
   });
 }
 

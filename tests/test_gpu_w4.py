@@ -143,6 +143,41 @@ def test_many_outputs(f, rows):
     within("many outputs", lin(x.cuda()), y, wo.rounded(y, bound))
 
 
+@pytest.mark.parametrize("f", FORMATS, ids=IDS)
+@pytest.mark.parametrize("rows,n", [(7, 6200), (8, 8300), (12, 6200), (12, 33000), (20, 4100),
+                                    (20, 12300), (20, 33000), (24, 500), (40, 2000), (40, 2100),
+                                    (70, 8200), (70, 33000)])
+def test_every_choice_of_rows_and_tiles(f, rows, n):
+    """Staged rows of every block count, one and two tiles a wave, and split
+    contractions of 4, 8 and 16 waves with passes side by side."""
+    k = 256 + f[1]
+    rng = np.random.default_rng([rows, n])
+    lin, codes, scales, zeros = make(rng, 1, n, k, f)
+    x = bf16(rng.standard_normal((rows, k)))
+    note(f"w4 choice {f} rows={rows} n={n}")
+    w, sabs = wo.values(codes, scales, zeros, f[0], f[1])
+    y, bound = wo.product(f64(x), w[0], sabs[0], f[0], f[1])
+    within("choice", lin(x.cuda()), y, wo.rounded(y, bound))
+
+
+@pytest.mark.parametrize("f", [FORMATS[0], FORMATS[5]], ids=[IDS[0], IDS[5]])
+@pytest.mark.parametrize("n", [100, 1500, 6200])
+def test_groups_longer_than_the_average(f, n):
+    """Passes side by side are counted from the average: a longer group's
+    workgroups walk on, an empty one's have nothing to do."""
+    groups, k, off = 3, 256, [0, 101, 101, 120]
+    rng = np.random.default_rng(n)
+    lin, codes, scales, zeros = make(rng, groups, n, k, f)
+    x = bf16(rng.standard_normal((off[-1], k)))
+    note(f"w4 long group {f} n={n}")
+    out = lin(x.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda"))
+    w, sabs = wo.values(codes, scales, zeros, f[0], f[1])
+    for g in range(groups):
+        rows = slice(off[g], off[g + 1])
+        y, bound = wo.product(f64(x[rows]), w[g], sabs[g], f[0], f[1])
+        within(f"group {g}", out[rows], y, wo.rounded(y, bound)) if off[g + 1] > off[g] else None
+
+
 def test_more_passes_than_a_grid_dimension():
     """More than 65535 passes of 32 rows (groups of 32 of INT4), the same 2048
     rows again and again: every one of their outputs is the same."""
