@@ -380,10 +380,10 @@ int moe_decode_fwd(const moe_shape *shape, const uint16_t *x,
  * Limits: 0 <= tokens <= 2^24, 1 <= top_k <= 16, 1 <= experts <= 1024,
  * 1 <= width <= 2^20, align <= 1024, strides of at least width and at most
  * 2^32 values.  Row buffers need their type's alignment only and must not
- * overlap the outputs.  No entry point reads a host copy of any of these
- * arrays, so all of them can be captured into a graph (with a workspace of
- * its own where calls may overlap).  counts, offsets and inv_perm are as
- * moe_sort_layout writes them and are not checked. */
+ * overlap the outputs (the same pointer is refused).  No entry point reads a
+ * host copy of any of these arrays, so all of them can be captured into a graph
+ * (with a workspace of its own where calls may overlap).  counts, offsets and
+ * inv_perm are as moe_sort_layout writes them and are not checked. */
 enum { MOE_ROW_BF16 = 0, MOE_ROW_F16 = 1, MOE_ROW_F32 = 2 };
 
 typedef struct moe_sort_shape {

@@ -73,7 +73,8 @@ int moe_sort_rows(const moe_sort_shape *shape, const void *x, const int32_t *cou
   SortDims d;
   const int rc = check_sort(shape, &d);
   if (rc) return rc;
-  if (!counts || !offsets || (d.R && (!x || !inv_perm || !x_sorted))) return MOE_ERR_INVALID_ARG;
+  if (!counts || !offsets || (d.R && (!x || !inv_perm || !x_sorted || x == x_sorted)))
+    return MOE_ERR_INVALID_ARG;
   launch_sort_rows(d, x, counts, offsets, inv_perm, x_sorted, (hipStream_t)stream);
   return status();
 }
@@ -86,7 +87,7 @@ int moe_sort_fwd(const moe_sort_shape *shape, const void *x, const int32_t *topk
   if (rc) return rc;
   rc = check_layout(d, topk_idx, counts, offsets, perm, inv_perm, ws, ws_bytes);
   if (rc) return rc;
-  if (d.R && (!x || !x_sorted)) return MOE_ERR_INVALID_ARG;
+  if (d.R && (!x || !x_sorted || x == x_sorted)) return MOE_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
   if (!launch_sort_small(d, x, topk_idx, counts, offsets, perm, inv_perm, x_sorted, s)) {
     launch_sort_layout(d, topk_idx, counts, offsets, perm, inv_perm, (int32_t *)ws, s);
@@ -105,7 +106,8 @@ int moe_unsort_fwd(const moe_sort_shape *shape, const void *y, const float *topk
   SortDims d;
   const int rc = check_sort(shape, &d);
   if (rc) return rc;
-  if (d.R && (!y || !inv_perm || !out)) return MOE_ERR_INVALID_ARG;
+  // the last 16 bytes of a row may be summed twice: not in place
+  if (d.R && (!y || !inv_perm || !out || out == y || out == add)) return MOE_ERR_INVALID_ARG;
   launch_unsort(d, y, topk_w, inv_perm, add, out, (hipStream_t)stream);
   return status();
 }
@@ -116,7 +118,8 @@ int moe_unsort_bwd(const moe_sort_shape *shape, const void *dout, const void *y,
   SortDims d;
   const int rc = check_sort(shape, &d);
   if (rc) return rc;
-  if (!counts || !offsets || (d.R && (!dout || !topk_w || !inv_perm || !dy || (dtopk_w && !y))))
+  if (!counts || !offsets ||
+      (d.R && (!dout || !topk_w || !inv_perm || !dy || (dtopk_w && !y) || dy == dout || dy == y)))
     return MOE_ERR_INVALID_ARG;
   launch_unsort_bwd(d, dout, y, topk_w, counts, offsets, inv_perm, dy, dtopk_w,
                     (hipStream_t)stream);

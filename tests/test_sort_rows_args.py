@@ -83,6 +83,18 @@ def test_missing_pointers_and_workspace(lib):
         assert lib.moe_sort_rows(s, *a, None) == _lib.MOE_ERR_INVALID_ARG
 
 
+def test_no_call_in_place(lib):
+    s, bad = ctypes.byref(OK.c()), _lib.MOE_ERR_INVALID_ARG
+    p, q, r = FAKE, FAKE + (1 << 30), FAKE + (1 << 31)
+    assert lib.moe_sort_rows(s, p, q, q, q, p, None) == bad
+    assert lib.moe_sort_fwd(s, p, q, q, q, q, q, p, q, 1 << 40, None) == bad
+    assert lib.moe_sort_bwd(s, p, q, p, None) == bad
+    assert lib.moe_unsort_fwd(s, p, q, q, None, p, None) == bad
+    assert lib.moe_unsort_fwd(s, r, q, q, p, p, None) == bad
+    assert lib.moe_unsort_bwd(s, p, r, q, q, q, q, p, q, None) == bad
+    assert lib.moe_unsort_bwd(s, r, p, q, q, q, q, p, q, None) == bad
+
+
 def test_sizes(lib):
     assert m.moe_sort_max_rows(OK) == 64
     assert m.moe_sort_max_rows(dataclasses.replace(OK, align=16)) == 64 + 8 * 15
