@@ -646,16 +646,18 @@ int sort_chunk(long R) {
   return (int)std::max<long>(kSortChunk, (c + 1023) / 1024 * 1024);
 }
 
-long sort_workspace_words(const SortDims &d) {
-  const int chunk = sort_chunk(d.R);
-  return (d.R + chunk - 1) / chunk * d.E;
+// Histograms of one layout.  No rows: one empty one, so that counts, offsets and
+// perm are written.
+int sort_chunks(long R) {
+  const int chunk = sort_chunk(R);
+  return (int)std::max<long>(1, (R + chunk - 1) / chunk);
 }
+
+long sort_workspace_words(const SortDims &d) { return (long)sort_chunks(d.R) * d.E; }
 
 void launch_sort_layout(const SortDims &d, const int32_t *idx, int32_t *counts, int32_t *offsets,
                         int32_t *perm, int32_t *inv, int32_t *ws, hipStream_t s) {
-  const int chunk = sort_chunk(d.R), E = d.E;
-  // no rows: one empty chunk, so that counts, offsets and perm are written
-  const int n = (int)std::max<long>(1, (d.R + chunk - 1) / chunk);
+  const int chunk = sort_chunk(d.R), n = sort_chunks(d.R), E = d.E;
   hipLaunchKernelGGL(sort_count_kernel, dim3(n), dim3(1024), E * sizeof(int32_t), s, idx, (int)d.R,
                      d.first, E, chunk, ws, perm, (int)d.cap);
   // more experts: fewer waves' counts, which all lie in 64 KB of LDS
