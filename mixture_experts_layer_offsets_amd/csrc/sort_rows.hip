@@ -24,11 +24,14 @@
 #include <algorithm>
 
 #include "common.h"
+#include "sort_grid.h"
 #include "sort_rows.h"
 
 namespace moe {
 
 namespace {
+
+inline dim3 to_dim3(const GridDims &g) { return dim3(g.x, g.y, g.z); }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4u __attribute__((ext_vector_type(4), aligned(2)));
@@ -36,8 +39,6 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSortMaxK = 16;   // top-k bound of the library
-constexpr int kRowBlock = 64;   // one wave per workgroup for the gathers (see combine_kernel)
-constexpr int kPadSplit = 8;    // workgroups that share one expert's padding rows
 // One-launch sort: slots it takes (512: 7.5 us, layout and rows apart 12.8; 1024:
 // 13.7 and 13.5), slots if aligned, where every workgroup makes the layout (256 of
 // 256 experts to 16 rows: 18.9 and 19.1; 512: 24.3 and 19.5), rows of the sorted
@@ -263,36 +264,9 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(
 // ---------------------------------------------------------------------------
 // Rows.
 
-// How a launch maps lanes to rows: 2^lsh lanes share a token (all 64 when its
-// row has 64 chunks or more, then grid x walks the row), 64 >> lsh tokens a
-// wave.  Grid y and z count the workgroups that differ in their tokens:
-// `token_blocks` of them hold tokens, the ones behind them (E x kPadSplit) zero
-// the padding rows.  The row's chunks are the fastest index, so that a row is
-// written at one time: with them as the slowest index the sort of 65536 rows of
-// 7168 bf16 took 232 us instead of 224, the backward sort of 8192 rows 24.8 us
-// instead of 20.4, and the weighted return of 32768 kept rows 55 instead of 48.
-struct RowGrid {
-  int lsh, token_blocks;
-  unsigned x;
-  dim3 grid(long blocks) const {
-    const long y = std::min<long>(blocks, 65535);
-    return dim3(x, (unsigned)y, (unsigned)((blocks + y - 1) / y));
-  }
-};
 __device__ __forceinline__ int row_block() { return blockIdx.z * gridDim.y + blockIdx.y; }
 __device__ __forceinline__ long row_chunk(int lsh) {
   return ((long)blockIdx.x << 6) + (threadIdx.x & ((1 << lsh) - 1));
-}
-
-RowGrid row_grid(int T, long row_bytes) {
-  const long nc = (row_bytes + 15) / 16;
-  RowGrid g;
-  g.lsh = 0;
-  while (g.lsh < 6 && (1L << g.lsh) < nc) g.lsh++;
-  const int per = 64 >> g.lsh;
-  g.token_blocks = (T + per - 1) / per;
-  g.x = (unsigned)((nc + 63) >> 6);
-  return g;
 }
 
 // Zeroes the padding rows [offsets[e] + counts[e], offsets[e + 1]) of one
@@ -518,22 +492,24 @@ __global__ __launch_bounds__(kRowBlock) void unsort_kernel(
 // token: four for rows of more than 128 chunks (one token a workgroup), else
 // one (four tokens a workgroup).
 template <class E, int KMAX, bool DW, int WPT>
-__global__ __launch_bounds__(256) void unsort_bwd_kernel(
+__global__ __launch_bounds__(kBwdBlock) void unsort_bwd_kernel(
     const char *__restrict__ dout, const char *__restrict__ y, const float *__restrict__ w,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets,
     const int32_t *__restrict__ inv, char *__restrict__ dy, float *__restrict__ dw, int T, int k,
-    long RB, long tstride, long rstride, int token_blocks) {
+    long RB, long tstride, long rstride, int token_blocks, int pad_blocks) {
   __shared__ float red[KMAX][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if ((int)blockIdx.x >= token_blocks) {
-    const int p = blockIdx.x - token_blocks, e = p / kPadSplit;
+  const int block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (block >= token_blocks) {
+    const int p = block - token_blocks, e = p / kPadSplit;
+    if (p >= pad_blocks) return;  // of the last, partly empty row of the grid
     const int end = offsets[e + 1];
     for (int r = offsets[e] + counts[e] + p % kPadSplit; r < end; r += kPadSplit)
       for (long c = tid; c * 16 < RB; c += 256)
         st16(dy + r * rstride + min(c * 16, RB - 16), (u32x4){0, 0, 0, 0});
     return;
   }
-  const int t = WPT == 4 ? blockIdx.x : blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wave);
+  const int t = WPT == 4 ? block : block * 4 + __builtin_amdgcn_readfirstlane(wave);
   const bool live = t < T;
   int row[KMAX];
   float wt[KMAX], part[KMAX];
@@ -700,8 +676,9 @@ void launch_sort_rows(const SortDims &d, const void *x, const int32_t *counts,
   if (d.align <= 1) offsets = nullptr;  // packed segments have no padding rows
   if (RB < 16) return launch_narrow(NARROW_SORT, d, x, nullptr, nullptr, counts, offsets, inv, xs,
                                     nullptr, s);
-  const RowGrid g = row_grid((int)d.T, RB);
-  const dim3 grid = g.grid(g.token_blocks + (offsets ? (long)d.E * kPadSplit : 0)), b(kRowBlock);
+  const RowGrid g = row_grid(d.T, RB);
+  const dim3 grid = to_dim3(g.dims(g.token_blocks + (offsets ? (long)d.E * kPadSplit : 0)));
+  const dim3 b(kRowBlock);
   const long xst = d.tstride * d.esize, rst = d.rstride * d.esize;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, b, 0, s, (const char *)x, inv, counts, offsets, (char *)xs,
@@ -737,10 +714,10 @@ template <class E, int KMAX, bool WEIGHT, bool ADD>
 void go_unsort(const SortDims &d, const void *y, const float *w, const int32_t *inv,
                const void *add, void *out, hipStream_t s) {
   const long RB = (long)d.D * d.esize;
-  const RowGrid g = row_grid((int)d.T, RB);
+  const RowGrid g = row_grid(d.T, RB);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, g.grid(g.token_blocks), dim3(kRowBlock), 0, s, (const char *)y, w,
-                       inv, (const char *)add, (char *)out, (int)d.T, d.k, RB, d.tstride * d.esize,
+    hipLaunchKernelGGL(kernel, to_dim3(g.dims(g.token_blocks)), dim3(kRowBlock), 0, s,
+                       (const char *)y, w, inv, (const char *)add, (char *)out, (int)d.T, d.k, RB, d.tstride * d.esize,
                        d.rstride * d.esize, g);
   };
   if (g.lsh == 6) go(unsort_kernel<E, KMAX, WEIGHT, ADD, true>);
@@ -768,18 +745,15 @@ void go_unsort_bwd(const SortDims &d, const void *dout, const void *y, const flo
                    const int32_t *counts, const int32_t *offsets, const int32_t *inv, void *dy,
                    float *dw, hipStream_t s) {
   const long RB = (long)d.D * d.esize;
-  const bool wide = RB > 128 * 16;
-  const int tb = wide ? (int)d.T : (int)((d.T + 3) / 4);
-  const dim3 grid(tb + (offsets ? d.E * kPadSplit : 0)), b(256);
-  const long ts = d.tstride * d.esize, rs = d.rstride * d.esize;
-  if (wide)
-    hipLaunchKernelGGL((unsort_bwd_kernel<E, KMAX, DW, 4>), grid, b, 0, s, (const char *)dout,
+  const BwdGrid g = bwd_grid(d.T, RB);
+  const int pads = offsets ? d.E * kPadSplit : 0;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, to_dim3(g.dims(pads)), dim3(kBwdBlock), 0, s, (const char *)dout,
                        (const char *)y, w, counts, offsets, inv, (char *)dy, dw, (int)d.T, d.k, RB,
-                       ts, rs, tb);
-  else
-    hipLaunchKernelGGL((unsort_bwd_kernel<E, KMAX, DW, 1>), grid, b, 0, s, (const char *)dout,
-                       (const char *)y, w, counts, offsets, inv, (char *)dy, dw, (int)d.T, d.k, RB,
-                       ts, rs, tb);
+                       d.tstride * d.esize, d.rstride * d.esize, g.token_blocks, pads);
+  };
+  if (g.wide) go(unsort_bwd_kernel<E, KMAX, DW, 4>);
+  else go(unsort_bwd_kernel<E, KMAX, DW, 1>);
 }
 
 template <class E>

@@ -38,3 +38,40 @@ def test_an_empty_batch_stays_in_its_workspace(experts, align):
         call(counts, offsets, buf[:need])
         assert torch.all(counts == 0) and torch.all(offsets == 0)
         assert torch.all(buf[need:] == 0x5A)
+
+
+@pytest.mark.parametrize("T,D", [(65530, 1032), (70000, 1032), (263000, 24)])
+@pytest.mark.parametrize("align", [1, 8])
+def test_more_workgroups_than_a_grid_dimension(T, D, align):
+    """Tokens enough that the workgroups of one call fill more than one row of
+    the grid: rows, padding and gradients as by their definitions.  Copies and
+    single products are exact; dw is a sum of D products in fp32."""
+    k, E = 2, 5
+    shape = m.SortShape(T, E, k, D, align=align)
+    note(f"grid rows: {shape}")
+    g = torch.Generator(device="cuda").manual_seed(T + D + align)
+    bf = torch.bfloat16
+    x = torch.randn((T, D), generator=g, device="cuda").to(bf)
+    dout = torch.randn((T, D), generator=g, device="cuda").to(bf)
+    idx = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((T, k), generator=g, device="cuda")
+    op = m.TokenSort(shape)
+    xs = op.sort(x, idx, out=op.sorted_rows().fill_(7))
+    end = int(op.offsets[-1])
+    perm, inv = op.perm.long(), op.inv_perm.long()
+    live = perm[:end] >= 0
+    f = perm[:end].clamp(min=0)
+    assert torch.equal(live.sum(), (idx >= 0).sum())
+    assert torch.equal(xs[:end], torch.where(live[:, None], x[f // k], 0))
+    dy, dw = op.unsort_backward(dout, xs, w, dy=op.sorted_rows().fill_(7))
+    want = (dout[f // k].float() * w.reshape(-1)[f][:, None]).to(bf)
+    assert torch.equal(dy[:end], torch.where(live[:, None], want, 0))
+    assert torch.all(xs[end:] == 7) and torch.all(dy[end:] == 7)
+    # a kept slot's row is its token's, so dw = <dout, x>
+    dot, size = (torch.where(inv >= 0, v[:, None], 0.0) for v in
+                 ((dout.double() * x.double()).sum(1), (dout.double() * x.double()).abs().sum(1)))
+    assert torch.all((dw.double() - dot).abs() <= D * 2.0 ** -24 * size)
+    out = op.unsort(xs, w)
+    ws = torch.where(inv >= 0, w.double(), 0.0).sum(1, keepdim=True)
+    ref = x.double() * ws
+    assert torch.all((out.double() - ref).abs() <= ref.abs() * (2.0 ** -8 + (k + 2) * 2.0 ** -23))
