@@ -15,8 +15,10 @@ class TokenSort:
 
     ``sort`` writes the layout (``counts``, ``offsets``, ``perm``,
     ``inv_perm``) into buffers of this object and returns the sorted rows;
-    ``sort_backward``, ``unsort`` and ``unsort_backward`` use that layout.
-    Every call enqueues on the current stream; the buffers are reused by the
+    ``sort_again``, ``sort_backward``, ``unsort`` and ``unsort_backward`` use
+    that layout, and raise ValueError on an object that has not sorted yet (a
+    captured ``sort`` writes its layout when the graph is replayed).  Every
+    call enqueues on the current stream; the buffers are reused by the
     next ``sort``, so calls on several streams need one object each, and so
     do graphs that may run at the same time.  Row tensors take the shape's
     type (bf16 also as int16 bit patterns) and its strides; a tensor that
@@ -38,6 +40,7 @@ class TokenSort:
         self.inv_perm = torch.empty((shape.tokens, shape.top_k), **i32)
         self.ws = torch.empty(_lib.moe_sort_workspace_bytes(shape), dtype=torch.uint8,
                               device=self.device)
+        self._has_layout = False  # until the first sort the layout is whatever lay in memory
 
     # -- buffers
     def token_rows(self) -> torch.Tensor:
@@ -78,6 +81,10 @@ class TokenSort:
         self._check(name, t, (self.max_rows, s.width), _ROW_DTYPES[s.row_type],
                     s.row_stride or s.width)
 
+    def _layout(self):
+        if not self._has_layout:
+            raise ValueError("no layout yet: sort first")
+
     def _slots(self, name, t, dtype):
         self._check(name, t, (self.shape.tokens, self.shape.top_k), (dtype,))
 
@@ -91,6 +98,7 @@ class TokenSort:
         with torch.cuda.device(self.device):
             _lib.moe_sort_fwd(self.shape, x, topk_idx, self.counts, self.offsets, self.perm,
                               self.inv_perm, out, self.ws)
+        self._has_layout = True
         return out
 
     def sort_again(self, x, out=None):
@@ -98,6 +106,7 @@ class TokenSort:
         out = self.sorted_rows() if out is None else out
         self._tokens("x", x)
         self._sorted("out", out)
+        self._layout()
         with torch.cuda.device(self.device):
             _lib.moe_sort_rows(self.shape, x, self.counts, self.offsets, self.inv_perm, out)
         return out
@@ -107,6 +116,7 @@ class TokenSort:
         out = self.token_rows() if out is None else out
         self._sorted("dx_sorted", dx_sorted)
         self._tokens("out", out)
+        self._layout()
         with torch.cuda.device(self.device):
             _lib.moe_sort_bwd(self.shape, dx_sorted, self.inv_perm, out)
         return out
@@ -120,6 +130,7 @@ class TokenSort:
         if add is not None:
             self._tokens("add", add)
         self._tokens("out", out)
+        self._layout()
         with torch.cuda.device(self.device):
             _lib.moe_unsort_fwd(self.shape, y, topk_w, self.inv_perm, add, out)
         return out
@@ -135,6 +146,7 @@ class TokenSort:
         self._slots("topk_w", topk_w, torch.float32)
         self._sorted("dy", dy)
         self._slots("dtopk_w", dtopk_w, torch.float32)
+        self._layout()
         with torch.cuda.device(self.device):
             _lib.moe_unsort_bwd(self.shape, dout, y, topk_w, self.counts, self.offsets,
                                 self.inv_perm, dy, dtopk_w)
