@@ -496,7 +496,10 @@ int moe_w4_pack(const moe_w4_shape *shape, const uint8_t *codes,
  * MOE_MXFP8_W4.  INT4 without zero
  * points: s = max|w| / 7, q = rint(w / s) + 8; with: s = (max(w, 0) -
  * min(w, 0)) / 15, z = rint(-min(w, 0) / s), q = rint(w / s) + z, clamped to
- * 0..15; s rounded to its type first; all steps in fp32. */
+ * 0..15; s rounded to its type first; all steps in fp32.  Any finite group
+ * stands for finite values: an s past its type's largest value is held there (z
+ * is then taken from s before that), so that codes saturate, and a code whose
+ * value would pass fp32's range is one step nearer to zero. */
 int moe_w4_quantize(const moe_w4_shape *shape, const uint16_t *w, void *packed,
                     void *stream);
 

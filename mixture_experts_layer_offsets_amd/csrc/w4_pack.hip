@@ -99,13 +99,23 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4Dims d, const uint16
     sx = amax > 0.0f ? min(max(floor_log2(amax) - 2, -127), 127) : -127;
     ps[to] = in ? (uint8_t)(sx + 127) : 127;
   } else {
-    s = d.zeros ? (hi - lo) / 15.0f : fmaxf(-lo, hi) / 7.0f;
-    const uint16_t bits = d.f16_scales ? __builtin_bit_cast(uint16_t, (_Float16)s)
-                                       : __builtin_bit_cast(uint16_t, (__bf16)s);
+    const float span = hi - lo;  // past fp32's range only where both ends are near bf16's
+    float step = fmaxf(-lo, hi) / 7.0f;
+    if (d.zeros) step = isinf(span) ? hi / 15.0f - lo / 15.0f : span / 15.0f;
+    uint32_t bits = d.f16_scales ? __builtin_bit_cast(uint16_t, (_Float16)step)
+                                 : __builtin_bit_cast(uint16_t, (__bf16)step);
     s = scale_value(bits, d.f16_scales ? ~0u : 0u);
+    float for_zero = s;
+    // a step past fp16's largest value is held there, and the codes saturate (an
+    // infinite weight's step stays infinite)
+    if (isinf(s) && !isinf(step)) {
+      bits = 0x7BFF;
+      s = scale_value(bits, ~0u);
+      for_zero = step;
+    }
     ((uint16_t *)ps)[to] = in ? bits : 0;
     if (d.zeros) {
-      z = s > 0.0f ? (int)fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 0;
+      z = s > 0.0f ? (int)fminf(fmaxf(rintf(-lo / for_zero), 0.0f), 15.0f) : 0;
       (ps + d.scale_bytes)[to] = in ? z : 0;
     }
   }
@@ -115,7 +125,11 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4Dims d, const uint16
       const float f = bf16_to_f32(src[(size_t)(q0 + q) * d.n]);
       uint32_t c;
       if (d.fmt == kW4Mx) c = e2m1_code(f, sx);
-      else c = s > 0.0f ? (uint32_t)fminf(fmaxf(rintf(f / s) + (float)z, 0.0f), 15.0f) : (uint32_t)z;
+      else {
+        c = s > 0.0f ? (uint32_t)fminf(fmaxf(rintf(f / s) + (float)z, 0.0f), 15.0f) : (uint32_t)z;
+        // rounding outwards next to bf16's largest value: one step back into fp32's range
+        if (isinf(s * (float)((int)c - z))) c += (int)c < z ? 1 : -1;
+      }
       v |= place_code(c, code_bit(d.fmt, q));
     }
     const int k0 = kg * d.group + q0, in128 = k0 & 127;
