@@ -32,19 +32,32 @@ class W4Linear:
     """Packed 4-bit matrices [groups][k][n] and their products with few rows.
 
     ``W4Linear.quantize`` takes bf16 weights [groups][k][n] (products x*W),
-    ``W4Linear.pack`` ready-made codes, scales and zero points.  Calls enqueue
-    on the current stream.
+    ``W4Linear.pack`` ready-made codes, scales and zero points; weights that are
+    packed already come as a uint8 tensor of moe_w4_bytes (checked at the first
+    call).  Calls enqueue on the current stream.
     """
 
     def __init__(self, shape: W4Shape, packed: torch.Tensor):
         self.shape, self.packed = shape, packed
+        self._fits = False
+
+    def _weights(self):
+        """The packed tensor: the kernels read all that the shape says of it."""
+        if not self._fits:
+            _check("packed", self.packed, (self._bytes(self.shape),), (torch.uint8,))
+            self._fits = True
+        return self.packed
 
     @staticmethod
-    def _buffer(shape, device):
+    def _bytes(shape):
         n = _lib.moe_w4_bytes(shape)
         if n == 0:
             raise ValueError(f"shape outside the limits of moe_w4_shape: {shape}")
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        return n
+
+    @classmethod
+    def _buffer(cls, shape, device):
+        return torch.empty(cls._bytes(shape), dtype=torch.uint8, device=device)
 
     @classmethod
     def quantize(cls, w, format=_lib.MOE_W4_MXFP4, group_size=32, scale_type=_lib.MOE_SCALE_BF16,
@@ -75,17 +88,18 @@ class W4Linear:
 
     def values(self):
         """The weights [groups][k][n] that the codes stand for, in fp32."""
-        s = self.shape
-        w = torch.empty((s.groups, s.k, s.n), dtype=torch.float32, device=self.packed.device)
-        with torch.cuda.device(self.packed.device):
-            _lib.moe_w4_unpack(s, self.packed, w)
+        s, packed = self.shape, self._weights()
+        w = torch.empty((s.groups, s.k, s.n), dtype=torch.float32, device=packed.device)
+        with torch.cuda.device(packed.device):
+            _lib.moe_w4_unpack(s, packed, w)
         return w
 
     def __call__(self, x, offsets=None, out=None):
         """x [rows][k] bf16 -> [rows][n] bf16; with ``offsets`` [groups + 1]
         int32 the rows of group g are [offsets[g], offsets[g + 1]), and rows
         in no group are left as they are (zeros in a new ``out``)."""
-        s, dev = self.shape, self.packed.device
+        s, packed = self.shape, self._weights()
+        dev = packed.device
         if x.dim() != 2:
             raise ValueError(f"x: {x.dim()} dimensions, expected [rows][k]")
         _check("x", x, (x.shape[0], s.k), _BF16, dev, rows=True)
@@ -98,7 +112,7 @@ class W4Linear:
             out = make((x.shape[0], s.n), dtype=x.dtype, device=dev)
         _check("out", out, (x.shape[0], s.n), _BF16, dev, rows=True)
         with torch.cuda.device(dev):
-            _lib.moe_w4_linear(s, x, offsets, self.packed, out)
+            _lib.moe_w4_linear(s, x, offsets, packed, out)
         return out
 
 
