@@ -125,6 +125,7 @@ class W4Experts:
                  format=_lib.MOE_W4_MXFP4, group_size=32, scale_type=_lib.MOE_SCALE_BF16, zeros=0,
                  first_expert=0):
         self.tensors = (gate, up, down, shared_gate, shared_up, shared_down)
+        self.shapes = None  # of the matrices, where they are known
         self._c = _lib.MoeW4Experts(format, group_size, scale_type, zeros, first_expert,
                                     *(None if t is None else t.data_ptr() for t in self.tensors))
 
@@ -138,10 +139,11 @@ class W4Experts:
         if len(kinds) != 1:
             raise ValueError(f"matrices of different formats: {sorted(kinds)}")
         fmt, group, scale, zeros = kinds.pop()
-        return cls(*(None if m is None else m.packed for m in (gate, up, down, shared_gate,
-                                                               shared_up, shared_down)),
-                   format=fmt, group_size=group, scale_type=scale, zeros=zeros,
-                   first_expert=first_expert)
+        mats = (gate, up, down, shared_gate, shared_up, shared_down)
+        experts = cls(*(None if m is None else m.packed for m in mats), format=fmt,
+                      group_size=group, scale_type=scale, zeros=zeros, first_expert=first_expert)
+        experts.shapes = tuple(None if m is None else m.shape for m in mats)
+        return experts
 
     def c(self):
         return self._c
@@ -159,21 +161,23 @@ class W4Decoder:
         s, e = shape, experts.c()
 
         def need(groups, nn, kk):
-            b = _lib.moe_w4_bytes(W4Shape(groups, nn, kk, e.format, e.group_size, e.scale_type,
-                                          e.zeros))
-            if b == 0:
-                raise ValueError("experts: format or group size does not fit the shape")
-            return b
-        sizes = [need(s.experts, s.inter, s.hidden)] * 2 + [need(s.experts, s.hidden, s.inter)]
+            return W4Shape(groups, nn, kk, e.format, e.group_size, e.scale_type, e.zeros)
+        wants = [need(s.experts, s.inter, s.hidden)] * 2 + [need(s.experts, s.hidden, s.inter)]
         if s.shared_inter:
-            sizes += [need(1, s.shared_inter, s.hidden)] * 2 + [need(1, s.hidden, s.shared_inter)]
+            wants += [need(1, s.shared_inter, s.hidden)] * 2 + [need(1, s.hidden, s.shared_inter)]
         else:
-            sizes += [None] * 3
-        for t, want in zip(experts.tensors, sizes):
+            wants += [None] * 3
+        for t, has, want in zip(experts.tensors, experts.shapes or wants, wants):
             if (t is None) != (want is None):
                 raise ValueError("experts: shared matrices given exactly when the shape has them")
-            if t is not None:
-                _check("experts", t, (want,), (torch.uint8,), self.device)
+            if t is None:
+                continue
+            size = _lib.moe_w4_bytes(want)
+            if size == 0:
+                raise ValueError("experts: format or group size does not fit the shape")
+            if has != want:
+                raise ValueError(f"experts: {has}, expected {want}")
+            _check("experts", t, (size,), (torch.uint8,), self.device)
         self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def __call__(self, x, w_router=None, bias=None, topk_idx=None, topk_w=None, out=None):

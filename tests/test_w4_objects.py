@@ -52,3 +52,23 @@ def test_packed_weights_that_fit_are_taken(monkeypatch):
     x, off = torch.zeros((3, 256), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
     assert lin(x, off).shape == (3, 48) and lin.values().shape == (2, 256, 48)
     assert calls == ["moe_w4_linear", "moe_w4_unpack"]
+
+
+def test_experts_of_the_wrong_orientation_or_number_are_refused():
+    """Matrices [k][n] and [n][k], and 2 groups of n or one of 2n, take the same
+    bytes: the layer compares the shapes that they were packed with."""
+    layer = m.Shape(4, 256, 8, 2, 128, 128)
+    mats = {s: m.W4Linear(s, packed(s)) for s in (
+        m.W4Shape(8, 128, 256), m.W4Shape(8, 256, 128), m.W4Shape(4, 256, 256), m.W4Shape(4, 512, 128),
+        m.W4Shape(1, 128, 256), m.W4Shape(1, 256, 128))}
+    up, down, up4, down4, up1, down1 = mats.values()
+    m.W4Decoder(layer, m.W4Experts.of(up, up, down, up1, up1, down1))
+    for wrong in ((down, up, down, up1, up1, down1), (up, down, down, up1, up1, down1),
+                  (up, up, up, up1, up1, down1), (up4, up4, down, up1, up1, down1),
+                  (up, up, down4, up1, up1, down1), (up, up, down, down1, up1, down1),
+                  (up, up, down, up1, up1, up1)):
+        with pytest.raises(ValueError, match="experts"):
+            m.W4Decoder(layer, m.W4Experts.of(*wrong))
+    # packed tensors by themselves say nothing but their size
+    m.W4Decoder(layer, m.W4Experts(up.packed, up.packed, down.packed, up1.packed, up1.packed,
+                                   down1.packed))
