@@ -215,12 +215,9 @@ class MoeW4Experts(ctypes.Structure):
 
 def _p(t):
     """Pointer of a torch tensor (or None -> NULL, or an int as it is)."""
-    try:
-        return t.data_ptr()
-    except AttributeError:
-        if t is None or isinstance(t, int):
-            return t
-        raise
+    if t is None or isinstance(t, int):
+        return t
+    return t.data_ptr()
 
 
 _current_stream = None
@@ -246,10 +243,7 @@ def _ck(rc: int, where: str):
 
 
 def _shape(shape):
-    try:
-        return ctypes.byref(shape._c)  # of the shapes that keep their struct
-    except AttributeError:
-        return ctypes.byref(shape if isinstance(shape, ctypes.Structure) else shape.c())
+    return ctypes.byref(shape if isinstance(shape, ctypes.Structure) else shape.c())
 
 
 def moe_workspace_bytes(shape) -> int:
