@@ -241,6 +241,15 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// What this wave's lanes wrote to LDS is there for its other lanes.  LDS takes a
+// wave's accesses in order, so the fences cost no instruction; they keep the
+// compiler from moving accesses across, which the barrier alone does not.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 
 // Chunk swizzle of the DMA-fed tiles (rows of 64 bf16 = eight 16-byte

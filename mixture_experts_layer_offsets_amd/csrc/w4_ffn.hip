@@ -268,7 +268,7 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
   if (WEIGHT)
 #pragma unroll
     for (int i = 0; i < kIds; i++) ws[64 * i + lane] = id[i] == r.e ? wt[i] : 0.0f;
-  __builtin_amdgcn_wave_barrier();  // a wave's own LDS accesses stay in order
+  wave_lds_sync();
   uint64_t prev = 0;
 #pragma unroll
   for (int i = 0; i < kIds; i++) {
@@ -291,7 +291,7 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
     r.n += __popcll(rows);
     prev = m;
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_sync();
   return r;
 }
 
