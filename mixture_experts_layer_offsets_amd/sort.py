@@ -136,18 +136,26 @@ class TokenSort:
         return out
 
     def unsort_backward(self, dout, y, topk_w, dy=None, dtopk_w=None):
-        """(dy, dtopk_w): the gradients of ``unsort``'s rows and weights."""
+        """(dy, dtopk_w): the gradients of ``unsort``'s rows and weights.
+        Without weights (``topk_w`` None) there is no gradient of them, and y
+        is not read: dtopk_w is None."""
         dy = self.sorted_rows() if dy is None else dy
-        if dtopk_w is None:
-            dtopk_w = torch.empty((self.shape.tokens, self.shape.top_k), dtype=torch.float32,
-                                  device=self.device)
+        if topk_w is None and dtopk_w is not None:
+            raise ValueError("dtopk_w: given without topk_w")
         self._tokens("dout", dout)
         self._sorted("y", y)
-        self._slots("topk_w", topk_w, torch.float32)
+        if topk_w is not None:
+            self._slots("topk_w", topk_w, torch.float32)
+            if dtopk_w is None:
+                dtopk_w = torch.empty((self.shape.tokens, self.shape.top_k), dtype=torch.float32,
+                                      device=self.device)
+            self._slots("dtopk_w", dtopk_w, torch.float32)
         self._sorted("dy", dy)
-        self._slots("dtopk_w", dtopk_w, torch.float32)
         self._layout()
         with torch.cuda.device(self.device):
-            _lib.moe_unsort_bwd(self.shape, dout, y, topk_w, self.counts, self.offsets,
-                                self.inv_perm, dy, dtopk_w)
+            if topk_w is None:  # weights of one: the rows' gradients are the tokens'
+                _lib.moe_sort_rows(self.shape, dout, self.counts, self.offsets, self.inv_perm, dy)
+            else:
+                _lib.moe_unsort_bwd(self.shape, dout, y, topk_w, self.counts, self.offsets,
+                                    self.inv_perm, dy, dtopk_w)
         return dy, dtopk_w

@@ -75,3 +75,19 @@ def test_more_workgroups_than_a_grid_dimension(T, D, align):
     ws = torch.where(inv >= 0, w.double(), 0.0).sum(1, keepdim=True)
     ref = x.double() * ws
     assert torch.all((out.double() - ref).abs() <= ref.abs() * (2.0 ** -8 + (k + 2) * 2.0 ** -23))
+
+
+@pytest.mark.parametrize("width,type", [(1032, "bf16"), (77, "f16"), (3, "f32")])
+def test_gradient_of_the_unweighted_return(width, type):
+    """The same rows, bit for bit, as with weights of one."""
+    code, dtype = {"bf16": (m.MOE_ROW_BF16, torch.bfloat16), "f16": (m.MOE_ROW_F16, torch.float16),
+                   "f32": (m.MOE_ROW_F32, torch.float32)}[type]
+    op = m.TokenSort(m.SortShape(50, 6, 3, width, code, align=4, first_expert=1))
+    g = torch.Generator(device="cuda").manual_seed(width)
+    idx = torch.randint(0, 8, (50, 3), generator=g, device="cuda", dtype=torch.int32)
+    x, dout = (torch.randn((50, width), generator=g, device="cuda").to(dtype) for _ in range(2))
+    y = op.sort(x, idx)
+    dy, none = op.unsort_backward(dout, y, None, dy=op.sorted_rows().fill_(7))
+    ones, _ = op.unsort_backward(dout, y, torch.ones((50, 3), device="cuda"),
+                                 dy=op.sorted_rows().fill_(7))
+    assert none is None and torch.equal(dy, ones)

@@ -51,3 +51,21 @@ def test_the_first_sort_makes_the_layout(monkeypatch):
     op.unsort(xs)
     op.unsort_backward(x, xs, torch.ones((6, 2)))
     assert calls == ["moe_sort_fwd", "moe_sort_rows", "moe_sort_bwd", "moe_unsort_fwd", "moe_unsort_bwd"]
+
+
+def test_the_unweighted_return_has_a_gradient(monkeypatch):
+    """unsort without weights: dy by the rows' copy, no dtopk_w; a buffer for it
+    has nothing to be filled with."""
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    calls = []
+    for name in ("moe_sort_fwd", "moe_sort_rows", "moe_unsort_bwd"):
+        monkeypatch.setattr(_lib, name, lambda *a, name=name: calls.append(name))
+    op = m.TokenSort(m.SortShape(6, 4, 2, 16), device="cpu")
+    dout, y = op.token_rows(), op.sort(op.token_rows(), torch.zeros((6, 2), dtype=torch.int32))
+    dy = op.sorted_rows()
+    got, dw = op.unsort_backward(dout, y, None, dy=dy)
+    assert got is dy and dw is None and calls == ["moe_sort_fwd", "moe_sort_rows"]
+    with pytest.raises(ValueError, match="dtopk_w"):
+        op.unsort_backward(dout, y, None, dtopk_w=torch.empty((6, 2)))
+    with pytest.raises(ValueError):
+        op.unsort_backward(dout, y[:-1], None)
