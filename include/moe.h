@@ -456,9 +456,9 @@ int moe_unsort_bwd(const moe_sort_shape *shape, const void *dout, const void *y,
  * camada MoE virou o gargalo" and [NA design]).  Activations are bf16, sums
  * fp32; no weight is rounded beyond its 4-bit form.
  *
- * MOE_W4_MXFP4: w = 2^(s - 127) * E2M1(code), group_size 32, s an E8M0 byte
- *   up to 252 (larger ones stand for values past bf16's range: the outputs
- *   they reach are not finite).
+ * MOE_W4_MXFP4: w = 2^(s - 127) * E2M1(code), group_size 32, s an E8M0 byte;
+ *   with 253 and 254 the largest codes pass bf16's range and are infinite, and
+ *   255 is the format's NaN: the outputs that they reach are not finite.
  * MOE_W4_INT4: w = s * (q - z), q in 0..15, group_size 32, 64 or 128, s bf16
  *   or fp16, z a zero point in 0..15 per group, or 8 everywhere (zeros = 0).
  *   The kernels form sums of x * (16 + q) over a group: |x| must stay below

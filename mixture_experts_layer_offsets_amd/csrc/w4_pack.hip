@@ -154,7 +154,8 @@ __global__ __launch_bounds__(256) void w4_unpack_kernel(W4Dims d, const uint8_t 
     if (d.fmt == kW4Mx) {
       const int e = (c >> 1) & 3, man = c & 1;
       const float mag = e ? ldexpf(1.0f + 0.5f * man, e - 1) : 0.5f * man;
-      v = ldexpf(c & 8 ? -mag : mag, (int)ps[at] - 127);
+      v = ps[at] == 255 ? __uint_as_float(0x7FC00000u)  // E8M0's NaN, as the products have it
+                        : ldexpf(c & 8 ? -mag : mag, (int)ps[at] - 127);
     } else {
       const int z = d.zeros ? (ps + d.scale_bytes)[at] : 8;
       v = scale_value(((const uint16_t *)ps)[at], d.f16_scales ? ~0u : 0u) * (float)((int)c - z);
