@@ -72,3 +72,25 @@ def test_tokens_that_name_an_expert_more_than_once(name, f):
     idx[1::5, k // 2] = -1                     # a masked slot between
     lins, experts, shared = matrices(rng, E, H, I, Is, f)
     check(name, m.Shape(T, H, E, k, I, Is), f, lins, experts, shared, idx.astype(np.int32), rng)
+
+
+# name: T, k, E, H, I, shared I: few routed rows an expert, all tokens the shared one
+SHARED = {
+    "in-the-workgroups": (32, 8, 128, 128, 64, 128),
+    "planned": (64, 8, 256, 128, 64, 192),
+    "staged-routed": (300, 4, 60, 64, 64, 64),
+    "one-slot": (1000, 1, 256, 64, 64, 64),
+}
+
+
+@pytest.mark.parametrize("f", [base.FORMATS[0], base.FORMATS[4]], ids=[base.IDS[0], base.IDS[4]])
+@pytest.mark.parametrize("name", list(SHARED))
+def test_shared_expert_of_many_tokens_beside_many_experts(name, f):
+    """The routed experts' average picks the kernels; the shared expert's rows,
+    many times that average, go through the same ones."""
+    T, k, E, H, I, Is = SHARED[name]
+    rng = np.random.default_rng([T, k, E, Is])
+    note(f"w4 layer, shared expert: {name} {f}")
+    lins, experts, shared = matrices(rng, E, H, I, Is, f)
+    idx = rng.integers(-1, E, (T, k)).astype(np.int32)
+    check(name, m.Shape(T, H, E, k, I, Is), f, lins, experts, shared, idx, rng)
