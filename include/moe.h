@@ -513,7 +513,7 @@ int moe_w4_unpack(const moe_w4_shape *shape, const void *packed, float *w,
  * x: rows of k bf16 values, x_stride apart; out: rows of n, out_stride apart
  * (strides in values, at most 2^32).  out must not overlap x.  Made for few rows
  * per group: the weights are read once per 16 to 64 rows of a group, more rows
- * at a time the more there are.  0 <= rows <= 2^30. */
+ * at a time the more there are of a group on average.  0 <= rows <= 2^30. */
 int moe_w4_linear(const moe_w4_shape *shape, int32_t rows, const uint16_t *x,
                   int64_t x_stride, const int32_t *offsets, const void *packed,
                   uint16_t *out, int64_t out_stride, void *stream);

@@ -8,7 +8,9 @@ namespace moe {
 
 constexpr int kRowBlock = 64;    // one wave per workgroup for the gathers (see combine_kernel)
 constexpr int kBwdBlock = 256;   // threads of a workgroup of the weighted return's gradient
-constexpr int kPadSplit = 8;     // workgroups that share one expert's padding rows
+// Workgroups that share one expert's padding rows (65536 rows of 7168 bf16 over 256
+// experts to 128 rows: 255 us with 8, 257 to 260 with 2, 4, 16 and 32).
+constexpr int kPadSplit = 8;
 
 struct GridDims {
   unsigned x, y, z;

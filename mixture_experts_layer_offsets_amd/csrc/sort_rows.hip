@@ -42,8 +42,11 @@ constexpr int kSortMaxK = 16;   // top-k bound of the library
 // One-launch sort: slots it takes (512: 7.5 us, layout and rows apart 12.8; 1024:
 // 13.7 and 13.5), slots if aligned, where every workgroup makes the layout (256 of
 // 256 experts to 16 rows: 18.9 and 19.1; 512: 24.3 and 19.5), rows of the sorted
-// buffer (one workgroup fills perm's end) and bytes of a row (a wave's worth); rows
-// a padding workgroup checks.
+// buffer (one workgroup fills perm's end) and bytes of a row: a wave's worth, which
+// is more than it needs (64 slots, rows of 16 to 512 bytes: 12.4 us apart, 5.9 us
+// in one launch; to 16 rows 12.7 and 10.4).  Rows that a padding workgroup checks
+// one after the other (64 slots of 256 experts to 16 rows of 7168 bf16: 16 rows
+// 14.1 us, 32 rows 23.5, 8 rows 9.6).
 constexpr int kSortSmallSlots = 512, kSortSmallAligned = 256;
 constexpr int kSortSmallRows = 16384, kSortSmallBytes = 1024;
 constexpr int kSmallPadRows = 16;

@@ -7,14 +7,21 @@
 //            rows, one behind the other, times its experts' matrices, one behind
 //            the other, is one long contraction.
 // No layout is made for up to 256 slots: each workgroup finds its expert's rows
-// itself, since a launch costs about 4 us here and the search about one.
+// itself, since a launch costs about 4 us here and the search 1.3 to 2.
 //
 // Bound by reading the used experts' codes and scales: some 3 us a kernel until
 // the first codes are there, then 6 to 7 TB/s until the workgroups end one by one.
-// MXFP4, 7168 x 2048, 8 of 48 experts, one token: gate_up 22.7 us (125 MB, which a
+// MXFP4, 7168 x 2048, 8 of 48 experts, one token: gate_up 23.4 us (125 MB, which a
 // plain read takes 19.5 for), down 17.8 us (62 MB, 10.3).  INT4 in groups of 64
-// with fp16 scales, 2048 x 1408, 32 tokens over about 30 of 32 experts: 24.5 us
-// (94 MB, 15.0), 13.9 us (47 MB, 8.2), combine 4.
+// with fp16 scales, 2048 x 1408, 32 tokens over about 30 of 32 experts: 24.8 us
+// (94 MB, 15.0), 13.5 us (47 MB, 8.2), combine 5.0.
+//
+// Where that does not hold: the kernels are chosen by the routed rows an expert has
+// on average.  A shared expert has every token's row and goes through the same
+// ones, and so does an expert that the routing favours: its rows beyond a pass read
+// its weights again, one pass after the other.  64 tokens x 8 over 256 experts, 64
+// of them here, 2048 x 512 MXFP4: 36 us without a shared expert, 60 with one; 7168
+// x 2048: 231 and 506.
 #include <algorithm>
 
 #include "w4_device.h"
@@ -202,8 +209,9 @@ constexpr int kFewSlots = 256;  // slots that a workgroup looks through by itsel
 // is none.  Up to kFewSlots slots are looked through here, by each wave for
 // itself: the expert's slots by ballots over the ids, four a lane.  With as many
 // slots as experts the u-th is expert u; with up to 64 slots the used experts are
-// counted by their first slots; else as bits in LDS (which costs two barriers:
-// 2.8 us until the rows are known at the 32 tokens above, 2.4 without).
+// counted by their first slots; else as bits in LDS (which costs two barriers).
+// Until the rows are known, at the median workgroup of the kernels above: 1.6 us of
+// the one-token gate_up, at 32 tokens 2.0 of gate_up and 1.3 of down.
 // WEIGHT: the rows' weights too.
 template <bool PLAN, bool WEIGHT>
 __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, int u) {
@@ -296,7 +304,9 @@ __device__ __forceinline__ Rows<PLAN> find_rows(const Ffn &q, const Plan &plan, 
 }
 
 // act[f] of one row and output, from the sums of its gate and up products:
-// rounded to bf16 once, weight included, as the matrix operand of down.
+// rounded to bf16 once, weight included, as the matrix operand of down.  That moves
+// the outputs by 2.6e-3 of their norm (their own bf16 rounding: 1.7e-3; both, from
+// the 64-bit values: 2.4e-3); keeping it out would take a second operand a row.
 template <bool PLAN>
 __device__ __forceinline__ void put_act(const Ffn &q, const Rows<PLAN> &rows, int r, int n, float g,
                                         float u) {
@@ -330,8 +340,8 @@ __device__ __forceinline__ void stream_pairs(const W4Row<F> (&mm)[2 * NP], uint3
 
 // gate_up, 16 rows a pass from memory: a workgroup takes tp sets of kGuPairs pairs
 // of tiles of one expert, one set after the other; its waves split the contraction.
-// Two pairs share a load of the rows: 22.7 us for the 125 MB above, and 24.3 with
-// one pair and two steps of the contraction loaded together.  Four workgroups fit
+// Two pairs share a load of the rows: 22.7 us for the 125 MB above when both were
+// timed, and 24.3 with one pair and two steps of the contraction loaded together.  Four workgroups fit
 // on a CU.  No faster, all at one token / at 32: a ring of steps over all sets
 // (25.2 / 31.6 us), four steps together (26.5 / 29.2), rows staged through LDS
 // (22.9 / 25.0), five workgroups (24.4 / 25.0); with the rows, the scales and the
@@ -419,9 +429,12 @@ struct Down {
 
 // One token: the hidden rows of its experts (and the shared one) lie in LDS one
 // behind the other, and their steps are one sequence, split over the waves, each
-// with D steps of codes in flight.  17.9 us for the 62 MB above, of which the
+// with D steps of codes in flight.  17.8 us for the 62 MB above, of which the
 // stream takes about 11; the batches of gate_up here took 18.9 (the rows' loads
 // keep registers that the codes need), waves that take every eighth step 18.3.
+// A wave's last D refills are of steps that it does not use (16 used, 24 loaded,
+// above); most are its neighbour's and come from the caches: 14 % more than the
+// codes and scales is read from memory.
 // Grid: output tiles.
 template <class F, int D>
 __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
@@ -494,9 +507,11 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
 }
 
 // More tokens: y[f] = act[f] Wd in fp32 at the places of the rows, 16 rows a
-// pass, kDownTiles tiles of one expert a workgroup: at the 32 tokens above 13.9 us
+// pass, kDownTiles tiles of one expert a workgroup: at the 32 tokens above 13.5 us
 // with four tiles; before other steps 14.4, where two took 18.5 and one 28 (the
-// search for the rows is the same for all).  With three waves a SIMD a second,
+// search for the rows is the same for all).  Of the 13.5 a workgroup searches 1.3,
+// takes its 2.75 steps a wave one memory round trip after the other in 4.9, and
+// joins and stores in 2.1; the first ends at 6.3 and the last at 12.7.  With three waves a SIMD a second,
 // mostly empty round of workgroups made it 16.5.  Grid (tiles / kDownTiles, used
 // experts [+ 1]).
 constexpr int kDownTiles = 4;
@@ -630,11 +645,15 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
   with_format(a.up, [&](auto f) {
     using F = decltype(f);
     const dim3 b(kGuWaves * 64), bb(kBlockThreads);
-    // Staged rows from an average of 16 a expert on (32 tokens x 8 slots over 8
-    // experts of 7168 x 2048: 58 us, and 122 us with rows from memory, which
-    // every tile reads again), 32 a pass up to an average of 32.
+    // Rows from memory up to an average of 16 an expert, where every tile reads
+    // them again; staged from there on, 32 a pass up to an average of 32, then 64
+    // (kLongBlocks).  8 experts of 7168 x 2048, MXFP4 / INT4 in groups of 64, us:
+    // 16 rows an expert 52.3 / 67.8 from memory, 52.3 / 63.6 staged; 17 rows 82.6 /
+    // 100.1 and 53.1 / 64.8; 32 rows 57.5 / 69.9, with 64 a pass 73.5 / 98.0; 40
+    // rows 83.3 / 105.7 with 64 a pass, 103.6 / 127.2 with 32.
     auto up = [&](auto kernel) {
-      // sets a workgroup, for about 768 of them: 32 tokens above 24.4 us, with 512 28.3
+      // one set a workgroup up to 1535 sets, then so many that 768 to 1151 workgroups
+      // are left.  The 32 tokens above, 1408 sets: one each 24.4 us, two each 28.3
       const int sets = (nt + kGuPairs - 1) / kGuPairs;
       const int tp = std::max(1, (int)((long)sets * gy / 768));
       hipLaunchKernelGGL(kernel, dim3((sets + tp - 1) / tp, gy), b, 0, s, r, sh, p, used, tp, a.x);

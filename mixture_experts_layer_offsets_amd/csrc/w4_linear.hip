@@ -82,7 +82,10 @@ void launch_w4_linear(const W4Dims &d, int rows, const uint16_t *x, long xstride
                       hipStream_t s) {
   if (rows <= 0) return;
   const W4Mat m = w4_view(d, packed);
-  // the rows of a group, if they were spread evenly
+  // The rows of a group, if they were spread evenly: the lengths are on the device.  A
+  // group far above the average takes its passes one after the other, its weights
+  // read again by each (256 rows over 16 groups of 2048 x 4096 MXFP4: 22 us spread
+  // evenly, 141 all in one; as a product of one group 12.6).
   const int avg = (rows + d.groups - 1) / d.groups;
   with_format(d, [&](auto f) {
     using F = decltype(f);
