@@ -554,6 +554,164 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts,
                       const float *topk_w_in, uint16_t *out, void *ws,
                       size_t ws_bytes, void *stream);
 
+/* ----------------------------------- 8-bit products with a scale per 128 values */
+
+/* Products x*W of 8-bit floating-point values (E4M3) with an fp32 scale for each
+ * block of 128, their gradients, and the few-token layer on such weights: the
+ * format in which DeepSeek-V3-shaped experts are trained and stored (the pages'
+ * own 8-bit format, MXFP8, has a power of two per 32 values: kucoin.com, §02).
+ *
+ * Weights [groups][k][n]: one scale per 128 x 128 block, s = max(max|w| / 448,
+ * 2^-100).  Rows of activations: one per 128 consecutive values; a weight gradient
+ * contracts over a group's rows, so there one per 128 rows of a column, from the
+ * group's first row on.  code = E4M3(v * (1 / s)), the quotient and the product in
+ * fp32, held at +-448 and rounded to nearest even.  A block that holds an infinity
+ * or NaN makes every output that it reaches infinite or NaN; no row's values reach
+ * another row's outputs (those of a column, in a weight gradient, another column's).
+ * Sums of 128 code products come from the matrix unit, which keeps fewer bits of
+ * them than fp32 (1.3e-5 of their norm); they are scaled and added in fp32.  The
+ * scales of two blocks that meet must have a finite product.
+ *
+ * Limits: 1 <= groups <= 1024, 1 <= n, k <= 2^20; rows are bf16 or fp16
+ * (row_type), of any n and k, strides in values of at least a row and at most
+ * 2^32.  Row tensors need their type's alignment only.  offsets (device, int32
+ * [groups+1], ascending, at most `rows`; NULL with one group: all rows) say that
+ * the rows of group g are [offsets[g], offsets[g+1]).  No entry point reads a host
+ * copy of them, so all can be captured into a graph (with a workspace of its own
+ * where calls may overlap). */
+typedef struct moe_f8_shape {
+  int32_t groups;
+  int32_t n;         /* outputs */
+  int32_t k;         /* contraction */
+  int32_t row_type;  /* MOE_ROW_BF16 or MOE_ROW_F16: x, out, dy, dw */
+} moe_f8_shape;
+
+/* Bytes of the packed weights (0: refused). */
+size_t moe_f8_bytes(const moe_f8_shape *shape);
+
+/* Lay ready-made codes out for the kernels (`packed` is opaque, aligned to 16
+ * bytes).  codes [groups][n][k] E4M3 bytes, scales fp32
+ * [groups][ceil(n / 128)][ceil(k / 128)]: a weight is code times scale. */
+int moe_f8_pack(const moe_f8_shape *shape, const uint8_t *codes,
+                const float *scales, void *packed, void *stream);
+
+/* Quantise weights w [groups][k][n] of w_type (MOE_ROW_*) into packed ones. */
+int moe_f8_quantize(const moe_f8_shape *shape, const void *w, int32_t w_type,
+                    void *packed, void *stream);
+
+/* The values that packed weights stand for: w [groups][k][n] fp32. */
+int moe_f8_unpack(const moe_f8_shape *shape, const void *packed, float *w,
+                  void *stream);
+
+/* The packed weights of the products x*W^T, of shape {groups, k, n}: the same
+ * codes and scales, turned.  With them moe_f8_linear of dy is the data gradient. */
+int moe_f8_transpose(const moe_f8_shape *shape, const void *packed,
+                     void *packed_t, void *stream);
+
+/* Rows quantised along k: codes [ceil(k / 128)][rows][128] and scales
+ * [ceil(k / 128)][rows], zero codes past k (codes aligned to 16 bytes).  Of the shape
+ * only k and row_type count. */
+int moe_f8_quantize_rows(const moe_f8_shape *shape, int32_t rows, const void *x,
+                         int64_t x_stride, uint8_t *codes, float *scales,
+                         void *stream);
+
+/* Bytes of workspace of moe_f8_linear (0: refused). */
+size_t moe_f8_linear_workspace_bytes(const moe_f8_shape *shape, int32_t rows);
+
+/* out[r] = x[r] * W_g for the rows r of each group (other rows of out are left
+ * as they were), x quantised on the way.  out must not overlap x. */
+int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x,
+                  int64_t x_stride, const int32_t *offsets, const void *packed,
+                  void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* The same of rows that moe_f8_quantize_rows has quantised. */
+int moe_f8_linear_codes(const moe_f8_shape *shape, int32_t rows,
+                        const uint8_t *codes, const float *scales,
+                        const int32_t *offsets, const void *packed, void *out,
+                        int64_t out_stride, void *stream);
+
+/* Bytes of workspace of moe_f8_wgrad (0: refused). */
+size_t moe_f8_wgrad_workspace_bytes(const moe_f8_shape *shape, int32_t rows);
+
+/* Weight gradients dw[g] = sum over the rows of group g of x[r]^T dy[r], x rows of
+ * k and dy rows of n values, both quantised down their columns: dw
+ * [groups][k][n] of row_type, zeros for a group without rows.  rows / 128 + groups
+ * <= 65535. */
+int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x,
+                 int64_t x_stride, const void *dy, int64_t dy_stride,
+                 const int32_t *offsets, void *dw, void *ws, size_t ws_bytes,
+                 void *stream);
+
+/* The experts of a layer in 8 bits: packed matrices, gate and up
+ * [experts][H][I], down [experts][I][H], and the shared expert's [1][H][Is] and
+ * [1][Is][H] (all three NULL without one). */
+typedef struct moe_f8_experts {
+  int32_t first_expert; /* as in moe_w4_experts */
+  const void *gate;
+  const void *up;
+  const void *down;
+  const void *shared_gate;
+  const void *shared_up;
+  const void *shared_down;
+} moe_f8_experts;
+
+/* Bytes of workspace of moe_f8_decode_fwd (0: refused). */
+size_t moe_f8_decode_workspace_bytes(const moe_shape *shape);
+
+/* Few-token inference forward on 8-bit experts: moe_w4_decode_fwd with these
+ * weights, its arguments, limits and rounding (H, I and the shared I multiples of
+ * 64).  Activations stay bf16: with few tokens the weights' bytes are the cost, and
+ * the rows are not rounded to 8 bits.  One token with supplied routing takes two
+ * launches. */
+int moe_f8_decode_fwd(const moe_shape *shape, const moe_f8_experts *experts,
+                      const uint16_t *x, const uint16_t *w_router,
+                      const float *bias, const int32_t *topk_idx_in,
+                      const float *topk_w_in, uint16_t *out, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------ gradient norm and clipping */
+
+/* What a training step does next with the gradients that moe_layer_bwd and
+ * moe_f8_wgrad leave: their norm over all tensors together, and
+ *
+ *   out = x * min(1, max_norm / (norm + 1e-6)), rounded once.
+ *
+ * Squares and their sums are held in 64 bits.  A norm that is not finite is not
+ * caught: an infinite one gives zeros (and NaN for the infinities), NaN gives NaN.
+ * Tensors are dense runs of numel values, of their type's alignment; out is x (in
+ * place) or does not overlap any x, and no value is named twice.  The list is host
+ * memory, read during the call. */
+enum { MOE_NORM_2 = 0, MOE_NORM_INF = 1 };
+
+typedef struct moe_grad_tensor {
+  const void *x;
+  void *out;      /* scaled values (moe_grad_norm ignores it) */
+  int64_t numel;  /* 0 is allowed; at most 2^40 */
+  int32_t type;   /* MOE_ROW_* */
+} moe_grad_tensor;
+
+/* Bytes of workspace of moe_grad_norm and moe_grad_clip (0: refused); at most
+ * 2^20 tensors, 0 is allowed. */
+size_t moe_grad_workspace_bytes(int32_t count, const moe_grad_tensor *tensors);
+
+/* norm (device fp32, or NULL) and total (device fp64, or NULL): the sum of squares,
+ * or the largest magnitude.  Ranks that hold parts of the gradients sum (or take
+ * the largest of) their totals and pass that to moe_grad_scale. */
+int moe_grad_norm(int32_t count, const moe_grad_tensor *tensors,
+                  int32_t norm_type, double *total, float *norm, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/* Scales by a total that is already there; norm (NULL: not wanted) as above. */
+int moe_grad_scale(int32_t count, const moe_grad_tensor *tensors,
+                   int32_t norm_type, const double *total, float max_norm,
+                   float *norm, void *stream);
+
+/* Both: the norm of the tensors, then their scaling. */
+int moe_grad_clip(int32_t count, const moe_grad_tensor *tensors,
+                  int32_t norm_type, float max_norm, float *norm, void *ws,
+                  size_t ws_bytes, void *stream);
+
 /* Device pointers into a forward context (host call, no device work):
  * where moe_layer_fwd left each intermediate.  Any field may be NULL in
  * the result when the shape has no such tensor. */

@@ -38,6 +38,8 @@ MOE_W4_MXFP4 = 0
 MOE_W4_INT4 = 1
 MOE_SCALE_BF16 = 0
 MOE_SCALE_F16 = 1
+MOE_NORM_2 = 0
+MOE_NORM_INF = 1
 
 c_void_p = ctypes.c_void_p
 c_size_t = ctypes.c_size_t
@@ -101,6 +103,30 @@ SIGNATURES = {
                       [c_void_p] * 3 + [ctypes.c_int64, c_void_p]),
     "moe_w4_decode_workspace_bytes": (c_size_t, [c_void_p]),
     "moe_w4_decode_fwd": (c_int, [c_void_p] * 8 + [c_void_p, c_size_t, c_void_p]),
+    "moe_f8_bytes": (c_size_t, [c_void_p]),
+    "moe_f8_pack": (c_int, [c_void_p] * 4 + [c_void_p]),
+    "moe_f8_quantize": (c_int, [c_void_p, c_void_p, ctypes.c_int32, c_void_p, c_void_p]),
+    "moe_f8_unpack": (c_int, [c_void_p] * 3 + [c_void_p]),
+    "moe_f8_transpose": (c_int, [c_void_p] * 3 + [c_void_p]),
+    "moe_f8_quantize_rows": (c_int, [c_void_p, ctypes.c_int32, c_void_p, ctypes.c_int64] +
+                             [c_void_p] * 3),
+    "moe_f8_linear_workspace_bytes": (c_size_t, [c_void_p, ctypes.c_int32]),
+    "moe_f8_linear": (c_int, [c_void_p, ctypes.c_int32, c_void_p, ctypes.c_int64] + [c_void_p] * 3 +
+                      [ctypes.c_int64, c_void_p, c_size_t, c_void_p]),
+    "moe_f8_linear_codes": (c_int, [c_void_p, ctypes.c_int32] + [c_void_p] * 5 +
+                            [ctypes.c_int64, c_void_p]),
+    "moe_f8_wgrad_workspace_bytes": (c_size_t, [c_void_p, ctypes.c_int32]),
+    "moe_f8_wgrad": (c_int, [c_void_p, ctypes.c_int32, c_void_p, ctypes.c_int64, c_void_p,
+                             ctypes.c_int64] + [c_void_p] * 3 + [c_size_t, c_void_p]),
+    "moe_f8_decode_workspace_bytes": (c_size_t, [c_void_p]),
+    "moe_f8_decode_fwd": (c_int, [c_void_p] * 8 + [c_void_p, c_size_t, c_void_p]),
+    "moe_grad_workspace_bytes": (c_size_t, [ctypes.c_int32, c_void_p]),
+    "moe_grad_norm": (c_int, [ctypes.c_int32, c_void_p, ctypes.c_int32] + [c_void_p] * 3 +
+                      [c_size_t, c_void_p]),
+    "moe_grad_scale": (c_int, [ctypes.c_int32, c_void_p, ctypes.c_int32, c_void_p, ctypes.c_float,
+                               c_void_p, c_void_p]),
+    "moe_grad_clip": (c_int, [ctypes.c_int32, c_void_p, ctypes.c_int32, ctypes.c_float] +
+                      [c_void_p] * 2 + [c_size_t, c_void_p]),
     "moe_saved_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
     "moe_packed_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
     "moe_workspace_pointers": (c_int, [c_void_p, c_void_p, c_void_p]),
@@ -211,6 +237,37 @@ class MoeW4Experts(ctypes.Structure):
                                               "first_expert")] + \
                [(n, c_void_p) for n in ("gate", "up", "down", "shared_gate", "shared_up",
                                         "shared_down")]
+
+
+class MoeF8Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("groups", "n", "k", "row_type")]
+
+
+@dataclass(frozen=True)
+class F8Shape:
+    """moe_f8_shape: 8-bit matrices [groups][k][n] of products x*W."""
+    groups: int
+    n: int
+    k: int
+    row_type: int = MOE_ROW_BF16
+
+    def c(self) -> MoeF8Shape:
+        s = self.__dict__.get("_c")
+        if s is None:
+            s = MoeF8Shape(self.groups, self.n, self.k, self.row_type)
+            object.__setattr__(self, "_c", s)
+        return s
+
+
+class MoeF8Experts(ctypes.Structure):
+    _fields_ = [("first_expert", ctypes.c_int32)] + \
+               [(n, c_void_p) for n in ("gate", "up", "down", "shared_gate", "shared_up",
+                                        "shared_down")]
+
+
+class MoeGradTensor(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("out", c_void_p), ("numel", ctypes.c_int64),
+                ("type", ctypes.c_int32)]
 
 
 def _p(t):
@@ -410,6 +467,106 @@ def moe_w4_decode_fwd(shape, experts, x, w_router, bias, topk_idx_in, topk_w_in,
                                  _p(topk_idx_in), _p(topk_w_in), _p(out), _p(ws),
                                  ws.numel() * ws.element_size(), _stream(stream)),
         "moe_w4_decode_fwd")
+
+
+def moe_f8_bytes(shape) -> int:
+    return load().moe_f8_bytes(_shape(shape))
+
+
+def moe_f8_pack(shape, codes, scales, packed, stream=None):
+    _ck(load().moe_f8_pack(_shape(shape), _p(codes), _p(scales), _p(packed), _stream(stream)),
+        "moe_f8_pack")
+
+
+def moe_f8_quantize(shape, w, w_type, packed, stream=None):
+    _ck(load().moe_f8_quantize(_shape(shape), _p(w), w_type, _p(packed), _stream(stream)),
+        "moe_f8_quantize")
+
+
+def moe_f8_unpack(shape, packed, w, stream=None):
+    _ck(load().moe_f8_unpack(_shape(shape), _p(packed), _p(w), _stream(stream)), "moe_f8_unpack")
+
+
+def moe_f8_transpose(shape, packed, packed_t, stream=None):
+    _ck(load().moe_f8_transpose(_shape(shape), _p(packed), _p(packed_t), _stream(stream)),
+        "moe_f8_transpose")
+
+
+def _row_stride(t):
+    # a single row's stride says nothing
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def moe_f8_quantize_rows(shape, x, codes, scales, stream=None):
+    """x [rows][k]: rows one stride apart, values contiguous."""
+    _ck(load().moe_f8_quantize_rows(_shape(shape), x.shape[0], _p(x), _row_stride(x), _p(codes),
+                                    _p(scales), _stream(stream)), "moe_f8_quantize_rows")
+
+
+def moe_f8_linear_workspace_bytes(shape, rows) -> int:
+    return load().moe_f8_linear_workspace_bytes(_shape(shape), rows)
+
+
+def moe_f8_linear(shape, x, offsets, packed, out, ws, stream=None):
+    """x [rows][k] and out [rows][n]: rows one stride apart, values contiguous."""
+    _ck(load().moe_f8_linear(_shape(shape), x.shape[0], _p(x), _row_stride(x), _p(offsets),
+                             _p(packed), _p(out), _row_stride(out), _p(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "moe_f8_linear")
+
+
+def moe_f8_linear_codes(shape, codes, scales, offsets, packed, out, stream=None):
+    """codes and scales as moe_f8_quantize_rows leaves them; out [rows][n]."""
+    _ck(load().moe_f8_linear_codes(_shape(shape), out.shape[0], _p(codes), _p(scales), _p(offsets),
+                                   _p(packed), _p(out), _row_stride(out), _stream(stream)),
+        "moe_f8_linear_codes")
+
+
+def moe_f8_wgrad_workspace_bytes(shape, rows) -> int:
+    return load().moe_f8_wgrad_workspace_bytes(_shape(shape), rows)
+
+
+def moe_f8_wgrad(shape, x, dy, offsets, dw, ws, stream=None):
+    """x [rows][k] and dy [rows][n]: rows one stride apart, values contiguous."""
+    _ck(load().moe_f8_wgrad(_shape(shape), x.shape[0], _p(x), _row_stride(x), _p(dy),
+                            _row_stride(dy), _p(offsets), _p(dw), _p(ws),
+                            ws.numel() * ws.element_size(), _stream(stream)), "moe_f8_wgrad")
+
+
+def moe_f8_decode_workspace_bytes(shape) -> int:
+    return load().moe_f8_decode_workspace_bytes(_shape(shape))
+
+
+def moe_f8_decode_fwd(shape, experts, x, w_router, bias, topk_idx_in, topk_w_in, out, ws,
+                      stream=None):
+    _ck(load().moe_f8_decode_fwd(_shape(shape), _shape(experts), _p(x), _p(w_router), _p(bias),
+                                 _p(topk_idx_in), _p(topk_w_in), _p(out), _p(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)),
+        "moe_f8_decode_fwd")
+
+
+def moe_grad_workspace_bytes(tensors) -> int:
+    """tensors: a GradSet, or an array of MoeGradTensor."""
+    return load().moe_grad_workspace_bytes(*_tensors(tensors))
+
+
+def _tensors(tensors):
+    array = tensors if isinstance(tensors, ctypes.Array) else tensors.c()
+    return len(array), array
+
+
+def moe_grad_norm(tensors, norm_type, total, norm, ws, stream=None):
+    _ck(load().moe_grad_norm(*_tensors(tensors), norm_type, _p(total), _p(norm), _p(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "moe_grad_norm")
+
+
+def moe_grad_scale(tensors, norm_type, total, max_norm, norm=None, stream=None):
+    _ck(load().moe_grad_scale(*_tensors(tensors), norm_type, _p(total), max_norm, _p(norm),
+                              _stream(stream)), "moe_grad_scale")
+
+
+def moe_grad_clip(tensors, norm_type, max_norm, norm, ws, stream=None):
+    _ck(load().moe_grad_clip(*_tensors(tensors), norm_type, max_norm, _p(norm), _p(ws),
+                             ws.numel() * ws.element_size(), _stream(stream)), "moe_grad_clip")
 
 
 def moe_saved_pointers(shape, saved) -> dict:

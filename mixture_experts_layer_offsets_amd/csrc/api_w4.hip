@@ -1,7 +1,9 @@
-// C ABI of the 4-bit expert weights: argument checks and launches (w4_*.hip).
+// C ABI of the 4-bit expert weights, and of the few-token layer on 8-bit ones: argument
+// checks and launches (w4_*.hip).
 #include <algorithm>
 
 #include "../../include/moe.h"
+#include "f8.h"
 #include "kernels.h"
 #include "w4.h"
 
@@ -91,6 +93,65 @@ size_t carve(const moe_shape *s, void *ws, Work *w) {
   return off;
 }
 
+// The few-token layer on packed experts of either kind.  dims(groups, n, k, &d): the
+// dims of one of its matrices, or an error.
+template <class Experts, class Dims>
+int decode_fwd(const moe_shape *shape, const Experts *experts, const uint16_t *x,
+               const uint16_t *w_router, const float *bias, const int32_t *topk_idx_in,
+               const float *topk_w_in, uint16_t *out, void *ws, size_t ws_bytes, void *stream,
+               Dims &&dims) {
+  int rc = check_layer(shape);
+  if (rc) return rc;
+  if (!experts || !experts->gate || !experts->up || !experts->down || !x || !out || !ws)
+    return MOE_ERR_INVALID_ARG;
+  const bool router = w_router != nullptr, shared = shape->shared_inter > 0;
+  if (router == (topk_idx_in != nullptr) || (topk_idx_in != nullptr) != (topk_w_in != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const int T = shape->tokens, H = shape->hidden, E = shape->experts, k = shape->top_k;
+  if (router && (k > E || experts->first_expert)) return MOE_ERR_INVALID_ARG;
+  if (router && E % 8) return MOE_ERR_UNSUPPORTED;
+  if (shared != (experts->shared_gate != nullptr) || shared != (experts->shared_up != nullptr) ||
+      shared != (experts->shared_down != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  // the matrices' own limits (of W4: format, group size against H, I and Is)
+  W4Dims up, down, up_s, down_s;
+  if ((rc = dims(E, shape->inter, H, &up)) || (rc = dims(E, H, shape->inter, &down))) return rc;
+  if (shared && ((rc = dims(1, shape->shared_inter, H, &up_s)) ||
+                 (rc = dims(1, H, shape->shared_inter, &down_s))))
+    return rc;
+  Work w;
+  if (ws_bytes < carve(shape, ws, &w)) return MOE_ERR_WORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  const int32_t *idx = topk_idx_in;
+  const float *wts = topk_w_in;
+  int first = experts->first_expert;
+  if (router) {
+    launch_dense_groups(w.offsets, w.tiles, w.order, T, kTileM, s);
+    GemmArgs lg{};
+    lg.A = x; lg.lda = H;
+    lg.B = w_router; lg.ldb = E;
+    lg.C = w.logits; lg.ldc = E;
+    lg.bias = bias;
+    lg.offsets = w.offsets; lg.tile_start = w.tiles;
+    lg.G = 1; lg.N = E; lg.K = H;
+    launch_gemm_rows(lg, EPI_F32, false, T, s);
+    launch_topk(w.logits, T, E, k, w.idx, w.w, s);
+    idx = w.idx;
+    wts = w.w;
+  }
+  W4Layer a{};
+  a.up = up; a.down = down;
+  a.shared = shared;
+  if (shared) { a.up_s = up_s; a.down_s = down_s; }
+  a.T = T; a.k = k; a.first = first;
+  a.x = x; a.idx = idx; a.w = wts;
+  a.w_gate = experts->gate; a.w_up = experts->up; a.w_down = experts->down;
+  a.ws_gate = experts->shared_gate; a.ws_up = experts->shared_up; a.ws_down = experts->shared_down;
+  a.act = w.act; a.act_s = w.act_s; a.y = w.y; a.y_s = w.y_s; a.plan = w.plan; a.out = out;
+  launch_w4_ffn(a, s);
+  return status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -155,61 +216,32 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts, con
                       const uint16_t *w_router, const float *bias, const int32_t *topk_idx_in,
                       const float *topk_w_in, uint16_t *out, void *ws, size_t ws_bytes,
                       void *stream) {
-  int rc = check_layer(shape);
-  if (rc) return rc;
-  if (!experts || !experts->gate || !experts->up || !experts->down || !x || !out || !ws)
-    return MOE_ERR_INVALID_ARG;
-  const bool router = w_router != nullptr, shared = shape->shared_inter > 0;
-  if (router == (topk_idx_in != nullptr) || (topk_idx_in != nullptr) != (topk_w_in != nullptr))
-    return MOE_ERR_INVALID_ARG;
-  const int T = shape->tokens, H = shape->hidden, E = shape->experts, k = shape->top_k;
-  if (router && (k > E || experts->first_expert)) return MOE_ERR_INVALID_ARG;
-  if (router && E % 8) return MOE_ERR_UNSUPPORTED;
-  if (shared != (experts->shared_gate != nullptr) || shared != (experts->shared_up != nullptr) ||
-      shared != (experts->shared_down != nullptr))
-    return MOE_ERR_INVALID_ARG;
-  // the matrices' own limits (format, group size against H, I and Is)
-  auto dims = [&](int groups, int n, int kk, W4Dims *d) {
-    const moe_w4_shape s = {groups, n, kk, experts->format, experts->group_size,
-                            experts->scale_type, experts->zeros};
-    return check_w4(&s, d);
-  };
-  W4Dims up, down, up_s, down_s;
-  if ((rc = dims(E, shape->inter, H, &up)) || (rc = dims(E, H, shape->inter, &down))) return rc;
-  if (shared && ((rc = dims(1, shape->shared_inter, H, &up_s)) ||
-                 (rc = dims(1, H, shape->shared_inter, &down_s))))
-    return rc;
-  Work w;
-  if (ws_bytes < carve(shape, ws, &w)) return MOE_ERR_WORKSPACE;
-  hipStream_t s = (hipStream_t)stream;
-  const int32_t *idx = topk_idx_in;
-  const float *wts = topk_w_in;
-  int first = experts->first_expert;
-  if (router) {
-    launch_dense_groups(w.offsets, w.tiles, w.order, T, kTileM, s);
-    GemmArgs lg{};
-    lg.A = x; lg.lda = H;
-    lg.B = w_router; lg.ldb = E;
-    lg.C = w.logits; lg.ldc = E;
-    lg.bias = bias;
-    lg.offsets = w.offsets; lg.tile_start = w.tiles;
-    lg.G = 1; lg.N = E; lg.K = H;
-    launch_gemm_rows(lg, EPI_F32, false, T, s);
-    launch_topk(w.logits, T, E, k, w.idx, w.w, s);
-    idx = w.idx;
-    wts = w.w;
-  }
-  W4Layer a{};
-  a.up = up; a.down = down;
-  a.shared = shared;
-  if (shared) { a.up_s = up_s; a.down_s = down_s; }
-  a.T = T; a.k = k; a.first = first;
-  a.x = x; a.idx = idx; a.w = wts;
-  a.w_gate = experts->gate; a.w_up = experts->up; a.w_down = experts->down;
-  a.ws_gate = experts->shared_gate; a.ws_up = experts->shared_up; a.ws_down = experts->shared_down;
-  a.act = w.act; a.act_s = w.act_s; a.y = w.y; a.y_s = w.y_s; a.plan = w.plan; a.out = out;
-  launch_w4_ffn(a, s);
-  return status();
+  return decode_fwd(shape, experts, x, w_router, bias, topk_idx_in, topk_w_in, out, ws, ws_bytes,
+                    stream, [&](int groups, int n, int kk, W4Dims *d) {
+                      const moe_w4_shape s = {groups, n, kk, experts->format, experts->group_size,
+                                              experts->scale_type, experts->zeros};
+                      return check_w4(&s, d);
+                    });
+}
+
+size_t moe_f8_decode_workspace_bytes(const moe_shape *shape) {
+  return moe_w4_decode_workspace_bytes(shape);
+}
+
+int moe_f8_decode_fwd(const moe_shape *shape, const moe_f8_experts *experts, const uint16_t *x,
+                      const uint16_t *w_router, const float *bias, const int32_t *topk_idx_in,
+                      const float *topk_w_in, uint16_t *out, void *ws, size_t ws_bytes,
+                      void *stream) {
+  return decode_fwd(shape, experts, x, w_router, bias, topk_idx_in, topk_w_in, out, ws, ws_bytes,
+                    stream, [&](int groups, int n, int kk, W4Dims *d) {
+                      const moe_f8_shape s = {groups, n, kk, MOE_ROW_BF16};
+                      F8Dims f;
+                      const int rc = f8_dims(&s, &f);
+                      if (rc) return rc;
+                      *d = {groups, n, kk, kW4F8, kF8Block, 0, 0, f.nt, f.ks, 1,
+                            f.code_bytes, f.scale_bytes, 0};
+                      return (int)MOE_OK;
+                    });
 }
 
 }  // extern "C"

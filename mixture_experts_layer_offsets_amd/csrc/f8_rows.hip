@@ -1,0 +1,186 @@
+// Quantisers of 16-bit rows for the 8-bit products: along the rows (forward and data
+// gradient) and down the columns of each group's rows (weight gradient).  Both read
+// the rows once and write codes and scales, 3 bytes a value: bound by memory.
+#include <algorithm>
+
+#include "f8_device.h"
+
+namespace moe {
+
+namespace {
+
+// 8 values of a row from column c on, zeros past its k values.
+template <bool F16>
+__device__ __forceinline__ void load8(const uint16_t *row, int c, int k, float *v) {
+  uint32_t u[4];
+  if (c + 8 <= k) {
+    const u32x4_a2 q = *(const u32x4_a2 *)(row + c);
+#pragma unroll
+    for (int i = 0; i < 4; i++) u[i] = q[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t lo = c + 2 * i < k ? row[c + 2 * i] : 0;
+      u[i] = lo | (c + 2 * i + 1 < k ? (uint32_t)row[c + 2 * i + 1] << 16 : 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = f8_from16((u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, F16);
+}
+
+// The largest of the 16 lanes of a row of lanes.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 16));
+  return v;
+}
+
+// 16 lanes take a block, 8 values each; a workgroup takes 16 rows x kBlocks blocks,
+// so that it reads kBlocks 256 bytes of each row and writes 2 KB runs of codes.  Grid
+// (blocks / kBlocks, rows / 16), rows past 2^16 workgroups in turn.
+constexpr int kBlocks = 4;
+
+template <bool F16>
+__global__ __launch_bounds__(256) void f8_quant_rows_kernel(const uint16_t *__restrict__ x, long stride,
+                                                            int rows, int k, int ks,
+                                                            uint8_t *__restrict__ codes,
+                                                            float *__restrict__ scales) {
+  const int tid = threadIdx.x, i = tid & 15, kb0 = blockIdx.x * kBlocks;
+  for (long r0 = (long)blockIdx.y * 16; r0 < rows; r0 += 16L * gridDim.y) {
+    const long r = r0 + (tid >> 4);
+    const long rr = r < rows ? r : rows - 1;
+    float v[kBlocks][8];
+#pragma unroll
+    for (int b = 0; b < kBlocks; b++)
+      load8<F16>(x + rr * stride, (kb0 + b) * kF8Block + 8 * i, k, v[b]);
+#pragma unroll
+    for (int b = 0; b < kBlocks; b++) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int q = 0; q < 8; q++) top = max(top, f8_mag(v[b][q]));
+      float inv;
+      const float s = f8_scale(max16(top), &inv);
+      if (r < rows && kb0 + b < ks) {
+        const size_t at = (size_t)(kb0 + b) * rows + r;
+        *(uint2 *)(codes + at * kF8Block + 8 * i) =
+            make_uint2(f8_codes4(v[b][0], v[b][1], v[b][2], v[b][3], inv),
+                       f8_codes4(v[b][4], v[b][5], v[b][6], v[b][7], inv));
+        if (i == 0) scales[at] = s;
+      }
+    }
+  }
+}
+
+// A workgroup takes 64 columns of one stage (128 rows of one group): the rows go
+// through LDS, then a thread converts 32 values of one column, and the columns' 128
+// codes leave through LDS in 16-byte chunks.  Grid (columns / 64, stages), stages
+// past 2^16 in turn.
+template <bool F16, bool TILES>
+__global__ __launch_bounds__(256) void f8_quant_cols_kernel(
+    const uint16_t *__restrict__ x, long stride, int rows, int cols,
+    const int32_t *__restrict__ offsets, int groups, long stages, uint8_t *__restrict__ codes,
+    float *__restrict__ scales) {
+  __shared__ u32x4_t tile[kF8Block][8];  // 128 rows x 64 values
+  // a column's codes at 144 bytes a column: the 16 more put the lanes' writes on
+  // different banks
+  constexpr int kLine = kF8Block + 16;
+  __shared__ __attribute__((aligned(16))) uint8_t lines[64 * kLine];
+  __shared__ uint32_t tops[4][64];
+  const int tid = threadIdx.x, c0 = blockIdx.x * 64;
+  const int cols16 = (cols + 15) & ~15;
+  for (long st = blockIdx.y; st < stages; st += gridDim.y) {
+    int first;
+    const int g = f8_group_at(offsets, groups, rows, kF8Block, (int)st, &first);
+    const F8Span sp = f8_span(offsets, g, rows);
+    const int r0 = sp.begin + (int)(st - first) * kF8Block;
+    if (st < first || r0 >= sp.end) continue;  // an empty place
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int at = tid + 256 * q, row = at >> 3, c8 = at & 7, c = c0 + 8 * c8;
+      u32x4_t v = {0, 0, 0, 0};
+      if (r0 + row < sp.end && c < cols) {
+        const uint16_t *src = x + (size_t)(r0 + row) * stride + c;
+        if (c + 8 <= cols) {
+          const u32x4_a2 u = *(const u32x4_a2 *)src;
+          v = (u32x4_t){u[0], u[1], u[2], u[3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            if (c + e < cols) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+        }
+      }
+      tile[row][c8] = v;
+    }
+    __syncthreads();
+    const int j = tid & 63, q = tid >> 6;
+    const uint16_t *t16 = (const uint16_t *)tile;
+    float v[32];
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 32; e++) {
+      v[e] = f8_from16(t16[(32 * q + e) * 64 + j], F16);
+      top = max(top, f8_mag(v[e]));
+    }
+    tops[q][j] = top;
+    __syncthreads();
+    float inv;
+    const float s = f8_scale(max(max(tops[0][j], tops[1][j]), max(tops[2][j], tops[3][j])), &inv);
+#pragma unroll
+    for (int e = 0; e < 32; e += 16)
+      *(u32x4_t *)(lines + j * kLine + 32 * q + e) =
+          (u32x4_t){f8_codes4(v[e], v[e + 1], v[e + 2], v[e + 3], inv),
+                    f8_codes4(v[e + 4], v[e + 5], v[e + 6], v[e + 7], inv),
+                    f8_codes4(v[e + 8], v[e + 9], v[e + 10], v[e + 11], inv),
+                    f8_codes4(v[e + 12], v[e + 13], v[e + 14], v[e + 15], inv)};
+    if (q == 0 && c0 + j < cols16) scales[(size_t)st * cols16 + c0 + j] = s;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+      const int at = tid + 256 * p;
+      int col, c;
+      uint8_t *dst;
+      if constexpr (TILES) {  // chunk by chunk in a tile's order
+        col = (at >> 7) * 16 + (at & 15);
+        c = ((at >> 6) & 1) * 4 + ((at >> 4) & 3);
+        dst = codes + ((size_t)((c0 + col) >> 4) * stages + st) * kF8Tile + f8_chunk(c, col & 15);
+      } else {
+        col = at >> 3;
+        c = at & 7;
+        dst = codes + ((size_t)st * cols + c0 + col) * kF8Block + 16 * c;
+      }
+      if (c0 + col < (TILES ? cols16 : cols))
+        *(u32x4_t *)dst = *(const u32x4_t *)(lines + col * kLine + 16 * c);
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+void launch_f8_quant_rows(const F8Rows &x, int rows, int k, uint8_t *codes, float *scales,
+                          hipStream_t s) {
+  if (rows <= 0) return;
+  const int ks = (k + kF8Block - 1) / kF8Block;
+  const dim3 grid((ks + kBlocks - 1) / kBlocks, std::min((rows + 15) / 16, 65535));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x.p, x.stride, rows, k, ks, codes, scales);
+  };
+  x.f16 ? go(f8_quant_rows_kernel<true>) : go(f8_quant_rows_kernel<false>);
+}
+
+long f8_stages(int rows, int groups) { return rows / kF8Block + groups; }
+
+void launch_f8_quant_cols(const F8Rows &x, int rows, int cols, const int32_t *offsets, int groups,
+                          bool tiles, uint8_t *codes, float *scales, hipStream_t s) {
+  if (rows <= 0) return;
+  const long stages = f8_stages(rows, groups);
+  const dim3 grid((cols + 63) / 64, (unsigned)std::min(stages, 65535L));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x.p, x.stride, rows, cols, offsets, groups,
+                       stages, codes, scales);
+  };
+  if (tiles) x.f16 ? go(f8_quant_cols_kernel<true, true>) : go(f8_quant_cols_kernel<false, true>);
+  else x.f16 ? go(f8_quant_cols_kernel<true, false>) : go(f8_quant_cols_kernel<false, false>);
+}
+
+}  // namespace moe

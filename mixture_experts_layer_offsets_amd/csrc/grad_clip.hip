@@ -1,0 +1,329 @@
+// The global norm over many tensors, and their scaling by it.
+//
+//   norm = sqrt(sum of all squares), or the largest magnitude
+//   out  = x * min(1, max_norm / (norm + 1e-6)), rounded once
+//
+// Bound by memory: every value is read for the norm and again for the scaling, and
+// written once.  The tensors are cut into chunks of 64 KB; a workgroup takes every
+// G-th chunk of a launch.  The launch's tensors (address, length, type) travel in the
+// kernel's arguments, up to kSet of them, so that a call needs no table on the device
+// and takes other addresses every time.  Sums of squares are held in 64 bits from the
+// first square on: no gradient over- or underflows them, and 64-bit multiply-adds
+// still take a fraction of the loads' time.  Every workgroup of the scaling adds the
+// partial sums up by itself, in one fixed order, instead of a launch between the two.
+#include <algorithm>
+
+#include "common.h"
+#include "grad_clip.h"
+
+namespace moe {
+
+namespace {
+
+typedef unsigned int u32x4_g __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4_g2 __attribute__((ext_vector_type(4), aligned(2)));
+
+constexpr int kSet = 128;           // tensors of a launch: 3 KB of arguments
+constexpr int kChunk = 65536;       // bytes
+constexpr int kThreads = 256;
+constexpr int kGroups = 2048;       // workgroups of all launches together, about
+constexpr int kLeastGroups = 256;   // ... but of each launch this many
+constexpr int kMostPartials = 4096;  // that a scaling workgroup adds up
+
+struct Set {
+  const void *x[kSet];
+  int64_t n[kSet];        // values; type in the top bits
+  int32_t start[kSet + 1];  // chunks before each tensor
+  int32_t count;
+};
+struct Outs {
+  void *out[kSet];
+};
+constexpr int kTypeShift = 60;
+
+// The chunk c of the set: its tensor, and where in it the chunk begins.
+struct Chunk {
+  int t, type, n;  // n: values of the chunk
+  int64_t at;
+};
+__device__ __forceinline__ Chunk chunk_of(const Set &s, int c) {
+  int lo = 0, hi = s.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.start[mid] <= c) lo = mid; else hi = mid;
+  }
+  Chunk k;
+  k.t = lo;
+  const int64_t n = s.n[lo];
+  k.type = (int)(n >> kTypeShift);
+  const int per = k.type == MOE_ROW_F32 ? kChunk / 4 : kChunk / 2;
+  k.at = (int64_t)(c - s.start[lo]) * per;
+  k.n = (int)min((int64_t)per, (n & ((1ll << kTypeShift) - 1)) - k.at);
+  return k;
+}
+
+// 16 bytes as values of a type.
+template <int TYPE>
+struct Vec {
+  static constexpr int N = TYPE == MOE_ROW_F32 ? 4 : 8;
+  typedef typename std::conditional<TYPE == MOE_ROW_F32, uint32_t, uint16_t>::type Raw;
+  static __device__ __forceinline__ float value(const u32x4_g &v, int i) {
+    if constexpr (TYPE == MOE_ROW_F32) return __uint_as_float(v[i]);
+    else return one((Raw)(v[i >> 1] >> (16 * (i & 1))));
+  }
+  static __device__ __forceinline__ float one(Raw r) {
+    if constexpr (TYPE == MOE_ROW_F32) return __uint_as_float(r);
+    else if constexpr (TYPE == MOE_ROW_F16) return (float)__builtin_bit_cast(_Float16, r);
+    else return bf16_to_f32(r);
+  }
+  static __device__ __forceinline__ Raw raw(float f) {
+    if constexpr (TYPE == MOE_ROW_F32) return __float_as_uint(f);
+    else if constexpr (TYPE == MOE_ROW_F16) return __builtin_bit_cast(uint16_t, (_Float16)f);
+    else return __builtin_bit_cast(uint16_t, (__bf16)f);
+  }
+};
+
+// The running result of one thread: a sum of squares, or the bits of the largest
+// magnitude (as integers they order as the magnitudes do, NaN above infinity).
+template <bool INF>
+struct Norm {
+  double sum = 0.0;
+  uint32_t top = 0;
+  __device__ __forceinline__ void add(float v) {
+    if constexpr (INF) top = max(top, __float_as_uint(v) & 0x7FFFFFFFu);
+    else sum = fma((double)v, (double)v, sum);
+  }
+  __device__ __forceinline__ double get() const { return INF ? (double)__uint_as_float(top) : sum; }
+};
+template <bool INF>
+__device__ __forceinline__ double joined(double a, double b) {
+  if constexpr (INF) return a > b || a != a ? a : b;  // NaN stays
+  else return a + b;
+}
+
+// Over the workgroup, in a fixed order; in every thread.
+template <bool INF>
+__device__ __forceinline__ double block_join(double v) {
+  __shared__ double part[kThreads / 64];
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = joined<INF>(v, __shfl_xor(v, o, 64));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; w++) v = joined<INF>(v, part[w]);
+  return v;
+}
+
+// f(values index, 16 bytes) for the whole vectors of a chunk, U of a thread together.
+template <int TYPE, class F>
+__device__ __forceinline__ void each_vector(const void *x, int n, F &&f) {
+  constexpr int N = Vec<TYPE>::N, U = 4;
+  const int whole = n / N;
+  const auto *p = (const u32x4_g2 *)x;
+  for (int i = threadIdx.x; i < whole; i += U * kThreads) {
+    u32x4_g v[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const u32x4_g2 q = p[min(i + u * kThreads, whole - 1)];
+      v[u] = (u32x4_g){q[0], q[1], q[2], q[3]};
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (i + u * kThreads < whole) f(i + u * kThreads, v[u]);
+  }
+}
+
+template <int TYPE, bool INF>
+__device__ __forceinline__ void norm_chunk(const void *x, int n, Norm<INF> &acc) {
+  typedef Vec<TYPE> V;
+  each_vector<TYPE>(x, n, [&](int, const u32x4_g &v) {
+#pragma unroll
+    for (int i = 0; i < V::N; i++) acc.add(V::value(v, i));
+  });
+  const int r = n / V::N * V::N + threadIdx.x;
+  if (r < n) acc.add(V::one(((const typename V::Raw *)x)[r]));
+}
+
+template <bool INF>
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(Set s, double *__restrict__ partials) {
+  Norm<INF> acc;
+  for (int c = blockIdx.x; c < s.start[s.count]; c += gridDim.x) {
+    const Chunk k = chunk_of(s, c);
+    const char *x = (const char *)s.x[k.t] + k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
+    if (k.type == MOE_ROW_F32) norm_chunk<MOE_ROW_F32, INF>(x, k.n, acc);
+    else if (k.type == MOE_ROW_F16) norm_chunk<MOE_ROW_F16, INF>(x, k.n, acc);
+    else norm_chunk<MOE_ROW_BF16, INF>(x, k.n, acc);
+  }
+  const double v = block_join<INF>(acc.get());
+  if (threadIdx.x == 0) partials[blockIdx.x] = v;
+}
+
+// The partial sums together.
+template <bool INF>
+__device__ __forceinline__ double total_of(const double *partials, int n) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) v = joined<INF>(v, partials[i]);
+  return block_join<INF>(v);
+}
+
+template <bool INF>
+__global__ __launch_bounds__(kThreads) void grad_total_kernel(const double *__restrict__ partials, int n,
+                                                              double *total, float *norm) {
+  const double v = total_of<INF>(partials, n);
+  if (threadIdx.x) return;
+  if (total) *total = v;
+  if (norm) *norm = (float)(INF ? v : sqrt(v));
+}
+
+template <int TYPE>
+__device__ __forceinline__ void scale_chunk(const void *x, void *out, int n, float coef) {
+  typedef Vec<TYPE> V;
+  auto *dst = (u32x4_g2 *)out;
+  each_vector<TYPE>(x, n, [&](int at, const u32x4_g &v) {
+    u32x4_g2 o;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if constexpr (V::N == 4)
+        o[i] = V::raw(V::value(v, i) * coef);
+      else
+        o[i] = V::raw(V::value(v, 2 * i) * coef) | (uint32_t)V::raw(V::value(v, 2 * i + 1) * coef) << 16;
+    }
+    dst[at] = o;
+  });
+  const int r = n / V::N * V::N + threadIdx.x;
+  typedef typename V::Raw Raw;
+  if (r < n) ((Raw *)out)[r] = V::raw(V::one(((const Raw *)x)[r]) * coef);
+}
+
+// Chunks from the last to the first: what the norm read last is still in the caches.
+template <bool INF>
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(Set s, Outs o,
+                                                              const double *__restrict__ partials,
+                                                              int n, float max_norm, float *norm) {
+  const double total = total_of<INF>(partials, n);
+  const double nm = INF ? total : sqrt(total);
+  double c = (double)max_norm / (nm + 1e-6);
+  if (c > 1.0) c = 1.0;  // NaN stays
+  const float coef = (float)c;
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nm;
+  for (int i = s.start[s.count] - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
+    const Chunk k = chunk_of(s, i);
+    const int64_t at = k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
+    const char *x = (const char *)s.x[k.t] + at;
+    char *out = (char *)o.out[k.t] + at;
+    if (x == out && coef == 1.0f) continue;
+    if (k.type == MOE_ROW_F32) scale_chunk<MOE_ROW_F32>(x, out, k.n, coef);
+    else if (k.type == MOE_ROW_F16) scale_chunk<MOE_ROW_F16>(x, out, k.n, coef);
+    else scale_chunk<MOE_ROW_BF16>(x, out, k.n, coef);
+  }
+}
+
+int64_t chunks_of(const moe_grad_tensor &t) {
+  const int64_t per = t.type == MOE_ROW_F32 ? kChunk / 4 : kChunk / 2;
+  return (t.numel + per - 1) / per;
+}
+
+// The next launch's tensors, from the first one that is not in one yet; those
+// without values are left out.
+int fill(Set *s, Outs *o, int at, int count, const moe_grad_tensor *t) {
+  s->count = 0;
+  s->start[0] = 0;
+  for (; at < count && s->count < kSet; at++) {
+    if (!t[at].numel) continue;
+    const int64_t c = s->start[s->count] + chunks_of(t[at]);
+    if (c > 0x7FFFFFFF) break;  // (a launch of its own then: one tensor has fewer)
+    s->x[s->count] = t[at].x;
+    o->out[s->count] = t[at].out;
+    s->n[s->count] = t[at].numel | (int64_t)t[at].type << kTypeShift;
+    s->start[++s->count] = (int32_t)c;
+  }
+  return at;
+}
+
+int launches(int count) { return std::max(1, (count + kSet - 1) / kSet); }
+
+int groups_of(const Set &s, int nl) {
+  return (int)std::min<int64_t>(s.start[s.count], std::max(kLeastGroups, kGroups / nl));
+}
+
+// Partial sums of every launch, one behind the other; returns how many.
+template <bool INF>
+int norm_launches(int count, const moe_grad_tensor *t, double *partials, hipStream_t s) {
+  int n = 0;
+  const int nl = launches(count);
+  for (int at = 0; at < count;) {
+    Set set;
+    Outs o;
+    at = fill(&set, &o, at, count, t);
+    if (!set.count) continue;
+    const int g = groups_of(set, nl);
+    if (partials)
+      hipLaunchKernelGGL(grad_norm_kernel<INF>, dim3(g), dim3(kThreads), 0, s, set, partials + n);
+    n += g;
+  }
+  return n;
+}
+
+template <bool INF>
+void scale_launches(int count, const moe_grad_tensor *t, const double *partials, int n, float max_norm,
+                    float *norm, hipStream_t s) {
+  const int nl = launches(count);
+  bool any = false;
+  for (int at = 0; at < count;) {
+    Set set;
+    Outs o;
+    at = fill(&set, &o, at, count, t);
+    if (!set.count) continue;
+    hipLaunchKernelGGL(grad_scale_kernel<INF>, dim3(groups_of(set, nl)), dim3(kThreads), 0, s, set, o,
+                       partials, n, max_norm, any ? nullptr : norm);
+    any = true;
+  }
+  if (!any && norm)
+    hipLaunchKernelGGL(grad_total_kernel<INF>, dim3(1), dim3(kThreads), 0, s, partials, n,
+                       (double *)nullptr, norm);
+}
+
+template <bool INF>
+void clip(int count, const moe_grad_tensor *t, double *partials, float max_norm, float *norm,
+          hipStream_t s) {
+  int n = norm_launches<INF>(count, t, partials, s);
+  if (n > kMostPartials) {  // one sum of them, behind them
+    hipLaunchKernelGGL(grad_total_kernel<INF>, dim3(1), dim3(kThreads), 0, s, partials, n, partials + n,
+                       (float *)nullptr);
+    partials += n;
+    n = 1;
+  }
+  scale_launches<INF>(count, t, partials, n, max_norm, norm, s);
+}
+
+}  // namespace
+
+size_t grad_partials(int count, const moe_grad_tensor *t) {
+  return norm_launches<false>(count, t, nullptr, nullptr) + 1;
+}
+
+void launch_grad_norm(int count, const moe_grad_tensor *t, bool inf, double *partials, double *total,
+                      float *norm, hipStream_t s) {
+  auto go = [&](auto is_inf) {
+    constexpr bool INF = decltype(is_inf)::value;
+    const int n = norm_launches<INF>(count, t, partials, s);
+    hipLaunchKernelGGL(grad_total_kernel<INF>, dim3(1), dim3(kThreads), 0, s, partials, n, total, norm);
+  };
+  inf ? go(std::true_type{}) : go(std::false_type{});
+}
+
+void launch_grad_scale(int count, const moe_grad_tensor *t, bool inf, const double *partials, int n,
+                       float max_norm, float *norm, hipStream_t s) {
+  inf ? scale_launches<true>(count, t, partials, n, max_norm, norm, s)
+      : scale_launches<false>(count, t, partials, n, max_norm, norm, s);
+}
+
+void launch_grad_clip(int count, const moe_grad_tensor *t, bool inf, double *partials,
+                      float max_norm, float *norm, hipStream_t s) {
+  inf ? clip<true>(count, t, partials, max_norm, norm, s)
+      : clip<false>(count, t, partials, max_norm, norm, s);
+}
+
+}  // namespace moe

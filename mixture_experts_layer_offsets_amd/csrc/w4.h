@@ -7,7 +7,8 @@
 
 namespace moe {
 
-constexpr int kW4Mx = 0, kW4Int = 1;
+// kW4F8: the 8-bit weights of f8_device.h, which the few-token layer takes too.
+constexpr int kW4Mx = 0, kW4Int = 1, kW4F8 = 2;
 constexpr int kW4MaxSlots = 4096;  // T*k of one few-token layer call, at most
 
 // A checked moe_w4_shape and the pieces of its packed buffer.  Tiles of 16

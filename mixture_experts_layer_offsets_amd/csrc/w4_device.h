@@ -71,7 +71,20 @@ __device__ __forceinline__ rsrc_t w4_buffer(const void *p, int bytes) {
 }
 
 // One lane's scales of one tile, as loaded.
+// Codes: one lane's of a tile, kTile bytes in all.  col(i, h): first of the 8
+// contraction values that lanes l / 16 = h hold in the i-th of a step's four products.
+typedef uint4 W4Codes;
+__device__ __forceinline__ int w4_col(int i, int h) { return 32 * i + 8 * h; }
+
 struct MxFmt {
+  typedef W4Codes Codes;
+  static constexpr int kTile = 1024;
+  static __device__ __forceinline__ int col(int i, int h) { return w4_col(i, h); }
+  static __device__ __forceinline__ uint32_t part(const Codes &c, int i) {
+    const uint32_t d[4] = {c.x, c.y, c.z, c.w};
+    return d[i];
+  }
+  static constexpr bool kBlock = false;
   static constexpr bool kGrouped = false;  // scaled while unpacking
   static constexpr int SPG = 4, kScaleBytes = 64;  // bytes of a tile's scales
   static constexpr bool ZERO = false;
@@ -94,6 +107,11 @@ struct MxFmt {
 
 template <int SPG_, bool ZERO_>
 struct IntFmt {
+  typedef W4Codes Codes;
+  static constexpr int kTile = 1024;
+  static __device__ __forceinline__ int col(int i, int h) { return w4_col(i, h); }
+  static __device__ __forceinline__ uint32_t part(const Codes &c, int i) { return MxFmt::part(c, i); }
+  static constexpr bool kBlock = false;
   static constexpr bool kGrouped = true;
   static constexpr int SPG = SPG_, kScaleBytes = 32 * SPG_;
   static constexpr bool ZERO = ZERO_;
@@ -137,6 +155,37 @@ struct IntFmt {
   }
 };
 
+// E4M3 with an fp32 scale per 128 x 128 block, in f8_device.h's tiles: codes become
+// bf16 pairs in one instruction (exact), and the scale multiplies the fp32 sum of a
+// step's products.  Lane l's two 16-byte loads are chunks l / 16 and l / 16 + 4.
+struct F8Fmt {
+  struct Codes { uint4 a, b; };
+  static constexpr int kTile = 2048;
+  static __device__ __forceinline__ int col(int i, int h) { return 64 * (i >> 1) + 16 * h + 8 * (i & 1); }
+  static __device__ __forceinline__ uint2 part(const Codes &c, int i) {
+    const uint4 v = i < 2 ? c.a : c.b;
+    return i & 1 ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+  }
+  static constexpr bool kBlock = true;   // one scale a step
+  static constexpr bool kGrouped = true;  // scaled sum by sum
+  static constexpr int SPG = 1, kScaleBytes = 4;
+  static constexpr bool ZERO = false;
+  struct Scales { float s; };
+  static __device__ __forceinline__ Scales load(rsrc_t s, rsrc_t, int step, int) {
+    return {__builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(s, 0, step * kScaleBytes, 0))};
+  }
+  static __device__ __forceinline__ bf16x8 unpack(uint2 d, const Scales &, int) {
+    bf16x8 v;
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d.x, 1.0f, false);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d.x, 1.0f, true);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d.y, 1.0f, false);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d.y, 1.0f, true);
+    v[0] = p0[0]; v[1] = p0[1]; v[2] = p1[0]; v[3] = p1[1];
+    v[4] = p2[0]; v[5] = p2[1]; v[6] = p3[0]; v[7] = p3[1];
+    return v;
+  }
+};
+
 // The steps of one row of tiles (16 outputs, the whole contraction) as buffers
 // of their own: a step's loads then need one scalar offset, and no address
 // registers.
@@ -145,14 +194,18 @@ struct W4Row {
   rsrc_t c, s, z;
   W4Row() = default;
   __device__ __forceinline__ W4Row(const W4Mat &m, size_t row) {
-    c = w4_buffer(m.codes + row * m.ks * 1024, m.ks * 1024);
+    c = w4_buffer(m.codes + row * m.ks * F::kTile, m.ks * F::kTile);
     s = w4_buffer(m.scales + row * m.ks * F::kScaleBytes, m.ks * F::kScaleBytes);
     z = F::ZERO ? w4_buffer(m.zeros + row * m.ks * (F::kScaleBytes / 2), m.ks * (F::kScaleBytes / 2))
                 : s;
   }
-  __device__ __forceinline__ uint4 codes(int step) const {  // read once: not kept in the caches
-    return __builtin_bit_cast(
-        uint4, __builtin_amdgcn_raw_buffer_load_b128(c, 16 * (threadIdx.x & 63), step * 1024, 2));
+  __device__ __forceinline__ typename F::Codes codes(int step) const {  // read once: not kept in the caches
+    auto load = [&](int at) {
+      return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           c, 16 * (threadIdx.x & 63) + at, step * F::kTile, 2));
+    };
+    if constexpr (F::kTile == 1024) return load(0);
+    else return {load(0), load(1024)};
   }
   __device__ __forceinline__ typename F::Scales scales(int step) const {
     return F::load(s, z, step, threadIdx.x & 15);
@@ -163,6 +216,7 @@ struct W4Row {
 template <class Fn>
 void with_format(const W4Dims &d, Fn &&f) {
   if (d.fmt == kW4Mx) f(MxFmt{});
+  else if (d.fmt == kW4F8) f(F8Fmt{});
   else if (d.spg == 1 && !d.zeros) f(IntFmt<1, false>{});
   else if (d.spg == 2 && !d.zeros) f(IntFmt<2, false>{});
   else if (d.spg == 4 && !d.zeros) f(IntFmt<4, false>{});
@@ -197,7 +251,7 @@ struct RowLds {
 // One step: acc[j][p] += a[p] times the codes of tile j, 128 contraction values.
 // V: values of a lane's results that are wanted (INT4 scales them one by one).
 template <class F, int V, int NTW, int NB>
-__device__ __forceinline__ void w4_step(uint32_t f16, const uint4 (&cw)[NTW],
+__device__ __forceinline__ void w4_step(uint32_t f16, const typename F::Codes (&cw)[NTW],
                                         const typename F::Scales (&sc)[NTW],
                                         const bf16x8 (&a)[NB][4], f32x4 (&acc)[NTW][NB]) {
   if constexpr (!F::kGrouped) {
@@ -205,13 +259,31 @@ __device__ __forceinline__ void w4_step(uint32_t f16, const uint4 (&cw)[NTW],
     for (int i = 0; i < 4; i++) {  // the tiles' chains of products side by side
 #pragma unroll
       for (int j = 0; j < NTW; j++) {
-        const uint32_t d[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
-        const bf16x8 b = F::unpack(d[i], sc[j], i);
+        const bf16x8 b = F::unpack(F::part(cw[j], i), sc[j], i);
 #pragma unroll
         for (int p = 0; p < NB; p++)
           acc[j][p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][i], b, acc[j][p], 0, 0, 0);
       }
     }
+  } else if constexpr (F::kBlock) {
+    f32x4 part[NTW][NB];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+#pragma unroll
+      for (int j = 0; j < NTW; j++) {
+        const bf16x8 b = F::unpack(F::part(cw[j], i), sc[j], i);
+#pragma unroll
+        for (int p = 0; p < NB; p++)
+          part[j][p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a[p][i], b, i ? part[j][p] : (f32x4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NTW; j++)
+#pragma unroll
+      for (int p = 0; p < NB; p++)
+#pragma unroll
+        for (int v = 0; v < V; v++) acc[j][p][v] = fmaf(sc[j].s, part[j][p][v], acc[j][p][v]);
   } else {
     constexpr int kPer = 4 / F::SPG;  // MFMA steps of one scale group
 #pragma unroll
@@ -229,14 +301,13 @@ __device__ __forceinline__ void w4_step(uint32_t f16, const uint4 (&cw)[NTW],
       }
 #pragma unroll
       for (int j = 0; j < NTW; j++) {
-        const uint32_t d[4] = {cw[j].x, cw[j].y, cw[j].z, cw[j].w};
         const float scale = scale_value(F::scale(sc[j], g), f16);
         f32x4 part[NB];
 #pragma unroll
         for (int p = 0; p < NB; p++) part[p] = F::ZERO ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : off[p];
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-          const bf16x8 b = F::unpack(d[g * kPer + i], sc[j], i);
+          const bf16x8 b = F::unpack(F::part(cw[j], g * kPer + i), sc[j], i);
 #pragma unroll
           for (int p = 0; p < NB; p++)
             part[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][g * kPer + i], b, part[p], 0, 0,
@@ -275,16 +346,16 @@ __device__ __forceinline__ int w4_row_of(int i) {  // of sum i of w4_join
 template <class F, int U, int V, int NTW, class Row>
 __device__ __forceinline__ void w4_batches(const W4Row<F> (&m)[NTW], uint32_t f16, const Row &x, int K,
                                            int s0, int s1, f32x4 (&acc)[NTW][1]) {
-  const int h8 = 8 * ((threadIdx.x & 63) >> 4);
+  const int h = (threadIdx.x & 63) >> 4;
   for (int s = s0; s < s1; s += U) {
-    uint4 cw[U][NTW];
+    typename F::Codes cw[U][NTW];
     typename F::Scales sc[U][NTW];
     bf16x8 a[U][1][4];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int st = min(s + u, s1 - 1);
 #pragma unroll
-      for (int i = 0; i < 4; i++) a[u][0][i] = x.load(min(128 * st + 32 * i + h8, K - 8));
+      for (int i = 0; i < 4; i++) a[u][0][i] = x.load(min(128 * st + F::col(i, h), K - 8));
 #pragma unroll
       for (int j = 0; j < NTW; j++) {
         cw[u][j] = m[j].codes(st);
@@ -311,7 +382,7 @@ __device__ __forceinline__ void w4_stream(const W4Row<F> (&m)[NTW], uint32_t f16
 // (the rows lie in LDS).
 template <class F, int NTW, int D>
 struct W4Ring {
-  uint4 cw[D][NTW];
+  typename F::Codes cw[D][NTW];
   typename F::Scales sc[D][NTW];
 
   template <int d>
@@ -401,7 +472,7 @@ __device__ __forceinline__ void w4_block(const W4Row<F> (&m)[NTW], uint32_t f16,
   const int most = (ks + kBlockGroups - 1) / kBlockGroups;  // both groups meet at every barrier
   const int gt = tid % (64 * kBlockWaves), chunk = gt % 16;
   char *mine = xs + group * (2 * 16 * NB * kBlockPitch);
-  uint4 cw[D][NTW];
+  typename F::Codes cw[D][NTW];
   typename F::Scales sc[D][NTW];
   w4_u32x4 xv[D][NB];
   auto load = [&](auto d, int i) __attribute__((always_inline)) {
@@ -435,7 +506,7 @@ __device__ __forceinline__ void w4_block(const W4Row<F> (&m)[NTW], uint32_t f16,
           for (int b = 0; b < 4; b++)
             a[p][b] = __builtin_bit_cast(
                 bf16x8, *(const w4_u32x4 *)(mine + ((d & 1) * 16 * NB + 16 * p + (lane & 15)) *
-                                                       kBlockPitch + 64 * b + 16 * (lane >> 4)));
+                                                       kBlockPitch + 2 * F::col(b, lane >> 4)));
         w4_step<F, 4>(f16, cw[d], sc[d], a, acc);
       }
       load(d, i + D);

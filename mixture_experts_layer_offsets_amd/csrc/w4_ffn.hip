@@ -1,4 +1,5 @@
-// Few-token FFN of experts with 4-bit weights (w4_device.h).  A row is a (token,
+// Few-token FFN of experts with 4-bit weights, and with 8-bit ones of f8_device.h (the
+// formats of w4_device.h).  A row is a (token,
 // expert) pair, at the place f of the token's first slot with that expert:
 //   gate_up: a[f] = w silu(x Wg) (x Wu), w the routing weight (summed if the token
 //            names the expert twice), rounded to bf16;
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void w4_down_token_kernel(Down q,
           bf16x8 x[1][4];
 #pragma unroll
           for (int b = 0; b < 4; b++)
-            x[0][b] = xr.load(min(128 * cs + 32 * b + 8 * (lane >> 4), K - 8));
+            x[0][b] = xr.load(min(128 * cs + F::col(b, lane >> 4), K - 8));
           w4_step<F, 1>(m.f16, ring.cw[d], ring.sc[d], x, acc);
           const bool last = cs + 1 == ks;
           cs = last ? 0 : cs + 1;

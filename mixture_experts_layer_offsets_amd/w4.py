@@ -28,6 +28,22 @@ def _check(name, t, shape, dtypes, device=None, rows=False):
         raise ValueError(f"{name}: strides {t.stride()} are not those of plain rows")
 
 
+def decode_args(s, dev, x, w_router, bias, topk_idx, topk_w, out):
+    """The checked arguments of a few-token layer's call; its ``out``."""
+    slots, tokens = (s.tokens, s.top_k), (s.tokens, s.hidden)
+    _check("x", x, tokens, _BF16, dev)
+    for name, t, shape, dtypes in (("w_router", w_router, (s.hidden, s.experts), _BF16),
+                                   ("bias", bias, (s.experts,), (torch.float32,)),
+                                   ("topk_idx", topk_idx, slots, (torch.int32,)),
+                                   ("topk_w", topk_w, slots, (torch.float32,))):
+        if t is not None:
+            _check(name, t, shape, dtypes, dev)
+    if out is None:
+        out = torch.empty(tokens, dtype=x.dtype, device=dev)
+    _check("out", out, tokens, _BF16, dev)
+    return out
+
+
 class W4Linear:
     """Packed 4-bit matrices [groups][k][n] and their products with few rows.
 
@@ -182,19 +198,8 @@ class W4Decoder:
 
     def __call__(self, x, w_router=None, bias=None, topk_idx=None, topk_w=None, out=None):
         """[tokens][hidden] bf16 -> the same; routing as MoeLayer.decode."""
-        s, dev = self.shape, self.device
-        slots, tokens = (s.tokens, s.top_k), (s.tokens, s.hidden)
-        _check("x", x, tokens, _BF16, dev)
-        for name, t, shape, dtypes in (("w_router", w_router, (s.hidden, s.experts), _BF16),
-                                       ("bias", bias, (s.experts,), (torch.float32,)),
-                                       ("topk_idx", topk_idx, slots, (torch.int32,)),
-                                       ("topk_w", topk_w, slots, (torch.float32,))):
-            if t is not None:
-                _check(name, t, shape, dtypes, dev)
-        if out is None:
-            out = torch.empty(tokens, dtype=x.dtype, device=dev)
-        _check("out", out, tokens, _BF16, dev)
-        with torch.cuda.device(dev):
-            _lib.moe_w4_decode_fwd(s, self.experts, x, w_router, bias, topk_idx, topk_w, out,
-                                   self.ws)
+        out = decode_args(self.shape, self.device, x, w_router, bias, topk_idx, topk_w, out)
+        with torch.cuda.device(self.device):
+            _lib.moe_w4_decode_fwd(self.shape, self.experts, x, w_router, bias, topk_idx, topk_w,
+                                   out, self.ws)
         return out
