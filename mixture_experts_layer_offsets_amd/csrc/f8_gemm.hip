@@ -10,6 +10,7 @@ namespace {
 
 constexpr int kTN = 256;       // outputs of a tile
 constexpr int kThreads = 512;  // eight waves, two a SIMD
+constexpr int kRing = 4;       // products of a wave in flight (no more than NJ)
 
 // Operands of either product.  "rows" are the instruction's second operand: rows of
 // x, or for the weight gradient its columns.
@@ -29,8 +30,7 @@ struct Geo {
   static constexpr int WN = TM == 256 ? 2 : TM == 128 ? 4 : 8;  // waves along the outputs
   static constexpr int NI = kTN / WN / 16, NJ = 4;              // 16 x 16 results of a wave
   static constexpr int XB = TM * kF8Block, WB = kTN * kF8Block;  // bytes of a stage
-  static constexpr int XQ = XB / 8192, WQ = WB / 8192;           // loads of a wave and stage
-  static constexpr int Lds = XB + WB + kThreads * 4;             // and the outputs' scales
+  static constexpr int XQ = XB / 8192;  // loads of a wave and stage, of rows
 };
 
 // One tile of TM rows x 256 outputs.  Operands move from memory straight into LDS, a
@@ -38,8 +38,11 @@ struct Geo {
 // next one arrives.  Rows lie in LDS 128 bytes apart with their chunks exchanged by
 // the row's low bits, tiles of weights in the order of the waves' reads.
 //   COLS: the weight gradient, whose outputs have scales of their own.
+// X, A, B: rows, first halves and second halves of the waves' tiles, of two stages: arrays
+// of their own, so that the compiler can tell what is read from what is being filled.
 template <int TM, bool COLS>
-__device__ __forceinline__ void f8_tile(const Args &p, uint8_t *L0, uint8_t *L1) {
+__device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1, uint8_t *A0,
+                                        uint8_t *A1, uint8_t *B0, uint8_t *B1) {
   using G = Geo<TM>;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -78,164 +81,222 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *L0, uint8_t *L1)
   const float *wsc = COLS ? p.ws + (size_t)step0 * p.npitch + n0
                           : p.ws + ((size_t)g * p.nt + min((n0 + wn0) / 16, p.nt - 1)) * p.wsteps;
   const int tiles = min(kTN / 16, p.nt - n0 / 16);
-  const int wbytes = (tiles * p.wsteps - (COLS ? step0 : 0)) * kF8Tile;
-  uint32_t ox[G::XQ], ow[G::WQ];
-#pragma unroll
-  for (int q = 0; q < G::XQ; q++) {
-    const int row = (wave * G::XQ + q) * 8 + (lane >> 3);
-    ox[q] = row * kF8Block + (((lane & 7) ^ (row & 7)) << 4);
-  }
-#pragma unroll
-  for (int q = 0; q < G::WQ; q++) {
-    const int piece = wave * G::WQ + q;
-    ow[q] = (piece >> 1) * p.wsteps * kF8Tile + (piece & 1) * 1024 + lane * 16;
-  }
-  // stage kt to L; past the end: zeros, from empty buffers (without a branch, which
-  // the scheduler would not move the loop's work across)
-  auto dma = [&](uint8_t *L, int kt) {
-    const int k1 = min(kt, steps - 1), live = kt < steps ? -1 : 0;
-    const f8_rsrc_t rX =
-        f8_buffer(xc + (size_t)k1 * p.xpitch * kF8Block, valid * kF8Block & live);
-#pragma unroll
-    for (int q = 0; q < G::XQ; q++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, (lds_ptr_t)(L + (wave * G::XQ + q) * 1024), 16,
-                                               ox[q], 0, 0, 0);
-    const f8_rsrc_t rW = f8_buffer(wc, wbytes & live);
-#pragma unroll
-    for (int q = 0; q < G::WQ; q++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rW,
-                                               (lds_ptr_t)(L + G::XB + (wave * G::WQ + q) * 1024), 16,
-                                               ow[q], k1 * kF8Tile, 0, 0);
-    if constexpr (COLS) {  // 4 bytes a lane, all waves alike: the second half is zeros
-      const f8_rsrc_t rS =
-          f8_buffer(wsc + (size_t)k1 * p.npitch, min(kTN, p.npitch - n0) * 4 & live);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_ptr_t)(L + G::XB + G::WB + wave * 256), 4,
-                                               tid * 4, 0, 0, 0);
-    }
+  const int lane16 = lane * 16;
+  // row (lane / 8) of the wave's first 8, its chunks exchanged by the row
+  const int ox = wave * G::XQ * 1024 + (lane >> 3) * kF8Block + (((lane & 7) ^ (lane >> 3)) << 4);
+  // Stage kt to L, load by load: q < XQ rows, then the outputs' scales (COLS).  Past the
+  // end: the last stage again, not used (without a branch, which the scheduler would
+  // not move the loop's work across).
+  auto dma_x = [&](uint8_t *X, int kt, int q) {
+    const int k1 = min(kt, steps - 1);
+    const f8_rsrc_t rX = f8_buffer(xc + (size_t)k1 * p.xpitch * kF8Block, valid * kF8Block);
+    const lds_ptr_t to = (lds_ptr_t)(X + wave * G::XQ * 1024);
+    // the constant offset moves both addresses
+    if (q == 0) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 0, 0);
+    if (q == 1) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 1024, 0);
+    if (q == 2) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 2048, 0);
+    if (q == 3) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 3072, 0);
   };
-  // the scales of this lane's rows, and of the wave's outputs (forward)
+  // ... and one tile a wave of the first or second half of each wave's tiles, in two
+  auto dma_w = [&](uint8_t *W, int kt, int half, int q) {
+    const int k1 = min(kt, steps - 1);
+    const int at = wave / (G::NI / 2) * G::NI + wave % (G::NI / 2) + half * (G::NI / 2);
+    const int t = min(at, tiles - 1);  // past the last one: that one again
+    const f8_rsrc_t rW = f8_buffer(wc + ((size_t)t * p.wsteps + k1) * kF8Tile, kF8Tile);
+    const lds_ptr_t to = (lds_ptr_t)(W + wave * kF8Tile);
+    if (q == 0) __builtin_amdgcn_raw_ptr_buffer_load_lds(rW, to, 16, lane16, 0, 0, 0);
+    if (q == 1) __builtin_amdgcn_raw_ptr_buffer_load_lds(rW, to, 16, lane16, 0, 1024, 0);
+  };
+  // ... the scales of the first or second half's outputs behind their tiles (COLS), 4
+  // bytes a lane, all waves alike: the last six's are zeros
+  const int osw = ((tid >> 4) / (G::NI / 2) * G::NI + (tid >> 4) % (G::NI / 2)) * 64 + l16 * 4;
+  auto dma_s = [&](uint8_t *W, int kt, int half) {
+    const int k1 = min(kt, steps - 1);
+    const f8_rsrc_t r = f8_buffer(wsc + (size_t)k1 * p.npitch,
+                                  wave < 2 ? min(kTN, p.npitch - n0) * 4 : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(W + G::WB / 2 + wave * 256), 4, osw,
+                                             half * (G::NI / 2) * 64, 0, 0);
+  };
+  // the rows' scales, and behind them that of the wave's outputs (forward)
+  constexpr int NS = COLS ? G::NJ : G::NJ + 1;
+  const int os = (wm0 + l16) * 4;
   auto scales = [&](int kt, float *s) {
     const int k1 = min(kt, steps - 1);
     const f8_rsrc_t r = f8_buffer(xs + (size_t)k1 * p.spitch, valid * 4);
 #pragma unroll
     for (int j = 0; j < G::NJ; j++)
-      s[j] = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(r, (wm0 + 16 * j + l16) * 4, 0, 0));
+      s[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, os + 64 * j, 0, 0));
+    if constexpr (!COLS)
+      s[G::NJ] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(f8_buffer(wsc, p.wsteps * 4), 0, k1 * 4, 0));
   };
   f32x4 acc[G::NI][G::NJ];
 #pragma unroll
   for (int i = 0; i < G::NI; i++)
 #pragma unroll
     for (int j = 0; j < G::NJ; j++) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  auto compute = [&](const uint8_t *L, const float *s) {
-    i32x8_t xf[G::NJ];
-    const uint8_t *X = L + (wm0 + l16) * kF8Block, *W = L + G::XB + (wn0 / 16) * kF8Tile + lane * 16;
-    const int c0 = (h ^ (l16 & 7)) << 4, c1 = ((h + 4) ^ (l16 & 7)) << 4;
+  const int xo = (wm0 + l16) * kF8Block + ((h ^ (l16 & 7)) << 4);  // and, 64 bytes on, h + 4
+  const int wo = (wave % G::WN) * (G::NI / 2) * kF8Tile + lane16;  // the wave's tiles, of either half
+  const int swo = G::WB / 2 + (wave % G::WN) * (G::NI / 2) * 64 + 16 * h;
+  i32x8_t xf[G::NJ], wf[2];
+  f32x4 d[kRing], sw[2];
+  auto load_x = [&](const uint8_t *X, int j) {
+    xf[j] = f8_frag(*(const u32x4_t *)(X + xo + j * 16 * kF8Block),
+                         *(const u32x4_t *)(X + (xo ^ 64) + j * 16 * kF8Block));
+  };
+  auto load_w = [&](const uint8_t *A, const uint8_t *B, int i) {
+    const uint8_t *W = (i < G::NI / 2 ? A : B) + wo + i % (G::NI / 2) * kF8Tile;
+    wf[i & 1] = f8_frag(*(const u32x4_t *)W, *(const u32x4_t *)(W + 1024));
+  };
+  auto load_s = [&](const uint8_t *A, const uint8_t *B, int i) {
+    if constexpr (COLS)
+      sw[i & 1] = *(const f32x4 *)((i < G::NI / 2 ? A : B) + swo + i % (G::NI / 2) * 64);
+  };
+  // product q = i NJ + j of a stage, whose rows have the scales s
+  auto scale = [&](int q, const float *s) {
+    const int i = q / G::NJ, j = q % G::NJ;
+#pragma unroll
+    for (int v = 0; v < 4; v++)
+      acc[i][j][v] = fmaf(COLS ? s[j] * sw[i & 1][v] : s[j], d[q % kRing][v], acc[i][j][v]);
+  };
+  // Xc, Ac, Bc hold stage kt, its rows and first tile read; the last products
+  // of the stage before are not scaled yet (so, sc, s1: the rows' scales of stages kt - 1,
+  // kt, kt + 1).  Xn and An hold stage kt + 1.  In the middle the waves meet: what was sent for a stage
+  // ago is there then; Xc, Ac and Bn (stage kt - 1) have been read and are refilled, load
+  // by load between the products (in a burst the loads would stall the wave).  The next
+  // stage's rows are read as the last tile's products leave theirs.
+  float so[G::NJ], sc[NS], s1[NS];
+  auto stage = [&](uint8_t *Xc, uint8_t *Ac, uint8_t *Bc, uint8_t *Xn, uint8_t *An, uint8_t *Bn,
+                   int kt) {
+    constexpr int NQ = G::NI * G::NJ, kLag = kRing - 1, kHalf = G::NI / 2;
+    float sn[NS];  // of stage kt + 2: loads that nothing waits for before the next meeting
 #pragma unroll
     for (int j = 0; j < G::NJ; j++)
-      xf[j] = f8_frag(*(const u32x4_t *)(X + j * 16 * kF8Block + c0),
-                      *(const u32x4_t *)(X + j * 16 * kF8Block + c1));
-    // one tile of outputs after the other: its products go out between the scaling of
-    // the one before, and the next one's weights are read meanwhile
-    i32x8_t wf[2];
-    f32x4 d[2][G::NJ], sw[2];
-    auto load = [&](int i) {
-      wf[i & 1] = f8_frag(*(const u32x4_t *)(W + i * kF8Tile),
-                          *(const u32x4_t *)(W + i * kF8Tile + 1024));
-      if constexpr (COLS)
-        sw[i & 1] = *(const f32x4 *)(L + G::XB + G::WB + (wn0 + 16 * i + 4 * h) * 4);
-    };
-    f32x4 sp;
-    auto scale = [&](int i, int j) {
-#pragma unroll
-      for (int v = 0; v < 4; v++)
-        acc[i][j][v] = fmaf(COLS ? s[j] * sp[v] : s[j], d[i & 1][j][v], acc[i][j][v]);
-    };
-    load(0);
+      if constexpr (!COLS) sc[j] *= sc[G::NJ];
 #pragma unroll
     for (int i = 0; i < G::NI; i++) {
-      if constexpr (COLS)
-        if (i) sp = sw[(i - 1) & 1];
-      if (i + 1 < G::NI) load(i + 1);
+      if (i == kHalf - 1) {
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+        lds_barrier();
+        scales(kt + 2, sn);
+      }
+      if (i + 1 < G::NI) load_w(Ac, Bc, i + 1);
+      else load_w(An, Bn, 0);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < G::NJ; j++) {
-        d[i & 1][j] = f8_dot(wf[i & 1], xf[j]);
-        if (i) scale(i - 1, j);
+        const int q = i * G::NJ + j;
+        d[q % kRing] = f8_dot(wf[i & 1], xf[j]);
+        if (i == G::NI - 1) load_x(Xn, j);
+        if (q >= kLag) scale(q - kLag, sc);
+        else scale(NQ - kLag + q, so);
+        // the scales of two tiles back have been used
+        if (j == kLag - 1) {
+          if (i + 1 < G::NI) load_s(Ac, Bc, i + 1);
+          else load_s(An, Bn, 0);
+        }
+        const int n = q - (kHalf - 1) * G::NJ;
+        if (n >= 0 && n < 2) dma_w(Bn, kt + 1, 1, n);
+        else if (n >= 2 && n < 2 + G::XQ) dma_x(Xc, kt + 2, n - 2);
+        else if (n >= 2 && n < 4 + G::XQ) dma_w(Ac, kt + 2, 0, n - 2 - G::XQ);
+        else if (COLS && n == 4 + G::XQ) dma_s(Ac, kt + 2, 0);
+        else if (COLS && n == 5 + G::XQ) dma_s(Bn, kt + 1, 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if constexpr (COLS) sp = sw[(G::NI - 1) & 1];
 #pragma unroll
-    for (int j = 0; j < G::NJ; j++) scale(G::NI - 1, j);
-  };
-  // Lc holds stage kt (its rows' scales in sc), Ln receives the next one.
-  auto stage = [&](uint8_t *Lc, uint8_t *Ln, int kt, float *sc, float *sn) {
-    dma(Ln, kt + 1);
-    if constexpr (!COLS) {
-      const float sw = wsc[kt];
-#pragma unroll
-      for (int j = 0; j < G::NJ; j++) sc[j] *= sw;
+    for (int j = 0; j < NS; j++) {
+      if (j < G::NJ) so[j] = sc[j];
+      sc[j] = s1[j];
+      s1[j] = sn[j];
     }
-    scales(kt + 1, sn);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(Lc, sc);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kVmcnt0);
-    barrier_after_wait();
   };
   if (steps > 0) {
-    float s0[G::NJ], s1[G::NJ];
-    dma(L0, 0);
-    scales(0, s0);
+#pragma unroll
+    for (int q = 0; q < G::XQ; q++) {
+      dma_x(X0, 0, q);
+      dma_x(X1, 1, q);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      dma_w(A0, 0, 0, q);
+      dma_w(B0, 0, 1, q);
+      dma_w(A1, 1, 0, q);
+    }
+    if constexpr (COLS) {
+      dma_s(A0, 0, 0);
+      dma_s(B0, 0, 1);
+      dma_s(A1, 1, 0);
+    }
+    scales(0, sc);
+    scales(1, s1);
+#pragma unroll
+    for (int j = 0; j < G::NJ; j++) so[j] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kRing; q++) d[q] = sw[q & 1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     __builtin_amdgcn_s_waitcnt(kVmcnt0);
     barrier_after_wait();
+#pragma unroll
+    for (int j = 0; j < G::NJ; j++) load_x(X0, j);
+    load_w(A0, B0, 0);
+    load_s(A0, B0, 0);
     int kt = 0;
     for (; kt + 2 <= steps; kt += 2) {
-      stage(L0, L1, kt, s0, s1);
-      stage(L1, L0, kt + 1, s1, s0);
+      stage(X0, A0, B0, X1, A1, B1, kt);
+      stage(X1, A1, B1, X0, A0, B0, kt + 1);
     }
-    if (kt < steps) stage(L0, L1, kt, s0, s1);
+    if (kt < steps) stage(X0, A0, B0, X1, A1, B1, kt);
+#pragma unroll
+    for (int q = 0; q < kRing - 1; q++) scale(G::NI * G::NJ - (kRing - 1) + q, so);
   }
+  __builtin_amdgcn_s_waitcnt(kVmcnt0);  // the last loads, not used
   __syncthreads();
-  // results to LDS, 512 bytes a row with its 16-byte chunks exchanged by the row, then
-  // out as whole rows
-  constexpr int kRows = TM / 2;  // rows of one buffer
-  static_assert(kRows * 512 <= G::Lds, "the tile's results fit");
-#pragma unroll
-  for (int j = 0; j < G::NJ; j++) {
-    const int r = wm0 + 16 * j + l16;
-    uint8_t *row = (r < kRows ? L0 : L1) + (r % kRows) * 512;
-#pragma unroll
-    for (int i = 0; i < G::NI; i++) {
-      const int c = wn0 + 16 * i + 4 * h;
-      uint16_t o[4];
-#pragma unroll
-      for (int v = 0; v < 4; v++) o[v] = f8_to16(acc[i][j][v], p.f16);
-      *(uint2 *)(row + ((((c >> 3) ^ r) & 31) << 4) + (c & 4) * 2) =
-          make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
-    }
-  }
-  __syncthreads();
+  // results to LDS, half of the rows a pass, 512 bytes a row with its 16-byte chunks
+  // exchanged by the row, then out as whole rows
+  constexpr int kRows = TM / 4;  // rows of X0, and of X1
   const int c = tid & 31, cols = p.n - n0 - 8 * c;
-  for (int r = tid >> 5; r < valid; r += kThreads / 32) {
-    const u32x4_t v =
-        *(const u32x4_t *)((r < kRows ? L0 : L1) + (r % kRows) * 512 + (((c ^ r) & 31) << 4));
-    uint16_t *dst = out + (size_t)r * p.ostride + n0 + 8 * c;
-    if (cols >= 8)
-      *(u32x4_a2 *)dst = (u32x4_a2){v[0], v[1], v[2], v[3]};
-    else
+  for (int r0 = 0; r0 < TM; r0 += 2 * kRows) {
 #pragma unroll
-      for (int e = 0; e < 8; e++)
-        if (e < cols) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    for (int j = 0; j < G::NJ; j++) {
+      const int r = wm0 + 16 * j + l16 - r0;
+      if (wm0 + 16 * j < r0 || wm0 + 16 * j >= r0 + 2 * kRows) continue;
+#pragma unroll
+      for (int i = 0; i < G::NI; i++) {
+        const int at = wn0 + 16 * i + 4 * h;
+        uint16_t o[4];
+#pragma unroll
+        for (int v = 0; v < 4; v++) o[v] = f8_to16(acc[i][j][v], p.f16);
+        const int b = r % kRows * 512 + ((((at >> 3) ^ r) & 31) << 4) + (at & 4) * 2;
+        const uint2 w = make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
+        if (wm0 + 16 * j - r0 < kRows) *(uint2 *)(X0 + b) = w;
+        else *(uint2 *)(X1 + b) = w;
+      }
+    }
+    __syncthreads();
+    for (int r = tid >> 5; r < min(2 * kRows, valid - r0); r += kThreads / 32) {
+      const int b = r % kRows * 512 + (((c ^ r) & 31) << 4);
+      u32x4_t v;
+      if (r < kRows) v = *(const u32x4_t *)(X0 + b);
+      else v = *(const u32x4_t *)(X1 + b);
+      uint16_t *dst = out + (size_t)(r0 + r) * p.ostride + n0 + 8 * c;
+      if (cols >= 8)
+        *(u32x4_a2 *)dst = (u32x4_a2){v[0], v[1], v[2], v[3]};
+      else
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+          if (e < cols) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
+    __syncthreads();
   }
 }
 
 template <int TM, bool COLS>
 __global__ __launch_bounds__(kThreads, 2) void f8_gemm_kernel(Args p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t L0[Geo<TM>::Lds];
-  __shared__ __attribute__((aligned(1024))) uint8_t L1[Geo<TM>::Lds];
-  f8_tile<TM, COLS>(p, L0, L1);
+  using G = Geo<TM>;
+  __shared__ __attribute__((aligned(1024))) uint8_t X0[G::XB], X1[G::XB];
+  constexpr int kHalf = G::WB / 2 + (COLS ? 2048 : 0);  // and scales
+  __shared__ __attribute__((aligned(1024))) uint8_t A0[kHalf], A1[kHalf], B0[kHalf], B1[kHalf];
+  f8_tile<TM, COLS>(p, X0, X1, A0, A1, B0, B1);
 }
 
 }  // namespace
