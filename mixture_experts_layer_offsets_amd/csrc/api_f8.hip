@@ -139,7 +139,7 @@ size_t moe_f8_linear_workspace_bytes(const moe_f8_shape *shape, int32_t rows) {
   F8Dims d;
   size_t scales;
   if (f8_dims(shape, &d) || check_rows(d, rows, (const int32_t *)1)) return 0;
-  return f8_few(d, rows) ? 256 : rows_bytes(d, rows, &scales);
+  return f8_few_staged(d, rows) ? 256 : rows_bytes(d, rows, &scales);
 }
 
 int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x, int64_t x_stride,
@@ -156,7 +156,7 @@ int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x, int64_
   if (!rows) return MOE_OK;
   const F8Rows xr{(const uint16_t *)x, x_stride, d.f16};
   hipStream_t s = (hipStream_t)stream;
-  if (f8_few(d, rows)) {
+  if (f8_few_staged(d, rows)) {
     launch_f8_few_rows(d, rows, xr, offsets, packed, (uint16_t *)out, out_stride, s);
     return status();
   }
@@ -166,7 +166,8 @@ int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x, int64_
   uint8_t *codes = (uint8_t *)ws;
   float *scales = (float *)(codes + at);
   launch_f8_quant_rows(xr, rows, d.k, codes, scales, s);
-  launch_f8_gemm(d, rows, codes, scales, offsets, packed, (uint16_t *)out, out_stride, s);
+  (f8_few(d, rows) ? launch_f8_few : launch_f8_gemm)(d, rows, codes, scales, offsets, packed,
+                                                     (uint16_t *)out, out_stride, s);
   return status();
 }
 

@@ -60,8 +60,9 @@ void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float 
                    hipStream_t s);
 void launch_f8_few_rows(const F8Dims &d, int rows, const F8Rows &x, const int32_t *offsets,
                         const void *packed, uint16_t *out, long ostride, hipStream_t s);
-// Whether launch_f8_few takes the product.
+// Whether launch_f8_few takes the product, and launch_f8_few_rows.
 bool f8_few(const F8Dims &d, int rows);
+bool f8_few_staged(const F8Dims &d, int rows);
 
 // dw[g][k][n] = sum over the rows of group g of x[r][k] dy[r][n], from
 // launch_f8_quant_cols of x (rows) and dy (tiles).

@@ -43,7 +43,6 @@ typedef float f32x2_f8 __attribute__((ext_vector_type(2)));
 typedef __amdgpu_buffer_rsrc_t f8_rsrc_t;
 
 constexpr int kF8Tile = 2048;            // bytes of a tile
-constexpr float kF8Most = 448.0f;        // E4M3's largest value
 constexpr float kF8Least = 0x1p-100f;    // smallest scale
 constexpr float kF8PerMost = 1.0f / 448.0f;
 
@@ -76,12 +75,43 @@ __device__ __forceinline__ float f8_scale(uint32_t top, float *inv) {
   return s;
 }
 
-// Four values to four codes: scaled in fp32, held at +-448 and rounded to nearest
-// even.
+// Four values to four codes: scaled in fp32 and rounded to nearest even.  What is scaled
+// is at most 448 (1 + 2^-21): s is off by two roundings and its reciprocal by one; below
+// 464 the conversion gives 448.
 __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d, float inv) {
-  auto put = [&](float v) { return fminf(fmaxf(v * inv, -kF8Most), kF8Most); };
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(put(a), put(b), 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(put(c), put(d), w, true);
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+}
+
+// 8 values of a 16-bit row from column c on, as loaded; zeros past its k values.
+__device__ __forceinline__ u32x4_t f8_load8(const uint16_t *row, int c, int k) {
+  if (c + 8 <= k) {
+    const u32x4_a2 q = *(const u32x4_a2 *)(row + c);
+    return (u32x4_t){q[0], q[1], q[2], q[3]};
+  }
+  u32x4_t u;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t lo = c + 2 * i < k ? row[c + 2 * i] : 0;
+    u[i] = lo | (c + 2 * i + 1 < k ? (uint32_t)row[c + 2 * i + 1] << 16 : 0);
+  }
+  return u;
+}
+
+// 16 lanes hold a block, 8 values each: this lane's 8 codes, and the scale.
+template <bool F16>
+__device__ __forceinline__ uint2 f8_quantize8(const u32x4_t &u, float *s) {
+  // the magnitudes of 16 bits order as those of 32 do
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; i++) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 16));
+  float inv, v[8];
+  *s = f8_scale(f8_mag(f8_from16(top, F16)), &inv);
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = f8_from16((u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, F16);
+  return make_uint2(f8_codes4(v[0], v[1], v[2], v[3], inv), f8_codes4(v[4], v[5], v[6], v[7], inv));
 }
 
 // 128 products of codes, summed from zero.

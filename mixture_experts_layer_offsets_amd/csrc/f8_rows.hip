@@ -9,32 +9,6 @@ namespace moe {
 
 namespace {
 
-// 8 values of a row from column c on, zeros past its k values.
-template <bool F16>
-__device__ __forceinline__ void load8(const uint16_t *row, int c, int k, float *v) {
-  uint32_t u[4];
-  if (c + 8 <= k) {
-    const u32x4_a2 q = *(const u32x4_a2 *)(row + c);
-#pragma unroll
-    for (int i = 0; i < 4; i++) u[i] = q[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t lo = c + 2 * i < k ? row[c + 2 * i] : 0;
-      u[i] = lo | (c + 2 * i + 1 < k ? (uint32_t)row[c + 2 * i + 1] << 16 : 0);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = f8_from16((u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, F16);
-}
-
-// The largest of the 16 lanes of a row of lanes.
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int o = 8; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 16));
-  return v;
-}
-
 // 16 lanes take a block, 8 values each; a workgroup takes 16 rows x kBlocks blocks,
 // so that it reads kBlocks 256 bytes of each row and writes 2 KB runs of codes.  Grid
 // (blocks / kBlocks, rows / 16), rows past 2^16 workgroups in turn.
@@ -49,22 +23,16 @@ __global__ __launch_bounds__(256) void f8_quant_rows_kernel(const uint16_t *__re
   for (long r0 = (long)blockIdx.y * 16; r0 < rows; r0 += 16L * gridDim.y) {
     const long r = r0 + (tid >> 4);
     const long rr = r < rows ? r : rows - 1;
-    float v[kBlocks][8];
+    u32x4_t u[kBlocks];
 #pragma unroll
-    for (int b = 0; b < kBlocks; b++)
-      load8<F16>(x + rr * stride, (kb0 + b) * kF8Block + 8 * i, k, v[b]);
+    for (int b = 0; b < kBlocks; b++) u[b] = f8_load8(x + rr * stride, (kb0 + b) * kF8Block + 8 * i, k);
 #pragma unroll
     for (int b = 0; b < kBlocks; b++) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int q = 0; q < 8; q++) top = max(top, f8_mag(v[b][q]));
-      float inv;
-      const float s = f8_scale(max16(top), &inv);
+      float s;
+      const uint2 c = f8_quantize8<F16>(u[b], &s);
       if (r < rows && kb0 + b < ks) {
         const size_t at = (size_t)(kb0 + b) * rows + r;
-        *(uint2 *)(codes + at * kF8Block + 8 * i) =
-            make_uint2(f8_codes4(v[b][0], v[b][1], v[b][2], v[b][3], inv),
-                       f8_codes4(v[b][4], v[b][5], v[b][6], v[b][7], inv));
+        *(uint2 *)(codes + at * kF8Block + 8 * i) = c;
         if (i == 0) scales[at] = s;
       }
     }
