@@ -27,11 +27,53 @@ struct Args {
 
 template <int TM>
 struct Geo {
-  static constexpr int WN = TM == 256 ? 2 : TM == 128 ? 4 : 8;  // waves along the outputs
+  static constexpr int WN = TM == 256 ? 2 : 4;  // waves along the outputs
   static constexpr int NI = kTN / WN / 16, NJ = 4;              // 16 x 16 results of a wave
   static constexpr int XB = TM * kF8Block, WB = kTN * kF8Block;  // bytes of a stage
   static constexpr int XQ = XB / 8192;  // loads of a wave and stage, of rows
 };
+
+// Tiles of T rows over the groups, one group behind the other: how many there are, and
+// where tile i lies.  Every wave adds the groups' lengths up by itself, 64 groups at a time.
+struct Place {
+  int g, first;  // group, and its first tile
+};
+template <class F>
+__device__ __forceinline__ int each_64_groups(const int32_t *offsets, int groups, int rows, int T, F &&f) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int g0 = 0; g0 < groups; g0 += 64) {
+    int n = 0;
+    if (g0 + lane < groups) {
+      const F8Span sp = f8_span(offsets, g0 + lane, rows);
+      n = (sp.end - sp.begin + T - 1) / T;
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    if (f(g0, before, n, before + upto)) break;
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return before;
+}
+__device__ __forceinline__ int tiles_of(const int32_t *offsets, int groups, int rows, int T) {
+  return each_64_groups(offsets, groups, rows, T, [](int, int, int, int) { return false; });
+}
+__device__ __forceinline__ Place place_of(const int32_t *offsets, int groups, int rows, int T, int i) {
+  Place p{0, 0};
+  each_64_groups(offsets, groups, rows, T, [&](int g0, int, int n, int upto) {
+    const uint64_t in = __ballot(i >= upto - n && i < upto);
+    if (!in) return false;
+    const int l = __ffsll((unsigned long long)in) - 1;
+    p.g = g0 + l;
+    p.first = __builtin_amdgcn_readlane(upto - n, l);
+    return true;
+  });
+  return p;
+}
 
 // One tile of TM rows x 256 outputs.  Operands move from memory straight into LDS, a
 // block of 128 contraction values a stage, two stages in turn: while one is used the
@@ -46,7 +88,7 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
   using G = Geo<TM>;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int mt, nt, g, first, m0, valid, step0, steps;
+  int mt, nt, g, m0, valid, step0, steps;
   size_t xrow;  // first row of the tile, in the operand
   uint16_t *out;
   if constexpr (COLS) {
@@ -61,11 +103,13 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     xrow = m0;
     out = p.out + ((size_t)g * p.xrows + m0) * p.ostride;
   } else {
-    tile_of_block(blockIdx.x, p.MT, p.nN, mt, nt);
-    g = f8_group_at(p.offsets, p.groups, p.rows, TM, mt, &first);
+    const int MT = tiles_of(p.offsets, p.groups, p.rows, TM);
+    if (blockIdx.x >= (unsigned)(MT * p.nN)) return;
+    tile_of_block(blockIdx.x, MT, p.nN, mt, nt);
+    const Place at = place_of(p.offsets, p.groups, p.rows, TM, mt);
+    g = at.g;
     const F8Span sp = f8_span(p.offsets, g, p.rows);
-    m0 = sp.begin + (mt - first) * TM;
-    if (mt < first || m0 >= sp.end) return;  // an empty place
+    m0 = sp.begin + (mt - at.first) * TM;
     valid = min(TM, sp.end - m0);
     step0 = 0;
     steps = p.wsteps;
@@ -315,13 +359,17 @@ void launch_f8_gemm(const F8Dims &d, int rows, const uint8_t *codes, const float
   a.wsteps = d.ks;
   a.nN = (d.n + kTN - 1) / kTN;
   auto go = [&](auto kernel, int TM) {
-    a.MT = rows / TM + d.groups;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((long)a.MT * a.nN)), dim3(kThreads), 0, s, a);
+    const long most = d.groups == 1 ? (rows + TM - 1) / TM : rows / TM + d.groups;  // row tiles
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(most * a.nN)), dim3(kThreads), 0, s, a);
   };
-  const int avg = (rows + d.groups - 1) / d.groups;
-  if (avg > 128) go(f8_gemm_kernel<256, false>, 256);
-  else if (avg > 64) go(f8_gemm_kernel<128, false>, 128);
-  else go(f8_gemm_kernel<64, false>, 64);
+  // Tiles of 256 rows read less for the same products; those of 128 take about 0.75 of
+  // their time, and fill the chip where tiles are few (4096 x 4096, us with 256 / 128: 1024
+  // rows 53 / 37, 2048 rows 57 / 46, 4096 rows 77 / 90; 64 groups of 384 rows, 2816 x 2048:
+  // 239 / 284): by the rounds of 256 workgroups that either takes.
+  const long avg = (rows + d.groups - 1) / d.groups;
+  auto rounds = [&](int TM) { return ((avg + TM - 1) / TM * d.groups * a.nN + 255) / 256; };
+  if (4 * rounds(256) <= 3 * rounds(128)) go(f8_gemm_kernel<256, false>, 256);
+  else go(f8_gemm_kernel<128, false>, 128);
 }
 
 void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *xs,

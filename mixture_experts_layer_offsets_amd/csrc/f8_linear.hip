@@ -38,8 +38,8 @@ __device__ __forceinline__ void add_scaled(f32x4 &acc, const f32x4 &d, float s) 
   for (int v = 0; v < 4; v++) acc[v] = fmaf(s, d[v], acc[v]);
 }
 
-// The waves' sums of NB blocks of 16 rows from row r0 on, nr of them, added in wave order
-// and written.
+// The waves' sums of NB blocks of 16 rows from row r0 on, nr of them, with tile t, added
+// in wave order and written.
 template <int WAVES, int NB>
 __device__ __forceinline__ void put(const Few &p, const f32x4 *acc, float *red, int t, long r0, int nr) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -58,35 +58,40 @@ __device__ __forceinline__ void put(const Few &p, const f32x4 *acc, float *red, 
   lds_barrier();
 }
 
-// Quantised rows, up to 16 NB a pass; the loads of U steps go out together.  Grid (output
-// tiles, groups, passes that run side by side).
-template <int WAVES, int NB, int U>
+// Quantised rows, up to 16 NB a pass, with TW tiles of outputs, which share the reading
+// of the rows; the loads of U steps go out together.  Grid (output tiles / TW, groups,
+// passes that run side by side).
+template <int WAVES, int TW, int NB, int U>
 __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t *__restrict__ codes,
                                                             const float *__restrict__ scales) {
   __shared__ float red[WAVES * NB * 256];
   constexpr int kPass = 16 * NB;
-  const int g = blockIdx.y, t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, h = lane >> 4;
+  const int g = blockIdx.y, t0 = blockIdx.x * TW, tid = threadIdx.x, lane = tid & 63, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const F8Span sp = f8_span(p.offsets, g, p.rows);
-  const TileRow tr(p, g, t);
   const int s0 = p.ks * wave / WAVES, s1 = p.ks * (wave + 1) / WAVES;
   for (long r0 = sp.begin + (long)kPass * blockIdx.z; r0 < sp.end; r0 += (long)kPass * gridDim.z) {
     const int nr = (int)min((long)kPass, sp.end - r0);
     long r[NB];
-    f32x4 acc[NB];
+    f32x4 acc[TW][NB];
 #pragma unroll
     for (int b = 0; b < NB; b++) {
       r[b] = r0 + min(16 * b + (lane & 15), nr - 1);
-      acc[b] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < TW; t++) acc[t][b] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     }
     for (int st = s0; st < s1; st += U) {
-      u32x4_t w[U][2], x[U][NB][2];
-      float sw[U], sx[U][NB];
+      u32x4_t w[U][TW][2], x[U][NB][2];
+      float sw[U][TW], sx[U][NB];
 #pragma unroll
       for (int u = 0; u < U; u++) {  // past the end: the last step again, not used
         const int at = min(st + u, s1 - 1);
-        tr.load(at, w[u]);
-        sw[u] = tr.ws[at];
+#pragma unroll
+        for (int t = 0; t < TW; t++) {
+          const TileRow tr(p, g, min(t0 + t, p.nt - 1));
+          tr.load(at, w[u][t]);
+          sw[u][t] = tr.ws[at];
+        }
 #pragma unroll
         for (int b = 0; b < NB; b++) {
           const size_t to = (size_t)at * p.rows + r[b];
@@ -101,11 +106,15 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
       for (int u = 0; u < U; u++)
         if (st + u < s1)
 #pragma unroll
-          for (int b = 0; b < NB; b++)
-            add_scaled(acc[b], f8_dot(f8_frag(w[u][0], w[u][1]), f8_frag(x[u][b][0], x[u][b][1])),
-                       sx[u][b] * sw[u]);
+          for (int t = 0; t < TW; t++)
+#pragma unroll
+            for (int b = 0; b < NB; b++)
+              add_scaled(acc[t][b],
+                         f8_dot(f8_frag(w[u][t][0], w[u][t][1]), f8_frag(x[u][b][0], x[u][b][1])),
+                         sx[u][b] * sw[u][t]);
     }
-    put<WAVES, NB>(p, acc, red, t, r0, nr);
+#pragma unroll
+    for (int t = 0; t < TW; t++) put<WAVES, NB>(p, acc[t], red, t0 + t, r0, nr);
   }
 }
 
@@ -178,29 +187,62 @@ int average(const F8Dims &d, int rows) { return (rows + d.groups - 1) / d.groups
 
 }  // namespace
 
-bool f8_few(const F8Dims &d, int rows) { return rows <= 32L * d.groups; }
+namespace {
 
+// Workgroups of tw tiles and 16 nb rows.
+long blocks(const F8Dims &d, int rows, int tw, int nb) {
+  return (long)((d.nt + tw - 1) / tw) * d.groups * ((average(d, rows) + 16 * nb - 1) / (16 * nb));
+}
+
+}  // namespace
+
+// From f8_gemm.hip on where tiles of 128 rows x 256 outputs fill the chip better: 32
+// groups of 16 rows, 2816 x 2048: 41 us here, 55 there; of 32 rows 65 and 57.  One group
+// of 4096 x 4096: 256 rows 24 here, 35 there; 512 rows 40 and 36.
+bool f8_few(const F8Dims &d, int rows) {
+  const int avg = average(d, rows);
+  return avg <= 24 || (avg <= 256 && blocks(d, rows, 4, 4) <= 512);
+}
+
+// Quantising again in every workgroup against a launch of its own: that is d.nt rows
+// d.ks blocks.  8 rows of 2048 x 7168 (57 thousand) 10.6 us against 11.5, 32 rows in 32
+// groups of 2816 x 2048 (90) 21.6 against 23.6; 8 rows of 7168 x 4096 (115) 12.7 against
+// 11.5, 96 rows in the 32 groups (270) 33.6 against 31.3.
 bool f8_few_staged(const F8Dims &d, int rows) {
-  return rows <= (long)kStaged * d.groups && staged_lds(d.ks) <= kStagedLds;
+  return average(d, rows) <= kStaged && (long)d.nt * rows * d.ks <= 100000 &&
+         staged_lds(d.ks) <= kStagedLds;
 }
 
 void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float *scales,
                    const int32_t *offsets, const void *packed, uint16_t *out, long ostride,
                    hipStream_t s) {
   const Few p = few_of(d, rows, offsets, packed, out, ostride);
-  const int avg = average(d, rows), nb = avg > 16 ? 2 : 1;
-  const int passes = std::min((avg + 16 * nb - 1) / (16 * nb), 65535);
-  auto go = [&](auto kernel, int waves) {
-    hipLaunchKernelGGL(kernel, dim3(d.nt, d.groups, passes), dim3(waves * 64), 0, s, p, codes, scales);
+  const int avg = average(d, rows);
+  auto go = [&](auto kernel, int waves, int tw, int nb) {
+    const int passes = std::min((avg + 16 * nb - 1) / (16 * nb), 65535);
+    hipLaunchKernelGGL(kernel, dim3((d.nt + tw - 1) / tw, d.groups, passes), dim3(waves * 64), 0, s, p,
+                       codes, scales);
   };
-  const long tasks = (long)d.nt * d.groups * passes;
-  if (nb == 2) {
-    if (tasks <= 512) go(f8_few_kernel<8, 2, 2>, 8);
-    else go(f8_few_kernel<4, 2, 2>, 4);
+  // The more tiles and rows a workgroup takes, the less often either is read again, as
+  // long as some 200 workgroups are left.  One group of 4096 x 4096, us with (tiles,
+  // blocks of rows) of (4, 4) / (2, 4) / (2, 2) / (1, 2): 256 rows 24 / 30 / 32 / 45, 128
+  // rows 23 / 17 / 19 / 26, 64 rows 22 / 17 / 13 / 16, 24 rows 19 / 14 / 12 / 11.
+  auto many = [&](int tw, int nb) { return blocks(d, rows, tw, nb) >= 200; };
+  const bool more = blocks(d, rows, 2, 2) > 512;  // then four waves each
+  if (avg <= 8) {
+    const long n = blocks(d, rows, 1, 1);
+    if (n <= 256) go(f8_few_kernel<16, 1, 1, 4>, 16, 1, 1);
+    else if (n <= 512) go(f8_few_kernel<8, 1, 1, 4>, 8, 1, 1);
+    else go(f8_few_kernel<4, 1, 1, 4>, 4, 1, 1);
+  } else if (avg > 32 && many(4, 4)) {
+    go(f8_few_kernel<8, 4, 4, 1>, 8, 4, 4);
+  } else if (avg > 32 && many(2, 4)) {
+    go(f8_few_kernel<8, 2, 4, 2>, 8, 2, 4);
+  } else if (many(2, 2)) {
+    if (more) go(f8_few_kernel<4, 2, 2, 2>, 4, 2, 2);
+    else go(f8_few_kernel<8, 2, 2, 2>, 8, 2, 2);
   } else {
-    if (tasks <= 256) go(f8_few_kernel<16, 1, 4>, 16);
-    else if (tasks <= 512) go(f8_few_kernel<8, 1, 4>, 8);
-    else go(f8_few_kernel<4, 1, 4>, 4);
+    go(f8_few_kernel<8, 1, 2, 2>, 8, 1, 2);
   }
 }
 
