@@ -210,10 +210,8 @@ int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x, int64_t
   uint8_t *xc = (uint8_t *)ws, *yc = xc + c.yc;
   float *xs = (float *)(xc + c.xs), *ys = (float *)(xc + c.ys);
   hipStream_t s = (hipStream_t)stream;
-  launch_f8_quant_cols({(const uint16_t *)x, x_stride, d.f16}, rows, d.k, offsets, d.groups, false,
-                       xc, xs, s);
-  launch_f8_quant_cols({(const uint16_t *)dy, dy_stride, d.f16}, rows, d.n, offsets, d.groups, true,
-                       yc, ys, s);
+  launch_f8_quant_cols({(const uint16_t *)x, x_stride, d.f16}, {(const uint16_t *)dy, dy_stride, d.f16},
+                       rows, d, offsets, xc, xs, yc, ys, s);
   launch_f8_wgrad(d, rows, xc, xs, yc, ys, offsets, (uint16_t *)dw, s);
   return status();
 }

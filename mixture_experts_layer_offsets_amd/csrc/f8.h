@@ -41,13 +41,14 @@ void launch_f8_transpose(const F8Dims &d, const void *packed, void *turned, hipS
 // values.
 void launch_f8_quant_rows(const F8Rows &x, int rows, int k, uint8_t *codes, float *scales,
                           hipStream_t s);
-// The same down the columns: blocks of 128 rows of each group's rows, block b of
-// group g at stage offsets[g] / 128 + g + b of the `f8_stages`.  Codes
-// [stage][cols][128], or with `tiles` as packed weights [cols / 16][stage][tile];
-// scales [stage][cols rounded up to 16].
+// The same down the columns of x [rows][d.k] and dy [rows][d.n]: blocks of 128 rows of
+// each group's rows, block b of group g at stage offsets[g] / 128 + g + b of the
+// `f8_stages`.  x's codes [stage][k][128], dy's as packed weights [n / 16][stage][tile];
+// scales [stage][columns rounded up to 16].
 long f8_stages(int rows, int groups);
-void launch_f8_quant_cols(const F8Rows &x, int rows, int cols, const int32_t *offsets, int groups,
-                          bool tiles, uint8_t *codes, float *scales, hipStream_t s);
+void launch_f8_quant_cols(const F8Rows &x, const F8Rows &dy, int rows, const F8Dims &d,
+                          const int32_t *offsets, uint8_t *xc, float *xs, uint8_t *yc, float *ys,
+                          hipStream_t s);
 
 // out[r] = x[r] W_g for the rows r of group g (offsets null: one group, all
 // rows), x as launch_f8_quant_rows leaves it.
@@ -65,7 +66,7 @@ bool f8_few(const F8Dims &d, int rows);
 bool f8_few_staged(const F8Dims &d, int rows);
 
 // dw[g][k][n] = sum over the rows of group g of x[r][k] dy[r][n], from
-// launch_f8_quant_cols of x (rows) and dy (tiles).
+// launch_f8_quant_cols.
 void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *xs,
                      const uint8_t *yc, const float *ys, const int32_t *offsets, uint16_t *dw,
                      hipStream_t s);

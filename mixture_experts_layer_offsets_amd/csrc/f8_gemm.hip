@@ -343,6 +343,15 @@ __global__ __launch_bounds__(kThreads, 2) void f8_gemm_kernel(Args p) {
   f8_tile<TM, COLS>(p, X0, X1, A0, A1, B0, B1);
 }
 
+// Tiles of 256 rows read less for the same products; those of 128 take about 0.75 of
+// their time, and fill the chip where tiles are few (4096 x 4096, us with 256 / 128: 1024
+// rows 53 / 37, 2048 rows 57 / 46, 4096 rows 77 / 90; 64 groups of 384 rows, 2816 x 2048:
+// 239 / 284): by the rounds of 256 workgroups that either takes.
+bool tall_tiles(long rows, long groups, int nN) {
+  auto rounds = [&](int TM) { return ((rows + TM - 1) / TM * groups * nN + 255) / 256; };
+  return 4 * rounds(256) <= 3 * rounds(128);
+}
+
 }  // namespace
 
 void launch_f8_gemm(const F8Dims &d, int rows, const uint8_t *codes, const float *scales,
@@ -362,13 +371,8 @@ void launch_f8_gemm(const F8Dims &d, int rows, const uint8_t *codes, const float
     const long most = d.groups == 1 ? (rows + TM - 1) / TM : rows / TM + d.groups;  // row tiles
     hipLaunchKernelGGL(kernel, dim3((unsigned)(most * a.nN)), dim3(kThreads), 0, s, a);
   };
-  // Tiles of 256 rows read less for the same products; those of 128 take about 0.75 of
-  // their time, and fill the chip where tiles are few (4096 x 4096, us with 256 / 128: 1024
-  // rows 53 / 37, 2048 rows 57 / 46, 4096 rows 77 / 90; 64 groups of 384 rows, 2816 x 2048:
-  // 239 / 284): by the rounds of 256 workgroups that either takes.
-  const long avg = (rows + d.groups - 1) / d.groups;
-  auto rounds = [&](int TM) { return ((avg + TM - 1) / TM * d.groups * a.nN + 255) / 256; };
-  if (4 * rounds(256) <= 3 * rounds(128)) go(f8_gemm_kernel<256, false>, 256);
+  const int avg = (rows + d.groups - 1) / d.groups;
+  if (tall_tiles(avg, d.groups, a.nN)) go(f8_gemm_kernel<256, false>, 256);
   else go(f8_gemm_kernel<128, false>, 128);
 }
 
@@ -390,7 +394,8 @@ void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *
     hipLaunchKernelGGL(kernel, dim3((unsigned)((long)d.groups * a.MT * a.nN)), dim3(kThreads), 0, s,
                        a);
   };
-  go(f8_gemm_kernel<256, true>, 256);
+  if (tall_tiles(d.k, d.groups, a.nN)) go(f8_gemm_kernel<256, true>, 256);
+  else go(f8_gemm_kernel<128, true>, 128);
 }
 
 }  // namespace moe

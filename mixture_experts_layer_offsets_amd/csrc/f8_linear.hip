@@ -68,8 +68,24 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
   constexpr int kPass = 16 * NB;
   const int g = blockIdx.y, t0 = blockIdx.x * TW, tid = threadIdx.x, lane = tid & 63, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const F8Span sp = f8_span(p.offsets, g, p.rows);
   const int s0 = p.ks * wave / WAVES, s1 = p.ks * (wave + 1) / WAVES;
+  u32x4_t w[U][TW][2];
+  float sw[U][TW];
+  auto load = [&](int st) {
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int t = 0; t < TW; t++) {  // past the end: the last step again, not used
+        const TileRow tr(p, g, min(t0 + t, p.nt - 1));
+        const int at = min(st + u, p.ks - 1);
+        tr.load(at, w[u][t]);
+        sw[u][t] = tr.ws[at];
+      }
+  };
+  // few groups of this many rows are empty: the first weights need not wait for the offsets
+  load(s0);
+  __builtin_amdgcn_sched_barrier(0);
+  const F8Span sp = f8_span(p.offsets, g, p.rows);
   for (long r0 = sp.begin + (long)kPass * blockIdx.z; r0 < sp.end; r0 += (long)kPass * gridDim.z) {
     const int nr = (int)min((long)kPass, sp.end - r0);
     long r[NB];
@@ -81,17 +97,11 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
       for (int t = 0; t < TW; t++) acc[t][b] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     }
     for (int st = s0; st < s1; st += U) {
-      u32x4_t w[U][TW][2], x[U][NB][2];
-      float sw[U][TW], sx[U][NB];
+      u32x4_t x[U][NB][2];
+      float sx[U][NB];
 #pragma unroll
-      for (int u = 0; u < U; u++) {  // past the end: the last step again, not used
+      for (int u = 0; u < U; u++) {
         const int at = min(st + u, s1 - 1);
-#pragma unroll
-        for (int t = 0; t < TW; t++) {
-          const TileRow tr(p, g, min(t0 + t, p.nt - 1));
-          tr.load(at, w[u][t]);
-          sw[u][t] = tr.ws[at];
-        }
 #pragma unroll
         for (int b = 0; b < NB; b++) {
           const size_t to = (size_t)at * p.rows + r[b];
@@ -112,7 +122,9 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
               add_scaled(acc[t][b],
                          f8_dot(f8_frag(w[u][t][0], w[u][t][1]), f8_frag(x[u][b][0], x[u][b][1])),
                          sx[u][b] * sw[u][t]);
+      if (st + U < s1) load(st + U);
     }
+    if (r0 + (long)kPass * gridDim.z < sp.end) load(s0);
 #pragma unroll
     for (int t = 0; t < TW; t++) put<WAVES, NB>(p, acc[t], red, t0 + t, r0, nr);
   }
@@ -135,20 +147,22 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_rows_kernel(Few p, const ui
   float *xs = (float *)(lds + kStaged * pitch);
   const TileRow tr(p, g, t);
   const int s0 = p.ks * wave / WAVES, s1 = p.ks * (wave + 1) / WAVES;
+  u32x4_t w[U][2];
+  float sw[U];
+  auto load = [&](int st) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int at = min(st + u, p.ks - 1);
+      tr.load(at, w[u]);
+      sw[u] = tr.ws[at];
+    }
+  };
+  // one group's first weights need not wait for the offsets; many may be empty
+  if (gridDim.y == 1) load(s0);
   const F8Span sp = f8_span(p.offsets, g, p.rows);
   for (long r0 = sp.begin + (long)kStaged * blockIdx.z; r0 < sp.end; r0 += (long)kStaged * gridDim.z) {
     const int nr = (int)min((long)kStaged, sp.end - r0);
-    u32x4_t w[U][2];
-    float sw[U];
-    auto load = [&](int st) {
-#pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int at = min(st + u, p.ks - 1);
-        tr.load(at, w[u]);
-        sw[u] = tr.ws[at];
-      }
-    };
-    load(s0);
+    if (gridDim.y > 1 || r0 >= sp.begin + (long)kStaged * gridDim.z) load(s0);
     for (int q = tid >> 4; q < nr * p.ks; q += WAVES * 4) {
       const int row = q / p.ks, kb = q - row * p.ks, i = tid & 15;
       float s;

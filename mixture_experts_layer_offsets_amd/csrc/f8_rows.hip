@@ -39,22 +39,36 @@ __global__ __launch_bounds__(256) void f8_quant_rows_kernel(const uint16_t *__re
   }
 }
 
+// The columns of one tensor; tiles: its codes go out as packed weights lie.
+struct Cols {
+  const uint16_t *x;
+  long stride;
+  int cols, tiles;
+  uint8_t *codes;
+  float *scales;
+};
+
 // A workgroup takes 64 columns of one stage (128 rows of one group): the rows go
 // through LDS, then a thread converts 32 values of one column, and the columns' 128
-// codes leave through LDS in 16-byte chunks.  Grid (columns / 64, stages), stages
-// past 2^16 in turn.
-template <bool F16, bool TILES>
-__global__ __launch_bounds__(256) void f8_quant_cols_kernel(
-    const uint16_t *__restrict__ x, long stride, int rows, int cols,
-    const int32_t *__restrict__ offsets, int groups, long stages, uint8_t *__restrict__ codes,
-    float *__restrict__ scales) {
+// codes leave through LDS in 16-byte chunks.  Grid (columns of a / 64 + those of b / 64,
+// stages), stages past 2^16 in turn.
+template <bool F16>
+__global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int rows,
+                                                            const int32_t *__restrict__ offsets,
+                                                            int groups, long stages) {
   __shared__ u32x4_t tile[kF8Block][8];  // 128 rows x 64 values
   // a column's codes at 144 bytes a column: the 16 more put the lanes' writes on
   // different banks
   constexpr int kLine = kF8Block + 16;
   __shared__ __attribute__((aligned(16))) uint8_t lines[64 * kLine];
   __shared__ uint32_t tops[4][64];
-  const int tid = threadIdx.x, c0 = blockIdx.x * 64;
+  const int ax = (a.cols + 63) / 64;
+  const bool first_of = (int)blockIdx.x < ax;
+  const Cols m = first_of ? a : b;
+  const uint16_t *x = m.x;
+  const long stride = m.stride;
+  const int cols = m.cols;
+  const int tid = threadIdx.x, c0 = (first_of ? blockIdx.x : blockIdx.x - ax) * 64;
   const int cols16 = (cols + 15) & ~15;
   for (long st = blockIdx.y; st < stages; st += gridDim.y) {
     int first;
@@ -100,23 +114,23 @@ __global__ __launch_bounds__(256) void f8_quant_cols_kernel(
                     f8_codes4(v[e + 4], v[e + 5], v[e + 6], v[e + 7], inv),
                     f8_codes4(v[e + 8], v[e + 9], v[e + 10], v[e + 11], inv),
                     f8_codes4(v[e + 12], v[e + 13], v[e + 14], v[e + 15], inv)};
-    if (q == 0 && c0 + j < cols16) scales[(size_t)st * cols16 + c0 + j] = s;
+    if (q == 0 && c0 + j < cols16) m.scales[(size_t)st * cols16 + c0 + j] = s;
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < 2; p++) {
       const int at = tid + 256 * p;
       int col, c;
       uint8_t *dst;
-      if constexpr (TILES) {  // chunk by chunk in a tile's order
+      if (m.tiles) {  // chunk by chunk in a tile's order
         col = (at >> 7) * 16 + (at & 15);
         c = ((at >> 6) & 1) * 4 + ((at >> 4) & 3);
-        dst = codes + ((size_t)((c0 + col) >> 4) * stages + st) * kF8Tile + f8_chunk(c, col & 15);
+        dst = m.codes + ((size_t)((c0 + col) >> 4) * stages + st) * kF8Tile + f8_chunk(c, col & 15);
       } else {
         col = at >> 3;
         c = at & 7;
-        dst = codes + ((size_t)st * cols + c0 + col) * kF8Block + 16 * c;
+        dst = m.codes + ((size_t)st * cols + c0 + col) * kF8Block + 16 * c;
       }
-      if (c0 + col < (TILES ? cols16 : cols))
+      if (c0 + col < (m.tiles ? cols16 : cols))
         *(u32x4_t *)dst = *(const u32x4_t *)(lines + col * kLine + 16 * c);
     }
     __syncthreads();
@@ -138,17 +152,17 @@ void launch_f8_quant_rows(const F8Rows &x, int rows, int k, uint8_t *codes, floa
 
 long f8_stages(int rows, int groups) { return rows / kF8Block + groups; }
 
-void launch_f8_quant_cols(const F8Rows &x, int rows, int cols, const int32_t *offsets, int groups,
-                          bool tiles, uint8_t *codes, float *scales, hipStream_t s) {
+void launch_f8_quant_cols(const F8Rows &x, const F8Rows &dy, int rows, const F8Dims &d,
+                          const int32_t *offsets, uint8_t *xc, float *xs, uint8_t *yc, float *ys,
+                          hipStream_t s) {
   if (rows <= 0) return;
-  const long stages = f8_stages(rows, groups);
-  const dim3 grid((cols + 63) / 64, (unsigned)std::min(stages, 65535L));
+  const long stages = f8_stages(rows, d.groups);
+  const Cols a{x.p, x.stride, d.k, 0, xc, xs}, b{dy.p, dy.stride, d.n, 1, yc, ys};
+  const dim3 grid((d.k + 63) / 64 + (d.n + 63) / 64, (unsigned)std::min(stages, 65535L));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, x.p, x.stride, rows, cols, offsets, groups,
-                       stages, codes, scales);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, b, rows, offsets, d.groups, stages);
   };
-  if (tiles) x.f16 ? go(f8_quant_cols_kernel<true, true>) : go(f8_quant_cols_kernel<false, true>);
-  else x.f16 ? go(f8_quant_cols_kernel<true, false>) : go(f8_quant_cols_kernel<false, false>);
+  d.f16 ? go(f8_quant_cols_kernel<true>) : go(f8_quant_cols_kernel<false>);
 }
 
 }  // namespace moe
