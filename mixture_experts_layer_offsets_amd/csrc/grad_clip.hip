@@ -10,7 +10,8 @@
 // and takes other addresses every time.  Sums of squares are held in 64 bits from the
 // first square on: no gradient over- or underflows them, and 64-bit multiply-adds
 // still take a fraction of the loads' time.  Every workgroup of the scaling adds the
-// partial sums up by itself, in one fixed order, instead of a launch between the two.
+// partial sums up by itself, in one fixed order, instead of a launch between the two.  A
+// few small tensors take one workgroup and one launch, cut into chunks of 4 KB a wave.
 #include <algorithm>
 
 #include "common.h"
@@ -29,6 +30,9 @@ constexpr int kThreads = 256;
 constexpr int kGroups = 2048;       // workgroups of all launches together, about
 constexpr int kLeastGroups = 256;   // ... but of each launch this many
 constexpr int kMostPartials = 4096;  // that a scaling workgroup adds up
+constexpr int kSmallChunk = 4096;   // bytes, of one wave
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallChunks = 64;    // of one workgroup, at most
 
 struct Set {
   const void *x[kSet];
@@ -41,11 +45,12 @@ struct Outs {
 };
 constexpr int kTypeShift = 60;
 
-// The chunk c of the set: its tensor, and where in it the chunk begins.
+// The chunk c of the set, of BYTES at most: its tensor, and where in it the chunk begins.
 struct Chunk {
   int t, type, n;  // n: values of the chunk
   int64_t at;
 };
+template <int BYTES>
 __device__ __forceinline__ Chunk chunk_of(const Set &s, int c) {
   int lo = 0, hi = s.count;
   while (hi - lo > 1) {
@@ -56,7 +61,7 @@ __device__ __forceinline__ Chunk chunk_of(const Set &s, int c) {
   k.t = lo;
   const int64_t n = s.n[lo];
   k.type = (int)(n >> kTypeShift);
-  const int per = k.type == MOE_ROW_F32 ? kChunk / 4 : kChunk / 2;
+  const int per = k.type == MOE_ROW_F32 ? BYTES / 4 : BYTES / 2;
   k.at = (int64_t)(c - s.start[lo]) * per;
   k.n = (int)min((int64_t)per, (n & ((1ll << kTypeShift) - 1)) - k.at);
   return k;
@@ -101,10 +106,10 @@ __device__ __forceinline__ double joined(double a, double b) {
   else return a + b;
 }
 
-// Over the workgroup, in a fixed order; in every thread.
-template <bool INF>
+// Over a workgroup of NT threads, in a fixed order; in every thread.
+template <bool INF, int NT>
 __device__ __forceinline__ double block_join(double v) {
-  __shared__ double part[kThreads / 64];
+  __shared__ double part[NT / 64];
 #pragma unroll
   for (int o = 32; o; o >>= 1) v = joined<INF>(v, __shfl_xor(v, o, 64));
   __syncthreads();
@@ -112,51 +117,57 @@ __device__ __forceinline__ double block_join(double v) {
   __syncthreads();
   v = part[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; w++) v = joined<INF>(v, part[w]);
+  for (int w = 1; w < NT / 64; w++) v = joined<INF>(v, part[w]);
   return v;
 }
 
-// f(values index, 16 bytes) for the whole vectors of a chunk, U of a thread together.
-template <int TYPE, class F>
+// f(values index, 16 bytes) for the whole vectors of a chunk that NT threads take, U of a
+// thread together.
+template <int TYPE, int NT, class F>
 __device__ __forceinline__ void each_vector(const void *x, int n, F &&f) {
   constexpr int N = Vec<TYPE>::N, U = 4;
   const int whole = n / N;
   const auto *p = (const u32x4_g2 *)x;
-  for (int i = threadIdx.x; i < whole; i += U * kThreads) {
+  for (int i = threadIdx.x % NT; i < whole; i += U * NT) {
     u32x4_g v[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const u32x4_g2 q = p[min(i + u * kThreads, whole - 1)];
+      const u32x4_g2 q = p[min(i + u * NT, whole - 1)];
       v[u] = (u32x4_g){q[0], q[1], q[2], q[3]};
     }
 #pragma unroll
     for (int u = 0; u < U; u++)
-      if (i + u * kThreads < whole) f(i + u * kThreads, v[u]);
+      if (i + u * NT < whole) f(i + u * NT, v[u]);
   }
 }
 
-template <int TYPE, bool INF>
-__device__ __forceinline__ void norm_chunk(const void *x, int n, Norm<INF> &acc) {
+template <int TYPE, bool INF, int NT>
+__device__ __forceinline__ void norm_values(const void *x, int n, Norm<INF> &acc) {
   typedef Vec<TYPE> V;
-  each_vector<TYPE>(x, n, [&](int, const u32x4_g &v) {
+  each_vector<TYPE, NT>(x, n, [&](int, const u32x4_g &v) {
 #pragma unroll
     for (int i = 0; i < V::N; i++) acc.add(V::value(v, i));
   });
-  const int r = n / V::N * V::N + threadIdx.x;
+  const int r = n / V::N * V::N + threadIdx.x % NT;
   if (r < n) acc.add(V::one(((const typename V::Raw *)x)[r]));
+}
+
+// NT threads take the chunk.
+template <bool INF, int NT>
+__device__ __forceinline__ void norm_chunk(const Set &s, const Chunk &k, Norm<INF> &acc) {
+  const char *x = (const char *)s.x[k.t] + k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
+  if (k.type == MOE_ROW_F32) norm_values<MOE_ROW_F32, INF, NT>(x, k.n, acc);
+  else if (k.type == MOE_ROW_F16) norm_values<MOE_ROW_F16, INF, NT>(x, k.n, acc);
+  else norm_values<MOE_ROW_BF16, INF, NT>(x, k.n, acc);
 }
 
 template <bool INF>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(Set s, double *__restrict__ partials) {
   Norm<INF> acc;
   for (int c = blockIdx.x; c < s.start[s.count]; c += gridDim.x) {
-    const Chunk k = chunk_of(s, c);
-    const char *x = (const char *)s.x[k.t] + k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
-    if (k.type == MOE_ROW_F32) norm_chunk<MOE_ROW_F32, INF>(x, k.n, acc);
-    else if (k.type == MOE_ROW_F16) norm_chunk<MOE_ROW_F16, INF>(x, k.n, acc);
-    else norm_chunk<MOE_ROW_BF16, INF>(x, k.n, acc);
+    norm_chunk<INF, kThreads>(s, chunk_of<kChunk>(s, c), acc);
   }
-  const double v = block_join<INF>(acc.get());
+  const double v = block_join<INF, kThreads>(acc.get());
   if (threadIdx.x == 0) partials[blockIdx.x] = v;
 }
 
@@ -165,7 +176,7 @@ template <bool INF>
 __device__ __forceinline__ double total_of(const double *partials, int n) {
   double v = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) v = joined<INF>(v, partials[i]);
-  return block_join<INF>(v);
+  return block_join<INF, kThreads>(v);
 }
 
 template <bool INF>
@@ -177,11 +188,11 @@ __global__ __launch_bounds__(kThreads) void grad_total_kernel(const double *__re
   if (norm) *norm = (float)(INF ? v : sqrt(v));
 }
 
-template <int TYPE>
-__device__ __forceinline__ void scale_chunk(const void *x, void *out, int n, float coef) {
+template <int TYPE, int NT>
+__device__ __forceinline__ void scale_values(const void *x, void *out, int n, float coef) {
   typedef Vec<TYPE> V;
   auto *dst = (u32x4_g2 *)out;
-  each_vector<TYPE>(x, n, [&](int at, const u32x4_g &v) {
+  each_vector<TYPE, NT>(x, n, [&](int at, const u32x4_g &v) {
     u32x4_g2 o;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -192,9 +203,29 @@ __device__ __forceinline__ void scale_chunk(const void *x, void *out, int n, flo
     }
     dst[at] = o;
   });
-  const int r = n / V::N * V::N + threadIdx.x;
+  const int r = n / V::N * V::N + threadIdx.x % NT;
   typedef typename V::Raw Raw;
   if (r < n) ((Raw *)out)[r] = V::raw(V::one(((const Raw *)x)[r]) * coef);
+}
+
+template <int NT>
+__device__ __forceinline__ void scale_chunk(const Set &s, const Outs &o, const Chunk &k, float coef) {
+  const int64_t at = k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
+  const char *x = (const char *)s.x[k.t] + at;
+  char *out = (char *)o.out[k.t] + at;
+  if (x == out && coef == 1.0f) return;
+  if (k.type == MOE_ROW_F32) scale_values<MOE_ROW_F32, NT>(x, out, k.n, coef);
+  else if (k.type == MOE_ROW_F16) scale_values<MOE_ROW_F16, NT>(x, out, k.n, coef);
+  else scale_values<MOE_ROW_BF16, NT>(x, out, k.n, coef);
+}
+
+// The coefficient, and the norm that it comes from.
+template <bool INF>
+__device__ __forceinline__ float coef_of(double total, float max_norm, double *norm) {
+  *norm = INF ? total : sqrt(total);
+  double c = (double)max_norm / (*norm + 1e-6);
+  if (c > 1.0) c = 1.0;  // NaN stays
+  return (float)c;
 }
 
 // Chunks from the last to the first: what the norm read last is still in the caches.
@@ -202,37 +233,42 @@ template <bool INF>
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Set s, Outs o,
                                                               const double *__restrict__ partials,
                                                               int n, float max_norm, float *norm) {
-  const double total = total_of<INF>(partials, n);
-  const double nm = INF ? total : sqrt(total);
-  double c = (double)max_norm / (nm + 1e-6);
-  if (c > 1.0) c = 1.0;  // NaN stays
-  const float coef = (float)c;
+  double nm;
+  const float coef = coef_of<INF>(total_of<INF>(partials, n), max_norm, &nm);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nm;
-  for (int i = s.start[s.count] - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
-    const Chunk k = chunk_of(s, i);
-    const int64_t at = k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
-    const char *x = (const char *)s.x[k.t] + at;
-    char *out = (char *)o.out[k.t] + at;
-    if (x == out && coef == 1.0f) continue;
-    if (k.type == MOE_ROW_F32) scale_chunk<MOE_ROW_F32>(x, out, k.n, coef);
-    else if (k.type == MOE_ROW_F16) scale_chunk<MOE_ROW_F16>(x, out, k.n, coef);
-    else scale_chunk<MOE_ROW_BF16>(x, out, k.n, coef);
-  }
+  for (int i = s.start[s.count] - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x)
+    scale_chunk<kThreads>(s, o, chunk_of<kChunk>(s, i), coef);
 }
 
-int64_t chunks_of(const moe_grad_tensor &t) {
-  const int64_t per = t.type == MOE_ROW_F32 ? kChunk / 4 : kChunk / 2;
+// All of it in one workgroup, a chunk a wave.
+template <bool INF>
+__global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(Set s, Outs o, float max_norm,
+                                                                   float *norm) {
+  constexpr int kWaves = kSmallThreads / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Norm<INF> acc;
+  for (int c = wave; c < s.start[s.count]; c += kWaves)
+    norm_chunk<INF, 64>(s, chunk_of<kSmallChunk>(s, c), acc);
+  double nm;
+  const float coef = coef_of<INF>(block_join<INF, kSmallThreads>(acc.get()), max_norm, &nm);
+  if (norm && threadIdx.x == 0) *norm = (float)nm;
+  for (int c = wave; c < s.start[s.count]; c += kWaves)
+    scale_chunk<64>(s, o, chunk_of<kSmallChunk>(s, c), coef);
+}
+
+int64_t chunks_of(const moe_grad_tensor &t, int bytes) {
+  const int64_t per = t.type == MOE_ROW_F32 ? bytes / 4 : bytes / 2;
   return (t.numel + per - 1) / per;
 }
 
 // The next launch's tensors, from the first one that is not in one yet; those
 // without values are left out.
-int fill(Set *s, Outs *o, int at, int count, const moe_grad_tensor *t) {
+int fill(Set *s, Outs *o, int at, int count, const moe_grad_tensor *t, int bytes = kChunk) {
   s->count = 0;
   s->start[0] = 0;
   for (; at < count && s->count < kSet; at++) {
     if (!t[at].numel) continue;
-    const int64_t c = s->start[s->count] + chunks_of(t[at]);
+    const int64_t c = s->start[s->count] + chunks_of(t[at], bytes);
     if (c > 0x7FFFFFFF) break;  // (a launch of its own then: one tensor has fewer)
     s->x[s->count] = t[at].x;
     o->out[s->count] = t[at].out;
@@ -288,6 +324,18 @@ void scale_launches(int count, const moe_grad_tensor *t, const double *partials,
 template <bool INF>
 void clip(int count, const moe_grad_tensor *t, double *partials, float max_norm, float *norm,
           hipStream_t s) {
+  // Six tensors of 131 KB together: 9.7 us in two launches.
+  int64_t small = 0;
+  for (int i = 0; i < count && small <= kSmallChunks; i++) small += chunks_of(t[i], kSmallChunk);
+  if (small && small <= kSmallChunks) {
+    Set set;
+    Outs o;
+    if (fill(&set, &o, 0, count, t, kSmallChunk) == count) {
+      hipLaunchKernelGGL(grad_small_kernel<INF>, dim3(1), dim3(kSmallThreads), 0, s, set, o, max_norm,
+                         norm);
+      return;
+    }
+  }
   int n = norm_launches<INF>(count, t, partials, s);
   if (n > kMostPartials) {  // one sum of them, behind them
     hipLaunchKernelGGL(grad_total_kernel<INF>, dim3(1), dim3(kThreads), 0, s, partials, n, partials + n,
