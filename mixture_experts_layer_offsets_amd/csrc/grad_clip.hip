@@ -31,41 +31,73 @@ constexpr int kGroups = 2048;       // workgroups of all launches together, abou
 constexpr int kLeastGroups = 256;   // ... but of each launch this many
 constexpr int kMostPartials = 4096;  // that a scaling workgroup adds up
 constexpr int kSmallChunk = 4096;   // bytes, of one wave
+constexpr int kSmallSet = 16;       // tensors: arguments of 0.5 KB instead of 3.6, 1 us of a launch
 constexpr int kSmallThreads = 1024;
-constexpr int kSmallChunks = 64;    // of one workgroup, at most
+constexpr int kPerWave = 3;
+constexpr int kSmallChunks = kPerWave * kSmallThreads / 64;  // of one workgroup, at most
 
-struct Set {
-  const void *x[kSet];
-  int64_t n[kSet];        // values; type in the top bits
-  int32_t start[kSet + 1];  // chunks before each tensor
+template <int K>
+struct SetOf {
+  const void *x[K];
+  int64_t n[K];          // values; type in the top bits
+  int32_t start[K + 1];  // chunks before each tensor
   int32_t count;
 };
-struct Outs {
-  void *out[kSet];
+template <int K>
+struct OutsOf {
+  void *out[K];
 };
+typedef SetOf<kSet> Set;
+typedef OutsOf<kSet> Outs;
 constexpr int kTypeShift = 60;
 
-// The chunk c of the set, of BYTES at most: its tensor, and where in it the chunk begins.
+// A chunk of the set.
 struct Chunk {
-  int t, type, n;  // n: values of the chunk
-  int64_t at;
+  const char *x;
+  char *out;
+  int type, n;  // n: values
 };
-template <int BYTES>
-__device__ __forceinline__ Chunk chunk_of(const Set &s, int c) {
-  int lo = 0, hi = s.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s.start[mid] <= c) lo = mid; else hi = mid;
+
+// Finds chunks of BYTES at most.  The tensors lie in the lanes, up to two each, loaded together: a
+// search in the arguments would wait for them once a step (250 tensors in two launches of
+// either kernel: 52.4 us with a search, 47.5 so).
+template <int BYTES, bool OUT, int K>
+struct Chunks {
+  static_assert(K <= 128, "two a lane");
+  int count, first[2];
+  int64_t n[2], x[2], out[2];
+  __device__ __forceinline__ Chunks(const SetOf<K> &s, const OutsOf<K> *o) : count(s.count) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int t = min(64 * i + lane, K - 1);
+      first[i] = s.start[t];
+      n[i] = s.n[t];
+      x[i] = (int64_t)s.x[t];
+      out[i] = OUT ? (int64_t)o->out[t] : 0;
+    }
   }
-  Chunk k;
-  k.t = lo;
-  const int64_t n = s.n[lo];
-  k.type = (int)(n >> kTypeShift);
-  const int per = k.type == MOE_ROW_F32 ? BYTES / 4 : BYTES / 2;
-  k.at = (int64_t)(c - s.start[lo]) * per;
-  k.n = (int)min((int64_t)per, (n & ((1ll << kTypeShift) - 1)) - k.at);
-  return k;
-}
+  __device__ __forceinline__ static int64_t lane64(const int64_t (&v)[2], int t) {
+    const int64_t w = t < 64 ? v[0] : v[1];
+    return (uint32_t)__builtin_amdgcn_readlane((int)w, t & 63) |
+           (int64_t)__builtin_amdgcn_readlane((int)(w >> 32), t & 63) << 32;
+  }
+  __device__ __forceinline__ Chunk operator()(int c) const {
+    const int lane = threadIdx.x & 63;
+    const int t = __popcll(__ballot(lane < count && first[0] <= c)) +
+                  __popcll(__ballot(64 + lane < count && first[1] <= c)) - 1;
+    const int c0 = __builtin_amdgcn_readlane(t < 64 ? first[0] : first[1], t & 63);
+    const int64_t typed = lane64(n, t);
+    Chunk k;
+    k.type = (int)(typed >> kTypeShift);
+    const int size = k.type == MOE_ROW_F32 ? 4 : 2;
+    const int64_t at = (int64_t)(c - c0) * (BYTES / size);
+    k.n = (int)min((int64_t)(BYTES / size), (typed & ((1ll << kTypeShift) - 1)) - at);
+    k.x = (const char *)lane64(x, t) + at * size;
+    k.out = OUT ? (char *)lane64(out, t) + at * size : nullptr;
+    return k;
+  }
+};
 
 // 16 bytes as values of a type.
 template <int TYPE>
@@ -85,6 +117,15 @@ struct Vec {
     if constexpr (TYPE == MOE_ROW_F32) return __float_as_uint(f);
     else if constexpr (TYPE == MOE_ROW_F16) return __builtin_bit_cast(uint16_t, (_Float16)f);
     else return __builtin_bit_cast(uint16_t, (__bf16)f);
+  }
+  static __device__ __forceinline__ u32x4_g2 scaled(const u32x4_g &v, float coef) {
+    u32x4_g2 o;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if constexpr (N == 4) o[i] = raw(value(v, i) * coef);
+      else o[i] = raw(value(v, 2 * i) * coef) | (uint32_t)raw(value(v, 2 * i + 1) * coef) << 16;
+    }
+    return o;
   }
 };
 
@@ -121,51 +162,49 @@ __device__ __forceinline__ double block_join(double v) {
   return v;
 }
 
-// f(values index, 16 bytes) for the whole vectors of a chunk that NT threads take, U of a
-// thread together.
-template <int TYPE, int NT, class F>
+// f(values index, 16 bytes) for the whole vectors of a chunk, U of a thread together.
+template <int TYPE, class F>
 __device__ __forceinline__ void each_vector(const void *x, int n, F &&f) {
   constexpr int N = Vec<TYPE>::N, U = 4;
   const int whole = n / N;
   const auto *p = (const u32x4_g2 *)x;
-  for (int i = threadIdx.x % NT; i < whole; i += U * NT) {
+  for (int i = threadIdx.x; i < whole; i += U * kThreads) {
     u32x4_g v[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const u32x4_g2 q = p[min(i + u * NT, whole - 1)];
+      const u32x4_g2 q = p[min(i + u * kThreads, whole - 1)];
       v[u] = (u32x4_g){q[0], q[1], q[2], q[3]};
     }
 #pragma unroll
     for (int u = 0; u < U; u++)
-      if (i + u * NT < whole) f(i + u * NT, v[u]);
+      if (i + u * kThreads < whole) f(i + u * kThreads, v[u]);
   }
 }
 
-template <int TYPE, bool INF, int NT>
+template <int TYPE, bool INF>
 __device__ __forceinline__ void norm_values(const void *x, int n, Norm<INF> &acc) {
   typedef Vec<TYPE> V;
-  each_vector<TYPE, NT>(x, n, [&](int, const u32x4_g &v) {
+  each_vector<TYPE>(x, n, [&](int, const u32x4_g &v) {
 #pragma unroll
     for (int i = 0; i < V::N; i++) acc.add(V::value(v, i));
   });
-  const int r = n / V::N * V::N + threadIdx.x % NT;
+  const int r = n / V::N * V::N + threadIdx.x;
   if (r < n) acc.add(V::one(((const typename V::Raw *)x)[r]));
 }
 
-// NT threads take the chunk.
-template <bool INF, int NT>
-__device__ __forceinline__ void norm_chunk(const Set &s, const Chunk &k, Norm<INF> &acc) {
-  const char *x = (const char *)s.x[k.t] + k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
-  if (k.type == MOE_ROW_F32) norm_values<MOE_ROW_F32, INF, NT>(x, k.n, acc);
-  else if (k.type == MOE_ROW_F16) norm_values<MOE_ROW_F16, INF, NT>(x, k.n, acc);
-  else norm_values<MOE_ROW_BF16, INF, NT>(x, k.n, acc);
+template <bool INF>
+__device__ __forceinline__ void norm_chunk(const Chunk &k, Norm<INF> &acc) {
+  if (k.type == MOE_ROW_F32) norm_values<MOE_ROW_F32, INF>(k.x, k.n, acc);
+  else if (k.type == MOE_ROW_F16) norm_values<MOE_ROW_F16, INF>(k.x, k.n, acc);
+  else norm_values<MOE_ROW_BF16, INF>(k.x, k.n, acc);
 }
 
 template <bool INF>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(Set s, double *__restrict__ partials) {
   Norm<INF> acc;
+  const Chunks<kChunk, false, kSet> chunk(s, nullptr);
   for (int c = blockIdx.x; c < s.start[s.count]; c += gridDim.x) {
-    norm_chunk<INF, kThreads>(s, chunk_of<kChunk>(s, c), acc);
+    norm_chunk<INF>(chunk(c), acc);
   }
   const double v = block_join<INF, kThreads>(acc.get());
   if (threadIdx.x == 0) partials[blockIdx.x] = v;
@@ -188,35 +227,21 @@ __global__ __launch_bounds__(kThreads) void grad_total_kernel(const double *__re
   if (norm) *norm = (float)(INF ? v : sqrt(v));
 }
 
-template <int TYPE, int NT>
+template <int TYPE>
 __device__ __forceinline__ void scale_values(const void *x, void *out, int n, float coef) {
   typedef Vec<TYPE> V;
   auto *dst = (u32x4_g2 *)out;
-  each_vector<TYPE, NT>(x, n, [&](int at, const u32x4_g &v) {
-    u32x4_g2 o;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if constexpr (V::N == 4)
-        o[i] = V::raw(V::value(v, i) * coef);
-      else
-        o[i] = V::raw(V::value(v, 2 * i) * coef) | (uint32_t)V::raw(V::value(v, 2 * i + 1) * coef) << 16;
-    }
-    dst[at] = o;
-  });
-  const int r = n / V::N * V::N + threadIdx.x % NT;
+  each_vector<TYPE>(x, n, [&](int at, const u32x4_g &v) { dst[at] = V::scaled(v, coef); });
+  const int r = n / V::N * V::N + threadIdx.x;
   typedef typename V::Raw Raw;
   if (r < n) ((Raw *)out)[r] = V::raw(V::one(((const Raw *)x)[r]) * coef);
 }
 
-template <int NT>
-__device__ __forceinline__ void scale_chunk(const Set &s, const Outs &o, const Chunk &k, float coef) {
-  const int64_t at = k.at * (k.type == MOE_ROW_F32 ? 4 : 2);
-  const char *x = (const char *)s.x[k.t] + at;
-  char *out = (char *)o.out[k.t] + at;
-  if (x == out && coef == 1.0f) return;
-  if (k.type == MOE_ROW_F32) scale_values<MOE_ROW_F32, NT>(x, out, k.n, coef);
-  else if (k.type == MOE_ROW_F16) scale_values<MOE_ROW_F16, NT>(x, out, k.n, coef);
-  else scale_values<MOE_ROW_BF16, NT>(x, out, k.n, coef);
+__device__ __forceinline__ void scale_chunk(const Chunk &k, float coef) {
+  if (k.x == k.out && coef == 1.0f) return;
+  if (k.type == MOE_ROW_F32) scale_values<MOE_ROW_F32>(k.x, k.out, k.n, coef);
+  else if (k.type == MOE_ROW_F16) scale_values<MOE_ROW_F16>(k.x, k.out, k.n, coef);
+  else scale_values<MOE_ROW_BF16>(k.x, k.out, k.n, coef);
 }
 
 // The coefficient, and the norm that it comes from.
@@ -233,27 +258,78 @@ template <bool INF>
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Set s, Outs o,
                                                               const double *__restrict__ partials,
                                                               int n, float max_norm, float *norm) {
+  const Chunks<kChunk, true, kSet> chunk(s, &o);
   double nm;
   const float coef = coef_of<INF>(total_of<INF>(partials, n), max_norm, &nm);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nm;
   for (int i = s.start[s.count] - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x)
-    scale_chunk<kThreads>(s, o, chunk_of<kChunk>(s, i), coef);
+    scale_chunk(chunk(i), coef);
 }
 
-// All of it in one workgroup, a chunk a wave.
+// All of it in one workgroup: a wave holds kPerWave chunks in registers from the one
+// reading of them to the scaling.
 template <bool INF>
-__global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(Set s, Outs o, float max_norm,
-                                                                   float *norm) {
-  constexpr int kWaves = kSmallThreads / 64;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(SetOf<kSmallSet> s,
+                                                                   OutsOf<kSmallSet> o,
+                                                                   float max_norm, float *norm) {
+  constexpr int kWaves = kSmallThreads / 64, V = kSmallChunk / 1024;  // vectors of a lane and chunk
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const Chunks<kSmallChunk, true, kSmallSet> chunk(s, &o);
+  const int total = s.start[s.count];
+  Chunk k[kPerWave];
+  u32x4_g v[kPerWave][V];
+  uint32_t tail[kPerWave];
+#pragma unroll
+  for (int q = 0; q < kPerWave; q++) {
+    k[q] = chunk(min(wave + q * kWaves, total - 1));
+    if (wave + q * kWaves >= total) k[q].n = 0;
+    const int N = k[q].type == MOE_ROW_F32 ? 4 : 8, whole = k[q].n / N;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      v[q][i] = (u32x4_g){0, 0, 0, 0};
+      if (64 * i + lane < whole) {
+        const u32x4_g2 u = ((const u32x4_g2 *)k[q].x)[64 * i + lane];
+        v[q][i] = (u32x4_g){u[0], u[1], u[2], u[3]};
+      }
+    }
+    const int r = whole * N + lane;
+    tail[q] = 0;
+    if (r < k[q].n)
+      tail[q] = k[q].type == MOE_ROW_F32 ? ((const uint32_t *)k[q].x)[r] : ((const uint16_t *)k[q].x)[r];
+  }
+  // f(Vec of the type) for each chunk; what lies past its end is zero, and adds nothing
+  auto each_type = [&](int q, auto &&f) {
+    if (k[q].type == MOE_ROW_F32) f(Vec<MOE_ROW_F32>{});
+    else if (k[q].type == MOE_ROW_F16) f(Vec<MOE_ROW_F16>{});
+    else f(Vec<MOE_ROW_BF16>{});
+  };
   Norm<INF> acc;
-  for (int c = wave; c < s.start[s.count]; c += kWaves)
-    norm_chunk<INF, 64>(s, chunk_of<kSmallChunk>(s, c), acc);
+#pragma unroll
+  for (int q = 0; q < kPerWave; q++)
+    if (k[q].n)
+      each_type(q, [&](auto vec) {
+        typedef decltype(vec) T;
+#pragma unroll
+        for (int i = 0; i < V; i++)
+#pragma unroll
+          for (int e = 0; e < T::N; e++) acc.add(T::value(v[q][i], e));
+        acc.add(T::one((typename T::Raw)tail[q]));
+      });
   double nm;
   const float coef = coef_of<INF>(block_join<INF, kSmallThreads>(acc.get()), max_norm, &nm);
   if (norm && threadIdx.x == 0) *norm = (float)nm;
-  for (int c = wave; c < s.start[s.count]; c += kWaves)
-    scale_chunk<64>(s, o, chunk_of<kSmallChunk>(s, c), coef);
+#pragma unroll
+  for (int q = 0; q < kPerWave; q++)
+    if (k[q].n && !(k[q].x == k[q].out && coef == 1.0f))
+      each_type(q, [&](auto vec) {
+        typedef decltype(vec) T;
+        const int whole = k[q].n / T::N, r = whole * T::N + lane;
+#pragma unroll
+        for (int i = 0; i < V; i++)
+          if (64 * i + lane < whole) ((u32x4_g2 *)k[q].out)[64 * i + lane] = T::scaled(v[q][i], coef);
+        if (r < k[q].n)
+          ((typename T::Raw *)k[q].out)[r] = T::raw(T::one((typename T::Raw)tail[q]) * coef);
+      });
 }
 
 int64_t chunks_of(const moe_grad_tensor &t, int bytes) {
@@ -263,10 +339,11 @@ int64_t chunks_of(const moe_grad_tensor &t, int bytes) {
 
 // The next launch's tensors, from the first one that is not in one yet; those
 // without values are left out.
-int fill(Set *s, Outs *o, int at, int count, const moe_grad_tensor *t, int bytes = kChunk) {
+template <int K>
+int fill(SetOf<K> *s, OutsOf<K> *o, int at, int count, const moe_grad_tensor *t, int bytes = kChunk) {
   s->count = 0;
   s->start[0] = 0;
-  for (; at < count && s->count < kSet; at++) {
+  for (; at < count && s->count < K; at++) {
     if (!t[at].numel) continue;
     const int64_t c = s->start[s->count] + chunks_of(t[at], bytes);
     if (c > 0x7FFFFFFF) break;  // (a launch of its own then: one tensor has fewer)
@@ -324,12 +401,12 @@ void scale_launches(int count, const moe_grad_tensor *t, const double *partials,
 template <bool INF>
 void clip(int count, const moe_grad_tensor *t, double *partials, float max_norm, float *norm,
           hipStream_t s) {
-  // Six tensors of 131 KB together: 9.7 us in two launches.
+  // Six tensors of 131 KB together: 10.3 us in two launches, 7.9 here.
   int64_t small = 0;
   for (int i = 0; i < count && small <= kSmallChunks; i++) small += chunks_of(t[i], kSmallChunk);
   if (small && small <= kSmallChunks) {
-    Set set;
-    Outs o;
+    SetOf<kSmallSet> set{};
+    OutsOf<kSmallSet> o{};
     if (fill(&set, &o, 0, count, t, kSmallChunk) == count) {
       hipLaunchKernelGGL(grad_small_kernel<INF>, dim3(1), dim3(kSmallThreads), 0, s, set, o, max_norm,
                          norm);
