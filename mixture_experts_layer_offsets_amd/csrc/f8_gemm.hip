@@ -33,53 +33,52 @@ struct Geo {
   static constexpr int XQ = XB / 8192;  // loads of a wave and stage, of rows
 };
 
-// Tiles of T rows over the groups, one group behind the other: how many there are, and
-// where tile i lies.  Every wave adds the groups' lengths up by itself, 64 groups at a time.
-struct Place {
-  int g, first;  // group, and its first tile
-};
-template <class F>
-__device__ __forceinline__ int each_64_groups(const int32_t *offsets, int groups, int rows, int T, F &&f) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int g0 = 0; g0 < groups; g0 += 64) {
-    int n = 0;
-    if (g0 + lane < groups) {
-      const F8Span sp = f8_span(offsets, g0 + lane, rows);
-      n = (sp.end - sp.begin + T - 1) / T;
-    }
-    int upto = n;
+// Tiles of T rows over the groups, one group behind the other, counted by every wave for
+// itself, 64 groups at a time.
+struct Tiles {
+  const int32_t *offsets;
+  int groups, rows, T;
+  int total;           // tiles of all groups
+  int begin, upto, n;  // lane's group of the 64 looked at last: its rows' begin, tiles up to
+                       // its end, its own
+  int g0;
+  __device__ __forceinline__ int count(int at, int before) {  // tiles up to the end of these 64
+    const int lane = threadIdx.x & 63;
+    g0 = at;
+    F8Span sp{0, 0};
+    if (at + lane < groups) sp = f8_span(offsets, at + lane, rows);
+    begin = sp.begin;
+    n = (sp.end - sp.begin + T - 1) / T;
+    upto = n;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(upto, o, 64);
       if (lane >= o) upto += v;
     }
-    if (f(g0, before, n, before + upto)) break;
-    before += __builtin_amdgcn_readlane(upto, 63);
+    upto += before;
+    return min(__builtin_amdgcn_readlane(upto, 63), 1 << 30);  // spans that overlap add up to more
   }
-  return before;
-}
-__device__ __forceinline__ int tiles_of(const int32_t *offsets, int groups, int rows, int T) {
-  return each_64_groups(offsets, groups, rows, T, [](int, int, int, int) { return false; });
-}
-__device__ __forceinline__ Place place_of(const int32_t *offsets, int groups, int rows, int T, int i) {
-  Place p{0, 0};
-  each_64_groups(offsets, groups, rows, T, [&](int g0, int, int n, int upto) {
-    const uint64_t in = __ballot(i >= upto - n && i < upto);
-    if (!in) return false;
-    const int l = __ffsll((unsigned long long)in) - 1;
-    p.g = g0 + l;
-    p.first = __builtin_amdgcn_readlane(upto - n, l);
-    return true;
-  });
-  return p;
-}
+  __device__ __forceinline__ Tiles(const int32_t *o, int g, int r, int t)
+      : offsets(o), groups(g), rows(r), T(t), total(0) {
+    for (int at = 0; at < groups; at += 64) total = count(at, total);
+    total = min(total, rows / T + groups);  // what ascending offsets reach
+  }
+  // The group of tile i < total, and the first row of that tile.
+  __device__ __forceinline__ int group_of(int i, int *row) {
+    if (groups > 64) {
+      int before = 0;
+      for (int at = 0; at < groups; at += 64) {
+        before = count(at, before);
+        if (i < before) break;
+      }
+    }
+    const int l = __ffsll((unsigned long long)__ballot(i < upto && i >= upto - n)) - 1;
+    const int first = __builtin_amdgcn_readlane(upto - n, l);
+    *row = __builtin_amdgcn_readlane(begin, l) + (i - first) * T;
+    return g0 + l;
+  }
+};
 
-// One tile of TM rows x 256 outputs.  Operands move from memory straight into LDS, a
-// block of 128 contraction values a stage, two stages in turn: while one is used the
-// next one arrives.  Rows lie in LDS 128 bytes apart with their chunks exchanged by
-// the row's low bits, tiles of weights in the order of the waves' reads.
-//   COLS: the weight gradient, whose outputs have scales of their own.
 // X, A, B: rows, first halves and second halves of the waves' tiles, of two stages: arrays
 // of their own, so that the compiler can tell what is read from what is being filled.
 template <int TM, bool COLS>
@@ -103,13 +102,11 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     xrow = m0;
     out = p.out + ((size_t)g * p.xrows + m0) * p.ostride;
   } else {
-    const int MT = tiles_of(p.offsets, p.groups, p.rows, TM);
-    if (blockIdx.x >= (unsigned)(MT * p.nN)) return;
-    tile_of_block(blockIdx.x, MT, p.nN, mt, nt);
-    const Place at = place_of(p.offsets, p.groups, p.rows, TM, mt);
-    g = at.g;
+    Tiles tiles(p.offsets, p.groups, p.rows, TM);
+    if (blockIdx.x >= (unsigned)(tiles.total * p.nN)) return;
+    tile_of_block(blockIdx.x, tiles.total, p.nN, mt, nt);
+    g = tiles.group_of(mt, &m0);
     const F8Span sp = f8_span(p.offsets, g, p.rows);
-    m0 = sp.begin + (mt - at.first) * TM;
     valid = min(TM, sp.end - m0);
     step0 = 0;
     steps = p.wsteps;
@@ -257,28 +254,35 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
   };
   if (steps > 0) {
 #pragma unroll
-    for (int q = 0; q < G::XQ; q++) {
-      dma_x(X0, 0, q);
-      dma_x(X1, 1, q);
-    }
+    for (int q = 0; q < G::XQ; q++) dma_x(X0, 0, q);
 #pragma unroll
     for (int q = 0; q < 2; q++) {
       dma_w(A0, 0, 0, q);
       dma_w(B0, 0, 1, q);
-      dma_w(A1, 1, 0, q);
     }
     if constexpr (COLS) {
       dma_s(A0, 0, 0);
       dma_s(B0, 0, 1);
-      dma_s(A1, 1, 0);
     }
     scales(0, sc);
+    // stage 0 is there before the first of stage 1, which the middle of stage 0 waits for:
+    // what follows is kLater loads
+    constexpr int kLater = G::XQ + 2 + (COLS ? 1 : 0) + NS;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < G::XQ; q++) dma_x(X1, 1, q);
+#pragma unroll
+    for (int q = 0; q < 2; q++) dma_w(A1, 1, 0, q);
+    if constexpr (COLS) dma_s(A1, 1, 0);
     scales(1, s1);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < G::NJ; j++) so[j] = 0.0f;
 #pragma unroll
     for (int q = 0; q < kRing; q++) d[q] = sw[q & 1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    __builtin_amdgcn_s_waitcnt(kVmcnt0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLater));
     barrier_after_wait();
 #pragma unroll
     for (int j = 0; j < G::NJ; j++) load_x(X0, j);
