@@ -14,6 +14,18 @@ int status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
+// Whether a value of `rows` rows of na values at a lies on one of rows of nb values at b,
+// strides and sizes in 16-bit values.  Rows of one stride may lie between each other's.
+bool overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t sb, int64_t nb,
+             int64_t rows) {
+  const int64_t d = ((int64_t)(uintptr_t)b - (int64_t)(uintptr_t)a) / 2;
+  const int64_t la = (rows - 1) * sa + na, lb = (rows - 1) * sb + nb;  // from first to last
+  if (d >= la || -d >= lb) return false;
+  if (rows == 1 || sa != sb) return true;
+  const int64_t at = ((d % sa) + sa) % sa;
+  return at < na || at + nb > sa;
+}
+
 // Quantised rows in a workspace.
 size_t rows_bytes(const F8Dims &d, int32_t rows, size_t *scales) {
   *scales = up256((size_t)d.ks * rows * kF8Block);
@@ -149,11 +161,12 @@ int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x, int64_
   int rc = f8_dims(shape, &d);
   if (rc) return rc;
   if (x_stride < d.k || out_stride < d.n || !packed || !aligned16(packed) ||
-      (rows > 0 && (!x || !out || x == out)))
+      (rows > 0 && (!x || !out)))
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_rows(d, rows, offsets))) return rc;
   if (x_stride > kMostStride || out_stride > kMostStride) return MOE_ERR_UNSUPPORTED;
   if (!rows) return MOE_OK;
+  if (overlap(x, x_stride, d.k, out, out_stride, d.n, rows)) return MOE_ERR_INVALID_ARG;
   const F8Rows xr{(const uint16_t *)x, x_stride, d.f16};
   hipStream_t s = (hipStream_t)stream;
   if (f8_few_staged(d, rows)) {
@@ -201,10 +214,15 @@ int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x, int64_t
   int rc = f8_dims(shape, &d);
   if (rc) return rc;
   if (x_stride < d.k || dy_stride < d.n || !dw || !ws || !aligned16(ws) ||
-      (rows > 0 && (!x || !dy || x == dw || dy == dw)) || (!offsets && d.groups != 1))
+      (rows > 0 && (!x || !dy)) || (!offsets && d.groups != 1))
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_wgrad(d, rows))) return rc;
   if (x_stride > kMostStride || dy_stride > kMostStride) return MOE_ERR_UNSUPPORTED;
+  // dw lies in one run; between a tensor's rows it would have to fit into one gap
+  const int64_t all = (int64_t)d.groups * d.k * d.n;
+  if (rows && (overlap(dw, all, all, x, (rows - 1) * x_stride + d.k, (rows - 1) * x_stride + d.k, 1) ||
+               overlap(dw, all, all, dy, (rows - 1) * dy_stride + d.n, (rows - 1) * dy_stride + d.n, 1)))
+    return MOE_ERR_INVALID_ARG;
   const Cols c = cols_of(d, rows);
   if (ws_bytes < c.bytes) return MOE_ERR_WORKSPACE;
   uint8_t *xc = (uint8_t *)ws, *yc = xc + c.yc;

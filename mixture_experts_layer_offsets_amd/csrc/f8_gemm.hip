@@ -200,12 +200,13 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     for (int v = 0; v < 4; v++)
       acc[i][j][v] = fmaf(COLS ? s[j] * sw[i & 1][v] : s[j], d[q % kRing][v], acc[i][j][v]);
   };
-  // Xc, Ac, Bc hold stage kt, its rows and first tile read; the last products
-  // of the stage before are not scaled yet (so, sc, s1: the rows' scales of stages kt - 1,
-  // kt, kt + 1).  Xn and An hold stage kt + 1.  In the middle the waves meet: what was sent for a stage
-  // ago is there then; Xc, Ac and Bn (stage kt - 1) have been read and are refilled, load
-  // by load between the products (in a burst the loads would stall the wave).  The next
-  // stage's rows are read as the last tile's products leave theirs.
+  // Xc, Ac, Bc hold stage kt, its rows and first tile read; the last products of the stage
+  // before are not scaled yet (so, sc, s1: the rows' scales of stages kt - 1, kt, kt + 1).
+  // Before the last tile of the first half the waves meet: what was sent for a stage ago is
+  // there then (Bc; Xn and An with stage kt + 1), and Xc, Ac and Bn (stage kt - 1) have been
+  // read and are refilled, load by load between the products (in a burst the loads would
+  // stall the wave).  The next stage's rows are read as the last tile's products leave
+  // theirs.
   float so[G::NJ], sc[NS], s1[NS];
   auto stage = [&](uint8_t *Xc, uint8_t *Ac, uint8_t *Bc, uint8_t *Xn, uint8_t *An, uint8_t *Bn,
                    int kt) {
