@@ -106,6 +106,7 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     if (blockIdx.x >= (unsigned)(tiles.total * p.nN)) return;
     tile_of_block(blockIdx.x, tiles.total, p.nN, mt, nt);
     g = tiles.group_of(mt, &m0);
+    if (g < 0) return;
     const F8Span sp = f8_span(p.offsets, g, p.rows);
     valid = min(TM, sp.end - m0);
     step0 = 0;
@@ -170,6 +171,18 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     if constexpr (!COLS)
       s[G::NJ] = __builtin_bit_cast(
           float, __builtin_amdgcn_raw_buffer_load_b32(f8_buffer(wsc, p.wsteps * 4), 0, k1 * 4, 0));
+  };
+  // load n of stage kt's refills: of Bn for the next stage, of Xc and Ac for the one after
+  auto refill_load = [&](uint8_t *Xc, uint8_t *Ac, uint8_t *Bn, int kt, int n) {
+    if (n >= 0 && n < 2) dma_w(Bn, kt + 1, 1, n);
+    else if (n >= 2 && n < 2 + G::XQ) dma_x(Xc, kt + 2, n - 2);
+    else if (n >= 2 && n < 4 + G::XQ) dma_w(Ac, kt + 2, 0, n - 2 - G::XQ);
+    else if (COLS && n == 4 + G::XQ) dma_s(Ac, kt + 2, 0);
+    else if (COLS && n == 5 + G::XQ) dma_s(Bn, kt + 1, 1);
+  };
+  auto refill = [&](uint8_t *Xc, uint8_t *Ac, uint8_t *Bn, int kt) {
+#pragma unroll
+    for (int n = 0; n < G::XQ + 6; n++) refill_load(Xc, Ac, Bn, kt, n);
   };
   f32x4 acc[G::NI][G::NJ];
 #pragma unroll
@@ -237,12 +250,7 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
           if (i + 1 < G::NI) load_s(Ac, Bc, i + 1);
           else load_s(An, Bn, 0);
         }
-        const int n = q - (kHalf - 1) * G::NJ;
-        if (n >= 0 && n < 2) dma_w(Bn, kt + 1, 1, n);
-        else if (n >= 2 && n < 2 + G::XQ) dma_x(Xc, kt + 2, n - 2);
-        else if (n >= 2 && n < 4 + G::XQ) dma_w(Ac, kt + 2, 0, n - 2 - G::XQ);
-        else if (COLS && n == 4 + G::XQ) dma_s(Ac, kt + 2, 0);
-        else if (COLS && n == 5 + G::XQ) dma_s(Bn, kt + 1, 1);
+        refill_load(Xc, Ac, Bn, kt, q - (kHalf - 1) * G::NJ);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -285,18 +293,29 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     for (int q = 0; q < kRing; q++) d[q] = sw[q & 1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLater));
     barrier_after_wait();
+    if (wm0 < valid) {
 #pragma unroll
-    for (int j = 0; j < G::NJ; j++) load_x(X0, j);
-    load_w(A0, B0, 0);
-    load_s(A0, B0, 0);
-    int kt = 0;
-    for (; kt + 2 <= steps; kt += 2) {
-      stage(X0, A0, B0, X1, A1, B1, kt);
-      stage(X1, A1, B1, X0, A0, B0, kt + 1);
+      for (int j = 0; j < G::NJ; j++) load_x(X0, j);
+      load_w(A0, B0, 0);
+      load_s(A0, B0, 0);
+      int kt = 0;
+      for (; kt + 2 <= steps; kt += 2) {
+        stage(X0, A0, B0, X1, A1, B1, kt);
+        stage(X1, A1, B1, X0, A0, B0, kt + 1);
+      }
+      if (kt < steps) stage(X0, A0, B0, X1, A1, B1, kt);
+#pragma unroll
+      for (int q = 0; q < kRing - 1; q++) scale(G::NI * G::NJ - (kRing - 1) + q, so);
+    } else {
+      // a wave without rows: its loads and the meetings only, which leaves its SIMD to the
+      // wave that shares it (waves w and w + 4; their rows lie half a tile apart)
+      for (int kt = 0; kt < steps; kt++) {
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+        barrier_after_wait();
+        if (kt & 1) refill(X1, A1, B0, kt);
+        else refill(X0, A0, B1, kt);
+      }
     }
-    if (kt < steps) stage(X0, A0, B0, X1, A1, B1, kt);
-#pragma unroll
-    for (int q = 0; q < kRing - 1; q++) scale(G::NI * G::NJ - (kRing - 1) + q, so);
   }
   __builtin_amdgcn_s_waitcnt(kVmcnt0);  // the last loads, not used
   __syncthreads();
