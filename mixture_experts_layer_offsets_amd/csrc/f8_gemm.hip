@@ -137,7 +137,7 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
     if (q == 0) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 0, 0);
     if (q == 1) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 1024, 0);
     if (q == 2) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 2048, 0);
-    if (q == 3) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 3072, 0);
+    if (q == 3) __builtin_amdgcn_raw_ptr_buffer_load_lds(rX, to, 16, ox, 0, 3 * 1024, 0);
   };
   // ... and one tile a wave of the first or second half of each wave's tiles, in two
   auto dma_w = [&](uint8_t *W, int kt, int half, int q) {
