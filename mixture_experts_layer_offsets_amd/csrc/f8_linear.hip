@@ -82,12 +82,17 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
         sw[u][t] = tr.ws[at];
       }
   };
-  // few groups of this many rows are empty: the first weights need not wait for the offsets
-  load(s0);
+  // Of groups with four rows or more on average few are empty: the first weights need not
+  // wait for the offsets.  Weights of empty groups are not read (64 rows, all in one of 64
+  // groups of 2816 x 2048: 62 us if they were, 19 so).
+  const bool early = p.rows >= 4 * (int)gridDim.y;
+  if (early) load(s0);
   __builtin_amdgcn_sched_barrier(0);
   const F8Span sp = f8_span(p.offsets, g, p.rows);
   for (long r0 = sp.begin + (long)kPass * blockIdx.z; r0 < sp.end; r0 += (long)kPass * gridDim.z) {
     const int nr = (int)min((long)kPass, sp.end - r0);
+    if (!early || r0 >= sp.begin + (long)kPass * gridDim.z) load(s0);
+    __builtin_amdgcn_sched_barrier(0);
     long r[NB];
     f32x4 acc[TW][NB];
 #pragma unroll
@@ -124,7 +129,6 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
                          sx[u][b] * sw[u][t]);
       if (st + U < s1) load(st + U);
     }
-    if (r0 + (long)kPass * gridDim.z < sp.end) load(s0);
 #pragma unroll
     for (int t = 0; t < TW; t++) put<WAVES, NB>(p, acc[t], red, t0 + t, r0, nr);
   }
@@ -210,12 +214,16 @@ long blocks(const F8Dims &d, int rows, int tw, int nb) {
 
 }  // namespace
 
-// From f8_gemm.hip on where tiles of 128 rows x 256 outputs fill the chip better: 32
-// groups of 16 rows, 2816 x 2048: 41 us here, 55 there; of 32 rows 65 and 57.  One group
-// of 4096 x 4096: 256 rows 24 here, 35 there; 512 rows 40 and 36.
+// Against f8_gemm.hip's tiles of 128 rows x 256 outputs.  One group of 4096 x 4096: 256
+// rows 21 us here, 35 there; 512 rows 40 and 36.  Groups that are longer than the others
+// cost more here, where a workgroup takes a group's rows in turn, so several groups stay
+// up to 16 rows on average, or 32 where tiles would be too few: 32 groups of 2816 x 2048,
+// 512 rows in even groups 40 here and 54 there, with lengths that fall off as 1 / g 57 and
+// 55, 1024 even rows 65 and 57; 16 groups of 4096 x 4096, 384 rows 62 and 59, falling off
+// 84 and 61; of 1001 x 1000, 300 rows 12 and 15, 17 and 17.
 bool f8_few(const F8Dims &d, int rows) {
-  const int avg = average(d, rows);
-  return avg <= 24 || (avg <= 256 && blocks(d, rows, 4, 4) <= 512);
+  const int avg = average(d, rows), most = d.groups == 1 ? 256 : 32;
+  return avg <= 16 || (avg <= most && blocks(d, rows, 4, 4) <= 512);
 }
 
 // Quantising again in every workgroup against a launch of its own: that is d.nt rows

@@ -311,6 +311,100 @@ def test_every_group_the_same():
     assert torch.equal(out, out[:16].repeat(1500, 1))
 
 
+def repeated(rng, groups, reps, k, dtype):
+    """F8Linear of 256 random outputs that follow one another `reps` times, and their values."""
+    codes, scales, w = fo.random_codes(rng, groups, 256, k)
+    lin = m.F8Linear.pack(m.F8Shape(groups, 256 * reps, k, ROW[dtype]),
+                          torch.from_numpy(codes).cuda().repeat(1, reps, 1),
+                          torch.from_numpy(scales).cuda().repeat(1, reps, 1))
+    return lin, w
+
+
+# each choice of workgroup by the numbers of rows, outputs and groups: (rows, end of every
+# group's rows, times 256 outputs, contraction)
+CHOICES = {
+    "8 rows quantised first, 16 waves": (8, None, 10, 62 * 128),
+    "8 waves": (8, None, 20, 40 * 128),
+    "4 waves": (8, None, 40, 20 * 128),
+    "8 rows on average, some groups longer": (24, [0, 1, 23], 14, 20 * 128),
+    "24 rows, few outputs": (24, None, 10, 390),
+    "pairs of tiles": (24, None, 40, 390),
+    "pairs of tiles, two passes": (50, None, 20, 130),
+    "pairs of tiles, 4 waves": (12, None, 80, 130),
+    "pairs of tiles, 4 waves, groups": (30, [3, 27, 27], 28, 130),
+    "pairs of tiles, 64 rows": (60, None, 40, 390),
+    "4 tiles, 64 rows": (60, None, 80, 390),
+    "4 tiles, 64 rows, two passes": (100, None, 50, 130),
+    "tiles of 128 rows": (270, None, 3, 390),
+    "tiles of 128 rows, groups": (200, [1, 66, 195], 2, 520),
+    "tiles of 256 rows": (500, None, 128, 390),
+    "tiles of 256 rows, groups": (2000, [5, 70, 1999], 28, 520),
+}
+
+
+@BOTH
+@pytest.mark.parametrize("name", list(CHOICES))
+def test_each_choice(name, dtype):
+    M, ends, reps, k = CHOICES[name]
+    rng = np.random.default_rng([M, reps, k])
+    ends = [M] if ends is None else ends
+    lin, w = repeated(rng, len(ends), reps, k, dtype)
+    x = rows(rng, M, k, dtype)
+    note(f"f8 {name} {dtype}")
+    out = lin(x.cuda(), offsets([0] + ends)).view(M, reps, 256)
+    assert torch.equal(out, out[:, :1].expand(M, reps, 256))
+    for g, (a, b) in enumerate(zip([0] + ends, ends)):
+        if b > a:
+            check(f"group {g}", out[a:b, 0], x[a:b], w[g], dtype)
+    assert torch.all(out[ends[-1]:] == 0)
+
+
+@pytest.mark.parametrize("k,reps", [(300, 3), (520, 128)], ids=["128", "256"])
+def test_each_choice_of_the_weight_gradient(k, reps):
+    """Tiles of 128 and 256 rows of dw."""
+    rng = np.random.default_rng([k, reps])
+    M, off = 420, [3, 3, 390]
+    lin, _ = repeated(rng, 2, reps, k, FP)
+    x, dy = rows(rng, M, k, FP), rows(rng, M, 256, FP)
+    note(f"f8 weight gradient {k} x {256 * reps}")
+    got = lin.weight_gradient(x.cuda(), dy.cuda().repeat(1, reps), offsets(off)).view(2, k, reps, 256)
+    assert torch.equal(got, got[:, :, :1].expand(2, k, reps, 256))
+    for g in range(2):
+        span = slice(off[g], off[g + 1])
+        dw, bound = fo.weight_gradient(x[span].float().numpy(), dy[span].float().numpy())
+        within(f"group {g}", got[g, :, 0], dw, fo.rounded(dw, bound, FP))
+
+
+def test_many_groups_of_many_rows():
+    """More groups than lanes, in tiles of 128 rows, empty ones among them."""
+    groups, n, k = 150, 20, 130
+    rng = np.random.default_rng(15)
+    lin, w = make(rng, groups, n, k)
+    lengths = rng.integers(0, 90, groups)
+    lengths[[0, 63, 64, 65, 149]] = 0
+    lengths[[5, 128]] = 300
+    off = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    x = rows(rng, int(off[-1]), k)
+    note("f8 150 groups")
+    out = lin(x.cuda(), torch.from_numpy(off).cuda())
+    for g in range(groups):
+        if lengths[g]:
+            check(f"group {g}", out[off[g]:off[g + 1]], x[off[g]:off[g + 1]], w[g], BF)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_out_beside_x_in_one_buffer(M):
+    """Rows of x and out that lie between each other's."""
+    rng = np.random.default_rng(M)
+    lin, w = make(rng, 1, 50, 200)
+    x = rows(rng, M, 200)
+    both = torch.zeros((M, 260), dtype=BF, device="cuda")
+    both[:, 60:] = x.cuda()
+    lin(both[:, 60:], out=both[:, 5:55])
+    check("beside", both[:, 5:55], x, w[0], BF)
+    assert torch.equal(both[:, 60:].cpu(), x)
+
+
 # ------------------------------------------------------------------ gradients
 
 @BOTH

@@ -91,6 +91,21 @@ def test_clip(name, norm_type, in_place):
             assert all(np.array_equal(f64(o), b) for o, b in zip(outs, before))
 
 
+@pytest.mark.parametrize("sizes", [
+    [1000] * 16, [1000] * 17, [16384] * 3, [16384, 16384, 16384, 1], [16383, 16385, 16384], [0] * 20 + [3] * 16],
+    ids=["16", "17", "48-chunks", "49-chunks", "49-by-one", "16-and-empty"])
+@pytest.mark.parametrize("norm_type", NORMS)
+def test_where_one_workgroup_ends(norm_type, sizes):
+    """Sets on both sides of what one workgroup takes."""
+    rng = np.random.default_rng(len(sizes))
+    for dtype in (F32, BF):
+        grads = tensors(rng, [n if dtype == F32 else 2 * n for n in sizes], [dtype])
+        before = [f64(t) for t in grads]
+        note(f"clip {len(sizes)} tensors norm {norm_type} {dtype}")
+        norm = m.GradClip(m.GradSet(grads), norm_type)(0.5)
+        check(grads, grads, before, norm, norm_type, 0.5)
+
+
 def test_past_the_partial_sums():
     """So many launches that their partial sums are added up before the scaling."""
     n = 128 * 40
