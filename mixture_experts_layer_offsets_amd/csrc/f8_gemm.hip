@@ -1,5 +1,27 @@
 // Products of many rows in 8 bits with a scale per block of 128 (f8_device.h): the
 // forward and data-gradient product of grouped rows, and the weight gradient.
+//
+//   acc[n][r] += (sx[r][b] sw[n][b]) dot(w codes, x codes)    a block b of 128 a stage
+//
+// A workgroup of eight waves computes 256 rows (or 128) x 256 outputs, one a CU: its
+// waves hold 128 x 64 results each (64 x 64), and two stages lie in LDS (128 KB, or 96;
+// with the outputs' scales 136 or 104), which loads fill directly.  The matrix unit
+// sums the 128 products of a block from zero, and the scales multiply that sum in fp32.
+//
+// What bounds it: at 16384 rows x 4096 x 7168 in 6 groups 509 us with the rows'
+// quantising (48), 2.1 PFLOP/s in the product, where the library's 8-bit product with one
+// scale a tensor takes 308 us.  The chip runs these products at a reduced clock (1.5 GHz
+// here, 2.2 in a loop of matrix instructions alone), so that every instruction between
+// them counts twice; a stage takes 2870 cycles where its matrix instructions take 2048.
+// In registers alone, without loads, the instruction reaches 4.7 PFLOP/s, 4.3 with a
+// multiply-add for each of its results as the forward has, and 3.2 with two operations as
+// the weight gradient has, whose scales differ along both sides: there 555 of 665 us (962
+// GFLOP), 4040 cycles a stage.  64 groups of 384 rows x 2816 x 2048: 228 us, 27 of a
+// tile's 35 us in the loop and the rest its offsets, first loads and results; half-empty
+// last tiles cost the rest.
+// Tried and not faster: the groups' last tiles last (254 us of 230: their weights are not
+// in the cache then), tiles of 64 rows, four waves a SIMD (spills), 128 outputs a tile
+// (1024 rows x 4096 x 4096 32 us of 37, but 57 of 46 at 2048 rows).
 #include <algorithm>
 
 #include "f8_device.h"
@@ -369,8 +391,8 @@ __global__ __launch_bounds__(kThreads, 2) void f8_gemm_kernel(Args p) {
 
 // Tiles of 256 rows read less for the same products; those of 128 take about 0.75 of
 // their time, and fill the chip where tiles are few (4096 x 4096, us with 256 / 128: 1024
-// rows 53 / 37, 2048 rows 57 / 46, 4096 rows 77 / 90; 64 groups of 384 rows, 2816 x 2048:
-// 239 / 284): by the rounds of 256 workgroups that either takes.
+// rows 53 / 37, 2048 rows 57 / 45, 4096 rows 75 / 83; 64 groups of 384 rows, 2816 x 2048:
+// 224 / 273): by the rounds of 256 workgroups that either takes.
 bool tall_tiles(long rows, long groups, int nN) {
   auto rounds = [&](int TM) { return ((rows + TM - 1) / TM * groups * nN + 255) / 256; };
   return 4 * rounds(256) <= 3 * rounds(128);

