@@ -1,5 +1,6 @@
 // Products of a few rows with 4-bit weights and group scales: formats, packed
-// layout and the streaming loop shared by w4_linear.hip and w4_ffn.hip.
+// layout and the streaming loop shared by w4_linear.hip and w4_ffn.hip, which takes
+// 8-bit weights too (F8Fmt, packed as f8_device.h says).
 //
 //   y[r][n] = sum_k x[r][k] w[k][n],  x bf16, sums in fp32
 //   MXFP4: w = 2^(s - 127) E2M1(code), one E8M0 scale s per 32 along k
@@ -70,9 +71,9 @@ __device__ __forceinline__ rsrc_t w4_buffer(const void *p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, bytes, kBufferDword3);
 }
 
-// One lane's scales of one tile, as loaded.
-// Codes: one lane's of a tile, kTile bytes in all.  col(i, h): first of the 8
-// contraction values that lanes l / 16 = h hold in the i-th of a step's four products.
+// Codes: one lane's of a tile, kTile bytes in all; Scales: those that it needs, as loaded.
+// col(i, h): first of the 8 contraction values that lanes l / 16 = h hold in the i-th of a
+// step's four products.
 typedef uint4 W4Codes;
 __device__ __forceinline__ int w4_col(int i, int h) { return 32 * i + 8 * h; }
 

@@ -1,6 +1,6 @@
 // Few-token FFN of experts with 4-bit weights, and with 8-bit ones of f8_device.h (the
-// formats of w4_device.h).  A row is a (token,
-// expert) pair, at the place f of the token's first slot with that expert:
+// formats of w4_device.h).  A row is a (token, expert) pair, at the place f of the
+// token's first slot with that expert:
 //   gate_up: a[f] = w silu(x Wg) (x Wu), w the routing weight (summed if the token
 //            names the expert twice), rounded to bf16;
 //   down:    y[f] = a[f] Wd in fp32, and out[t] = the sum of the token's y (+ the
@@ -15,7 +15,8 @@
 // MXFP4, 7168 x 2048, 8 of 48 experts, one token: gate_up 23.4 us (125 MB, which a
 // plain read takes 19.5 for), down 17.8 us (62 MB, 10.3).  INT4 in groups of 64
 // with fp16 scales, 2048 x 1408, 32 tokens over about 30 of 32 experts: 24.8 us
-// (94 MB, 15.0), 13.5 us (47 MB, 8.2), combine 5.0.
+// (94 MB, 15.0), 13.5 us (47 MB, 8.2), combine 5.0.  8 bits, the same two: 38.9 us (235 MB,
+// 40.0) and 27.0 (117 MB, 20.0); 35.6 (173 MB, 29.5) and 18.6 (87 MB, 14.7), combine 4.6.
 //
 // Where that does not hold: the kernels are chosen by the routed rows an expert has
 // on average.  A shared expert has every token's row and goes through the same
