@@ -34,7 +34,7 @@ size_t rows_bytes(const F8Dims &d, int32_t rows, size_t *scales) {
 
 // Quantised columns of x and dy in a workspace.
 struct Cols {
-  size_t xs, yc, ys, bytes;  // where each piece begins; x's codes first
+  size_t xs, yc, ys, parts, bytes;  // where each piece begins; x's codes first
 };
 Cols cols_of(const F8Dims &d, int32_t rows) {
   const size_t st = f8_stages(rows, d.groups);
@@ -42,7 +42,9 @@ Cols cols_of(const F8Dims &d, int32_t rows) {
   c.xs = up256(st * d.k * kF8Block);
   c.yc = c.xs + up256(st * ((d.k + 15) & ~15) * 4);
   c.ys = c.yc + up256(st * d.nt * 2048);
-  c.bytes = c.ys + up256(st * d.nt * 16 * 4);
+  c.parts = c.ys + up256(st * d.nt * 16 * 4);
+  const int splits = f8_splits(d, rows);
+  c.bytes = c.parts + (splits > 1 ? up256((size_t)splits * d.groups * d.k * d.nt * 16 * 4) : 0);
   return c;
 }
 
@@ -230,7 +232,7 @@ int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x, int64_t
   hipStream_t s = (hipStream_t)stream;
   launch_f8_quant_cols({(const uint16_t *)x, x_stride, d.f16}, {(const uint16_t *)dy, dy_stride, d.f16},
                        rows, d, offsets, xc, xs, yc, ys, s);
-  launch_f8_wgrad(d, rows, xc, xs, yc, ys, offsets, (uint16_t *)dw, s);
+  launch_f8_wgrad(d, rows, xc, xs, yc, ys, offsets, (uint16_t *)dw, (float *)(xc + c.parts), s);
   return status();
 }
 

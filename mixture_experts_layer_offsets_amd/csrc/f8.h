@@ -69,6 +69,9 @@ bool f8_few_staged(const F8Dims &d, int rows);
 // launch_f8_quant_cols.
 void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *xs,
                      const uint8_t *yc, const float *ys, const int32_t *offsets, uint16_t *dw,
-                     hipStream_t s);
+                     float *parts, hipStream_t s);
+// In how many pieces launch_f8_wgrad takes each group's rows: past one, `parts` holds that
+// many fp32 results, columns rounded up to 16.
+int f8_splits(const F8Dims &d, int rows);
 
 }  // namespace moe

@@ -41,8 +41,9 @@ struct Args {
   const float *xs, *ws;    // scales [step][spitch]; [n / 16][wsteps], or [step][npitch]
   const int32_t *offsets;
   uint16_t *out;
+  float *parts;  // split weight gradient: sums [split][group][xrows][npitch]
   long ostride;
-  int rows, groups, n, nt, f16;
+  int rows, groups, n, nt, f16, splits;
   int xrows, xpitch, spitch;  // weight gradient: rows of the result, their pitches
   int wsteps, npitch, nN, MT;
 };
@@ -103,7 +104,7 @@ struct Tiles {
 
 // X, A, B: rows, first halves and second halves of the waves' tiles, of two stages: arrays
 // of their own, so that the compiler can tell what is read from what is being filled.
-template <int TM, bool COLS>
+template <int TM, bool COLS, bool SPLIT>
 __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1, uint8_t *A0,
                                         uint8_t *A1, uint8_t *B0, uint8_t *B1) {
   using G = Geo<TM>;
@@ -113,12 +114,17 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
   size_t xrow;  // first row of the tile, in the operand
   uint16_t *out;
   if constexpr (COLS) {
-    const int per = p.MT * p.nN;
-    g = blockIdx.x / per;
-    tile_of_block(blockIdx.x - g * per, p.MT, p.nN, mt, nt);
+    const int per = p.MT * p.nN, at = blockIdx.x / per;  // split by split, group by group
+    g = SPLIT ? at % p.groups : at;
+    tile_of_block(blockIdx.x - at * per, p.MT, p.nN, mt, nt);
     const F8Span sp = f8_span(p.offsets, g, p.rows);
     step0 = sp.begin / kF8Block + g;
     steps = (sp.end - sp.begin + kF8Block - 1) / kF8Block;
+    if constexpr (SPLIT) {
+      const int z = at / p.groups, from = (int)((long)steps * z / p.splits);
+      steps = (int)((long)steps * (z + 1) / p.splits) - from;
+      step0 += from;
+    }
     m0 = mt * TM;
     valid = min(TM, p.xrows - m0);
     xrow = m0;
@@ -341,6 +347,17 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
   }
   __builtin_amdgcn_s_waitcnt(kVmcnt0);  // the last loads, not used
   __syncthreads();
+  if constexpr (SPLIT) {
+    float *to = p.parts + ((size_t)(blockIdx.x / (p.MT * p.nN)) * p.xrows + m0) * p.npitch + n0;
+#pragma unroll
+    for (int j = 0; j < G::NJ; j++)
+#pragma unroll
+      for (int i = 0; i < G::NI; i++) {
+        const int r = wm0 + 16 * j + l16, c = wn0 + 16 * i + 4 * h;
+        if (r < valid && n0 + c < p.npitch) *(f32x4 *)(to + (size_t)r * p.npitch + c) = acc[i][j];
+      }
+    return;
+  }
   // results to LDS, half of the rows a pass, 512 bytes a row with its 16-byte chunks
   // exchanged by the row, then out as whole rows
   constexpr int kRows = TM / 4;  // rows of X0, and of X1
@@ -380,13 +397,34 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
   }
 }
 
-template <int TM, bool COLS>
+template <int TM, bool COLS, bool SPLIT = false>
 __global__ __launch_bounds__(kThreads, 2) void f8_gemm_kernel(Args p) {
   using G = Geo<TM>;
   __shared__ __attribute__((aligned(1024))) uint8_t X0[G::XB], X1[G::XB];
   constexpr int kHalf = G::WB / 2 + (COLS ? 2048 : 0);  // and scales
   __shared__ __attribute__((aligned(1024))) uint8_t A0[kHalf], A1[kHalf], B0[kHalf], B1[kHalf];
-  f8_tile<TM, COLS>(p, X0, X1, A0, A1, B0, B1);
+  f8_tile<TM, COLS, SPLIT>(p, X0, X1, A0, A1, B0, B1);
+}
+
+// dw from the splits' sums, added in their order.  A thread takes 4 values of a row.
+__global__ __launch_bounds__(256) void f8_join_kernel(const float *__restrict__ parts, int splits,
+                                                      long rows, int n, int npitch, int f16,
+                                                      uint16_t *__restrict__ out) {
+  const int per = (n + 3) / 4;
+  const long at = (long)blockIdx.x * 256 + threadIdx.x, r = at / per;
+  const int c = (int)(at - r * per) * 4;
+  if (r >= rows) return;
+  const float *from = parts + r * npitch + c;
+  f32x4 s = *(const f32x4 *)from;
+#pragma unroll 8
+  for (int z = 1; z < splits; z++) {
+    const f32x4 v = *(const f32x4 *)(from + (size_t)z * rows * npitch);
+#pragma unroll
+    for (int e = 0; e < 4; e++) s[e] += v[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; e++)
+    if (c + e < n) out[r * n + c + e] = f8_to16(s[e], f16);
 }
 
 // Tiles of 256 rows read less for the same products; those of 128 take about 0.75 of
@@ -422,9 +460,21 @@ void launch_f8_gemm(const F8Dims &d, int rows, const uint8_t *codes, const float
   else go(f8_gemm_kernel<128, false>, 128);
 }
 
+// Few results of many rows: a group's stages in pieces of 4 or more on average, as many
+// as the chip takes at once, whose sums a second kernel adds.  One group, us without and
+// with: 256 x 256 of 1000 rows (7 stages) 17 and 18, so not there, of 4000 39 and 21, of
+// 16000 124 and 25 (pieces of 8: 28); 1024 x 1024 of 16000 138 and 60; 2048 x 2048 of 4000
+// 48 and 50, of 16000 162 and 135.
+int f8_splits(const F8Dims &d, int rows) {
+  const long tiles = (long)d.groups * ((d.k + 127) / 128) * ((d.n + 255) / 256);
+  const long stages = rows / kF8Block / d.groups;
+  if (stages < 12) return 1;
+  return (int)std::max(1L, std::min({256 / tiles, stages / 4, 32L}));
+}
+
 void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *xs,
                      const uint8_t *yc, const float *ys, const int32_t *offsets, uint16_t *dw,
-                     hipStream_t s) {
+                     float *parts, hipStream_t s) {
   Args a{};
   a.xc = xc; a.xs = xs; a.wc = yc; a.ws = ys;
   a.offsets = offsets;
@@ -440,8 +490,21 @@ void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *
     hipLaunchKernelGGL(kernel, dim3((unsigned)((long)d.groups * a.MT * a.nN)), dim3(kThreads), 0, s,
                        a);
   };
-  if (tall_tiles(d.k, d.groups, a.nN)) go(f8_gemm_kernel<256, true>, 256);
-  else go(f8_gemm_kernel<128, true>, 128);
+  const int splits = f8_splits(d, rows);
+  if (splits > 1) {
+    a.MT = (d.k + 127) / 128;
+    a.splits = splits;
+    a.parts = parts;
+    hipLaunchKernelGGL((f8_gemm_kernel<128, true, true>),
+                       dim3((unsigned)(splits * d.groups * a.MT * a.nN)), dim3(kThreads), 0, s, a);
+    const long all = (long)d.groups * d.k * ((d.n + 3) / 4);
+    hipLaunchKernelGGL(f8_join_kernel, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, parts,
+                       splits, (long)d.groups * d.k, d.n, a.npitch, d.f16, dw);
+  } else if (tall_tiles(d.k, d.groups, a.nN)) {
+    go(f8_gemm_kernel<256, true>, 256);
+  } else {
+    go(f8_gemm_kernel<128, true>, 128);
+  }
 }
 
 }  // namespace moe

@@ -22,6 +22,7 @@ struct Few {
   uint16_t *out;
   long ostride;
   int rows, n, k, nt, ks, f16;
+  int early;  // passes whose first weights need not wait for the offsets
 };
 
 // The weights of one tile row, and its scales.
@@ -88,10 +89,7 @@ __global__ __launch_bounds__(WAVES * 64) void f8_few_kernel(Few p, const uint8_t
         sw[u][t] = tr.ws[at];
       }
   };
-  // Of groups with four rows or more on average few are empty: the first weights need not
-  // wait for the offsets.  Weights of empty groups are not read (64 rows, all in one of 64
-  // groups of 2816 x 2048: 62 us if they were, 19 so).
-  const bool early = p.rows >= 4 * (int)gridDim.y;
+  const bool early = (int)blockIdx.z < p.early;
   if (early) load(s0);
   __builtin_amdgcn_sched_barrier(0);
   const F8Span sp = f8_span(p.offsets, g, p.rows);
@@ -204,7 +202,7 @@ Few few_of(const F8Dims &d, int rows, const int32_t *offsets, const void *packed
            long ostride) {
   const uint8_t *tiles = (const uint8_t *)packed;
   return {tiles, (const float *)(tiles + d.code_bytes), offsets, out, ostride,
-          rows, d.n, d.k, d.nt, d.ks, d.f16};
+          rows, d.n, d.k, d.nt, d.ks, d.f16, 0};
 }
 
 int average(const F8Dims &d, int rows) { return (rows + d.groups - 1) / d.groups; }
@@ -220,16 +218,15 @@ long blocks(const F8Dims &d, int rows, int tw, int nb) {
 
 }  // namespace
 
-// Against f8_gemm.hip's tiles of 128 rows x 256 outputs.  One group of 4096 x 4096: 256
-// rows 21 us here, 35 there; 512 rows 40 and 36.  Groups that are longer than the others
-// cost more here, where a workgroup takes a group's rows in turn, so several groups stay
-// up to 16 rows on average, or 32 where tiles would be too few: 32 groups of 2816 x 2048,
-// 512 rows in even groups 40 here and 54 there, with lengths that fall off as 1 / g 57 and
-// 55, 1024 even rows 65 and 57; 16 groups of 4096 x 4096, 384 rows 62 and 59, falling off
-// 84 and 61; of 1001 x 1000, 300 rows 12 and 15, 17 and 17.
+// Against f8_gemm.hip's tiles of 128 rows x 256 outputs: as long as 64 rows x 64 outputs a
+// workgroup take the chip once.  One group, us here and there: 4096 x 4096, 256 rows 21 and
+// 35, 300 rows 33 and 34; 1024 x 7168, 1000 rows 30 and 56, 4000 rows 105 and 76; 16 x
+// 7168, 4000 rows 29 and 61.  8 groups of 1024 x 2048, even lengths and lengths that fall
+// off as 1 / g: 512 rows 18 and 22, 20 and 23; 1024 rows 23 and 24, 25 and 23.  Up to 16
+// rows on average the weights are all there is to read: 32 groups of 2816 x 2048, 512 rows
+// in even groups 40 here and 54 there, falling off 57 and 55, 1024 even rows 65 and 57.
 bool f8_few(const F8Dims &d, int rows) {
-  const int avg = average(d, rows), most = d.groups == 1 ? 256 : 32;
-  return avg <= 16 || (avg <= most && blocks(d, rows, 4, 4) <= 512);
+  return average(d, rows) <= 16 || blocks(d, rows, 4, 4) <= 256;
 }
 
 // Quantising again in every workgroup against a launch of its own: that is d.nt rows
@@ -244,18 +241,30 @@ bool f8_few_staged(const F8Dims &d, int rows) {
 void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float *scales,
                    const int32_t *offsets, const void *packed, uint16_t *out, long ostride,
                    hipStream_t s) {
-  const Few p = few_of(d, rows, offsets, packed, out, ostride);
+  Few p = few_of(d, rows, offsets, packed, out, ostride);
   const int avg = average(d, rows);
   auto go = [&](auto kernel, int waves, int tw, int nb) {
-    const int passes = std::min((avg + 16 * nb - 1) / (16 * nb), 65535);
+    const int need = (avg + 16 * nb - 1) / (16 * nb), most = (rows + 16 * nb - 1) / (16 * nb);
+    // Of groups with four rows or more on average few are empty: the first weights need not
+    // wait for the offsets.  Weights of empty groups are not read (64 rows, all in one of 64
+    // groups of 2816 x 2048: 62 us if they were, 19 so).
+    p.early = rows >= 4 * d.groups ? need : 0;
+    // Groups longer than the average: their further passes side by side, where that takes
+    // no more workgroups than the chip runs at once (8 groups of 1024 x 2048, 512 rows
+    // falling off as 1 / g: 31 us without, 20 so, even ones 18 and 18).
+    const long free = 2048 / ((long)((d.nt + tw - 1) / tw) * d.groups);
+    const int passes = (int)std::min<long>({std::max<long>(need, free), most, 65535});
     hipLaunchKernelGGL(kernel, dim3((d.nt + tw - 1) / tw, d.groups, passes), dim3(waves * 64), 0, s, p,
                        codes, scales);
   };
   // The more tiles and rows a workgroup takes, the less often either is read again, as
-  // long as some 200 workgroups are left.  One group of 4096 x 4096, us with (tiles,
+  // long as some 200 workgroups are left (and half of its tiles exist: 16000 rows of 16 x
+  // 512 in tiles of one 12.7 us, of four 14.2).  One group of 4096 x 4096, us with (tiles,
   // blocks of rows) of (4, 4) / (2, 4) / (2, 2) / (1, 2): 256 rows 24 / 30 / 32 / 45, 128
   // rows 23 / 17 / 19 / 26, 64 rows 22 / 17 / 13 / 16, 24 rows 19 / 14 / 12 / 11.
-  auto many = [&](int tw, int nb) { return blocks(d, rows, tw, nb) >= 200; };
+  auto many = [&](int tw, int nb) {
+    return blocks(d, rows, tw, nb) >= 200 && 2 * d.nt > tw;
+  };
   const bool more = blocks(d, rows, 2, 2) > 512;  // then four waves each
   if (avg <= 8) {
     const long n = blocks(d, rows, 1, 1);

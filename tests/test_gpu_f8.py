@@ -193,7 +193,7 @@ SPANS = {
 
 
 @BOTH
-@pytest.mark.parametrize("n,k", [(45, 3 * 128), (300, 200)])
+@pytest.mark.parametrize("n,k", [(45, 3 * 128), (300, 200), (4999, 200)])
 @pytest.mark.parametrize("name", list(SPANS))
 def test_grouped_strided_product(name, n, k, dtype):
     """x and out at odd offsets and strides; rows in no group are left as they were."""
@@ -232,14 +232,14 @@ def test_no_rows_and_bad_offsets():
     lin, _ = make(rng, 3, 20, 128)
     assert lin(torch.empty((0, 128), dtype=BF, device="cuda"), offsets([0] * 4)).shape == (0, 20)
     # offsets outside [0, rows] are kept inside: memory-safe, rows still in range
-    for M in (4, 400):
+    for M in (4, 400, 40000):
         out = lin(torch.ones((M, 128), dtype=BF, device="cuda"), offsets([-5, 1, 2, 100000]))
         assert torch.all(torch.isfinite(out.float()))
         out = lin(torch.ones((M, 128), dtype=BF, device="cuda"), offsets([M, 1, 5, 0]))
         assert torch.all(torch.isfinite(out.float()))
 
 
-@pytest.mark.parametrize("M", [12, 300])
+@pytest.mark.parametrize("M", [12, 300, 20000])
 def test_rows_do_not_mix(M):
     """A NaN or infinity in one row leaves the other rows' bits alone."""
     rng = np.random.default_rng(2)
@@ -254,7 +254,7 @@ def test_rows_do_not_mix(M):
     assert not torch.any(torch.isfinite(out[4].float())) and not torch.any(torch.isfinite(out[11].float()))
 
 
-@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("M", [5, 200, 20000])
 def test_large_and_small_rows(M):
     """Rows next to bf16's largest and smallest values: as the oracle's."""
     rng = np.random.default_rng(9)
@@ -282,6 +282,19 @@ def test_strides_past_four_gib():
         big[:M, :256] = x.cuda()
         lin(big[:M, :256], out=big[:M, 512:552])
         check("strides", big[:M, 512:552], x, w[0], BF)
+
+
+def test_strides_past_four_gib_in_tiles():
+    """The same in tiles of 128 rows: the rows behind 4 GiB."""
+    rng = np.random.default_rng(14)
+    M, n = 600, 8192
+    lin, w = make(rng, 1, n, 256)
+    big = torch.empty((M, 1 << 23), dtype=BF, device="cuda")
+    x = rows(rng, M, 256)
+    big[:, :256] = x.cuda()
+    note("f8 strides past 4 GiB in tiles")
+    lin(big[:, :256], out=big[:, 512:512 + n])
+    check("strides", big[:, 512:512 + n], x, w[0], BF)
 
 
 def test_packed_past_four_gib():
@@ -333,10 +346,11 @@ CHOICES = {
     "pairs of tiles, 4 waves": (12, None, 80, 130),
     "pairs of tiles, 4 waves, groups": (30, [3, 27, 27], 28, 130),
     "pairs of tiles, 64 rows": (60, None, 40, 390),
-    "4 tiles, 64 rows": (60, None, 80, 390),
-    "4 tiles, 64 rows, two passes": (100, None, 50, 130),
-    "tiles of 128 rows": (270, None, 3, 390),
-    "tiles of 128 rows, groups": (200, [1, 66, 195], 2, 520),
+    "4 tiles, 64 rows": (60, None, 60, 390),
+    "4 tiles, 64 rows, two passes": (100, None, 30, 130),
+    "one group long": (96, [2, 3, 95], 4, 390),
+    "tiles of 128 rows": (600, None, 40, 390),
+    "tiles of 128 rows, groups": (500, [1, 166, 495], 28, 520),
     "tiles of 256 rows": (500, None, 128, 390),
     "tiles of 256 rows, groups": (2000, [5, 70, 1999], 28, 520),
 }
@@ -377,22 +391,22 @@ def test_each_choice_of_the_weight_gradient(k, reps):
 
 def test_many_groups_of_many_rows():
     """More groups than lanes, in tiles of 128 rows, empty ones among them."""
-    groups, n, k = 150, 20, 130
+    groups, n, k = 300, 20, 130
     rng = np.random.default_rng(15)
     lin, w = make(rng, groups, n, k)
     lengths = rng.integers(0, 90, groups)
-    lengths[[0, 63, 64, 65, 149]] = 0
+    lengths[[0, 63, 64, 65, 299]] = 0
     lengths[[5, 128]] = 300
     off = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
     x = rows(rng, int(off[-1]), k)
-    note("f8 150 groups")
+    note("f8 300 groups")
     out = lin(x.cuda(), torch.from_numpy(off).cuda())
     for g in range(groups):
         if lengths[g]:
             check(f"group {g}", out[off[g]:off[g + 1]], x[off[g]:off[g + 1]], w[g], BF)
 
 
-@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("M", [3, 40, 300, 20000])
 def test_out_beside_x_in_one_buffer(M):
     """Rows of x and out that lie between each other's."""
     rng = np.random.default_rng(M)
@@ -408,7 +422,8 @@ def test_out_beside_x_in_one_buffer(M):
 # ------------------------------------------------------------------ gradients
 
 @BOTH
-@pytest.mark.parametrize("groups,M,n,k", [(1, 5, 40, 130), (3, 90, 150, 64), (2, 700, 260, 300)])
+@pytest.mark.parametrize("groups,M,n,k", [(1, 5, 40, 130), (3, 90, 150, 64), (2, 700, 260, 300),
+                                            (3, 9000, 130, 300)])
 def test_data_gradient(groups, M, n, k, dtype):
     """dx of x*W is dy's 8-bit values times W^T."""
     rng = np.random.default_rng([M, n])
@@ -436,6 +451,23 @@ def test_weight_gradient(name, n, k, dtype):
     for g in range(len(off) - 1):
         span = slice(off[g], off[g + 1])
         dw, bound = fo.weight_gradient(x[span, 1:k + 1].float().numpy(), dy[span, 2:n + 2].float().numpy())
+        within(f"group {g}", got[g], dw, fo.rounded(dw, bound, dtype))
+
+
+@BOTH
+@pytest.mark.parametrize("M,off,n,k", [
+    (17000, [0, 17000], 33, 40), (5000, [7, 4000, 4990], 45, 300), (8000, [5, 5, 6, 7999], 300, 130)])
+def test_weight_gradient_of_many_rows(M, off, n, k, dtype):
+    """Each group's rows in pieces, some of them without a stage."""
+    rng = np.random.default_rng([M, n])
+    x, dy = rows(rng, M, k, dtype), rows(rng, M, n + 1, dtype)
+    groups = len(off) - 1
+    lin, _ = make(rng, groups, n, k, dtype)
+    note(f"f8 weight gradient of {M} rows n={n} k={k} {dtype}")
+    got = lin.weight_gradient(x.cuda(), dy.cuda()[:, 1:], offsets(off))
+    for g in range(groups):
+        span = slice(off[g], off[g + 1])
+        dw, bound = fo.weight_gradient(x[span].float().numpy(), dy[span, 1:].float().numpy())
         within(f"group {g}", got[g], dw, fo.rounded(dw, bound, dtype))
 
 
@@ -505,15 +537,16 @@ def test_gradients_against_differences():
 
 # ------------------------------------------------------------------ as they are used
 
-def test_captured_and_replayed_on_another_stream():
+@pytest.mark.parametrize("M,n", [(300, 140), (9000, 300)])
+def test_captured_and_replayed_on_another_stream(M, n):
     """Forward, data and weight gradient captured into one graph on a side stream,
     replayed with new inputs and offsets, bitwise equal to eager calls."""
     rng = np.random.default_rng(11)
-    groups, M, n, k = 3, 300, 140, 200
+    groups, k = 3, 200
     lin, _ = make(rng, groups, n, k)
     turned = lin.transposed()
     x, dy = rows(rng, M, k).cuda(), rows(rng, M, n).cuda()
-    off = offsets([0, 20, 250, 300])
+    off = offsets([0, 20, 250, M])
     y, dx = torch.zeros_like(dy), torch.zeros_like(x)
     dw = torch.zeros((groups, k, n), dtype=BF, device="cuda")
     few = torch.zeros((groups, n), dtype=BF, device="cuda")
@@ -551,7 +584,7 @@ def test_captured_and_replayed_on_another_stream():
 def test_products_at_once_on_three_streams():
     rng = np.random.default_rng(12)
     lin, _ = make(rng, 1, 300, 500)
-    xs = [rows(rng, M, 500).cuda() for M in (4, 90, 600)]
+    xs = [rows(rng, M, 500).cuda() for M in (4, 90, 600, 9000)]
     want = [(lin(x), lin.weight_gradient(x, x[:, :300])) for x in xs]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in xs]
