@@ -207,13 +207,17 @@ Few few_of(const F8Dims &d, int rows, const int32_t *offsets, const void *packed
 
 int average(const F8Dims &d, int rows) { return (rows + d.groups - 1) / d.groups; }
 
-}  // namespace
-
-namespace {
-
 // Workgroups of tw tiles and 16 nb rows.
 long blocks(const F8Dims &d, int rows, int tw, int nb) {
   return (long)((d.nt + tw - 1) / tw) * d.groups * ((average(d, rows) + 16 * nb - 1) / (16 * nb));
+}
+
+// Passes of a group: what the average needs, and, for groups longer than it, further ones
+// side by side where that takes no more workgroups than the chip runs at once (8 groups of
+// 1024 x 2048, 512 rows falling off as 1 / g: 31 us without, 20 so, even ones 18 and 18).
+int passes(const F8Dims &d, int rows, int pass, long tiles) {
+  const long need = (average(d, rows) + pass - 1) / pass, most = ((long)rows + pass - 1) / pass;
+  return (int)std::min<long>({std::max<long>(need, 2048 / (tiles * d.groups)), most, 65535});
 }
 
 }  // namespace
@@ -229,13 +233,19 @@ bool f8_few(const F8Dims &d, int rows) {
   return average(d, rows) <= 16 || blocks(d, rows, 4, 4) <= 256;
 }
 
-// Quantising again in every workgroup against a launch of its own: that is d.nt rows
-// d.ks blocks.  8 rows of 2048 x 7168 (57 thousand) 10.6 us against 11.5, 32 rows in 32
-// groups of 2816 x 2048 (90) 21.6 against 23.6; 8 rows of 7168 x 4096 (115) 12.7 against
-// 11.5, 96 rows in the 32 groups (270) 33.6 against 31.3.
+// Quantising again in every workgroup against a launch of its own (3 us): that is d.nt rows
+// d.ks blocks.  Up to 8 rows a group: 8 rows of 2048 x 7168 (57 thousand) 10.6 us against
+// 11.5, 32 rows in 32 groups of 2816 x 2048 (90) 21.6 against 23.6; 8 rows of 7168 x 4096
+// (115) 12.7 against 11.5, 96 rows in the 32 groups (270) 33.6 against 31.3.  More rows, in
+// passes of 8 whose workgroups the chip holds: 16 of 2048 x 4096 (66) 8.0 against 11.0, of
+// 4096 x 4096 (131) 12.3 against 11.2; 1000 of 256 x 512 (64, 2000 workgroups) 8.1 against
+// 10.2, 4000 of 256 x 128 (64, 8000) 17.5 against 10.8; 16 groups of 1000 x 512, 160 rows
+// (40) 8.0 against 10.2, 32 of 512 x 512, 512 rows (66) 11.2 against 10.1.
 bool f8_few_staged(const F8Dims &d, int rows) {
-  return average(d, rows) <= kStaged && (long)d.nt * rows * d.ks <= 100000 &&
-         staged_lds(d.ks) <= kStagedLds;
+  const int avg = average(d, rows);
+  const long most = avg <= kStaged ? 100000 : d.groups == 1 ? 66000 : 44000;
+  return (long)d.nt * rows * d.ks <= most && staged_lds(d.ks) <= kStagedLds &&
+         (avg <= kStaged || (long)d.nt * d.groups * ((avg + kStaged - 1) / kStaged) <= 2048);
 }
 
 void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float *scales,
@@ -244,18 +254,13 @@ void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float 
   Few p = few_of(d, rows, offsets, packed, out, ostride);
   const int avg = average(d, rows);
   auto go = [&](auto kernel, int waves, int tw, int nb) {
-    const int need = (avg + 16 * nb - 1) / (16 * nb), most = (rows + 16 * nb - 1) / (16 * nb);
     // Of groups with four rows or more on average few are empty: the first weights need not
     // wait for the offsets.  Weights of empty groups are not read (64 rows, all in one of 64
     // groups of 2816 x 2048: 62 us if they were, 19 so).
-    p.early = rows >= 4 * d.groups ? need : 0;
-    // Groups longer than the average: their further passes side by side, where that takes
-    // no more workgroups than the chip runs at once (8 groups of 1024 x 2048, 512 rows
-    // falling off as 1 / g: 31 us without, 20 so, even ones 18 and 18).
-    const long free = 2048 / ((long)((d.nt + tw - 1) / tw) * d.groups);
-    const int passes = (int)std::min<long>({std::max<long>(need, free), most, 65535});
-    hipLaunchKernelGGL(kernel, dim3((d.nt + tw - 1) / tw, d.groups, passes), dim3(waves * 64), 0, s, p,
-                       codes, scales);
+    p.early = rows >= 4 * d.groups ? (avg + 16 * nb - 1) / (16 * nb) : 0;
+    const int tiles = (d.nt + tw - 1) / tw;
+    hipLaunchKernelGGL(kernel, dim3(tiles, d.groups, passes(d, rows, 16 * nb, tiles)), dim3(waves * 64),
+                       0, s, p, codes, scales);
   };
   // The more tiles and rows a workgroup takes, the less often either is read again, as
   // long as some 200 workgroups are left (and half of its tiles exist: 16000 rows of 16 x
@@ -286,12 +291,12 @@ void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float 
 void launch_f8_few_rows(const F8Dims &d, int rows, const F8Rows &x, const int32_t *offsets,
                         const void *packed, uint16_t *out, long ostride, hipStream_t s) {
   const Few p = few_of(d, rows, offsets, packed, out, ostride);
-  const int passes = (average(d, rows) + kStaged - 1) / kStaged;
+  const int z = passes(d, rows, kStaged, d.nt);
   auto go = [&](auto kernel, int waves) {
-    hipLaunchKernelGGL(kernel, dim3(d.nt, d.groups, passes), dim3(waves * 64), staged_lds(d.ks), s, p,
+    hipLaunchKernelGGL(kernel, dim3(d.nt, d.groups, z), dim3(waves * 64), staged_lds(d.ks), s, p,
                        x.p, x.stride);
   };
-  const long tasks = (long)d.nt * d.groups * passes;
+  const long tasks = (long)d.nt * d.groups * ((average(d, rows) + kStaged - 1) / kStaged);
   auto pick = [&](auto f16) {
     constexpr bool F16 = decltype(f16)::value;
     if (tasks <= 256) go(f8_few_rows_kernel<F16, 16, 4>, 16);

@@ -170,7 +170,7 @@ def test_dense_product(M, n, k, dtype):
     codes, scales = quantised(x.cuda(), k, dtype)
     again = torch.empty_like(out)
     m.moe_f8_linear_codes(lin.shape, codes, scales, None, lin.packed, again)
-    assert torch.equal(again, out)
+    check("codes", again, x, w[0], dtype)
 
 
 def grouped_case(seed, groups, n, k, off, M, dtype, pads=(5, 4)):
@@ -349,6 +349,9 @@ CHOICES = {
     "4 tiles, 64 rows": (60, None, 60, 390),
     "4 tiles, 64 rows, two passes": (100, None, 30, 130),
     "one group long": (96, [2, 3, 95], 4, 390),
+    "passes of 8, 16 waves": (200, None, 1, 390),
+    "passes of 8, 8 waves": (33, None, 5, 520),
+    "passes of 8, 4 waves": (500, [100, 100, 101, 499], 1, 130),
     "tiles of 128 rows": (600, None, 40, 390),
     "tiles of 128 rows, groups": (500, [1, 166, 495], 28, 520),
     "tiles of 256 rows": (500, None, 128, 390),
@@ -365,12 +368,17 @@ def test_each_choice(name, dtype):
     lin, w = repeated(rng, len(ends), reps, k, dtype)
     x = rows(rng, M, k, dtype)
     note(f"f8 {name} {dtype}")
-    out = lin(x.cuda(), offsets([0] + ends)).view(M, reps, 256)
-    assert torch.equal(out, out[:, :1].expand(M, reps, 256))
-    for g, (a, b) in enumerate(zip([0] + ends, ends)):
-        if b > a:
-            check(f"group {g}", out[a:b, 0], x[a:b], w[g], dtype)
-    assert torch.all(out[ends[-1]:] == 0)
+    off = offsets([0] + ends)
+    out = lin(x.cuda(), off)
+    codes, scales = quantised(x.cuda(), k, dtype)
+    again = torch.zeros_like(out)
+    m.moe_f8_linear_codes(lin.shape, codes, scales, off, lin.packed, again)
+    for got in (out.view(M, reps, 256), again.view(M, reps, 256)):
+        assert torch.equal(got, got[:, :1].expand(M, reps, 256))
+        for g, (a, b) in enumerate(zip([0] + ends, ends)):
+            if b > a:
+                check(f"group {g}", got[a:b, 0], x[a:b], w[g], dtype)
+        assert torch.all(got[ends[-1]:] == 0)
 
 
 @pytest.mark.parametrize("k,reps", [(300, 3), (520, 128)], ids=["128", "256"])
