@@ -66,13 +66,13 @@ def wgrad(lib, shape=S, rows=3, x=FAKE, xs=256, dy=FAKE, ys=48, off=FAKE, dw=OTH
 
 def test_linear_refusals(lib):
     for kw in (dict(off=None), dict(xs=255), dict(os_=47), dict(rows=-1), dict(x=None), dict(out=None),
-               dict(packed=None), dict(packed=FAKE + 8), dict(rows=3000, ws=None), dict(rows=3000, ws=FAKE + 8)):
+               dict(packed=None), dict(packed=FAKE + 8), dict(rows=30000, ws=None), dict(rows=30000, ws=FAKE + 8)):
         assert linear(lib, **kw) == INVALID, kw
     for kw in (dict(xs=(1 << 32) + 1), dict(os_=(1 << 32) + 1), dict(rows=(1 << 30) + 1),
                dict(shape=m.F8Shape(2, 1 << 20, 256), rows=1 << 26, os_=1 << 20)):
         assert linear(lib, **kw) == UNSUPPORTED, kw
-    need = m.moe_f8_linear_workspace_bytes(S, 3000)
-    assert need >= 3000 * 256 + 3000 * 8 and linear(lib, rows=3000, n=need - 1) == _lib.MOE_ERR_WORKSPACE
+    need = m.moe_f8_linear_workspace_bytes(S, 30000)
+    assert need >= 30000 * 256 + 30000 * 8 and linear(lib, rows=30000, n=need - 1) == _lib.MOE_ERR_WORKSPACE
     assert linear(lib, rows=0, x=None, out=None, ws=None, n=0) == _lib.MOE_OK
     assert m.moe_f8_linear_workspace_bytes(S, -1) == 0
     codes = lambda **k: lib.moe_f8_linear_codes(*{**dict(s=ctypes.byref(S.c()), rows=3, c=FAKE, sc=FAKE, off=FAKE,  # noqa: E731
@@ -92,8 +92,8 @@ def test_outputs_over_inputs(lib):
     assert linear(lib, rows=1, out=at(255)) == INVALID and linear(lib, rows=1, out=at(-47)) == INVALID
     assert linear(lib, rows=2, xs=300, os_=301, out=at(256)) == INVALID
     # between the rows, and behind the last one: past the check (to the workspace's)
-    big = dict(rows=3000, n=0)
-    for o in (256, 304 - 48, 256 + 304 * 5, 2999 * 304 + 256, -48):
+    big = dict(rows=30000, n=0)
+    for o in (256, 304 - 48, 256 + 304 * 5, 29999 * 304 + 256, -48):
         assert linear(lib, xs=304, os_=304, out=at(o), **big) == _lib.MOE_ERR_WORKSPACE, o
     assert wgrad(lib, dw=at(2 * 256 + 255)) == INVALID and wgrad(lib, dw=at(-1)) == INVALID
     assert wgrad(lib, dy=OTHER, dw=OTHER) == INVALID
