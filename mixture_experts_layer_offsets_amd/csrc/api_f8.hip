@@ -230,8 +230,12 @@ int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x, int64_t
   uint8_t *xc = (uint8_t *)ws, *yc = xc + c.yc;
   float *xs = (float *)(xc + c.xs), *ys = (float *)(xc + c.ys);
   hipStream_t s = (hipStream_t)stream;
-  launch_f8_quant_cols({(const uint16_t *)x, x_stride, d.f16}, {(const uint16_t *)dy, dy_stride, d.f16},
-                       rows, d, offsets, xc, xs, yc, ys, s);
+  const F8Rows xr{(const uint16_t *)x, x_stride, d.f16}, yr{(const uint16_t *)dy, dy_stride, d.f16};
+  if (f8_wgrad_few(d, rows)) {
+    launch_f8_wgrad_few(xr, yr, rows, d, offsets, (uint16_t *)dw, s);
+    return status();
+  }
+  launch_f8_quant_cols(xr, yr, rows, d, offsets, xc, xs, yc, ys, s);
   launch_f8_wgrad(d, rows, xc, xs, yc, ys, offsets, (uint16_t *)dw, (float *)(xc + c.parts), s);
   return status();
 }

@@ -70,6 +70,10 @@ bool f8_few_staged(const F8Dims &d, int rows);
 void launch_f8_wgrad(const F8Dims &d, int rows, const uint8_t *xc, const float *xs,
                      const uint8_t *yc, const float *ys, const int32_t *offsets, uint16_t *dw,
                      float *parts, hipStream_t s);
+// The same from 16-bit rows, in one launch; whether it takes the product.
+void launch_f8_wgrad_few(const F8Rows &x, const F8Rows &dy, int rows, const F8Dims &d,
+                         const int32_t *offsets, uint16_t *dw, hipStream_t s);
+bool f8_wgrad_few(const F8Dims &d, int rows);
 // In how many pieces launch_f8_wgrad takes each group's rows: past one, `parts` holds that
 // many fp32 results, columns rounded up to 16.
 int f8_splits(const F8Dims &d, int rows);

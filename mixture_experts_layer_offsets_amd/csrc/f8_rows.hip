@@ -1,5 +1,6 @@
 // Quantisers of 16-bit rows for the 8-bit products: along the rows (forward and data
-// gradient) and down the columns of each group's rows (weight gradient).  Both read
+// gradient) and down the columns of each group's rows (weight gradient; a small one is
+// computed in the same launch).  Both read
 // the rows once and write codes and scales, 3 bytes a value: bound by memory (16384 rows of
 // 7168: 59 us, 5.9 TB/s; down the columns, with 16384 of 4096 beside them, 118 us, 4.7
 // TB/s).
@@ -50,73 +51,87 @@ struct Cols {
   float *scales;
 };
 
-// A workgroup takes 64 columns of one stage (128 rows of one group): the rows go
-// through LDS, then a thread converts 32 values of one column, and the columns' 128
-// codes leave through LDS in 16-byte chunks.  Grid (columns of a / 64 + those of b / 64,
-// stages), stages past 2^16 in turn.
+// 128 rows x 64 columns of a tensor in LDS; their codes, column by column, at 144 bytes a
+// column (the 16 more put the lanes' writes on different banks).
+constexpr int kLine = kF8Block + 16;
+struct ColsLds {
+  u32x4_t tile[kF8Block][8];
+  __attribute__((aligned(16))) uint8_t lines[64 * kLine];
+  uint32_t tops[4][64];
+};
+
+// Rows r0 .. of those before `end`, columns c0 .. + 63: 4 x 8 values a thread, zeros outside.
+__device__ __forceinline__ void cols_load(const Cols &m, int r0, int end, int c0, u32x4_t (&v)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const int at = threadIdx.x + 256 * q, row = at >> 3, c = c0 + 8 * (at & 7);
+    v[q] = (u32x4_t){0, 0, 0, 0};
+    if (r0 + row < end && c < m.cols) v[q] = f8_load8(m.x + (size_t)(r0 + row) * m.stride, c, m.cols);
+  }
+}
+__device__ __forceinline__ void cols_put(ColsLds &l, const u32x4_t (&v)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const int at = threadIdx.x + 256 * q;
+    l.tile[at >> 3][at & 7] = v[q];
+  }
+}
+// A thread takes 32 values of column threadIdx.x % 64, the quarter that its wave names.
+template <bool F16>
+__device__ __forceinline__ void cols_top(ColsLds &l, float (&v)[32]) {
+  const int j = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const uint16_t *t16 = (const uint16_t *)l.tile;
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 32; e++) {
+    v[e] = f8_from16(t16[(32 * q + e) * 64 + j], F16);
+    top = max(top, f8_mag(v[e]));
+  }
+  l.tops[q][j] = top;
+}
+// ... and puts their codes; returns the column's scale.
+__device__ __forceinline__ float cols_codes(ColsLds &l, const float (&v)[32]) {
+  const int j = threadIdx.x & 63, q = threadIdx.x >> 6;
+  float inv;
+  const float s = f8_scale(max(max(l.tops[0][j], l.tops[1][j]), max(l.tops[2][j], l.tops[3][j])), &inv);
+#pragma unroll
+  for (int e = 0; e < 32; e += 16)
+    *(u32x4_t *)(l.lines + j * kLine + 32 * q + e) =
+        (u32x4_t){f8_codes4(v[e], v[e + 1], v[e + 2], v[e + 3], inv),
+                  f8_codes4(v[e + 4], v[e + 5], v[e + 6], v[e + 7], inv),
+                  f8_codes4(v[e + 8], v[e + 9], v[e + 10], v[e + 11], inv),
+                  f8_codes4(v[e + 12], v[e + 13], v[e + 14], v[e + 15], inv)};
+  return s;
+}
+
+// A workgroup takes 64 columns of one stage (128 rows of one group), which leave in
+// 16-byte chunks.  Grid (columns of a / 64 + those of b / 64, stages), stages past 2^16 in
+// turn.
 template <bool F16>
 __global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int rows,
                                                             const int32_t *__restrict__ offsets,
                                                             int groups, long stages) {
-  __shared__ u32x4_t tile[kF8Block][8];  // 128 rows x 64 values
-  // a column's codes at 144 bytes a column: the 16 more put the lanes' writes on
-  // different banks
-  constexpr int kLine = kF8Block + 16;
-  __shared__ __attribute__((aligned(16))) uint8_t lines[64 * kLine];
-  __shared__ uint32_t tops[4][64];
+  __shared__ ColsLds lds;
   const int ax = (a.cols + 63) / 64;
   const bool first_of = (int)blockIdx.x < ax;
   const Cols m = first_of ? a : b;
-  const uint16_t *x = m.x;
-  const long stride = m.stride;
-  const int cols = m.cols;
   const int tid = threadIdx.x, c0 = (first_of ? blockIdx.x : blockIdx.x - ax) * 64;
-  const int cols16 = (cols + 15) & ~15;
+  const int cols16 = (m.cols + 15) & ~15;
   for (long st = blockIdx.y; st < stages; st += gridDim.y) {
     int first;
     const int g = f8_group_at(offsets, groups, rows, kF8Block, (int)st, &first);
     const F8Span sp = f8_span(offsets, g, rows);
     const int r0 = sp.begin + (int)(st - first) * kF8Block;
     if (st < first || r0 >= sp.end) continue;  // an empty place
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const int at = tid + 256 * q, row = at >> 3, c8 = at & 7, c = c0 + 8 * c8;
-      u32x4_t v = {0, 0, 0, 0};
-      if (r0 + row < sp.end && c < cols) {
-        const uint16_t *src = x + (size_t)(r0 + row) * stride + c;
-        if (c + 8 <= cols) {
-          const u32x4_a2 u = *(const u32x4_a2 *)src;
-          v = (u32x4_t){u[0], u[1], u[2], u[3]};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; e++)
-            if (c + e < cols) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-        }
-      }
-      tile[row][c8] = v;
-    }
+    u32x4_t u[4];
+    cols_load(m, r0, sp.end, c0, u);
+    cols_put(lds, u);
     __syncthreads();
-    const int j = tid & 63, q = tid >> 6;
-    const uint16_t *t16 = (const uint16_t *)tile;
     float v[32];
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 32; e++) {
-      v[e] = f8_from16(t16[(32 * q + e) * 64 + j], F16);
-      top = max(top, f8_mag(v[e]));
-    }
-    tops[q][j] = top;
+    cols_top<F16>(lds, v);
     __syncthreads();
-    float inv;
-    const float s = f8_scale(max(max(tops[0][j], tops[1][j]), max(tops[2][j], tops[3][j])), &inv);
-#pragma unroll
-    for (int e = 0; e < 32; e += 16)
-      *(u32x4_t *)(lines + j * kLine + 32 * q + e) =
-          (u32x4_t){f8_codes4(v[e], v[e + 1], v[e + 2], v[e + 3], inv),
-                    f8_codes4(v[e + 4], v[e + 5], v[e + 6], v[e + 7], inv),
-                    f8_codes4(v[e + 8], v[e + 9], v[e + 10], v[e + 11], inv),
-                    f8_codes4(v[e + 12], v[e + 13], v[e + 14], v[e + 15], inv)};
-    if (q == 0 && c0 + j < cols16) m.scales[(size_t)st * cols16 + c0 + j] = s;
+    const float s = cols_codes(lds, v);
+    if (tid < 64 && c0 + tid < cols16) m.scales[(size_t)st * cols16 + c0 + tid] = s;
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < 2; p++) {
@@ -130,13 +145,69 @@ __global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int 
       } else {
         col = at >> 3;
         c = at & 7;
-        dst = m.codes + ((size_t)st * cols + c0 + col) * kF8Block + 16 * c;
+        dst = m.codes + ((size_t)st * m.cols + c0 + col) * kF8Block + 16 * c;
       }
-      if (c0 + col < (m.tiles ? cols16 : cols))
-        *(u32x4_t *)dst = *(const u32x4_t *)(lines + col * kLine + 16 * c);
+      if (c0 + col < (m.tiles ? cols16 : m.cols))
+        *(u32x4_t *)dst = *(const u32x4_t *)(lds.lines + col * kLine + 16 * c);
     }
     __syncthreads();
   }
+}
+
+// A small weight gradient in one launch: a workgroup takes 64 x 64 of dw and quantises its
+// columns of x and dy stage by stage, the next stage's loads on their way.  A wave holds 16
+// rows of dw.  Grid (tiles, groups).
+template <bool F16>
+__global__ __launch_bounds__(256) void f8_wgrad_few_kernel(Cols x, Cols y, int rows,
+                                                           const int32_t *__restrict__ offsets,
+                                                           uint16_t *__restrict__ dw) {
+  __shared__ ColsLds xl, yl;
+  __shared__ float xs[64], ys[64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, h = lane >> 4;
+  const int nN = (y.cols + 63) / 64, m0 = blockIdx.x / nN * 64, n0 = blockIdx.x % nN * 64;
+  const F8Span sp = f8_span(offsets, blockIdx.y, rows);
+  f32x4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4_t u[4], w[4];
+  cols_load(x, sp.begin, sp.end, m0, u);
+  cols_load(y, sp.begin, sp.end, n0, w);
+  for (int r0 = sp.begin; r0 < sp.end; r0 += kF8Block) {
+    cols_put(xl, u);
+    cols_put(yl, w);
+    __syncthreads();
+    cols_load(x, r0 + kF8Block, sp.end, m0, u);
+    cols_load(y, r0 + kF8Block, sp.end, n0, w);
+    float v[32], t[32];
+    cols_top<F16>(xl, v);
+    cols_top<F16>(yl, t);
+    __syncthreads();
+    const float sx = cols_codes(xl, v), sy = cols_codes(yl, t);
+    if (tid < 64) xs[tid] = sx, ys[tid] = sy;
+    __syncthreads();
+    auto frag = [&](const uint8_t *lines, int c) {
+      const uint8_t *p = lines + (c + l16) * kLine + 16 * h;
+      return f8_frag(*(const u32x4_t *)p, *(const u32x4_t *)(p + 64));
+    };
+    const i32x8_t xf = frag(xl.lines, 16 * wave);
+    const float s = xs[16 * wave + l16];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const f32x4 d = f8_dot(frag(yl.lines, 16 * i), xf);
+#pragma unroll
+      for (int e = 0; e < 4; e++) acc[i][e] = fmaf(s * ys[16 * i + 4 * h + e], d[e], acc[i][e]);
+    }
+  }
+  const int r = m0 + 16 * wave + l16;
+  if (r >= x.cols) return;
+  uint16_t *to = dw + ((size_t)blockIdx.y * x.cols + r) * y.cols;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const int c = n0 + 16 * i + 4 * h + e;
+      if (c < y.cols) to[c] = f8_to16(acc[i][e], F16);
+    }
 }
 
 }  // namespace
@@ -165,6 +236,28 @@ void launch_f8_quant_cols(const F8Rows &x, const F8Rows &dy, int rows, const F8D
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, b, rows, offsets, d.groups, stages);
   };
   d.f16 ? go(f8_quant_cols_kernel<true>) : go(f8_quant_cols_kernel<false>);
+}
+
+// Against two launches: as long as its workgroups, one a CU, take few stages, which are 2 us
+// each here (1 there).  us here and there: 64 x 64 of 100 rows 7.4 and 11.6; 256 x 256 of
+// 300 10.8 and 12.7, of 1000 22 and 17; 1024 x 1024 of 100 (256 workgroups) 7.5 and 11.9;
+// 2048 x 2048 of 128 (1024) 15.8 and 12.7; 4 groups of 512 x 512, 1000 rows in even groups
+// 10.9 and 13.9, in groups that fall off as 1 / g 13.9 and 15.2; 5 of 500 x 333, 777 rows
+// 11.2 and 14.2, falling off 17.4 and 14.6.
+bool f8_wgrad_few(const F8Dims &d, int rows) {
+  const long stages = ((long)rows + (long)d.groups * kF8Block - 1) / ((long)d.groups * kF8Block);
+  return (long)((d.k + 63) / 64) * ((d.n + 63) / 64) * d.groups <= 256 &&
+         stages <= (d.groups == 1 ? 4 : 2);
+}
+
+void launch_f8_wgrad_few(const F8Rows &x, const F8Rows &dy, int rows, const F8Dims &d,
+                         const int32_t *offsets, uint16_t *dw, hipStream_t s) {
+  const Cols a{x.p, x.stride, d.k, 0, nullptr, nullptr}, b{dy.p, dy.stride, d.n, 0, nullptr, nullptr};
+  const dim3 grid((unsigned)(((d.k + 63) / 64) * ((d.n + 63) / 64)), d.groups);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, b, rows, offsets, dw);
+  };
+  d.f16 ? go(f8_wgrad_few_kernel<true>) : go(f8_wgrad_few_kernel<false>);
 }
 
 }  // namespace moe

@@ -381,11 +381,12 @@ def test_each_choice(name, dtype):
         assert torch.all(got[ends[-1]:] == 0)
 
 
-@pytest.mark.parametrize("k,reps", [(300, 3), (520, 128)], ids=["128", "256"])
+@pytest.mark.parametrize("k,reps", [(300, 1), (300, 3), (520, 24), (520, 128)],
+                         ids=["64", "64-uneven", "128", "256"])
 def test_each_choice_of_the_weight_gradient(k, reps):
-    """Tiles of 128 and 256 rows of dw."""
+    """Tiles of 64, 128 and 256 rows of dw."""
     rng = np.random.default_rng([k, reps])
-    M, off = 420, [3, 3, 390]
+    M, off = 420, [3, 3, 390] if reps > 1 else [3, 200, 390]
     lin, _ = repeated(rng, 2, reps, k, FP)
     x, dy = rows(rng, M, k, FP), rows(rng, M, 256, FP)
     note(f"f8 weight gradient {k} x {256 * reps}")
@@ -446,7 +447,8 @@ def test_data_gradient(groups, M, n, k, dtype):
 @BOTH
 @pytest.mark.parametrize("name,n,k", [
     ("few", 1, 1), ("few", 45, 300), ("one-long", 300, 130), ("tiles", 33, 520), ("middle", 257, 64),
-    ("empty", 40, 40)])
+    ("empty", 40, 40), ("few", 1031, 300), ("one-long", 1030, 170), ("middle", 301, 1027), ("tiles", 720, 520),
+    ("empty", 700, 700)])
 def test_weight_gradient(name, n, k, dtype):
     M, off = SPANS[name]
     rng = np.random.default_rng([n, k])
