@@ -51,52 +51,60 @@ struct Cols {
   float *scales;
 };
 
-// 128 rows x 64 columns of a tensor in LDS; their codes, column by column, at 144 bytes a
-// column (the 16 more put the lanes' writes on different banks).
+// 128 rows x 64 columns of a tensor in LDS, and their codes by T threads, column by column,
+// at 144 bytes a column (the 16 more put the lanes' writes on different banks).
 constexpr int kLine = kF8Block + 16;
+template <int T>
 struct ColsLds {
+  static constexpr int N = kF8Block * 64 / T;  // values of a thread
   u32x4_t tile[kF8Block][8];
   __attribute__((aligned(16))) uint8_t lines[64 * kLine];
-  uint32_t tops[4][64];
+  uint32_t tops[T / 64][64];
 };
 
-// Rows r0 .. of those before `end`, columns c0 .. + 63: 4 x 8 values a thread, zeros outside.
-__device__ __forceinline__ void cols_load(const Cols &m, int r0, int end, int c0, u32x4_t (&v)[4]) {
+// Rows r0 .. of those before `end`, columns c0 .. + 63: 8 values a load, zeros outside.
+template <int T>
+__device__ __forceinline__ void cols_load(const Cols &m, int r0, int end, int c0, u32x4_t (&v)[1024 / T]) {
 #pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const int at = threadIdx.x + 256 * q, row = at >> 3, c = c0 + 8 * (at & 7);
+  for (int q = 0; q < 1024 / T; q++) {
+    const int at = threadIdx.x + T * q, row = at >> 3, c = c0 + 8 * (at & 7);
     v[q] = (u32x4_t){0, 0, 0, 0};
     if (r0 + row < end && c < m.cols) v[q] = f8_load8(m.x + (size_t)(r0 + row) * m.stride, c, m.cols);
   }
 }
-__device__ __forceinline__ void cols_put(ColsLds &l, const u32x4_t (&v)[4]) {
+template <int T>
+__device__ __forceinline__ void cols_put(ColsLds<T> &l, const u32x4_t (&v)[1024 / T]) {
 #pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const int at = threadIdx.x + 256 * q;
+  for (int q = 0; q < 1024 / T; q++) {
+    const int at = threadIdx.x + T * q;
     l.tile[at >> 3][at & 7] = v[q];
   }
 }
-// A thread takes 32 values of column threadIdx.x % 64, the quarter that its wave names.
-template <bool F16>
-__device__ __forceinline__ void cols_top(ColsLds &l, float (&v)[32]) {
+// A thread takes N values of column threadIdx.x % 64, the piece that its wave names.
+template <bool F16, int T, int N>
+__device__ __forceinline__ void cols_top(ColsLds<T> &l, float (&v)[N]) {
   const int j = threadIdx.x & 63, q = threadIdx.x >> 6;
   const uint16_t *t16 = (const uint16_t *)l.tile;
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 32; e++) {
-    v[e] = f8_from16(t16[(32 * q + e) * 64 + j], F16);
+  for (int e = 0; e < N; e++) {
+    v[e] = f8_from16(t16[(N * q + e) * 64 + j], F16);
     top = max(top, f8_mag(v[e]));
   }
   l.tops[q][j] = top;
 }
 // ... and puts their codes; returns the column's scale.
-__device__ __forceinline__ float cols_codes(ColsLds &l, const float (&v)[32]) {
+template <int T, int N>
+__device__ __forceinline__ float cols_codes(ColsLds<T> &l, const float (&v)[N]) {
   const int j = threadIdx.x & 63, q = threadIdx.x >> 6;
-  float inv;
-  const float s = f8_scale(max(max(l.tops[0][j], l.tops[1][j]), max(l.tops[2][j], l.tops[3][j])), &inv);
+  uint32_t top = l.tops[0][j];
 #pragma unroll
-  for (int e = 0; e < 32; e += 16)
-    *(u32x4_t *)(l.lines + j * kLine + 32 * q + e) =
+  for (int w = 1; w < T / 64; w++) top = max(top, l.tops[w][j]);
+  float inv;
+  const float s = f8_scale(top, &inv);
+#pragma unroll
+  for (int e = 0; e < N; e += 16)
+    *(u32x4_t *)(l.lines + j * kLine + N * q + e) =
         (u32x4_t){f8_codes4(v[e], v[e + 1], v[e + 2], v[e + 3], inv),
                   f8_codes4(v[e + 4], v[e + 5], v[e + 6], v[e + 7], inv),
                   f8_codes4(v[e + 8], v[e + 9], v[e + 10], v[e + 11], inv),
@@ -111,7 +119,7 @@ template <bool F16>
 __global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int rows,
                                                             const int32_t *__restrict__ offsets,
                                                             int groups, long stages) {
-  __shared__ ColsLds lds;
+  __shared__ ColsLds<256> lds;
   const int ax = (a.cols + 63) / 64;
   const bool first_of = (int)blockIdx.x < ax;
   const Cols m = first_of ? a : b;
@@ -124,10 +132,10 @@ __global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int 
     const int r0 = sp.begin + (int)(st - first) * kF8Block;
     if (st < first || r0 >= sp.end) continue;  // an empty place
     u32x4_t u[4];
-    cols_load(m, r0, sp.end, c0, u);
+    cols_load<256>(m, r0, sp.end, c0, u);
     cols_put(lds, u);
     __syncthreads();
-    float v[32];
+    float v[ColsLds<256>::N];
     cols_top<F16>(lds, v);
     __syncthreads();
     const float s = cols_codes(lds, v);
@@ -155,30 +163,35 @@ __global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int 
 }
 
 // A small weight gradient in one launch: a workgroup takes 64 x 64 of dw and quantises its
-// columns of x and dy stage by stage, the next stage's loads on their way.  A wave holds 16
-// rows of dw.  Grid (tiles, groups).
+// columns of x and dy stage by stage, the next stage's loads on their way.  Eight waves: one
+// holds 16 rows x 32 columns of dw (four waves: 12.2 us for 777 rows in 5 uneven groups of
+// 500 x 333, eight 9.1).  Grid (tiles, groups).
+constexpr int kFewThreads = 512;
+
 template <bool F16>
-__global__ __launch_bounds__(256) void f8_wgrad_few_kernel(Cols x, Cols y, int rows,
+__global__ __launch_bounds__(kFewThreads) void f8_wgrad_few_kernel(Cols x, Cols y, int rows,
                                                            const int32_t *__restrict__ offsets,
                                                            uint16_t *__restrict__ dw) {
-  __shared__ ColsLds xl, yl;
+  constexpr int T = kFewThreads, N = ColsLds<T>::N;
+  __shared__ ColsLds<T> xl, yl;
   __shared__ float xs[64], ys[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, h = lane >> 4;
+  const int r16 = 16 * (wave & 3), c32 = 32 * (wave >> 2);  // of the wave, in the tile
   const int nN = (y.cols + 63) / 64, m0 = blockIdx.x / nN * 64, n0 = blockIdx.x % nN * 64;
   const F8Span sp = f8_span(offsets, blockIdx.y, rows);
-  f32x4 acc[4];
+  f32x4 acc[2];
 #pragma unroll
-  for (int i = 0; i < 4; i++) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4_t u[4], w[4];
-  cols_load(x, sp.begin, sp.end, m0, u);
-  cols_load(y, sp.begin, sp.end, n0, w);
+  for (int i = 0; i < 2; i++) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4_t u[1024 / T], w[1024 / T];
+  cols_load<T>(x, sp.begin, sp.end, m0, u);
+  cols_load<T>(y, sp.begin, sp.end, n0, w);
   for (int r0 = sp.begin; r0 < sp.end; r0 += kF8Block) {
     cols_put(xl, u);
     cols_put(yl, w);
     __syncthreads();
-    cols_load(x, r0 + kF8Block, sp.end, m0, u);
-    cols_load(y, r0 + kF8Block, sp.end, n0, w);
-    float v[32], t[32];
+    cols_load<T>(x, r0 + kF8Block, sp.end, m0, u);
+    cols_load<T>(y, r0 + kF8Block, sp.end, n0, w);
+    float v[N], t[N];
     cols_top<F16>(xl, v);
     cols_top<F16>(yl, t);
     __syncthreads();
@@ -189,23 +202,23 @@ __global__ __launch_bounds__(256) void f8_wgrad_few_kernel(Cols x, Cols y, int r
       const uint8_t *p = lines + (c + l16) * kLine + 16 * h;
       return f8_frag(*(const u32x4_t *)p, *(const u32x4_t *)(p + 64));
     };
-    const i32x8_t xf = frag(xl.lines, 16 * wave);
-    const float s = xs[16 * wave + l16];
+    const i32x8_t xf = frag(xl.lines, r16);
+    const float s = xs[r16 + l16];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const f32x4 d = f8_dot(frag(yl.lines, 16 * i), xf);
+    for (int i = 0; i < 2; i++) {
+      const f32x4 d = f8_dot(frag(yl.lines, c32 + 16 * i), xf);
 #pragma unroll
-      for (int e = 0; e < 4; e++) acc[i][e] = fmaf(s * ys[16 * i + 4 * h + e], d[e], acc[i][e]);
+      for (int e = 0; e < 4; e++) acc[i][e] = fmaf(s * ys[c32 + 16 * i + 4 * h + e], d[e], acc[i][e]);
     }
   }
-  const int r = m0 + 16 * wave + l16;
+  const int r = m0 + r16 + l16;
   if (r >= x.cols) return;
   uint16_t *to = dw + ((size_t)blockIdx.y * x.cols + r) * y.cols;
 #pragma unroll
-  for (int i = 0; i < 4; i++)
+  for (int i = 0; i < 2; i++)
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      const int c = n0 + 16 * i + 4 * h + e;
+      const int c = n0 + c32 + 16 * i + 4 * h + e;
       if (c < y.cols) to[c] = f8_to16(acc[i][e], F16);
     }
 }
@@ -238,16 +251,16 @@ void launch_f8_quant_cols(const F8Rows &x, const F8Rows &dy, int rows, const F8D
   d.f16 ? go(f8_quant_cols_kernel<true>) : go(f8_quant_cols_kernel<false>);
 }
 
-// Against two launches: as long as its workgroups, one a CU, take few stages, which are 2 us
-// each here (1 there).  us here and there: 64 x 64 of 100 rows 7.4 and 11.6; 256 x 256 of
-// 300 10.8 and 12.7, of 1000 22 and 17; 1024 x 1024 of 100 (256 workgroups) 7.5 and 11.9;
-// 2048 x 2048 of 128 (1024) 15.8 and 12.7; 4 groups of 512 x 512, 1000 rows in even groups
-// 10.9 and 13.9, in groups that fall off as 1 / g 13.9 and 15.2; 5 of 500 x 333, 777 rows
-// 11.2 and 14.2, falling off 17.4 and 14.6.
+// Against two launches: as long as its workgroups, two a CU, take few stages, which are 1.5
+// to 2 us each here (1 there).  us here and there: 64 x 64 of 100 rows 6.4 and 11.6; 256 x
+// 256 of 300 9.0 and 12.7, of 600 12.2 and 15.1, of 1000 17.3 and 17.2; 1400 x 1400 of 300
+// (484 workgroups) 13.5 and 14.6, 2048 x 2048 of 128 (1024) 14.0 and 12.8.  In even groups,
+// and in groups that fall off as 1 / g: 5 of 500 x 333, 777 rows 8.2 and 14.0, 12.1 and 14.8;
+// 4 of 512 x 512, 2000 rows 13.4 and 16.3, 18.5 and 19.0.
 bool f8_wgrad_few(const F8Dims &d, int rows) {
   const long stages = ((long)rows + (long)d.groups * kF8Block - 1) / ((long)d.groups * kF8Block);
-  return (long)((d.k + 63) / 64) * ((d.n + 63) / 64) * d.groups <= 256 &&
-         stages <= (d.groups == 1 ? 4 : 2);
+  return (long)((d.k + 63) / 64) * ((d.n + 63) / 64) * d.groups <= 512 &&
+         stages <= (d.groups == 1 ? 6 : 4);
 }
 
 void launch_f8_wgrad_few(const F8Rows &x, const F8Rows &dy, int rows, const F8Dims &d,
@@ -255,7 +268,7 @@ void launch_f8_wgrad_few(const F8Rows &x, const F8Rows &dy, int rows, const F8Di
   const Cols a{x.p, x.stride, d.k, 0, nullptr, nullptr}, b{dy.p, dy.stride, d.n, 0, nullptr, nullptr};
   const dim3 grid((unsigned)(((d.k + 63) / 64) * ((d.n + 63) / 64)), d.groups);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, b, rows, offsets, dw);
+    hipLaunchKernelGGL(kernel, grid, dim3(kFewThreads), 0, s, a, b, rows, offsets, dw);
   };
   d.f16 ? go(f8_wgrad_few_kernel<true>) : go(f8_wgrad_few_kernel<false>);
 }

@@ -448,7 +448,7 @@ def test_data_gradient(groups, M, n, k, dtype):
 @pytest.mark.parametrize("name,n,k", [
     ("few", 1, 1), ("few", 45, 300), ("one-long", 300, 130), ("tiles", 33, 520), ("middle", 257, 64),
     ("empty", 40, 40), ("few", 1031, 300), ("one-long", 1030, 170), ("middle", 301, 1027), ("tiles", 720, 520),
-    ("empty", 700, 700)])
+    ("empty", 700, 700), ("one-long", 1030, 670), ("middle", 301, 2027)])
 def test_weight_gradient(name, n, k, dtype):
     M, off = SPANS[name]
     rng = np.random.default_rng([n, k])
