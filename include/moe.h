@@ -619,8 +619,9 @@ int moe_f8_quantize_rows(const moe_f8_shape *shape, int32_t rows, const void *x,
 size_t moe_f8_linear_workspace_bytes(const moe_f8_shape *shape, int32_t rows);
 
 /* out[r] = x[r] * W_g for the rows r of each group (other rows of out are left
- * as they were), x quantised on the way.  out must not overlap x (rows of one
- * stride may lie between each other's; of others, neither's run in the other's). */
+ * as they were), x quantised on the way; (rows / 128 + groups) ceil(n / 256) < 2^23.
+ * out must not overlap x (rows of one stride may lie between each other's; of others,
+ * neither's run in the other's). */
 int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x,
                   int64_t x_stride, const int32_t *offsets, const void *packed,
                   void *out, int64_t out_stride, void *ws, size_t ws_bytes,
@@ -639,7 +640,7 @@ size_t moe_f8_wgrad_workspace_bytes(const moe_f8_shape *shape, int32_t rows);
 /* Weight gradients dw[g] = sum over the rows of group g of x[r]^T dy[r], x rows of
  * k and dy rows of n values, both quantised down their columns: dw
  * [groups][k][n] of row_type, not inside either's run; zeros for a group without
- * rows.  rows / 128 + groups <= 65535. */
+ * rows.  rows / 128 + groups <= 65535, and groups ceil(k / 128) ceil(n / 256) < 2^23. */
 int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x,
                  int64_t x_stride, const void *dy, int64_t dy_stride,
                  const int32_t *offsets, void *dw, void *ws, size_t ws_bytes,

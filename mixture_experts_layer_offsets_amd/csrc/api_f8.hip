@@ -7,6 +7,7 @@ using namespace moe;
 namespace {
 
 constexpr int64_t kMostStride = 1L << 32;
+constexpr int64_t kMostTiles = 1L << 23;
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -50,18 +51,18 @@ Cols cols_of(const F8Dims &d, int32_t rows) {
 
 int check_rows(const F8Dims &d, int32_t rows, const int32_t *offsets) {
   if (rows < 0 || (!offsets && d.groups != 1)) return MOE_ERR_INVALID_ARG;
-  // tiles of 64 rows x 256 outputs, and rows past them, are counted in 31 bits
-  if (rows > (1 << 30) || (rows / 64 + (int64_t)d.groups) * ((d.n + 255) / 256) >= (1L << 31))
+  // tiles of 128 rows x 256 outputs take 512 threads each, less than 2^32 in all
+  if (rows > (1 << 30) || (rows / 128 + (int64_t)d.groups) * ((d.n + 255) / 256) >= kMostTiles)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
 int check_wgrad(const F8Dims &d, int32_t rows) {
   if (rows < 0) return MOE_ERR_INVALID_ARG;
-  // a tile's codes of one operand, of all stages, are addressed in 31 bits; tiles are
-  // counted in 31
+  // a tile's codes of one operand, of all stages, are addressed in 31 bits, and stages are
+  // a grid's dimension; tiles as in check_rows
   if (f8_stages(rows, d.groups) > 65535 ||
-      (int64_t)d.groups * ((d.k + 63) / 64) * ((d.n + 255) / 256) >= (1L << 31))
+      (int64_t)d.groups * ((d.k + 127) / 128) * ((d.n + 255) / 256) >= kMostTiles)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

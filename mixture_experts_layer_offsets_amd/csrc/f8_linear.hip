@@ -217,7 +217,7 @@ long blocks(const F8Dims &d, int rows, int tw, int nb) {
 // 1024 x 2048, 512 rows falling off as 1 / g: 31 us without, 20 so, even ones 18 and 18).
 int passes(const F8Dims &d, int rows, int pass, long tiles) {
   const long need = (average(d, rows) + pass - 1) / pass, most = ((long)rows + pass - 1) / pass;
-  return (int)std::min<long>({std::max<long>(need, 2048 / (tiles * d.groups)), most, 65535});
+  return (int)std::min(std::max(need, 2048 / (tiles * d.groups)), most);
 }
 
 }  // namespace

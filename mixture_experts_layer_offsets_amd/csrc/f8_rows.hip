@@ -113,52 +113,48 @@ __device__ __forceinline__ float cols_codes(ColsLds<T> &l, const float (&v)[N]) 
 }
 
 // A workgroup takes 64 columns of one stage (128 rows of one group), which leave in
-// 16-byte chunks.  Grid (columns of a / 64 + those of b / 64, stages), stages past 2^16 in
-// turn.
+// 16-byte chunks.  Grid (columns of a / 64 + those of b / 64, stages).
 template <bool F16>
 __global__ __launch_bounds__(256) void f8_quant_cols_kernel(Cols a, Cols b, int rows,
                                                             const int32_t *__restrict__ offsets,
-                                                            int groups, long stages) {
+                                                            int groups, int stages) {
   __shared__ ColsLds<256> lds;
   const int ax = (a.cols + 63) / 64;
   const bool first_of = (int)blockIdx.x < ax;
   const Cols m = first_of ? a : b;
   const int tid = threadIdx.x, c0 = (first_of ? blockIdx.x : blockIdx.x - ax) * 64;
-  const int cols16 = (m.cols + 15) & ~15;
-  for (long st = blockIdx.y; st < stages; st += gridDim.y) {
-    int first;
-    const int g = f8_group_at(offsets, groups, rows, kF8Block, (int)st, &first);
-    const F8Span sp = f8_span(offsets, g, rows);
-    const int r0 = sp.begin + (int)(st - first) * kF8Block;
-    if (st < first || r0 >= sp.end) continue;  // an empty place
-    u32x4_t u[4];
-    cols_load<256>(m, r0, sp.end, c0, u);
-    cols_put(lds, u);
-    __syncthreads();
-    float v[ColsLds<256>::N];
-    cols_top<F16>(lds, v);
-    __syncthreads();
-    const float s = cols_codes(lds, v);
-    if (tid < 64 && c0 + tid < cols16) m.scales[(size_t)st * cols16 + c0 + tid] = s;
-    __syncthreads();
+  const int cols16 = (m.cols + 15) & ~15, st = blockIdx.y;
+  int first;
+  const int g = f8_group_at(offsets, groups, rows, kF8Block, st, &first);
+  const F8Span sp = f8_span(offsets, g, rows);
+  const int r0 = sp.begin + (st - first) * kF8Block;
+  if (st < first || r0 >= sp.end) return;  // an empty place
+  u32x4_t u[4];
+  cols_load<256>(m, r0, sp.end, c0, u);
+  cols_put(lds, u);
+  __syncthreads();
+  float v[ColsLds<256>::N];
+  cols_top<F16>(lds, v);
+  __syncthreads();
+  const float s = cols_codes(lds, v);
+  if (tid < 64 && c0 + tid < cols16) m.scales[(size_t)st * cols16 + c0 + tid] = s;
+  __syncthreads();
 #pragma unroll
-    for (int p = 0; p < 2; p++) {
-      const int at = tid + 256 * p;
-      int col, c;
-      uint8_t *dst;
-      if (m.tiles) {  // chunk by chunk in a tile's order
-        col = (at >> 7) * 16 + (at & 15);
-        c = ((at >> 6) & 1) * 4 + ((at >> 4) & 3);
-        dst = m.codes + ((size_t)((c0 + col) >> 4) * stages + st) * kF8Tile + f8_chunk(c, col & 15);
-      } else {
-        col = at >> 3;
-        c = at & 7;
-        dst = m.codes + ((size_t)st * m.cols + c0 + col) * kF8Block + 16 * c;
-      }
-      if (c0 + col < (m.tiles ? cols16 : m.cols))
-        *(u32x4_t *)dst = *(const u32x4_t *)(lds.lines + col * kLine + 16 * c);
+  for (int p = 0; p < 2; p++) {
+    const int at = tid + 256 * p;
+    int col, c;
+    uint8_t *dst;
+    if (m.tiles) {  // chunk by chunk in a tile's order
+      col = (at >> 7) * 16 + (at & 15);
+      c = ((at >> 6) & 1) * 4 + ((at >> 4) & 3);
+      dst = m.codes + ((size_t)((c0 + col) >> 4) * stages + st) * kF8Tile + f8_chunk(c, col & 15);
+    } else {
+      col = at >> 3;
+      c = at & 7;
+      dst = m.codes + ((size_t)st * m.cols + c0 + col) * kF8Block + 16 * c;
     }
-    __syncthreads();
+    if (c0 + col < (m.tiles ? cols16 : m.cols))
+      *(u32x4_t *)dst = *(const u32x4_t *)(lds.lines + col * kLine + 16 * c);
   }
 }
 
@@ -242,9 +238,9 @@ void launch_f8_quant_cols(const F8Rows &x, const F8Rows &dy, int rows, const F8D
                           const int32_t *offsets, uint8_t *xc, float *xs, uint8_t *yc, float *ys,
                           hipStream_t s) {
   if (rows <= 0) return;
-  const long stages = f8_stages(rows, d.groups);
+  const int stages = (int)f8_stages(rows, d.groups);
   const Cols a{x.p, x.stride, d.k, 0, xc, xs}, b{dy.p, dy.stride, d.n, 1, yc, ys};
-  const dim3 grid((d.k + 63) / 64 + (d.n + 63) / 64, (unsigned)std::min(stages, 65535L));
+  const dim3 grid((d.k + 63) / 64 + (d.n + 63) / 64, stages);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, b, rows, offsets, d.groups, stages);
   };

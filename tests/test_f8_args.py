@@ -71,6 +71,10 @@ def test_linear_refusals(lib):
     for kw in (dict(xs=(1 << 32) + 1), dict(os_=(1 << 32) + 1), dict(rows=(1 << 30) + 1),
                dict(shape=m.F8Shape(2, 1 << 20, 256), rows=1 << 26, os_=1 << 20)):
         assert linear(lib, **kw) == UNSUPPORTED, kw
+    # the tiles' threads are less than 2^32: 2^23 tiles of 512
+    for rows, rc in (((1 << 30) - 256, 0), (1 << 30, UNSUPPORTED)):
+        assert linear(lib, shape=m.F8Shape(1, 256, 256), rows=rows, os_=256, out=1 << 50, n=0) == \
+            (rc or _lib.MOE_ERR_WORKSPACE), rows
     need = m.moe_f8_linear_workspace_bytes(S, 30000)
     assert need >= 30000 * 256 + 30000 * 8 and linear(lib, rows=30000, n=need - 1) == _lib.MOE_ERR_WORKSPACE
     assert linear(lib, rows=0, x=None, out=None, ws=None, n=0) == _lib.MOE_OK
@@ -106,6 +110,8 @@ def test_wgrad_refusals(lib):
         assert wgrad(lib, **kw) == INVALID, kw
     for kw in (dict(xs=(1 << 32) + 1), dict(ys=(1 << 32) + 1), dict(rows=65534 * 128)):
         assert wgrad(lib, **kw) == UNSUPPORTED, kw
+    for k, rc in (((1 << 20) - 128, _lib.MOE_ERR_WORKSPACE), (1 << 20, UNSUPPORTED)):
+        assert wgrad(lib, shape=m.F8Shape(1024, 256, k), xs=k, ys=256, dw=1 << 50, n=0) == rc, k
     assert m.moe_f8_wgrad_workspace_bytes(S, 65534 * 128) == 0
     assert m.moe_f8_wgrad_workspace_bytes(S, 65533 * 128 + 127) > 0
     wide = m.F8Shape(1024, 1 << 20, 1 << 20)
