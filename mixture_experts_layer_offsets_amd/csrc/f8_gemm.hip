@@ -8,14 +8,14 @@
 // with the outputs' scales 136 or 104), which loads fill directly.  The matrix unit
 // sums the 128 products of a block from zero, and the scales multiply that sum in fp32.
 //
-// What bounds it: at 16384 rows x 4096 x 7168 in 6 groups 509 us with the rows'
-// quantising (48), 2.1 PFLOP/s in the product, where the library's 8-bit product with one
+// What bounds it: at 16384 rows x 4096 x 7168 in 6 groups 510 to 524 us with the
+// rows' quantising (59), 2.1 PFLOP/s in the product, where the library's 8-bit product with one
 // scale a tensor takes 308 us.  The chip runs these products at a reduced clock (1.5 GHz
 // here, 2.2 in a loop of matrix instructions alone), so that every instruction between
 // them counts twice; a stage takes 2870 cycles where its matrix instructions take 2048.
 // In registers alone, without loads, the instruction reaches 4.7 PFLOP/s, 4.3 with a
 // multiply-add for each of its results as the forward has, and 3.2 with two operations as
-// the weight gradient has, whose scales differ along both sides: there 555 of 665 us (962
+// the weight gradient has, whose scales differ along both sides: there 570 of 685 us (962
 // GFLOP), 4040 cycles a stage.  64 groups of 384 rows x 2816 x 2048: 228 us, 27 of a
 // tile's 35 us in the loop and the rest its offsets, first loads and results; half-empty
 // last tiles cost the rest.
