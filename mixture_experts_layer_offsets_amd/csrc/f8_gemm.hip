@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "f8_device.h"
+#include "f8_scales.h"
 
 namespace moe {
 
@@ -179,13 +180,12 @@ __device__ __forceinline__ void f8_tile(const Args &p, uint8_t *X0, uint8_t *X1,
   };
   // ... the scales of the first or second half's outputs behind their tiles (COLS), 4
   // bytes a lane, all waves alike: the last six's are zeros
-  const int osw = ((tid >> 4) / (G::NI / 2) * G::NI + (tid >> 4) % (G::NI / 2)) * 64 + l16 * 4;
+  const int osw[2] = {f8_scale_at(tid, 0, G::NI), f8_scale_at(tid, 1, G::NI)};
   auto dma_s = [&](uint8_t *W, int kt, int half) {
     const int k1 = min(kt, steps - 1);
-    const f8_rsrc_t r = f8_buffer(wsc + (size_t)k1 * p.npitch,
-                                  wave < 2 ? min(kTN, p.npitch - n0) * 4 : 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(W + G::WB / 2 + wave * 256), 4, osw,
-                                             half * (G::NI / 2) * 64, 0, 0);
+    const f8_rsrc_t r = f8_buffer(wsc + (size_t)k1 * p.npitch, f8_scale_bytes(wave, p.npitch - n0));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(W + G::WB / 2 + wave * 256), 4, osw[half],
+                                             0, 0, 0);
   };
   // the rows' scales, and behind them that of the wave's outputs (forward)
   constexpr int NS = COLS ? G::NJ : G::NJ + 1;
