@@ -213,11 +213,10 @@ struct W4Row {
   }
 };
 
-// f(F{}) for the format of d.
+// f(F{}) for the 4-bit format of d.
 template <class Fn>
 void with_format(const W4Dims &d, Fn &&f) {
   if (d.fmt == kW4Mx) f(MxFmt{});
-  else if (d.fmt == kW4F8) f(F8Fmt{});
   else if (d.spg == 1 && !d.zeros) f(IntFmt<1, false>{});
   else if (d.spg == 2 && !d.zeros) f(IntFmt<2, false>{});
   else if (d.spg == 4 && !d.zeros) f(IntFmt<4, false>{});

@@ -615,6 +615,13 @@ __global__ __launch_bounds__(256) void w4_combine_kernel(const float4 *__restric
                                        __builtin_bit_cast(uint32_t, hi));
 }
 
+// The layer takes 8-bit weights beside the formats of the 4-bit products.
+template <class Fn>
+void with_layer_format(const W4Dims &d, Fn &&f) {
+  if (d.fmt == kW4F8) f(F8Fmt{});
+  else with_format(d, f);
+}
+
 }  // namespace
 
 size_t w4_plan_words(int slots, int E) { return 64 + 2 * (size_t)E + 64 + 2 * (size_t)slots; }
@@ -644,7 +651,7 @@ void launch_w4_ffn(const W4Layer &a, hipStream_t s) {
     hipLaunchKernelGGL(w4_plan_kernel, dim3(1), dim3(kPlanThreads),
                        (17 * E + (slots + 1) / 2) * sizeof(int32_t), s, a.idx, a.w, slots, a.k,
                        a.first, E, p);
-  with_format(a.up, [&](auto f) {
+  with_layer_format(a.up, [&](auto f) {
     using F = decltype(f);
     const dim3 b(kGuWaves * 64), bb(kBlockThreads);
     // Rows from memory up to an average of 16 an expert, where every tile reads
