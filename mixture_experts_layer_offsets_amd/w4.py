@@ -49,19 +49,20 @@ class W4Linear:
 
     ``W4Linear.quantize`` takes bf16 weights [groups][k][n] (products x*W),
     ``W4Linear.pack`` ready-made codes, scales and zero points; weights that are
-    packed already come as a uint8 tensor of moe_w4_bytes (checked at the first
-    call).  Calls enqueue on the current stream.
+    packed already come as a uint8 tensor of moe_w4_bytes (checked in every call).
+    Calls enqueue on the current stream.
     """
 
     def __init__(self, shape: W4Shape, packed: torch.Tensor):
         self.shape, self.packed = shape, packed
-        self._fits = False
+        self._need = None, 0  # a shape and its bytes
 
     def _weights(self):
-        """The packed tensor: the kernels read all that the shape says of it."""
-        if not self._fits:
-            _check("packed", self.packed, (self._bytes(self.shape),), (torch.uint8,))
-            self._fits = True
+        """The packed tensor: the kernels read all that the shape says of it.  Looked at in
+        every call: it, its memory or the shape may have been exchanged."""
+        if self._need[0] is not self.shape:
+            self._need = self.shape, self._bytes(self.shape)
+        _check("packed", self.packed, (self._need[1],), (torch.uint8,))
         return self.packed
 
     @staticmethod

@@ -1,0 +1,62 @@
+"""Objects that hold tensors by address, when the tensors are given other memory: checked
+again, or refused (no GPU: the entry points are replaced)."""
+import contextlib
+import os
+
+import pytest
+import torch
+
+import mixture_experts_layer_offsets_amd as m
+from mixture_experts_layer_offsets_amd import _lib
+
+ENTRIES = ("moe_f8_linear", "moe_f8_unpack", "moe_f8_transpose", "moe_w4_linear", "moe_w4_unpack",
+           "moe_f8_decode_fwd", "moe_w4_decode_fwd", "moe_grad_clip", "moe_grad_norm", "moe_grad_scale")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from mixture_experts_layer_offsets_amd import build
+        build.build(verbose=False)
+    return _lib.load()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    made = []
+    for name in ENTRIES:
+        monkeypatch.setattr(_lib, name, lambda *a, name=name: made.append((name, a)))
+    return made
+
+
+def linears():
+    f8, w4 = m.F8Shape(1, 48, 256), m.W4Shape(1, 48, 256)
+    return [(m.F8Linear, f8, m.moe_f8_bytes(f8)), (m.W4Linear, w4, m.moe_w4_bytes(w4))]
+
+
+@pytest.mark.parametrize("which", [0, 1], ids=["f8", "w4"])
+def test_weights_of_a_product(which, calls):
+    """Another packed tensor, the same one with other memory, and another shape."""
+    cls, shape, size = linears()[which]
+    x = torch.zeros((3, 256), dtype=torch.bfloat16)
+    for exchange in (lambda lin: setattr(lin, "packed", torch.empty(size - 256, dtype=torch.uint8)),
+                     lambda lin: setattr(lin, "packed", lin.packed[::2]),
+                     lambda lin: setattr(lin.packed, "data", torch.empty(8, dtype=torch.uint8)),
+                     lambda lin: setattr(lin, "shape", type(shape)(1, 64, 256))):
+        lin = cls(shape, torch.empty(size, dtype=torch.uint8))
+        lin(x)
+        made = len(calls)
+        exchange(lin)
+        for call in (lambda: lin(x), lin.values):
+            with pytest.raises(ValueError, match="packed"):
+                call()
+        assert len(calls) == made
+    # weights of the same size are taken, wherever they lie
+    lin = cls(shape, torch.empty(size, dtype=torch.uint8))
+    lin(x)
+    lin.packed.data = torch.empty(size, dtype=torch.uint8)
+    lin(x)
+    lin.packed = torch.empty(size, dtype=torch.uint8)
+    lin(x)
+    assert len(calls) == made + 3 and calls[-1][1][3] is lin.packed
