@@ -6,7 +6,7 @@ import torch
 
 from . import _lib
 from ._lib import F8Shape, Shape
-from .w4 import _check, decode_args
+from .w4 import _check, check_places, decode_args, places
 
 _ROWS = {_lib.MOE_ROW_BF16: (torch.bfloat16, torch.int16), _lib.MOE_ROW_F16: (torch.float16,)}
 _TYPES = {torch.bfloat16: _lib.MOE_ROW_BF16, torch.int16: _lib.MOE_ROW_BF16,
@@ -141,14 +141,15 @@ class F8Linear:
 class F8Experts:
     """moe_f8_experts: the packed matrices of a layer's experts (gate, up [E][H][I],
     down [E][I][H]; the shared expert's with one group), uint8 tensors as moe_f8_pack
-    and moe_f8_quantize leave them, kept alive here."""
+    and moe_f8_quantize leave them, kept alive here.  A tensor that is given other memory
+    afterwards (``t.data = ...``) ends them: calls raise ValueError."""
 
     def __init__(self, gate, up, down, shared_gate=None, shared_up=None, shared_down=None, *,
                  first_expert=0):
         self.tensors = (gate, up, down, shared_gate, shared_up, shared_down)
         self.shapes = None  # (groups, n, k) of the matrices, where they are known
-        self._c = _lib.MoeF8Experts(first_expert,
-                                    *(None if t is None else t.data_ptr() for t in self.tensors))
+        self._at = places(self.tensors)
+        self._c = _lib.MoeF8Experts(first_expert, *(a and a[0] for a in self._at))
 
     @classmethod
     def of(cls, gate: F8Linear, up: F8Linear, down: F8Linear, shared_gate=None, shared_up=None,
@@ -161,6 +162,7 @@ class F8Experts:
         return experts
 
     def c(self):
+        check_places(self.tensors, self._at)
         return self._c
 
 

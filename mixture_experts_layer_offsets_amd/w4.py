@@ -28,6 +28,16 @@ def _check(name, t, shape, dtypes, device=None, rows=False):
         raise ValueError(f"{name}: strides {t.stride()} are not those of plain rows")
 
 
+def places(tensors):
+    """Where each tensor (or None) lies, and how many values are there."""
+    return [None if t is None else (t.data_ptr(), t.numel()) for t in tensors]
+
+
+def check_places(tensors, at):
+    if places(tensors) != at:
+        raise ValueError("experts: a matrix was given other memory since")
+
+
 def decode_args(s, dev, x, w_router, bias, topk_idx, topk_w, out):
     """The checked arguments of a few-token layer's call; its ``out``."""
     slots, tokens = (s.tokens, s.top_k), (s.tokens, s.hidden)
@@ -136,15 +146,17 @@ class W4Linear:
 class W4Experts:
     """moe_w4_experts: the packed matrices of a layer's experts (gate, up
     [E][H][I], down [E][I][H]; the shared expert's with one group), uint8
-    tensors as moe_w4_pack and moe_w4_quantize leave them, kept alive here."""
+    tensors as moe_w4_pack and moe_w4_quantize leave them, kept alive here.  A tensor that
+    is given other memory afterwards (``t.data = ...``) ends them: calls raise ValueError."""
 
     def __init__(self, gate, up, down, shared_gate=None, shared_up=None, shared_down=None, *,
                  format=_lib.MOE_W4_MXFP4, group_size=32, scale_type=_lib.MOE_SCALE_BF16, zeros=0,
                  first_expert=0):
         self.tensors = (gate, up, down, shared_gate, shared_up, shared_down)
         self.shapes = None  # of the matrices, where they are known
+        self._at = places(self.tensors)
         self._c = _lib.MoeW4Experts(format, group_size, scale_type, zeros, first_expert,
-                                    *(None if t is None else t.data_ptr() for t in self.tensors))
+                                    *(a and a[0] for a in self._at))
 
     @classmethod
     def of(cls, gate: W4Linear, up: W4Linear, down: W4Linear, shared_gate=None, shared_up=None,
@@ -163,6 +175,7 @@ class W4Experts:
         return experts
 
     def c(self):
+        check_places(self.tensors, self._at)
         return self._c
 
 

@@ -60,3 +60,33 @@ def test_weights_of_a_product(which, calls):
     lin.packed = torch.empty(size, dtype=torch.uint8)
     lin(x)
     assert len(calls) == made + 3 and calls[-1][1][3] is lin.packed
+
+
+def experts(cls, shape_of, size_of):
+    """A layer's experts of 4- or 8-bit matrices, and the layer."""
+    layer = m.Shape(4, 256, 8, 2, 128, 128)
+    mats = [shape_of(8, 128, 256)] * 2 + [shape_of(8, 256, 128)] + \
+        [shape_of(1, 128, 256)] * 2 + [shape_of(1, 256, 128)]
+    return layer, cls(*[torch.zeros(size_of(s), dtype=torch.uint8) for s in mats])
+
+
+@pytest.mark.parametrize("kind", ["f8", "w4"])
+@pytest.mark.parametrize("which", [0, 2, 5])
+def test_experts_of_a_layer(kind, which, calls):
+    """A matrix given other memory, of the same size or not."""
+    cls, shape_of, size_of, dec_of = {
+        "f8": (m.F8Experts, m.F8Shape, m.moe_f8_bytes, m.F8Decoder),
+        "w4": (m.W4Experts, m.W4Shape, m.moe_w4_bytes, m.W4Decoder)}[kind]
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    idx, w = torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
+    for size in (0, 5, None):
+        layer, e = experts(cls, shape_of, size_of)
+        dec = dec_of(layer, e)
+        dec(x, topk_idx=idx, topk_w=w)
+        assert calls[-1][1][1] is e and e.c().gate == e.tensors[0].data_ptr()
+        t = e.tensors[which]
+        t.data = torch.zeros(t.numel() if size is None else size, dtype=torch.uint8)
+        with pytest.raises(ValueError, match="memory"):
+            _lib._shape(e)
+        with pytest.raises(ValueError, match="memory"):
+            e.c()
