@@ -90,3 +90,25 @@ def test_experts_of_a_layer(kind, which, calls):
             _lib._shape(e)
         with pytest.raises(ValueError, match="memory"):
             e.c()
+
+
+@pytest.mark.parametrize("with_outs", [False, True])
+def test_gradients_of_a_set(with_outs, calls):
+    """A gradient or out with other memory: refused by every call of GradClip, and the old
+    memory is not given away while the set has its address."""
+    for which in range(3 if with_outs else 2):
+        grads = [torch.zeros((4, 6)), torch.zeros(5, dtype=torch.half)]
+        outs = [torch.zeros((4, 6)), torch.zeros(5, dtype=torch.half)] if with_outs else None
+        clip = m.GradClip(m.GradSet(grads, outs))
+        clip(1.0)
+        clip.scale(clip.total(), 1.0)
+        made = len(calls)
+        t = (grads + (outs or []))[which]
+        old = t.data_ptr()
+        t.data = torch.zeros_like(t)
+        assert t.data_ptr() != old
+        assert all(torch.zeros_like(t).data_ptr() != old for _ in range(8))
+        for call in (clip.set.check, lambda: clip(1.0), clip.total, lambda: clip.scale(clip._total, 1.0)):
+            with pytest.raises(ValueError, match="memory"):
+                call()
+        assert len(calls) == made
