@@ -239,6 +239,12 @@ class MoeW4Experts(ctypes.Structure):
                                         "shared_down")]
 
 
+def _i32(v):
+    """v, or the end of an int32's range that it lies beyond: ctypes would take its low
+    bits, and the library what they say."""
+    return min(max(v, -0x80000000), 0x7FFFFFFF)
+
+
 class MoeF8Shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("groups", "n", "k", "row_type")]
 
@@ -254,7 +260,7 @@ class F8Shape:
     def c(self) -> MoeF8Shape:
         s = self.__dict__.get("_c")
         if s is None:
-            s = MoeF8Shape(self.groups, self.n, self.k, self.row_type)
+            s = MoeF8Shape(*map(_i32, (self.groups, self.n, self.k, self.row_type)))
             object.__setattr__(self, "_c", s)
         return s
 
@@ -499,35 +505,35 @@ def _row_stride(t):
 
 def moe_f8_quantize_rows(shape, x, codes, scales, stream=None):
     """x [rows][k]: rows one stride apart, values contiguous."""
-    _ck(load().moe_f8_quantize_rows(_shape(shape), x.shape[0], _p(x), _row_stride(x), _p(codes),
+    _ck(load().moe_f8_quantize_rows(_shape(shape), _i32(x.shape[0]), _p(x), _row_stride(x), _p(codes),
                                     _p(scales), _stream(stream)), "moe_f8_quantize_rows")
 
 
 def moe_f8_linear_workspace_bytes(shape, rows) -> int:
-    return load().moe_f8_linear_workspace_bytes(_shape(shape), rows)
+    return load().moe_f8_linear_workspace_bytes(_shape(shape), _i32(rows))
 
 
 def moe_f8_linear(shape, x, offsets, packed, out, ws, stream=None):
     """x [rows][k] and out [rows][n]: rows one stride apart, values contiguous."""
-    _ck(load().moe_f8_linear(_shape(shape), x.shape[0], _p(x), _row_stride(x), _p(offsets),
+    _ck(load().moe_f8_linear(_shape(shape), _i32(x.shape[0]), _p(x), _row_stride(x), _p(offsets),
                              _p(packed), _p(out), _row_stride(out), _p(ws),
                              ws.numel() * ws.element_size(), _stream(stream)), "moe_f8_linear")
 
 
 def moe_f8_linear_codes(shape, codes, scales, offsets, packed, out, stream=None):
     """codes and scales as moe_f8_quantize_rows leaves them; out [rows][n]."""
-    _ck(load().moe_f8_linear_codes(_shape(shape), out.shape[0], _p(codes), _p(scales), _p(offsets),
+    _ck(load().moe_f8_linear_codes(_shape(shape), _i32(out.shape[0]), _p(codes), _p(scales), _p(offsets),
                                    _p(packed), _p(out), _row_stride(out), _stream(stream)),
         "moe_f8_linear_codes")
 
 
 def moe_f8_wgrad_workspace_bytes(shape, rows) -> int:
-    return load().moe_f8_wgrad_workspace_bytes(_shape(shape), rows)
+    return load().moe_f8_wgrad_workspace_bytes(_shape(shape), _i32(rows))
 
 
 def moe_f8_wgrad(shape, x, dy, offsets, dw, ws, stream=None):
     """x [rows][k] and dy [rows][n]: rows one stride apart, values contiguous."""
-    _ck(load().moe_f8_wgrad(_shape(shape), x.shape[0], _p(x), _row_stride(x), _p(dy),
+    _ck(load().moe_f8_wgrad(_shape(shape), _i32(x.shape[0]), _p(x), _row_stride(x), _p(dy),
                             _row_stride(dy), _p(offsets), _p(dw), _p(ws),
                             ws.numel() * ws.element_size(), _stream(stream)), "moe_f8_wgrad")
 

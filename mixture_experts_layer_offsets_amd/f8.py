@@ -149,7 +149,7 @@ class F8Experts:
         self.tensors = (gate, up, down, shared_gate, shared_up, shared_down)
         self.shapes = None  # (groups, n, k) of the matrices, where they are known
         self._at = places(self.tensors)
-        self._c = _lib.MoeF8Experts(first_expert, *(a and a[0] for a in self._at))
+        self._c = _lib.MoeF8Experts(_lib._i32(first_expert), *(a and a[0] for a in self._at))
 
     @classmethod
     def of(cls, gate: F8Linear, up: F8Linear, down: F8Linear, shared_gate=None, shared_up=None,
