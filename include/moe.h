@@ -574,7 +574,9 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts,
  *
  * Limits: 1 <= groups <= 1024, 1 <= n, k <= 2^20; rows are bf16 or fp16
  * (row_type), of any n and k, strides in values of at least a row and at most
- * 2^32.  Row tensors need their type's alignment only.  offsets (device, int32
+ * 2^32.  Row tensors need their type's alignment only.  A call that finds what it
+ * writes among the rows, codes, scales or weights that it computes it from refuses
+ * (from a tensor's first to its last value; moe_f8_linear looks more closely).  offsets (device, int32
  * [groups+1], ascending, at most `rows`; NULL with one group: all rows) say that
  * the rows of group g are [offsets[g], offsets[g+1]).  No entry point reads a host
  * copy of them, so all can be captured into a graph (with a workspace of its own

@@ -27,6 +27,19 @@ bool overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t sb, i
   return at < na || at + nb > sa;
 }
 
+// Whether two runs of bytes meet.
+bool meet(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return na && nb && x < y + nb && y < x + na;
+}
+
+size_t values(const F8Dims &d) { return (size_t)d.groups * d.n * d.k; }
+
+// Bytes from the first to the last value of rows of n values, `size` bytes each.
+size_t run_of(int64_t rows, int64_t stride, int64_t n, size_t size) {
+  return rows ? ((rows - 1) * stride + n) * size : 0;
+}
+
 // Quantised rows in a workspace.
 size_t rows_bytes(const F8Dims &d, int32_t rows, size_t *scales) {
   *scales = up256((size_t)d.ks * rows * kF8Block);
@@ -103,6 +116,9 @@ int moe_f8_pack(const moe_f8_shape *shape, const uint8_t *codes, const float *sc
   const int rc = f8_dims(shape, &d);
   if (rc) return rc;
   if (!codes || !scales || !packed || !aligned16(packed)) return MOE_ERR_INVALID_ARG;
+  if (meet(packed, d.bytes(), codes, values(d)) ||
+      meet(packed, d.bytes(), scales, (size_t)d.groups * d.nb * d.ks * 4))
+    return MOE_ERR_INVALID_ARG;
   launch_f8_pack(d, codes, scales, packed, (hipStream_t)stream);
   return status();
 }
@@ -114,6 +130,8 @@ int moe_f8_quantize(const moe_f8_shape *shape, const void *w, int32_t w_type, vo
   if (rc) return rc;
   if (!w || !packed || !aligned16(packed) || w_type < MOE_ROW_BF16 || w_type > MOE_ROW_F32)
     return MOE_ERR_INVALID_ARG;
+  if (meet(packed, d.bytes(), w, values(d) * (w_type == MOE_ROW_F32 ? 4 : 2)))
+    return MOE_ERR_INVALID_ARG;
   launch_f8_quantize(d, w, w_type, packed, (hipStream_t)stream);
   return status();
 }
@@ -122,7 +140,8 @@ int moe_f8_unpack(const moe_f8_shape *shape, const void *packed, float *w, void 
   F8Dims d;
   const int rc = f8_dims(shape, &d);
   if (rc) return rc;
-  if (!w || !packed || !aligned16(packed)) return MOE_ERR_INVALID_ARG;
+  if (!w || !packed || !aligned16(packed) || meet(w, values(d) * 4, packed, d.bytes()))
+    return MOE_ERR_INVALID_ARG;
   launch_f8_unpack(d, packed, w, (hipStream_t)stream);
   return status();
 }
@@ -131,8 +150,10 @@ int moe_f8_transpose(const moe_f8_shape *shape, const void *packed, void *packed
   F8Dims d;
   const int rc = f8_dims(shape, &d);
   if (rc) return rc;
-  if (!packed || !packed_t || packed == packed_t || !aligned16(packed) || !aligned16(packed_t))
-    return MOE_ERR_INVALID_ARG;
+  if (!packed || !packed_t || !aligned16(packed) || !aligned16(packed_t)) return MOE_ERR_INVALID_ARG;
+  const moe_f8_shape turned = {d.groups, d.k, d.n, shape->row_type};
+  F8Dims t;
+  if (f8_dims(&turned, &t) || meet(packed, d.bytes(), packed_t, t.bytes())) return MOE_ERR_INVALID_ARG;
   launch_f8_transpose(d, packed, packed_t, (hipStream_t)stream);
   return status();
 }
@@ -145,6 +166,10 @@ int moe_f8_quantize_rows(const moe_f8_shape *shape, int32_t rows, const void *x,
   if (rows < 0 || x_stride < d.k || (rows && (!x || !codes || !scales)) || !aligned16(codes))
     return MOE_ERR_INVALID_ARG;
   if (x_stride > kMostStride || rows > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  const size_t nx = run_of(rows, x_stride, d.k, 2), at = (size_t)d.ks * rows;
+  if (meet(codes, at * kF8Block, x, nx) || meet(scales, at * 4, x, nx) ||
+      meet(codes, at * kF8Block, scales, at * 4))
+    return MOE_ERR_INVALID_ARG;
   launch_f8_quant_rows({(const uint16_t *)x, x_stride, d.f16}, rows, d.k, codes, scales,
                        (hipStream_t)stream);
   return status();
@@ -199,6 +224,8 @@ int moe_f8_linear_codes(const moe_f8_shape *shape, int32_t rows, const uint8_t *
   if ((rc = check_rows(d, rows, offsets))) return rc;
   if (out_stride > kMostStride) return MOE_ERR_UNSUPPORTED;
   if (!rows) return MOE_OK;
+  const size_t no = run_of(rows, out_stride, d.n, 2), at = (size_t)d.ks * rows;
+  if (meet(out, no, codes, at * kF8Block) || meet(out, no, scales, at * 4)) return MOE_ERR_INVALID_ARG;
   (f8_few(d, rows) ? launch_f8_few : launch_f8_gemm)(d, rows, codes, scales, offsets, packed,
                                                      (uint16_t *)out, out_stride,
                                                      (hipStream_t)stream);
@@ -222,9 +249,8 @@ int moe_f8_wgrad(const moe_f8_shape *shape, int32_t rows, const void *x, int64_t
   if ((rc = check_wgrad(d, rows))) return rc;
   if (x_stride > kMostStride || dy_stride > kMostStride) return MOE_ERR_UNSUPPORTED;
   // dw lies in one run; between a tensor's rows it would have to fit into one gap
-  const int64_t all = (int64_t)d.groups * d.k * d.n;
-  if (rows && (overlap(dw, all, all, x, (rows - 1) * x_stride + d.k, (rows - 1) * x_stride + d.k, 1) ||
-               overlap(dw, all, all, dy, (rows - 1) * dy_stride + d.n, (rows - 1) * dy_stride + d.n, 1)))
+  if (meet(dw, values(d) * 2, x, run_of(rows, x_stride, d.k, 2)) ||
+      meet(dw, values(d) * 2, dy, run_of(rows, dy_stride, d.n, 2)))
     return MOE_ERR_INVALID_ARG;
   const Cols c = cols_of(d, rows);
   if (ws_bytes < c.bytes) return MOE_ERR_WORKSPACE;
