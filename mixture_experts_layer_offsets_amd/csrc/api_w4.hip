@@ -232,6 +232,10 @@ int moe_f8_decode_fwd(const moe_shape *shape, const moe_f8_experts *experts, con
                       const uint16_t *w_router, const float *bias, const int32_t *topk_idx_in,
                       const float *topk_w_in, uint16_t *out, void *ws, size_t ws_bytes,
                       void *stream) {
+  if (experts)
+    for (const void *p : {experts->gate, experts->up, experts->down, experts->shared_gate,
+                          experts->shared_up, experts->shared_down})
+      if ((uintptr_t)p & 15) return MOE_ERR_INVALID_ARG;
   return decode_fwd(shape, experts, x, w_router, bias, topk_idx_in, topk_w_in, out, ws, ws_bytes,
                     stream, [&](int groups, int n, int kk, W4Dims *d) {
                       const moe_f8_shape s = {groups, n, kk, MOE_ROW_BF16};

@@ -1,5 +1,5 @@
-"""8-bit entry points whose output lies on what it is computed from refuse (no GPU: the
-refusals come first, and what is not refused is stopped by its alignment or not called)."""
+"""8-bit entry points whose output lies on what it is computed from, or whose weights lie
+askew, refuse (no GPU: the refusals come first, and nothing else is called)."""
 import ctypes
 import os
 
@@ -66,3 +66,14 @@ def test_rows(lib):
         assert lib.moe_f8_linear_codes(s, rows, far, A, far, far, at, stride, None) == INVALID, hex(at)
     # without rows there is nothing to meet
     assert lib.moe_f8_linear_codes(s, 0, A, far, far, far, A, stride, None) == _lib.MOE_OK
+
+
+@pytest.mark.parametrize("which", ["gate", "up", "down", "shared_gate", "shared_up", "shared_down"])
+def test_experts_are_aligned(lib, which):
+    """Packed matrices lie on 16 bytes, as every other entry point asks of them."""
+    layer = m.Shape(4, 256, 8, 2, 128, 128)
+    for off, rc in ((0, _lib.MOE_ERR_WORKSPACE), (8, INVALID), (1, INVALID)):
+        e = _lib.MoeF8Experts(0, *[A] * 6)
+        setattr(e, which, A + off)
+        assert lib.moe_f8_decode_fwd(ctypes.byref(layer.c()), ctypes.byref(e), A, None, None, A, A, A, A, 0,
+                                     None) == rc, off
