@@ -629,8 +629,7 @@ int moe_f8_linear(const moe_f8_shape *shape, int32_t rows, const void *x,
                   void *out, int64_t out_stride, void *ws, size_t ws_bytes,
                   void *stream);
 
-/* The same of rows that moe_f8_quantize_rows has quantised (blocks may be added in
- * another order than there: each entry point repeats its own bits). */
+/* The same of rows that moe_f8_quantize_rows has quantised, to the same bits. */
 int moe_f8_linear_codes(const moe_f8_shape *shape, int32_t rows,
                         const uint8_t *codes, const float *scales,
                         const int32_t *offsets, const void *packed, void *out,

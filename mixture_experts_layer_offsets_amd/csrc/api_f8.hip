@@ -226,9 +226,10 @@ int moe_f8_linear_codes(const moe_f8_shape *shape, int32_t rows, const uint8_t *
   if (!rows) return MOE_OK;
   const size_t no = run_of(rows, out_stride, d.n, 2), at = (size_t)d.ks * rows;
   if (meet(out, no, codes, at * kF8Block) || meet(out, no, scales, at * 4)) return MOE_ERR_INVALID_ARG;
-  (f8_few(d, rows) ? launch_f8_few : launch_f8_gemm)(d, rows, codes, scales, offsets, packed,
-                                                     (uint16_t *)out, out_stride,
-                                                     (hipStream_t)stream);
+  // sizes that moe_f8_linear takes in one launch go to the kernel that adds in its order
+  const bool few = f8_few(d, rows) || f8_few_staged(d, rows);
+  (few ? launch_f8_few : launch_f8_gemm)(d, rows, codes, scales, offsets, packed, (uint16_t *)out,
+                                         out_stride, (hipStream_t)stream);
   return status();
 }
 

@@ -212,6 +212,41 @@ long blocks(const F8Dims &d, int rows, int tw, int nb) {
   return (long)((d.nt + tw - 1) / tw) * d.groups * ((average(d, rows) + 16 * nb - 1) / (16 * nb));
 }
 
+// How a product is split: waves of a workgroup, over the contraction; tiles and blocks of 16
+// rows that they take.
+struct Split {
+  int waves, tw, nb;
+};
+
+// The more tiles and rows a workgroup takes, the less often either is read again, as
+// long as some 200 workgroups are left (and half of its tiles exist: 16000 rows of 16 x
+// 512 in tiles of one 12.7 us, of four 14.2).  One group of 4096 x 4096, us with (tiles,
+// blocks of rows) of (4, 4) / (2, 4) / (2, 2) / (1, 2): 256 rows 24 / 30 / 32 / 45, 128
+// rows 23 / 17 / 19 / 26, 64 rows 22 / 17 / 13 / 16, 24 rows 19 / 14 / 12 / 11.
+// Up to 8 rows a group: one tile, and the more waves the fewer workgroups.
+//
+// The waves decide the order of addition, and 16-bit rows that launch_f8_few_rows quantises on
+// the way get the bits of their codes: both take these.  That many workgroups of one tile and 8
+// rows take four waves (1000 rows of 256 x 512, us from rows: 8.6, with eight 11.3; from codes
+// 4.3 either way), fewer take eight (16 rows of 2048 x 4096: 8.3, with 16 8.1; from codes 6.0,
+// with 16 7.9).
+Split split_of(const F8Dims &d, int rows) {
+  const int avg = average(d, rows);
+  if (avg <= kStaged) {
+    const long n = blocks(d, rows, 1, 1);
+    return {n <= 256 ? 16 : n <= 512 ? 8 : 4, 1, 1};
+  }
+  if (f8_few_staged(d, rows) && (long)d.nt * d.groups * ((avg + kStaged - 1) / kStaged) > 512)
+    return {4, d.nt > 1 ? 2 : 1, 2};
+  auto many = [&](int tw, int nb) {
+    return blocks(d, rows, tw, nb) >= 200 && 2 * d.nt > tw;
+  };
+  if (avg > 32 && many(4, 4)) return {8, 4, 4};
+  if (avg > 32 && many(2, 4)) return {8, 2, 4};
+  if (many(2, 2)) return {blocks(d, rows, 2, 2) > 512 ? 4 : 8, 2, 2};
+  return {8, 1, 2};
+}
+
 // Passes of a group: what the average needs, and, for groups longer than it, further ones
 // side by side where that takes no more workgroups than the chip runs at once (8 groups of
 // 1024 x 2048, 512 rows falling off as 1 / g: 31 us without, 20 so, even ones 18 and 18).
@@ -237,7 +272,7 @@ bool f8_few(const F8Dims &d, int rows) {
 // d.ks blocks.  Up to 8 rows a group: 8 rows of 2048 x 7168 (57 thousand) 10.6 us against
 // 11.5, 32 rows in 32 groups of 2816 x 2048 (90) 21.6 against 23.6; 8 rows of 7168 x 4096
 // (115) 12.7 against 11.5, 96 rows in the 32 groups (270) 33.6 against 31.3.  More rows, in
-// passes of 8 whose workgroups the chip holds: 16 of 2048 x 4096 (66) 8.0 against 11.0, of
+// passes of 8 whose workgroups the chip holds: 16 of 2048 x 4096 (66) 8.3 against 11.0, of
 // 4096 x 4096 (131) 12.3 against 11.2; 1000 of 256 x 512 (64, 2000 workgroups) 8.1 against
 // 10.2, 4000 of 256 x 128 (64, 8000) 17.5 against 10.8; 16 groups of 1000 x 512, 160 rows
 // (40) 8.0 against 10.2, 32 of 512 x 512, 512 rows (66) 11.2 against 10.1.
@@ -262,30 +297,16 @@ void launch_f8_few(const F8Dims &d, int rows, const uint8_t *codes, const float 
     hipLaunchKernelGGL(kernel, dim3(tiles, d.groups, passes(d, rows, 16 * nb, tiles)), dim3(waves * 64),
                        0, s, p, codes, scales);
   };
-  // The more tiles and rows a workgroup takes, the less often either is read again, as
-  // long as some 200 workgroups are left (and half of its tiles exist: 16000 rows of 16 x
-  // 512 in tiles of one 12.7 us, of four 14.2).  One group of 4096 x 4096, us with (tiles,
-  // blocks of rows) of (4, 4) / (2, 4) / (2, 2) / (1, 2): 256 rows 24 / 30 / 32 / 45, 128
-  // rows 23 / 17 / 19 / 26, 64 rows 22 / 17 / 13 / 16, 24 rows 19 / 14 / 12 / 11.
-  auto many = [&](int tw, int nb) {
-    return blocks(d, rows, tw, nb) >= 200 && 2 * d.nt > tw;
-  };
-  const bool more = blocks(d, rows, 2, 2) > 512;  // then four waves each
-  if (avg <= 8) {
-    const long n = blocks(d, rows, 1, 1);
-    if (n <= 256) go(f8_few_kernel<16, 1, 1, 4>, 16, 1, 1);
-    else if (n <= 512) go(f8_few_kernel<8, 1, 1, 4>, 8, 1, 1);
-    else go(f8_few_kernel<4, 1, 1, 4>, 4, 1, 1);
-  } else if (avg > 32 && many(4, 4)) {
-    go(f8_few_kernel<8, 4, 4, 1>, 8, 4, 4);
-  } else if (avg > 32 && many(2, 4)) {
-    go(f8_few_kernel<8, 2, 4, 2>, 8, 2, 4);
-  } else if (many(2, 2)) {
-    if (more) go(f8_few_kernel<4, 2, 2, 2>, 4, 2, 2);
-    else go(f8_few_kernel<8, 2, 2, 2>, 8, 2, 2);
-  } else {
-    go(f8_few_kernel<8, 1, 2, 2>, 8, 1, 2);
-  }
+  const Split c = split_of(d, rows);
+  if (c.tw == 4) go(f8_few_kernel<8, 4, 4, 1>, 8, 4, 4);
+  else if (c.nb == 4) go(f8_few_kernel<8, 2, 4, 2>, 8, 2, 4);
+  else if (c.tw == 2 && c.waves == 4) go(f8_few_kernel<4, 2, 2, 2>, 4, 2, 2);
+  else if (c.tw == 2) go(f8_few_kernel<8, 2, 2, 2>, 8, 2, 2);
+  else if (c.nb == 2 && c.waves == 4) go(f8_few_kernel<4, 1, 2, 2>, 4, 1, 2);
+  else if (c.nb == 2) go(f8_few_kernel<8, 1, 2, 2>, 8, 1, 2);
+  else if (c.waves == 16) go(f8_few_kernel<16, 1, 1, 4>, 16, 1, 1);
+  else if (c.waves == 8) go(f8_few_kernel<8, 1, 1, 4>, 8, 1, 1);
+  else go(f8_few_kernel<4, 1, 1, 4>, 4, 1, 1);
 }
 
 void launch_f8_few_rows(const F8Dims &d, int rows, const F8Rows &x, const int32_t *offsets,
@@ -296,11 +317,11 @@ void launch_f8_few_rows(const F8Dims &d, int rows, const F8Rows &x, const int32_
     hipLaunchKernelGGL(kernel, dim3(d.nt, d.groups, z), dim3(waves * 64), staged_lds(d.ks), s, p,
                        x.p, x.stride);
   };
-  const long tasks = (long)d.nt * d.groups * ((average(d, rows) + kStaged - 1) / kStaged);
+  const int waves = split_of(d, rows).waves;
   auto pick = [&](auto f16) {
     constexpr bool F16 = decltype(f16)::value;
-    if (tasks <= 256) go(f8_few_rows_kernel<F16, 16, 4>, 16);
-    else if (tasks <= 512) go(f8_few_rows_kernel<F16, 8, 4>, 8);
+    if (waves == 16) go(f8_few_rows_kernel<F16, 16, 4>, 16);
+    else if (waves == 8) go(f8_few_rows_kernel<F16, 8, 4>, 8);
     else go(f8_few_rows_kernel<F16, 4, 4>, 4);
   };
   x.f16 ? pick(std::true_type{}) : pick(std::false_type{});
