@@ -570,7 +570,9 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts,
  * another row's outputs (those of a column, in a weight gradient, another column's).
  * Sums of 128 code products come from the matrix unit, which keeps fewer bits of
  * them than fp32 (1.3e-5 of their norm); they are scaled and added in fp32.  The
- * scales of two blocks that meet must have a finite product.
+ * scales of two blocks that meet are multiplied first, in fp32: the product must be
+ * finite, and full precision takes one of 2^-126 or more.  A smaller one is held in
+ * steps of 2^-149, so that a block of 128 adds an error of up to 2^-125 there.
  *
  * Limits: 1 <= groups <= 1024, 1 <= n, k <= 2^20; rows are bf16 or fp16
  * (row_type), of any n and k, strides in values of at least a row and at most

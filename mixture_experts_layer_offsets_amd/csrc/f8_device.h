@@ -7,7 +7,12 @@
 //
 // The inner sum, 128 products of codes, is one v_mfma_f32_16x16x128_f8f6f4 with a
 // zero accumulator; the scales multiply its result in fp32, into accumulators in
-// registers.  Per instruction (32 cycles of the matrix pipe) that is one
+// registers.  The two scales are multiplied with each other first, in the forward once for
+// a lane's four results: one after the other they would cost an operation more a result.
+// Where their product is below 2^-126 it is subnormal, and the block's sum off by up to
+// 2^-125 (2^-150 times 128 448^2): half a step of bf16 at 2^-117.
+//
+// Per instruction (32 cycles of the matrix pipe) that is one
 // multiply-add a result value, 4 a lane (16 cycles of the vector pipe): the two
 // overlap between the waves of a SIMD.  The instruction keeps fewer bits than fp32 of
 // its sum: random codes give 1.33e-5 of the results' norm, the scaled and the

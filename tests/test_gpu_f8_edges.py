@@ -90,3 +90,42 @@ def test_codes_give_the_bits_of_their_rows(M, ends, n, k, dtype):
     lin(x, off, out=a)
     m.moe_f8_linear_codes(shape, xc, xs, off, lin.packed, b)
     assert torch.equal(a, b)
+
+
+# Two blocks' scales meet as one fp32 product.  Below 2^-126 that is held in steps of 2^-149:
+# off by 2^-150 times a sum of code products, at most 128 448^2 < 2^25 of them, each block.
+SMALL = 2.0 ** -125
+
+
+@pytest.mark.parametrize("sx,sw", [(-60, -63), (-97, -20), (-70, -70), (-75, -50), (-99, -99)])
+@pytest.mark.parametrize("M", [3, 20, 300, 600])
+def test_small_scales_on_both_sides(M, sx, sw):
+    """Down to a scales' product of 2^-126 as precise as anywhere; below, to SMALL a block."""
+    rng = np.random.default_rng([M, -sx, -sw])
+    n, k = (10240, 390) if M == 600 else (200, 390)
+    codes, _, _ = fo.random_codes(rng, 1, n, k)
+    scales = np.full((1, -(-n // 128), 4), 2.0 ** sw, np.float32)
+    lin = m.F8Linear.pack(m.F8Shape(1, n, k), torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    x = rng.standard_normal((M, k))
+    x[:, ::128] = 448 / 2                         # scales between 2^(sx - 1) and 2^sx
+    x = torch.from_numpy((x * 2.0 ** sx).astype(np.float32)).to(BF)
+    note(f"f8 small scales rows={M} 2^{sx} 2^{sw}")
+    part = slice(0, 200)
+    w = fo.weight_values(codes[:, part], scales[:, :2])[0]
+    y, bound = fo.product(fo.rows_quantised(x.float().numpy())[2], w)
+    tol = fo.rounded(y, bound, BF) + (4 * SMALL if sx - 1 + sw < -126 else 0.0)
+    within("y", lin(x.cuda())[:, part], y, tol)
+
+
+@pytest.mark.parametrize("M", [200, 3000], ids=["one launch", "two"])
+@pytest.mark.parametrize("sx,sy", [(-60, -63), (-70, -70), (-75, -50)])
+def test_small_scales_of_a_weight_gradient(M, sx, sy):
+    rng = np.random.default_rng([M, -sx, -sy])
+    k, n = 40, 300
+    x, dy = rng.standard_normal((M, k)), rng.standard_normal((M, n))
+    x[::128], dy[::128] = 448 / 2, 448 / 2
+    x, dy = (torch.from_numpy((v * 2.0 ** s).astype(np.float32)).to(BF) for v, s in ((x, sx), (dy, sy)))
+    lin = m.F8Linear(m.F8Shape(1, n, k), torch.empty(0, dtype=torch.uint8, device="cuda"))
+    want, bound = fo.weight_gradient(x.float().numpy(), dy.float().numpy())
+    tol = fo.rounded(want, bound, BF) + (-(-M // 128) * SMALL if sx - 1 + sy - 1 < -126 else 0.0)
+    within("dw", lin.weight_gradient(x.cuda(), dy.cuda())[0], want, tol)
