@@ -26,12 +26,16 @@ class F8Linear:
         self.shape, self.packed = shape, packed
         self._need = None, 0  # a shape and its bytes
 
+    def _size(self):
+        """Bytes of the packed tensor; ValueError for a shape outside the limits."""
+        if self._need[0] is not self.shape:
+            self._need = self.shape, self._bytes(self.shape)
+        return self._need[1]
+
     def _weights(self):
         """The packed tensor: the kernels read all that the shape says of it.  Looked at in
         every call: it, its memory or the shape may have been exchanged."""
-        if self._need[0] is not self.shape:
-            self._need = self.shape, self._bytes(self.shape)
-        _check("packed", self.packed, (self._need[1],), (torch.uint8,))
+        _check("packed", self.packed, (self._size(),), (torch.uint8,))
         return self.packed
 
     @staticmethod
@@ -122,6 +126,7 @@ class F8Linear:
         """dw [groups][k][n] of the shape's row type: per group x^T dy, both in 8 bits
         with a scale per 128 rows of a column."""
         s, dev = self.shape, self.packed.device
+        self._size()
         self._rows("x", x, s.k, dev)
         rows = x.shape[0]
         self._rows("dy", dy, s.n, dev, rows)
@@ -167,7 +172,10 @@ class F8Experts:
 
 
 class F8Decoder:
-    """Few-token forward of a layer whose experts are 8-bit (workspace owner)."""
+    """Few-token forward of a layer whose experts are 8-bit (workspace owner).
+
+    The workspace is the next call's too, so calls on several streams need one object
+    each, and so do graphs that may run at the same time."""
 
     def __init__(self, shape: Shape, experts: F8Experts):
         self.shape, self.experts = shape, experts

@@ -76,3 +76,12 @@ def test_first_expert():
     e = m.F8Experts(*[torch.zeros(1)] * 3, first_expert=1 << 32)
     assert e.c().first_expert == (1 << 31) - 1
     assert m.F8Experts(*[torch.zeros(1)] * 3, first_expert=-3).c().first_expert == -3
+
+
+@pytest.mark.parametrize("change", [dict(row_type=m.MOE_ROW_F32), dict(row_type=7), dict(groups=0), dict(n=1 << 21)])
+def test_weight_gradient_of_a_refused_shape(change):
+    """The class's own error, before its tensors are looked at."""
+    sizes = {**dict(groups=1, n=48, k=256, row_type=m.MOE_ROW_BF16), **change}
+    lin = m.F8Linear(m.F8Shape(**sizes), torch.empty(0, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="limits"):
+        lin.weight_gradient(torch.zeros((3, 256)), torch.zeros((3, 48)))
