@@ -54,7 +54,7 @@ class GradSet:
                     raise ValueError(f"{name} {i}: on {t.device}, expected {self.device}")
                 if t.dtype not in _TYPES:
                     raise ValueError(f"{name} {i}: {t.dtype}, expected bf16, fp16 or fp32")
-                if t.numel() and not _dense(t):
+                if t.numel() and not t.is_contiguous() and not _dense(t):
                     raise ValueError(f"{name} {i}: strides {t.stride()} of shape {tuple(t.shape)} "
                                      "are not dense")
             if o is not x and (o.dtype != x.dtype or o.shape != x.shape or
