@@ -576,9 +576,11 @@ int moe_w4_decode_fwd(const moe_shape *shape, const moe_w4_experts *experts,
  *
  * Limits: 1 <= groups <= 1024, 1 <= n, k <= 2^20; rows are bf16 or fp16
  * (row_type), of any n and k, strides in values of at least a row and at most
- * 2^32.  Row tensors need their type's alignment only.  A call that finds what it
- * writes among the rows, codes, scales or weights that it computes it from refuses
- * (from a tensor's first to its last value; moe_f8_linear looks more closely).  offsets (device, int32
+ * 2^32.  Row tensors need their type's alignment only.  Refused: results over the
+ * rows, codes or scales that they are computed from, and packed weights over what they
+ * are made from or the reverse (from a tensor's first to its last value; moe_f8_linear
+ * looks row by row).  Not looked for, and not allowed: a product's results over its
+ * packed weights or offsets, and a workspace over anything.  offsets (device, int32
  * [groups+1], ascending, at most `rows`; NULL with one group: all rows) say that
  * the rows of group g are [offsets[g], offsets[g+1]).  No entry point reads a host
  * copy of them, so all can be captured into a graph (with a workspace of its own
@@ -666,10 +668,13 @@ typedef struct moe_f8_experts {
 size_t moe_f8_decode_workspace_bytes(const moe_shape *shape);
 
 /* Few-token inference forward on 8-bit experts: moe_w4_decode_fwd with these
- * weights, its arguments, limits and rounding (H, I and the shared I multiples of
- * 64).  Activations stay bf16: with few tokens the weights' bytes are the cost, and
- * the rows are not rounded to 8 bits.  One token with supplied routing takes two
- * launches. */
+ * weights, its arguments and limits (H, I and the shared I multiples of 64; packed
+ * matrices on 16 bytes).  Activations stay bf16: with few tokens the weights' bytes are the
+ * cost, and the rows are not rounded to 8 bits.  As there the hidden rows are rounded to
+ * bf16 once, their routing weight included, and are the down product's operand: with the
+ * output's own rounding (1.7e-3 of the outputs' norm) that makes 2.4e-3.  Sums are fp32, the
+ * codes' unscaled over 128 values: |x| and hidden values past 2^128 / (448 128) can
+ * overflow there.  One token with supplied routing takes two launches. */
 int moe_f8_decode_fwd(const moe_shape *shape, const moe_f8_experts *experts,
                       const uint16_t *x, const uint16_t *w_router,
                       const float *bias, const int32_t *topk_idx_in,
@@ -681,13 +686,15 @@ int moe_f8_decode_fwd(const moe_shape *shape, const moe_f8_experts *experts,
 /* What a training step does next with the gradients that moe_layer_bwd and
  * moe_f8_wgrad leave: their norm over all tensors together, and
  *
- *   out = x * min(1, max_norm / (norm + 1e-6)), rounded once.
+ *   out = x * min(1, max_norm / (norm + 1e-6)).
  *
- * Squares and their sums are held in 64 bits.  A norm that is not finite is not
+ * Squares and their sums are held in 64 bits; the coefficient is rounded to fp32, and so is
+ * its product with a value, before that goes to a 16-bit type.  A norm that is not finite is not
  * caught: an infinite one gives zeros (and NaN for the infinities), NaN gives NaN.
  * Tensors are dense runs of numel values, of their type's alignment; out is x (in
- * place) or does not overlap any x, and no value is named twice.  The list is host
- * memory, read during the call. */
+ * place) or does not overlap any x, and no value is named twice: the caller's duty, of
+ * which a call looks at each tensor's out against its own x only (values named twice may
+ * be scaled twice).  The list is host memory, read during the call. */
 enum { MOE_NORM_2 = 0, MOE_NORM_INF = 1 };
 
 typedef struct moe_grad_tensor {

@@ -72,8 +72,7 @@ int check_rows(const F8Dims &d, int32_t rows, const int32_t *offsets) {
 
 int check_wgrad(const F8Dims &d, int32_t rows) {
   if (rows < 0) return MOE_ERR_INVALID_ARG;
-  // a tile's codes of one operand, of all stages, are addressed in 31 bits, and stages are
-  // a grid's dimension; tiles as in check_rows
+  // stages are a grid's dimension; tiles as in check_rows
   if (f8_stages(rows, d.groups) > 65535 ||
       (int64_t)d.groups * ((d.k + 127) / 128) * ((d.n + 255) / 256) >= kMostTiles)
     return MOE_ERR_UNSUPPORTED;

@@ -9,16 +9,18 @@
 // sums the 128 products of a block from zero, and the scales multiply that sum in fp32.
 //
 // What bounds it: at 16384 rows x 4096 x 7168 in 6 groups 510 to 524 us with the
-// rows' quantising (59), 2.1 PFLOP/s in the product, where the library's 8-bit product with one
-// scale a tensor takes 308 us.  The chip runs these products at a reduced clock (1.5 GHz
-// here, 2.2 in a loop of matrix instructions alone), so that every instruction between
-// them counts twice; a stage takes 2870 cycles where its matrix instructions take 2048.
-// In registers alone, without loads, the instruction reaches 4.7 PFLOP/s, 4.3 with a
-// multiply-add for each of its results as the forward has, and 3.2 with two operations as
-// the weight gradient has, whose scales differ along both sides: there 570 of 685 us (962
-// GFLOP), 4040 cycles a stage.  64 groups of 384 rows x 2816 x 2048: 228 us, 27 of a
-// tile's 35 us in the loop and the rest its offsets, first loads and results; half-empty
-// last tiles cost the rest.
+// rows' quantising (59), 2.0 PFLOP/s in the product, where the library's 8-bit product with one
+// scale a tensor takes 308 us.  Of the cycles in which a CU has work (80 % of the launch: the
+// last of five rounds of tiles is a fifth full) the matrix unit is busy in 61 %, and the other
+// vector instructions, 5 for each product, take 38: the two hardly overlap, though without
+// loads, in registers alone, the instruction reaches 4.7 PFLOP/s, and 4.3 with a multiply-add
+// for each of its results.  The weight gradient's scales differ along both sides, two
+// operations a result (3.2 PFLOP/s in registers) and 10 vector instructions a product: 572 of
+// 672 us (962 GFLOP), 43 % and 54 % of the busy cycles.  Reads of LDS take a quarter of
+// them in both, at 4 cycles each, conflicts 2 and 4 % of those.  64 groups of 384 rows x 2816
+// x 2048: 221 to 228 us, 39 % and 34 %, the waves waiting 39 % of their time: 27 of a tile's
+// 35 us are its loop and the rest its offsets, first loads and results; half-empty last tiles
+// cost the rest.
 // Tried and not faster: the groups' last tiles last (254 us of 230: their weights are not
 // in the cache then), tiles of 64 rows, four waves a SIMD (spills), 128 outputs a tile
 // (1024 rows x 4096 x 4096 32 us of 37, but 57 of 46 at 2048 rows).

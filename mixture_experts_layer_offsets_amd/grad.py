@@ -32,7 +32,7 @@ class GradSet:
     by being the same tensor, raise ValueError.  The tensors and their memory are kept
     alive here; where gradients are new tensors every step, so is their set.  A tensor
     that is given other memory afterwards (``t.data = ...``) ends the set: the calls of
-    GradClip, and ``check``, raise ValueError then.  ``c`` itself does not look (60 ns a
+    GradClip, and ``check``, raise ValueError then.  ``c`` itself does not look (40 ns a
     tensor): it names the memory that the tensors had.
     """
 
