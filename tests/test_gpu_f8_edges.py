@@ -129,3 +129,55 @@ def test_small_scales_of_a_weight_gradient(M, sx, sy):
     want, bound = fo.weight_gradient(x.float().numpy(), dy.float().numpy())
     tol = fo.rounded(want, bound, BF) + (-(-M // 128) * SMALL if sx - 1 + sy - 1 < -126 else 0.0)
     within("dw", lin.weight_gradient(x.cuda(), dy.cuda())[0], want, tol)
+
+
+# Whole codes up to 15, and a 448 that gives every block the scale 1: a block's products are
+# whole numbers below 2^13 and their sums below 2^17, which the matrix unit keeps.  What is
+# left are the fp32 roundings of the scaled sums, without the bound's share of the unit.
+
+def whole(rng, *shape):
+    return rng.integers(-15, 16, shape).astype(np.float32)
+
+
+def exact_within(name, got, blocks, scales, dtype):
+    """blocks: sums of a block's products [..][block], scales the same shape."""
+    terms = blocks * scales
+    y, size = terms.sum(-1), np.abs(terms).sum(-1)
+    within(name, got, y, fo.rounded(y, (blocks.shape[-1] + 24) * fo.ULP * size, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("M,n,k", [(1, 40, 7168), (8, 300, 2000), (24, 5120, 390), (60, 15360, 390), (200, 256, 390),
+                                   (300, 512, 7168), (600, 5120, 2560), (3000, 2304, 390)])
+def test_whole_codes(M, n, k, dtype):
+    rng = np.random.default_rng([M, n, k])
+    x, w = whole(rng, M, k), whole(rng, n, k)
+    x[:, ::128] = 448
+    scales = np.exp(rng.uniform(-12, -10, (-(-n // 128), -(-k // 128)))).astype(np.float32)
+    codes = torch.from_numpy(w).to(torch.float8_e4m3fn).view(torch.uint8)
+    lin = m.F8Linear.pack(m.F8Shape(1, n, k, ROW[dtype]), codes[None].cuda(), torch.from_numpy(scales)[None].cuda())
+    note(f"f8 whole codes rows={M} n={n} k={k} {dtype}")
+    got = lin(torch.from_numpy(x).to(dtype).cuda())
+    part = rng.permutation(M)[:32]
+    sums = np.matmul(fo.blocks(x[part], 1).transpose(1, 0, 2).astype(np.float64),
+                     fo.blocks(w, 1).transpose(1, 2, 0).astype(np.float64)).transpose(1, 2, 0)
+    exact_within("y", got[torch.from_numpy(part).cuda()], sums,
+                 np.repeat(scales.astype(np.float64), 128, 0)[:n][None], dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("M,n,k", [(300, 64, 64), (420, 2304, 520), (1000, 300, 272), (1000, 20000, 300), (9000, 130, 300)])
+def test_whole_codes_of_a_weight_gradient(M, n, k, dtype):
+    """Rows 0 and 1 of every block hold the 448s, where the other operand has zeros."""
+    rng = np.random.default_rng([M, n, k, 1])
+    x, dy = whole(rng, M, k), whole(rng, M, n)
+    x[::128], dy[::128], x[1::128], dy[1::128] = 448, 0, 0, 448
+    sx, sy = (2.0 ** -rng.integers(4, 8, c) for c in (k, n))  # a column's own scale
+    lin = m.F8Linear(m.F8Shape(1, n, k, ROW[dtype]), torch.empty(0, dtype=torch.uint8, device="cuda"))
+    note(f"f8 whole codes, weight gradient {M} rows n={n} k={k} {dtype}")
+    got = lin.weight_gradient(*(torch.from_numpy((v * s).astype(np.float32)).to(dtype).cuda()
+                                for v, s in ((x, sx), (dy, sy))))[0]
+    cols = rng.permutation(n)[:128]
+    xb, yb = (fo.blocks(v.T, 1).transpose(1, 0, 2).astype(np.float64) for v in (x, dy[:, cols]))
+    sums = np.matmul(xb, yb.transpose(0, 2, 1)).transpose(1, 2, 0)
+    exact_within("dw", got[:, torch.from_numpy(cols).cuda()], sums, (sx[:, None] * sy[cols])[..., None], dtype)
